@@ -214,7 +214,7 @@ def prepare(case, seed):
          "cu": torch.cat([torch.zeros(1, dtype=torch.int64), torch.cumsum(new, 0)]).to(torch.int32).to(DEV),
          "most_new": int(new.max()), "heads": (Hq, case["kv_heads"], d)}
     # a server keeps one scratch buffer for its attention calls
-    s["workspace"] = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+    s["workspace"] = torch.empty(256 << 20, dtype=torch.uint8, device=DEV)
     return s
 
 

@@ -26,6 +26,7 @@ GDN_BF16, GDN_F32 = 0, 1
 GDN_CONV_DIM_FIRST, GDN_CONV_TAP_FIRST = 0, 1
 GDN_GATE_FUSED, GDN_GATE_DIRECT = 0, 1
 GDN_DEVERR_SLOT_RANGE, GDN_DEVERR_SEQLENS, GDN_DEVERR_TIMEOUT = 1, 2, 4
+GDN_DEVERR_BLOCKS, GDN_DEVERR_BLOCK_RANGE = 8, 16
 GDN_TEST_FAULT_NONE, GDN_TEST_FAULT_DECODE_CONSUMER, GDN_TEST_FAULT_PREFILL_PASS = 0, 1, 2
 GDN_ACT_SILU, GDN_ACT_SIGMOID = 0, 1
 
@@ -56,6 +57,11 @@ class Dims:
 
     def c(self, state_bf16: bool = False) -> gdn_dims:
         return gdn_dims(self.Hk, self.Hv, self.dk, self.dv, self.W, int(bool(state_bf16)))
+
+
+class gdn_cache_dims(ctypes.Structure):
+    _fields_ = [("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32)]
 
 
 class gdn_output_gate(ctypes.Structure):
@@ -130,6 +136,17 @@ def lib():
         L.gdn_graph_launch.argtypes = [P, P]
         L.gdn_graph_destroy.restype = None
         L.gdn_graph_destroy.argtypes = [P]
+        I64, SZ = ctypes.c_int64, ctypes.c_size_t
+        L.gdn_cache_tables.restype = I32
+        L.gdn_cache_tables.argtypes = [P, P, I32, P, I32, P, I32, P, P, I32, I32, P, P, P, P, P, P]
+        L.gdn_cache_append.restype = I32
+        L.gdn_cache_append.argtypes = [P, I64, P, I64, P, I32, P, P, P, P, I32, gdn_cache_dims, P,
+                                       P]
+        L.gdn_attn_decode_workspace_size.restype = SZ
+        L.gdn_attn_decode_workspace_size.argtypes = [I32, I32, gdn_cache_dims]
+        L.gdn_attn_decode.restype = I32
+        L.gdn_attn_decode.argtypes = [P, I64, P, P, P, P, I32, P, I32, P, I32, gdn_cache_dims, F, P,
+                                      P, SZ, P, P]
         L.gdn_validate_slots.restype = I32
         L.gdn_validate_slots.argtypes = [P, I32, I32]
         L.gdn_status_string.restype = ctypes.c_char_p
@@ -277,6 +294,96 @@ def gdn_mixed_step(mixed_qkv, a, b, A_log, dt_bias, conv_weight, conv_bias, conv
         _ptr(has_initial_state), N, T, ssm_state.shape[0], _sdims(dims, ssm_state),
         float(scale), int(bool(qk_l2norm)), int(chunk), _gate(gate), _ptr(out), _dt(out),
         _ptr(workspace), ws_bytes, _ptr(err), _stream(stream)))
+
+
+# ------------------------------------------------- paged 8-bit cache and its attention
+
+def _rows(t):
+    """(pointer, elements from one token to the next) of a [tokens, heads, d] bf16 tensor whose
+    heads are dense; the token stride is free (a slice of a wider projection)."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError("a bfloat16 tensor [tokens, heads, d] is expected")
+    if t.numel() == 0:
+        return None, t.shape[1] * t.shape[2]
+    if not t.is_cuda:
+        raise ValueError("device tensors expected")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError("the heads of a token must be dense")
+    step = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+    return ctypes.c_void_p(t.data_ptr()), step
+
+
+def _want(t, dtype, shape, name):
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, q_heads=None):
+    """Checked pointers of the cache, its number of blocks and its gdn_cache_dims."""
+    if k_cache.dim() != 4 or k_cache.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise ValueError("the caches must be float8_e4m3fn (or its bytes) [num_blocks, Hkv, "
+                         "block_size, head_dim]")
+    NB, H, bs, d = k_cache.shape
+    return ([_ptr(k_cache), _want(v_cache, k_cache.dtype, k_cache.shape, "v_cache"),
+             _want(k_scale, torch.float32, (NB, H), "k_scale"),
+             _want(v_scale, torch.float32, (NB, H), "v_scale")],
+            NB, gdn_cache_dims(H if q_heads is None else q_heads, H, d, bs))
+
+
+def gdn_cache_tables(lens_old, lens_new, block_table, free_ring, pool, pool_out, cu_tokens,
+                     slot_map, positions, lens, block_size, *, err=None, stream=None):
+    """The step's block tables, slots and positions from its requests' lengths (include/gdn.h).
+    block_table [B, max_blocks], free_ring [num_blocks], pool and pool_out [2] (head, free
+    count): in place; writes cu_tokens [B + 1], slot_map and positions [capacity], lens [B]."""
+    i32, B = torch.int32, lens_old.shape[0]
+    T = slot_map.shape[0]
+    _check(lib().gdn_cache_tables(
+        _want(lens_old, i32, (B,), "lens_old"), _want(lens_new, i32, (B,), "lens_new"), B,
+        _want(block_table, i32, (B, block_table.shape[-1]), "block_table"),
+        block_table.shape[-1], _want(free_ring, i32, (free_ring.numel(),), "free_ring"),
+        free_ring.numel(), _want(pool, i32, (2,), "pool"), _want(pool_out, i32, (2,), "pool_out"),
+        int(block_size), T, _want(cu_tokens, i32, (B + 1,), "cu_tokens"),
+        _want(slot_map, i32, (T,), "slot_map"), _want(positions, i32, (T,), "positions"),
+        _want(lens, i32, (B,), "lens"), _ptr(err), _stream(stream)))
+
+
+def gdn_cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, *, err=None,
+                     stream=None):
+    """Writes k, v [T, Hkv, d] (bf16, any token stride) into the 8-bit cache at slot_map [T]."""
+    ptrs, NB, dims = _cache(k_cache, v_cache, k_scale, v_scale)
+    T = slot_map.shape[0]
+    if tuple(k.shape) != (T, dims.num_kv_heads, dims.head_dim) or k.shape != v.shape:
+        raise ValueError("k and v must be [tokens, Hkv, head_dim]")
+    (kp, ks), (vp, vs) = _rows(k), _rows(v)
+    _check(lib().gdn_cache_append(kp, ks, vp, vs, _want(slot_map, torch.int32, (T,), "slot_map"),
+                                  T, *ptrs, NB, dims, _ptr(err), _stream(stream)))
+
+
+def gdn_attn_decode_workspace_size(batch, max_blocks, num_q_heads, num_kv_heads, head_dim,
+                                   block_size) -> int:
+    return int(lib().gdn_attn_decode_workspace_size(
+        int(batch), int(max_blocks),
+        gdn_cache_dims(num_q_heads, num_kv_heads, head_dim, block_size)))
+
+
+def gdn_attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, out, workspace, *,
+                    scale=None, err=None, stream=None):
+    """Attention of one token per request over the 8-bit cache. q, out: [B, Hq, d] bf16 (q with
+    any token stride); scale: head_dim ** -0.5 if None."""
+    B, Hq, d = q.shape
+    ptrs, NB, dims = _cache(k_cache, v_cache, k_scale, v_scale, Hq)
+    if d != dims.head_dim:
+        raise ValueError("q and the cache differ in head_dim")
+    qp, qs = _rows(q)
+    _check(lib().gdn_attn_decode(
+        qp, qs, *ptrs, NB, _want(block_table, torch.int32, (B, block_table.shape[-1]), "block_table"),
+        block_table.shape[-1], _want(lens, torch.int32, (B,), "lens"), B, dims,
+        float(d ** -0.5 if scale is None else scale),
+        _want(out, torch.bfloat16, (B, Hq, d), "out"), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream)))
 
 
 class DecodeGraph:

@@ -126,6 +126,12 @@ typedef struct {
                                    call does not address are untouched, and the context stays
                                    usable (include/gdn_testing.h makes one wait run out) */
 
+#define GDN_DEVERR_BLOCKS 8       /* gdn_cache_tables: the pool of free blocks ran short (or its head or
+                                     count is out of range): the rows that it could not serve keep
+                                     their old length and get no slots */
+#define GDN_DEVERR_BLOCK_RANGE 16 /* a block or slot id that is not in the cache: its tokens are not
+                                     written, or not seen */
+
 /*
  * gdn_conv_update -- one decode step of the causal depthwise conv1d ([P1]
  * Summary, "The conv half of the decode step"; Notes, "The conv half").
@@ -366,6 +372,114 @@ gdn_status gdn_decode_graph_create(const void* mixed_qkv, const void* a, const v
                                    gdn_dtype out_dtype, int32_t* err, gdn_graph** graph_out);
 gdn_status gdn_graph_launch(gdn_graph* graph, void* stream);
 void gdn_graph_destroy(gdn_graph* graph);
+
+/*
+ * The attention side of a hybrid model's step. Models that hold GDN layers also hold layers of
+ * ordinary attention; these calls serve their cache next to the recurrent states above: the
+ * step's block tables, the writer of an 8-bit paged cache, and the attention that reads it for
+ * single tokens and for prompts. The conventions are those of the calls above: device pointers,
+ * no allocation, no synchronisation, work enqueued on `stream`, argument errors before any
+ * launch, graph-capturable, results that do not depend on the rest of the batch.
+ *
+ * Cache: k_cache and v_cache [num_blocks, Hkv, block_size, head_dim] in e4m3 (one byte, 1-4-3,
+ * largest value 448), k_scale and v_scale [num_blocks, Hkv] f32: an element stands for byte *
+ * scale of its block and head. Scales are positive and normal. A request's token at position p
+ * lies in block block_table[b, p / block_size] at offset p % block_size; its slot is
+ * block * block_size + offset.
+ */
+typedef struct {
+  int32_t num_q_heads;  /* Hq (a multiple of Hkv) */
+  int32_t num_kv_heads; /* Hkv */
+  int32_t head_dim;     /* d: 64, 128 or 256 */
+  int32_t block_size;   /* tokens of a block: 16, 32, 64 or 128 */
+} gdn_cache_dims;
+
+/*
+ * gdn_cache_tables -- the tables of a step from its requests' lengths, built on the GPU.
+ *
+ * Row b holds lens_old[b] tokens and is to hold lens_new[b]: more (its new tokens: one for a
+ * decode row, many for a prompt), fewer (speculation taken back) or none (a finished request).
+ * With n(l) = ceil(l / block_size):
+ *   - a row with n(new) > n(old) takes blocks from the head of the free ring, in row order, into
+ *     block_table[b, n(old) ..]; rows are served until the blocks that were free when the call
+ *     began run out: a row that needs more than is left is refused (GDN_DEVERR_BLOCKS), keeps its
+ *     length, and its new tokens get slot -1;
+ *   - a row with n(new) < n(old) puts block_table[b, n(new) .. n(old)) back at the ring's tail, in
+ *     row order. Its table entries stay as they are and mean nothing; the blocks can be
+ *     taken from the next call on;
+ *   - cu_tokens[b] is the number of new tokens of the rows before b (a refused row's among them);
+ *     new token t of row b has position lens_old[b] + t - cu_tokens[b] and its slot.
+ * A row with a length outside [0, max_blocks * block_size] sets GDN_DEVERR_SEQLENS and counts as
+ * empty.
+ *
+ *   lens_old, lens_new [batch] int32;  block_table [batch, max_blocks] int32, in place
+ *   free_ring  [num_blocks] int32, in place: a ring of block ids
+ *   pool       [2] int32: the ring's head (0 .. num_blocks - 1) and how many blocks are free
+ *   pool_out   [2] int32: the same after the call; may be `pool` itself
+ *   total_tokens  the size of slot_map and positions; entries past the step's new tokens are
+ *              filled with -1 (a padded step), and a step with more sets GDN_DEVERR_SEQLENS
+ *   cu_tokens  [batch + 1] int32;  slot_map, positions [total_tokens] int32 (NULL if 0)
+ *   lens       [batch] int32: each row's length after the call; may be lens_old or lens_new
+ * Supported: batch <= 8192. batch == 0 is a no-op.
+ */
+gdn_status gdn_cache_tables(const int32_t* lens_old, const int32_t* lens_new, int32_t batch,
+                            int32_t* block_table, int32_t max_blocks, int32_t* free_ring,
+                            int32_t num_blocks, const int32_t* pool, int32_t* pool_out,
+                            int32_t block_size, int32_t total_tokens, int32_t* cu_tokens,
+                            int32_t* slot_map, int32_t* positions, int32_t* lens, int32_t* err,
+                            void* stream);
+
+/*
+ * gdn_cache_append -- writes the step's keys and values into the cache, as 8-bit values with a
+ * scale per block and head.
+ *
+ * Tokens with consecutive slots of one block are written together; call them a run. Per run and
+ * kv head, with a = max |x| over the run's finite values:
+ *   s = max(a * (1/448), 2^-64, and, if the run does not start the block, the block's old scale)
+ *   byte = e4m3(x * (1/s)), rounded to nearest even, +-448 beyond that; NaN stays NaN
+ * and if s grew, the tokens before the run become e4m3((byte * s_old) * (1/s)). Everything is
+ * IEEE fp32, so the bytes are the same on every run and in every batch. A run that starts a block
+ * ignores what the block held, its scale included. Tokens must come in an order in which a
+ * block's run is contiguous (gdn_cache_tables gives it), and no block may be written by two runs.
+ *
+ *   k, v       [total_tokens] rows of Hkv * head_dim bf16, k_stride and v_stride elements apart
+ *              (slices of one projection are fine); 16-byte aligned, strides multiples of 8
+ *   slot_map   [total_tokens] int32; negative: the token is skipped; past the cache:
+ *              GDN_DEVERR_BLOCK_RANGE, skipped
+ *   k_cache, v_cache (16-byte aligned), k_scale, v_scale: in place. dims.num_q_heads is not used.
+ * total_tokens == 0 is a no-op.
+ */
+gdn_status gdn_cache_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                            const int32_t* slot_map, int32_t total_tokens, void* k_cache,
+                            void* v_cache, float* k_scale, float* v_scale, int32_t num_blocks,
+                            gdn_cache_dims dims, int32_t* err, void* stream);
+
+/*
+ * gdn_attn_decode -- attention of one token per request over the cache (the token's own key
+ * and value included: append first).
+ *
+ * Per request b and query head h (kv head h / (Hq / Hkv)), over its lens[b] cached tokens:
+ *   out[b, h] = sum_j softmax_j(scale * q[b, h] . k_j) v_j
+ * A request of length 0 (or with no readable block) gives zeros. A length outside [0, max_blocks *
+ * block_size] sets GDN_DEVERR_SEQLENS and is clamped. What lies in a block past the request's
+ * length is never used, NaN bytes included. Softmax statistics and sums are fp32; the
+ * probabilities are rounded to f16 for the product with V.
+ *
+ *   q          [batch] rows of Hq * head_dim bf16, q_stride elements apart (16-byte aligned, a
+ *              multiple of 8)
+ *   block_table [batch, max_blocks] int32;  lens [batch] int32
+ *   out        [batch, Hq, head_dim] bf16, 16-byte aligned
+ *   workspace  device scratch of >= gdn_attn_decode_workspace_size bytes, 256-byte aligned; its
+ *              contents on entry do not matter
+ * batch == 0 is a no-op.
+ */
+size_t gdn_attn_decode_workspace_size(int32_t batch, int32_t max_blocks, gdn_cache_dims dims);
+gdn_status gdn_attn_decode(const void* q, int64_t q_stride, const void* k_cache,
+                           const void* v_cache, const float* k_scale, const float* v_scale,
+                           int32_t num_blocks, const int32_t* block_table, int32_t max_blocks,
+                           const int32_t* lens, int32_t batch, gdn_cache_dims dims, float scale,
+                           void* out, void* workspace, size_t workspace_bytes, int32_t* err,
+                           void* stream);
 
 /*
  * gdn_validate_slots -- host-side check of a HOST slot table ([P1] Notes,

@@ -147,6 +147,11 @@ def lib():
         L.gdn_attn_decode.restype = I32
         L.gdn_attn_decode.argtypes = [P, I64, P, P, P, P, I32, P, I32, P, I32, gdn_cache_dims, F, P,
                                       P, SZ, P, P]
+        L.gdn_attn_prefill_workspace_size.restype = SZ
+        L.gdn_attn_prefill_workspace_size.argtypes = [I32, I32, I32, gdn_cache_dims]
+        L.gdn_attn_prefill.restype = I32
+        L.gdn_attn_prefill.argtypes = [P, I64, P, P, P, P, P, I32, P, I32, P, I32, I32,
+                                       gdn_cache_dims, F, P, P, SZ, P, P]
         L.gdn_validate_slots.restype = I32
         L.gdn_validate_slots.argtypes = [P, I32, I32]
         L.gdn_status_string.restype = ctypes.c_char_p
@@ -383,6 +388,32 @@ def gdn_attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, ou
         block_table.shape[-1], _want(lens, torch.int32, (B,), "lens"), B, dims,
         float(d ** -0.5 if scale is None else scale),
         _want(out, torch.bfloat16, (B, Hq, d), "out"), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream)))
+
+
+def gdn_attn_prefill_workspace_size(total_tokens, num_seqs, max_blocks, num_q_heads,
+                                    num_kv_heads, head_dim, block_size) -> int:
+    return int(lib().gdn_attn_prefill_workspace_size(
+        int(total_tokens), int(num_seqs), int(max_blocks),
+        gdn_cache_dims(num_q_heads, num_kv_heads, head_dim, block_size)))
+
+
+def gdn_attn_prefill(q, cu_tokens, k_cache, v_cache, k_scale, v_scale, block_table, lens, out,
+                     workspace, *, scale=None, err=None, stream=None):
+    """Causal attention of packed prompt tokens over the 8-bit cache, which holds them already.
+    q, out: [T, Hq, d] bf16 (q with any token stride); cu_tokens [B + 1], lens [B] int32."""
+    T, Hq, d = q.shape
+    B = lens.shape[0]
+    ptrs, NB, dims = _cache(k_cache, v_cache, k_scale, v_scale, Hq)
+    if d != dims.head_dim:
+        raise ValueError("q and the cache differ in head_dim")
+    qp, qs = _rows(q)
+    _check(lib().gdn_attn_prefill(
+        qp, qs, _want(cu_tokens, torch.int32, (B + 1,), "cu_tokens"), *ptrs, NB,
+        _want(block_table, torch.int32, (B, block_table.shape[-1]), "block_table"),
+        block_table.shape[-1], _want(lens, torch.int32, (B,), "lens"), B, T, dims,
+        float(d ** -0.5 if scale is None else scale),
+        _want(out, torch.bfloat16, (T, Hq, d), "out"), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream)))
 
 

@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(32 * NW) attn_decode_kernel(const __grid_const
             t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 4));
             t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 8));
             t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 16));
-            t = fmaxf(t, m[nt][x]);
+            t = t > m[nt][x] + 8.0f ? t : m[nt][x];  // by the head alone, whatever the others do
             const float corr = t == -INFINITY ? 1.0f : ex2(m[nt][x] - t);
             m[nt][x] = t;
             l[nt][x] *= corr;

@@ -76,6 +76,8 @@ constexpr int kMaxTableBatch = 8192;
 
 size_t attn_decode_workspace(int B, int max_blocks, int Hq, int H, int d, int bs);
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s);
+size_t attn_prefill_workspace(int T, int B, int max_blocks, int Hq, int H, int d, int bs);
+cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t s);
 
 // Tensor map of one cache pool as rows of d bytes, read in boxes of `rows` rows by
 // min(d, 128) bytes that land swizzled (128-byte pattern; 64-byte for d = 64) in shared memory.

@@ -135,4 +135,33 @@ gdn_status gdn_attn_decode(const void* q, int64_t q_stride, const void* k_cache,
   return from_cuda(gdn::launch_attn_decode(a, static_cast<cudaStream_t>(stream)));
 }
 
+size_t gdn_attn_prefill_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_t max_blocks,
+                                       gdn_cache_dims dims) {
+  if (total_tokens < 0 || num_seqs <= 0 || max_blocks <= 0 || check_cache(dims, 1, true) != GDN_OK) return 0;
+  return gdn::attn_prefill_workspace(total_tokens, num_seqs, max_blocks, dims.num_q_heads, dims.num_kv_heads,
+                                     dims.head_dim, dims.block_size);
+}
+
+gdn_status gdn_attn_prefill(const void* q, int64_t q_stride, const int32_t* cu_tokens,
+                            const void* k_cache, const void* v_cache, const float* k_scale,
+                            const float* v_scale, int32_t num_blocks, const int32_t* block_table,
+                            int32_t max_blocks, const int32_t* lens, int32_t num_seqs,
+                            int32_t total_tokens, gdn_cache_dims dims, float scale, void* out,
+                            void* workspace, size_t workspace_bytes, int32_t* err, void* stream) {
+  if (total_tokens < 0 || num_seqs < 0) return GDN_ERR_INVALID_ARG;
+  if (num_seqs == 0 || total_tokens == 0) return GDN_OK;
+  gdn::AttnArgs a;
+  const gdn_status st = check_attn(q, q_stride, k_cache, v_cache, k_scale, v_scale, num_blocks, block_table,
+                                   max_blocks, lens, num_seqs, dims, scale, out, workspace, err, a);
+  if (st != GDN_OK) return st;
+  if (!cu_tokens || !aligned(cu_tokens, 4)) return GDN_ERR_INVALID_ARG;
+  // a request's (token, head) rows are counted in 32 bits
+  if (static_cast<int64_t>(total_tokens) * dims.num_q_heads > 0x7fffffffLL - 65536) return GDN_ERR_UNSUPPORTED;
+  if (workspace_bytes < gdn_attn_prefill_workspace_size(total_tokens, num_seqs, max_blocks, dims))
+    return GDN_ERR_INVALID_ARG;
+  a.cu_tokens = cu_tokens;
+  a.T = total_tokens;
+  return from_cuda(gdn::launch_attn_prefill(a, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -482,6 +482,32 @@ gdn_status gdn_attn_decode(const void* q, int64_t q_stride, const void* k_cache,
                            void* stream);
 
 /*
+ * gdn_attn_prefill -- attention of prompt tokens over the cache, causal. Request b's new tokens
+ * are rows cu_tokens[b] .. cu_tokens[b + 1] of q; their keys and values are in the cache already
+ * (append first) as the last of its lens[b] tokens. With n new tokens, token i attends to
+ * positions 0 .. lens[b] - n + i; a token that sees nothing (lens[b] < n: its row was refused)
+ * gives zeros. Otherwise as gdn_attn_decode: the probabilities keep 8 significant bits for
+ * the product with V (two e4m3 parts), queries are exact to 2^-18 of a row's largest element. A NaN
+ * among a request's values reaches the rows that do not see it, too, if they share a 128-token tile.
+ *
+ *   q          [total_tokens] rows of Hq * head_dim bf16, q_stride elements apart
+ *   cu_tokens  [num_seqs + 1] int32, non-decreasing, at most total_tokens; rows of q outside it
+ *              are not read, and their out is not written (a padded step). A request whose
+ *              range is not within total_tokens sets GDN_DEVERR_SEQLENS and counts as empty
+ *   out        [total_tokens, Hq, head_dim] bf16, 16-byte aligned
+ *   workspace  device scratch of >= gdn_attn_prefill_workspace_size bytes, 256-byte aligned
+ * num_seqs == 0 or total_tokens == 0 is a no-op.
+ */
+size_t gdn_attn_prefill_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_t max_blocks,
+                                       gdn_cache_dims dims);
+gdn_status gdn_attn_prefill(const void* q, int64_t q_stride, const int32_t* cu_tokens,
+                            const void* k_cache, const void* v_cache, const float* k_scale,
+                            const float* v_scale, int32_t num_blocks, const int32_t* block_table,
+                            int32_t max_blocks, const int32_t* lens, int32_t num_seqs,
+                            int32_t total_tokens, gdn_cache_dims dims, float scale, void* out,
+                            void* workspace, size_t workspace_bytes, int32_t* err, void* stream);
+
+/*
  * gdn_validate_slots -- host-side check of a HOST slot table ([P1] Notes,
  * "State ABI": the goldens raise on an active index that is out of range or
  * repeated). Returns 0 if every active slot (> 0) is < num_slots and no

@@ -1,52 +1,59 @@
-// gdn_attn_decode.cu -- attention of single tokens over the 8-bit paged cache.
+// gdn_attn_decode.cu -- attention of single tokens over the 8-bit paged cache, on the tcgen05 tensor
+// cores.
 //
 // Per request b (len keys), kv head h and the G query heads that share it:
 //   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j - m),  k_j = ks * byte, v_j = vs * byte
 // with one ks, vs per (block, kv head). Bound by memory: every cached byte is read once
-// (2 d bytes per token and kv head) for 4 G operations per byte.
+// (2 d bytes per token and kv head) for 4 G operations per byte, so the kernel's job is to keep
+// copies in flight and to spend few instructions on a byte. It spends none: a tile of 128 keys goes by
+// TMA (page by page: pages end inside a tile) to shared memory and from
+// there, as 8-bit operands, into two products,
+//   S^T[key, head] = K Q^T  (M = 128 keys, N = query heads, K = d)
+//   O^T[d, head]  += V^T P^T (M = 128 of d, N = query heads, K = 128 keys),
+// keys and d on the 128-row side, the few query heads on the narrow one, so G <= 8 wastes nothing
+// that matters. K is used K-major and V MN-major, both as they lie in the page. A first version
+// that converted K and V to f16 for the warp-level instruction spent 640 instructions on 8 KB and stopped at
+// 5.1 TB/s (256 requests of about 8,000 tokens); this one spends about 60.
+//
+// Eight-bit queries and probabilities are split into parts, side by side in N: a query into two e4m3
+// values (scaled per head so that its largest element lies in [128, 256): exact down to 2^-18 of that),
+// a probability into four with factors 1, 1/16, 1/256, 1/4096 (16 bits, and 2^-22 of the largest). The running
+// maximum moves when a score passes it by 2^8 and the reference for vs when one passes it by 2, so that almost
+// only a unit's first tile stops for them: 0.87 p vs / vs_ref <= 448, the largest e4m3.
 //
 // Split. A (request, kv head) is cut into units of 256, 512 or 1,024 keys by its OWN length
-// (unit_keys), never by the batch: a row's result depends on its own inputs alone, bit for bit,
-// as for every other call of the library. A persistent grid walks the units; a unit's 16-key
-// groups are dealt to the CTA's warps. A request of one unit is finished in the kernel, a longer
-// one leaves fp32 partial sums (with their maximum and sum) that a second, programmatically
-// dependent kernel joins in unit order.
+// (unit_keys), never by the batch: a row's result depends on its own inputs alone, bit for bit, as
+// for every other call of the library. A persistent grid walks the units. A request of one unit is
+// finished here, a longer one leaves fp32 partial sums (with their maximum and sum) that a second,
+// programmatically dependent kernel joins in unit order.
 //
-// A warp works on its own: it fetches its groups by TMA into a private ring (rows of d bytes,
-// hardware swizzle), so nothing in the loop waits for another warp, and the next unit's keys are
-// in flight while this one is joined. Groups are 16 keys because the smallest block is 16 tokens:
-// a group never crosses a block, so it has one page, one ks and one vs.
-//
-// Products on the warp-level f16 tensor instruction (16 x 8 x 16). A decode step has at most 8
-// (or 16) query rows per kv head; the 128-row tcgen05 tile would be over 90% padding, and the
-// kernel needs 4 G operations per byte, a few percent of even the warp-level rate. The keys are the
-// 16-row operand and the query heads the 8-wide one, so G <= 8 wastes nothing:
-//   S^T[key, head] = K Q^T,  O^T[d, head] = V^T P^T.
-// Both operands come from the bytes with exact conversions (e4m3 -> f16). Any order of the d
-// (and of the keys) is right for a sum, so the fragments are taken in the order in which one
-// 16-byte load per lane delivers them: lane (r, j) reads the d-chunks j, j+4, .. of its key for
-// S^T, and the d-chunk r of keys 2j, 2j^5 (+8) for O^T. group_key() orders the keys so that with
-// the swizzle both loads are free of bank conflicts.
-//
-// Precision. Queries are scaled per head by a power of two (largest element in [1, 2)) and are
-// then exact in f16 down to 2^-24 of that element. Maxima, sums and accumulators are fp32. P is
-// rounded to f16 (11 bits; the output is bf16, 8 bits); it is taken relative to a running maximum
-// that moves only when a score passes it by 2^8, so P <= 2^8, and vs enters relative to the
-// largest vs seen within 2^4: |P| < 2^13 stays in f16's range.
+// Roles of a CTA: four softmax warps (thread = key, then thread = d), one warp that issues MMAs, one that
+// issues TMA, one that looks up pages and scales (four tiles at a time, a lane per 16 keys: a lookup is
+// two dependent loads from memory), one that converts queries a unit ahead. Scores of the next tile are
+// computed while this one's softmax runs; lookups and copies run ahead across units. A TMA instruction
+// takes about 60 cycles to issue whatever its box, so a whole page is one box (two for d = 256) and
+// only a request's last page goes in boxes of 16 keys.
 #include <cudaTypedefs.h>
 
-#include "gdn_cache.cuh"
+#include <atomic>
+
+#include "gdn_attn.cuh"
 #include "gdn_internal.h"
-#include "gdn_ptx.cuh"
 
 namespace gdn {
 
+namespace {
+
 cudaError_t encode_cache_map(CUtensorMap* map, const uint8_t* cache, int64_t total_rows, int d, int rows) {
-  void* fn = nullptr;
-  cudaDriverEntryPointQueryResult found;
-  cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
-  if (e != cudaSuccess) return e;
-  if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+  static std::atomic<void*> entry{nullptr};  // the driver's function, looked up once
+  void* fn = entry.load(std::memory_order_acquire);
+  if (!fn) {
+    cudaDriverEntryPointQueryResult found;
+    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+    entry.store(fn, std::memory_order_release);
+  }
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(total_rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d)};
   const cuuint32_t box[2] = {static_cast<cuuint32_t>(d < 128 ? d : 128), static_cast<cuuint32_t>(rows)};
@@ -54,178 +61,256 @@ cudaError_t encode_cache_map(CUtensorMap* map, const uint8_t* cache, int64_t tot
   const CUresult r = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)(
       map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(cache), dims, strides, box, step,
       CU_TENSOR_MAP_INTERLEAVE_NONE, d < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-      CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t encode_cache_maps(CacheMaps* maps, const AttnArgs& a) {
+  const int64_t rows = static_cast<int64_t>(a.num_blocks) * a.H * a.bs;
+  cudaError_t e = encode_cache_map(&maps->k_group, a.k_cache, rows, a.d, kGroup);
+  if (e == cudaSuccess) e = encode_cache_map(&maps->v_group, a.v_cache, rows, a.d, kGroup);
+  if (e == cudaSuccess) e = encode_cache_map(&maps->k_page, a.k_cache, rows, a.d, a.bs);
+  if (e == cudaSuccess) e = encode_cache_map(&maps->v_page, a.v_cache, rows, a.d, a.bs);
+  return e;
 }
 
 namespace {
 
-constexpr int kGroup = 16;          // keys of one group
 constexpr int kMaxUnitKeys = 1024;
-constexpr int kBatchPerLaunch = 2048;  // requests of one launch (their unit counts stay in shared memory)
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kBatchPerLaunch = 384;   // requests of one launch (their lengths stay in shared memory)
+constexpr int kCoarse = 16;            // requests between two kept tile sums
+constexpr int kThreads = 32 * 8;
+constexpr int kSmemPerSm = 228 * 1024;  // 1 KB of it taken by each resident CTA
+constexpr float kRise = 8.0f;          // log2 of what a score may pass the running maximum by
 
-// Keys of one unit of a request of `len` keys.
-__host__ __device__ __forceinline__ int unit_keys(int len) {
-  return len <= 4096 ? 256 : len <= 8192 ? 512 : kMaxUnitKeys;
-}
+// log2 of the keys of one unit of a request of `len` keys, and its units.
+__host__ __device__ __forceinline__ int unit_shift(int len) { return len <= 2048 ? 8 : len <= 8192 ? 9 : 10; }
 __host__ __device__ __forceinline__ int units_of(int len) {
-  const int u = unit_keys(len);
-  return (len + u - 1) / u;
+  const int s = unit_shift(len);
+  return (len + (1 << s) - 1) >> s;
 }
 // The most units that any length up to `cap` has.
 int64_t most_units(int64_t cap) {
-  if (cap <= 4096) return (cap + 255) / 256;
-  return cap <= 16384 ? 16 : (cap + kMaxUnitKeys - 1) / kMaxUnitKeys;
+  if (cap <= 2048) return (cap + 255) / 256;
+  if (cap <= 4096) return 8;
+  return cap <= 8192 ? (cap + 511) / 512 : cap <= 16384 ? 16 : (cap + kMaxUnitKeys - 1) / kMaxUnitKeys;
 }
-
-// The key, within a group, of fragment row r (0..7; rows 8..15 are 8 keys on). With 128-byte
-// rows and the hardware swizzle (16-byte chunk ^ (row mod 8)), rows r and r + 1 have to differ in
-// chunk bit 2 for S^T's loads and rows 0, 2, 4, 6 in chunk bits 1, 2 for O^T's.
-__device__ __forceinline__ int group_key(int r) { return (r & 6) ^ ((r & 1) * 5); }
-
-template <int D>
-__device__ __forceinline__ uint32_t tile_at(int key, int chunk) {  // byte of a 16-byte chunk of a row
-  if (D == 64) return key * 64 + ((chunk ^ ((key >> 1) & 3)) << 4);
-  return (chunk >> 3) * (kGroup * 128) + key * 128 + (((chunk & 7) ^ (key & 7)) << 4);
-}
-
-__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int row, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
-          "r"(dst), "l"(map), "r"(x), "r"(row), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-// the low and the high e4m3 pair of a word as f16 pairs
-__device__ __forceinline__ void to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b;}"
-      : "=r"(lo), "=r"(hi) : "r"(w));
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-  return r;
-}
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float bf2f_(uint32_t h) { return __uint_as_float(h << 16); }
 
 struct DecodeParams {
   AttnArgs a;
   int heads;      // query heads of one unit: min(G, 16)
   int chunks;     // units' head chunks per kv head: ceil(G / 16)
   int b0, nb;     // the launch's requests
-  int32_t* pre;   // workspace: [nb + 1] units before request b (of one kv head and chunk)
-  float2* ml;     // [units][heads] (maximum, sum) of a unit that is one of several
-  float* part;    // [units][heads][D]
+  int each;       // the most units of a request's (kv head, chunk): unit u of it has slot (b * HC + hc) * each + u
+  float2* ml;     // workspace: [slots][heads] (maximum, sum) of a unit that is one of several
+  float* part;    // [slots][heads][D]
 };
 
-template <int D, int NT, int NW>
+__host__ __device__ constexpr int tmem_columns(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : n <= 256 ? 256 : 512; }
+
+// HP: the unit's query heads, padded to 4, 8 or 16.
+template <int D, int HP>
 struct DecodeCfg {
-  static constexpr int kThreads = 32 * NW;
-  static constexpr int kStage = 2 * kGroup * D;                  // a group's keys and values
-  static constexpr int kStages = D == 64 ? 4 : 2;
-  static constexpr int kRing = NW * kStages * kStage;
-  static constexpr int kHeadStride = D + 4;                      // floats; padded against bank conflicts
-  static constexpr int kJoin = NW * 8 * kHeadStride * 4;
-  static constexpr int kSlots = kMaxUnitKeys / (kGroup * NW);    // a warp's group slots of the longest unit
-  static constexpr int kInfo = NW * 64 * 16;
-  static constexpr int kMl = NW * (8 * NT * 2 + 1) * 4;
-  static constexpr int kFixed = kRing + kJoin + kInfo + ((kMl + 15) & ~15) + NW * kStages * 8;  // then pre[nb + 1]
-  static constexpr int kAlign = 1024;                            // the swizzle repeats every 1,024 bytes
-  static_assert(kSlots <= 32, "a batch of 32 lanes covers whole units");
+  static constexpr int kNQ = HP == 16 ? 32 : 16;                 // columns of S^T: high parts, low parts
+  static constexpr int kNP = 4 * HP;                             // columns of O^T: four parts
+  static constexpr int kHalves = D == 256 ? 2 : 1;               // of d, 128 rows each
+  // Tiles of keys or values in the ring: two CTAs an SM (their latencies overlap) with 96 KB each where they fit.
+  static constexpr int kStages = D == 256 ? (HP == 16 ? 6 : 3) : HP == 16 ? 5 : 6;
+  static constexpr int kStage = Tile<D>::kBytes;
+  static constexpr int kQ = kNQ * D;
+  static constexpr int kP = kTile * kNP;
+  static constexpr int kBatch = 4;                               // tiles looked up at a time
+  static constexpr int kBatches = 4;                             // batches that are kept
+  static constexpr int kInfoRing = kBatch * kBatches;
+  static constexpr int kFactorRing = 4;                          // units whose query factors are kept
+  static constexpr int kColumns = tmem_columns(2 * kNQ + kHalves * kNP);
+  static constexpr int kO = 2 * kNQ;                             // first column of O^T
+  // shared memory, after alignment to 1,024 bytes (the swizzle repeats)
+  static constexpr int kAtQ = kStages * kStage;
+  static constexpr int kAtP = kAtQ + 2 * kQ;
+  static constexpr int kAtScale = kAtP + kP;
+  static constexpr int kAtRow = kAtScale + kInfoRing * kGroups * 8;
+  static constexpr int kAtKeys = kAtRow + kInfoRing * kGroups * 4;
+  static constexpr int kAtFactor = kAtKeys + kInfoRing * 4;
+  static constexpr int kAtRed = kAtFactor + kFactorRing * 16 * 4;
+  static constexpr int kBars = 2 * kStages + 2 * kBatches + kFactorRing + 11;
+  static constexpr int kAtBars = kAtRed + 4 * 16 * 4;
+  static constexpr int kAtPre = kAtBars + kBars * 8;             // then lens[nb], tsum[nb / kCoarse + 2]
+  static constexpr int kSmem = 1024 + kAtPre;
+  static_assert(kAtBars % 8 == 0 && kQ % 1024 == 0, "alignment");
 };
 
-// One unit of the launch: request, kv head, head chunk, its first key and the keys it holds.
-struct Unit {
-  int b, h, chunk, first, keys, index, count;  // index: the unit's place in its request's `count`
-};
+// The units of one CTA, in order: those whose first tile lies in its equal share of the launch's tiles (all
+// requests, kv heads and head chunks end to end). A share holds whole units, so CTAs differ by a unit's
+// tiles at most, and neighbours in a CTA are neighbours in memory.
+struct Walk {
+  const int32_t* lens;
+  const int32_t* tsum;  // tiles before request kCoarse * i
+  int nb, end;
+  int H, chunks;
+  int b, h, chunk, index;  // request, kv head, head chunk, the unit's place in its (request, head, chunk)
+  int len, shift, count;   // the request's keys, log2 of the keys of a unit, units
+  int pos;              // the unit's first tile
 
-__device__ __forceinline__ Unit find_unit(const int32_t* pre, int nb, int HC, int chunks, int f,
-                                          const int32_t* lens, int cap) {
-  int lo = 0, hi = nb - 1;  // the last request whose units start at or before f and that has some
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (static_cast<int64_t>(pre[mid]) * HC <= f) lo = mid; else hi = mid - 1;
+  __device__ __forceinline__ static int tiles_of(int len) { return (len + kTile - 1) / kTile; }
+  __device__ __forceinline__ void request() {
+    len = lens[b];
+    shift = unit_shift(len);
+    count = units_of(len);
   }
-  Unit u;
-  u.b = lo;
-  u.count = pre[lo + 1] - pre[lo];
-  const int rem = f - pre[lo] * HC;
-  const int hc = rem / u.count;
-  u.index = rem % u.count;
-  u.h = hc / chunks;
-  u.chunk = hc % chunks;
-  const int len = min(max(lens[lo], 0), cap);
-  const int uk = unit_keys(len);
-  u.first = u.index * uk;
-  u.keys = min(uk, len - u.first);
-  return u;
+  __device__ __forceinline__ void next_head() {
+    index = 0;
+    if (++chunk == chunks) {
+      chunk = 0;
+      ++h;
+    }
+    if (h == H) {
+      h = 0;
+      do ++b;
+      while (b < nb && lens[b] == 0);
+      if (b == nb) {
+        pos = end;
+        return;
+      }
+      request();
+    }
+  }
+  __device__ __forceinline__ void start(int share, int shares) {
+    const int HC = H * chunks;
+    const int all = tsum[(nb + kCoarse - 1) / kCoarse] * HC, each = all / shares, more = all - each * shares;
+    const int from = each * share + min(share, more);
+    end = from + each + (share < more);
+    pos = from;
+    if (from == end) return;
+    // the last request whose tiles start at or before `from`: not an empty one
+    int lo = 0;
+#pragma unroll 1
+    while ((lo + 1) * kCoarse < nb && tsum[lo + 1] * HC <= from) ++lo;
+    int before = tsum[lo];
+    b = lo * kCoarse;
+#pragma unroll 1
+    while ((before + tiles_of(lens[b])) * HC <= from) before += tiles_of(lens[b++]);
+    request();
+    const int tiles = tiles_of(len), rem = from - before * HC, ut = shift - 7;  // (a tile is 2^7 keys)
+    const int hc = rem / tiles, in = rem - hc * tiles;
+    h = hc / chunks;
+    chunk = hc - h * chunks;
+    index = (in + (1 << ut) - 1) >> ut;
+    pos += min(index << ut, tiles) - in;
+    if (index == count) next_head();
+  }
+  __device__ __forceinline__ bool more() const { return pos < end; }
+  __device__ __forceinline__ void next() {
+    pos += tiles();
+    if (++index == count) next_head();
+  }
+  __device__ __forceinline__ int first() const { return index << shift; }
+  __device__ __forceinline__ int keys() const { return min(1 << shift, len - first()); }
+  __device__ __forceinline__ int tiles() const { return (keys() + kTile - 1) / kTile; }
+};
+
+__device__ __forceinline__ bool any_of_128(bool x) {  // over the softmax warps
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<int>(x))
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void sync_128() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(x));
+  return r;
+}
+// two values to e4m3 (RNE); the values that the bytes stand for are taken off and the rest is scaled by 16
+__device__ __forceinline__ uint32_t split_off(float& a, float& b) {
+  uint32_t r, w;
+  asm("{.reg .b16 x; cvt.rn.satfinite.e4m3x2.f32 x, %3, %2; cvt.rn.f16x2.e4m3x2 %1, x; mov.b32 %0, {x, 0};}"
+      : "=r"(r), "=r"(w) : "f"(a), "f"(b));
+  float fa, fb;
+  asm("{.reg .b16 x, y; mov.b32 {x, y}, %2; cvt.f32.f16 %0, x; cvt.f32.f16 %1, y;}" : "=f"(fa), "=f"(fb) : "r"(w));
+  a = (a - fa) * 16.0f;
+  b = (b - fb) * 16.0f;
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[N]) {
+  if constexpr (N % 32 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 32) tmem_ld32(taddr + i, v + i);
+  } else {
+    static_assert(N == 16, "16 columns, or multiples of 32");
+    tc::tmem_ld16(taddr, v);
+  }
+  tc::tmem_wait_ld();
 }
 
-template <int D, int NT, int NW>
-__global__ void __launch_bounds__(32 * NW) attn_decode_kernel(const __grid_constant__ DecodeParams p,
-                                                              const __grid_constant__ CUtensorMap kmap,
-                                                              const __grid_constant__ CUtensorMap vmap) {
-  using C = DecodeCfg<D, NT, NW>;
+template <int D, int HP>
+__global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_constant__ DecodeParams p,
+                                                               const __grid_constant__ CacheMaps maps) {
+  using C = DecodeCfg<D, HP>;
+  using TL = Tile<D>;
+  using TQ = Tile<D, C::kNQ>;
   extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = smem_raw + (-smem_addr(smem_raw) & (C::kAlign - 1));
-  unsigned char* ring = smem;
-  float* join = reinterpret_cast<float*>(smem + C::kRing);
-  int4* info = reinterpret_cast<int4*>(smem + C::kRing + C::kJoin);
-  float* s_m = reinterpret_cast<float*>(smem + C::kRing + C::kJoin + C::kInfo);  // [NW][8 NT]
-  float* s_l = s_m + NW * 8 * NT;
-  float* s_vs = s_l + NW * 8 * NT;                                               // [NW]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kFixed - NW * C::kStages * 8);
-  int32_t* pre = reinterpret_cast<int32_t*>(smem + C::kFixed);                    // [nb + 1]
-  __shared__ int32_t s_scan[NW];
+  unsigned char* smem = smem_raw + (-smem_addr(smem_raw) & 1023u);
+  const uint32_t base = smem_addr(smem), s_q = base + C::kAtQ, s_p = base + C::kAtP;
+  float2* s_scale = reinterpret_cast<float2*>(smem + C::kAtScale);  // [tile % kInfoRing][group] (ks, vs)
+  int32_t* s_row = reinterpret_cast<int32_t*>(smem + C::kAtRow);    // [tile % kInfoRing][group] row of the cache
+  int32_t* s_keys = reinterpret_cast<int32_t*>(smem + C::kAtKeys);  // [tile % kInfoRing] keys of the tile, 0: no more
+  float* s_factor = reinterpret_cast<float*>(smem + C::kAtFactor);  // [unit % kFactorRing][16]
+  float* s_red = reinterpret_cast<float*>(smem + C::kAtRed);        // [warp][16]
+  int32_t* lens = reinterpret_cast<int32_t*>(smem + C::kAtPre);
+  int32_t* tsum = lens + p.nb;
+  const uint32_t b_full = base + C::kAtBars, b_empty = b_full + 8 * C::kStages, b_info = b_empty + 8 * C::kStages,
+                 b_infoe = b_info + 8 * C::kBatches, b_factor = b_infoe + 8 * C::kBatches, b_s = b_factor + 8 * C::kFactorRing, b_p = b_s + 16,
+                 b_pv = b_p + 8, b_qfull = b_pv + 16, b_qempty = b_qfull + 16, b_drain = b_qempty + 16;
+  __shared__ int32_t s_scan[kThreads / 32];
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_fail;
 
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int r = lane >> 2, j = lane & 3;
   const int cap = a.max_blocks * a.bs;
-  const int32_t* lens = a.lens + p.b0;
 
-  if (lane == 0)
-    for (int s = 0; s < C::kStages; ++s) mbar_init(smem_addr(&bars[warp * C::kStages + s]), 1);
+  if (tid < 4) prefetch_map(tid == 0 ? &maps.k_page : tid == 1 ? &maps.v_page : tid == 2 ? &maps.k_group : &maps.v_group);
+  if (tid == 0) {
+    for (int i = 0; i < 2 * C::kStages + 2 * C::kBatches + C::kFactorRing; ++i)
+      mbar_init(b_full + 8 * i, b_full + 8 * i >= b_infoe && b_full + 8 * i < b_factor ? 4 : 1);
+    mbar_init(b_s, 1);
+    mbar_init(b_s + 8, 1);
+    mbar_init(b_p, 128);
+    mbar_init(b_pv, 1);
+    mbar_init(b_pv + 8, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(b_qfull + 8 * i, 32);
+      mbar_init(b_qempty + 8 * i, 1);
+    }
+    mbar_init(b_drain, 1);
+    s_fail = 0;
+  }
   fence_mbar_init();
-  // units before each request
+  if (warp == 4) {
+    tc::tmem_alloc(&s_tmem, C::kColumns);
+    tc::tmem_relinquish();
+  }
+  // lengths, and tiles before every kCoarse-th request
   {
     int carry = 0, flags = 0;
-    for (int base = 0; base < p.nb; base += C::kThreads) {
-      const int b = base + tid;
+    for (int at = 0; at < p.nb; at += kThreads) {
+      const int b = at + tid;
       int len = 0;
       if (b < p.nb) {
-        len = lens[b];
+        len = a.lens[p.b0 + b];
         if (len < 0 || len > cap) flags = GDN_DEVERR_SEQLENS;
         len = min(max(len, 0), cap);
+        lens[b] = len;
       }
-      int v = units_of(len);
+      int v = Walk::tiles_of(len);
+      const int own = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xFFFFFFFFu, v, o);
@@ -234,386 +319,472 @@ __global__ void __launch_bounds__(32 * NW) attn_decode_kernel(const __grid_const
       if (lane == 31) s_scan[warp] = v;
       __syncthreads();
       int before = carry;
-      for (int w = 0; w < warp; ++w) before += s_scan[w];
-      if (b < p.nb) pre[b + 1] = before + v;
-      for (int w = 0; w < NW; ++w) carry += s_scan[w];
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += s_scan[w];
+        carry += s_scan[w];
+      }
+      if (b < p.nb && b % kCoarse == 0) tsum[b / kCoarse] = before + v - own;
       __syncthreads();
     }
-    if (tid == 0) pre[0] = 0;
+    if (tid == 0) tsum[(p.nb + kCoarse - 1) / kCoarse] = carry;
     if (flags && a.err && blockIdx.x == 0) atomicOr(a.err, flags);
   }
+  tc::fence_before_sync();
   __syncthreads();
-  if (blockIdx.x == 0)
-    for (int b = tid; b <= p.nb; b += C::kThreads) p.pre[b] = pre[b];
+  tc::fence_after_sync();
+  const uint32_t tmem = s_tmem;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may take its place
 
-  const int HC = a.H * p.chunks;
-  const int units = pre[p.nb] * HC;
   const int G = a.Hq / a.H;
-  const int mine = units > static_cast<int>(blockIdx.x)
-                       ? (units - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x)
-                       : 0;
-  const int nslots = mine * C::kSlots;  // this warp's group slots, empty ones among them
-  int4* my_info = info + warp * 64;
-  const uint32_t my_ring = smem_addr(ring) + warp * C::kStages * C::kStage;
-  const uint32_t my_bars = smem_addr(bars) + warp * C::kStages * 8;
-  int next = 0, issued = 0, consumed = 0;  // the slot to fetch next; groups fetched and used
-  bool ok = true;
+  __shared__ Walk s_walk;  // where every role starts
+  if (tid == 0) {
+    Walk w;
+    w.lens = lens;
+    w.tsum = tsum;
+    w.nb = p.nb;
+    w.H = a.H;
+    w.chunks = p.chunks;
+    w.start(blockIdx.x, gridDim.x);
+    s_walk = w;
+  }
+  __syncthreads();
+  auto walk = [&]() { return s_walk; };
+  // a unit's first query head, and its query heads
+  auto first_head = [&](const Walk& w) { return w.h * G + w.chunk * 16; };
+  auto unit_heads = [&](const Walk& w) { return min(p.heads, G - w.chunk * 16); };
+  auto wait = [&](uint32_t b, int parity) { return wait_or_fail(b, parity, &s_fail); };
+  // the ring's n-th use: keys of tile i are use 2 i, its values 2 i + 1
+  auto full = [&](int n) { return b_full + 8 * (n % C::kStages); };
+  auto empty = [&](int n) { return b_empty + 8 * (n % C::kStages); };
+  auto phase = [&](int n) { return (n / C::kStages) & 1; };
 
-  // Fetches ahead: every free stage gets the warp's next group. Slot n is group (n % kSlots) * NW + warp of
-  // the CTA's unit n / kSlots; 32 slots are looked up at a time, one per lane.
-  auto fetch = [&](int at) {
-    while (ok && next < nslots && issued - consumed < C::kStages && next < ((at >> 5) + 2) * 32) {
-      if ((next & 31) == 0) {
-        const int n = next + lane;
-        int4 e = make_int4(0, 0, 0, 0);  // row of the cache, keys, ks, vs
-        if (n < nslots) {
-          const Unit u = find_unit(pre, p.nb, HC, p.chunks, blockIdx.x + (n / C::kSlots) * gridDim.x, lens, cap);
-          const int key = ((n % C::kSlots) * NW + warp) * kGroup;
-          if (key < u.keys) {
-            const int pos = u.first + key;
-            const int page = a.block_table[static_cast<int64_t>(p.b0 + u.b) * a.max_blocks + pos / a.bs];
-            if (page >= 0 && page < a.num_blocks) {
-              e.x = (page * a.H + u.h) * a.bs + pos % a.bs;
-              e.y = min(kGroup, u.keys - key);
-              e.z = __float_as_int(a.k_scale[static_cast<int64_t>(page) * a.H + u.h]);
-              e.w = __float_as_int(a.v_scale[static_cast<int64_t>(page) * a.H + u.h]);
-            } else if (a.err) {
-              atomicOr(a.err, GDN_DEVERR_BLOCK_RANGE);  // a page that is none: its tokens are not seen
-            }
-          }
+  int copies = 0;  // of the copying warp
+  if (warp == 7) {
+    // ---- lookups: lane = (tile of the batch, 16-key group)
+    const int none = a.num_blocks * a.H * a.bs;  // a row past the cache: zeros
+    const int shift = 31 - __clz(a.bs);
+    Walk w = walk();
+    int t = 0;  // the next tile of the walk's unit
+    bool ok = true;
+    for (int batch = 0; ok; ++batch) {
+      int keys = 0, pos = 0, b = 0, h = 0;  // this lane's tile
+#pragma unroll 1
+      for (int j = 0; j < C::kBatch && w.more(); ++j) {
+        if (j == lane / kGroups) {
+          keys = min(kTile, w.keys() - t * kTile);
+          pos = w.first() + t * kTile + (lane % kGroups) * kGroup;
+          b = w.b;
+          h = w.h;
         }
-        my_info[n & 63] = e;
+        if (++t == w.tiles()) {
+          t = 0;
+          w.next();
+        }
+      }
+      const bool last = __shfl_sync(0xFFFFFFFFu, keys, 31) == 0;  // a batch with room left: the end is in it
+      int row = none;
+      float2 sc = make_float2(-1.0f, 0.0f);  // a page that is none, or no key: not seen
+      if ((lane % kGroups) * kGroup < keys) {
+        const int page = a.block_table[static_cast<int64_t>(p.b0 + b) * a.max_blocks + (pos >> shift)];
+        if (page >= 0 && page < a.num_blocks) {
+          const int64_t at = static_cast<int64_t>(page) * a.H + h;
+          sc = make_float2(a.k_scale[at], a.v_scale[at]);
+          row = (static_cast<int>(at) << shift) + (pos & (a.bs - 1));
+        } else if (a.err) {
+          atomicOr(a.err, GDN_DEVERR_BLOCK_RANGE);
+        }
+      }
+      const int slot = batch % C::kBatches;
+      ok = __all_sync(0xFFFFFFFFu, wait(b_infoe + 8 * slot, ((batch / C::kBatches) & 1) ^ 1));
+      if (!ok) break;
+      s_scale[slot * 32 + lane] = sc;
+      s_row[slot * 32 + lane] = row;
+      if (lane % kGroups == 0) s_keys[slot * C::kBatch + lane / kGroups] = keys;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_info + 8 * slot);
+      if (last) break;
+    }
+  } else if (warp == 5) {
+    // ---- copies: lane g < 8 has the 16-key group g of each tile
+    const int rows = a.bs;                                 // of a page
+    const bool head = ((lane * kGroup) & (rows - 1)) == 0; // the group starts a page
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      if (i % C::kBatch == 0) ok = __all_sync(0xFFFFFFFFu, wait(b_info + 8 * ((i / C::kBatch) % C::kBatches), (i / C::kInfoRing) & 1));
+      if (!ok) break;
+      const int keys = s_keys[i % C::kInfoRing];
+      if (keys == 0) break;
+      const int row = s_row[(i % C::kInfoRing) * kGroups + lane % kGroups];
+      const bool whole = ((lane * kGroup) & -rows) + rows <= keys;  // every token of the group's page is the request's
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        const int n = 2 * i + which;
+        ok = __all_sync(0xFFFFFFFFu, wait(empty(n), phase(n) ^ 1));
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(full(n), C::kStage);
+        __syncwarp();
+        if (lane < kGroups && (head || !whole)) {
+          const CUtensorMap* map = which ? (whole ? &maps.v_page : &maps.v_group) : (whole ? &maps.k_page : &maps.k_group);
+#pragma unroll
+          for (int x = 0; x < D; x += 128)
+            tma_rows(base + (n % C::kStages) * C::kStage + (x / 128) * TL::kHalf + lane * kGroup * TL::kRow, map, x, row, full(n));
+        }
+        copies = n + 1;
+      }
+    }
+  } else if (warp == 4) {
+    // ---- MMAs
+    constexpr uint32_t iqk = idesc_f8(128, C::kNQ, false, false), ipv = idesc_f8(128, C::kNP, true, true);
+    bool ok = true;
+    // descriptors but for their start address (bits 0 .. 13, in 16 bytes), which each MMA adds
+    const uint64_t dk = TL::desc(base, 16), dq = TQ::desc(s_q, 16), dv = TL::desc(base, 512), dp = tc::smem_desc(s_p, 128, kTile * 16);
+    auto k_off = [](int ks, int half) { return static_cast<uint64_t>((ks / (TL::kRow / 32)) * half + (ks % (TL::kRow / 32)) * 32) >> 4; };
+    int qi = 0;             // tiles whose scores are issued
+    Walk qw = walk();       // where that stands: unit,
+    int qk_k = 0, qk_t = 0; // its number, tile
+    auto qk = [&]() {       // scores of the next tile, if there is one
+      if (!qw.more()) return true;
+      if (qk_t == 0 && !wait(b_qfull + 8 * (qk_k & 1), (qk_k >> 1) & 1)) return false;
+      const int n = 2 * qi;
+      if (!wait(full(n), phase(n))) return false;
+      tc::fence_after_sync();
+      const bool last = qk_t + 1 == qw.tiles();
+      if (lane == 0) {
+        const uint64_t kt = dk + (n % C::kStages) * (C::kStage >> 4), qt = dq + (qk_k & 1) * (C::kQ >> 4);
+        const uint32_t d = tmem + C::kNQ * (qi & 1);
+#pragma unroll
+        for (int ks = 0; ks < D / 32; ++ks) mma_f8_ss(d, kt + k_off(ks, TL::kHalf), qt + k_off(ks, TQ::kHalf), iqk, ks > 0);
+        tc::mma_commit(b_s + 8 * (qi & 1));
+        tc::mma_commit(empty(n));
+        if (last) tc::mma_commit(b_qempty + 8 * (qk_k & 1));
+      }
+      __syncwarp();
+      ++qi;
+      ++qk_t;
+      if (last) {
+        qk_t = 0;
+        ++qk_k;
+        qw.next();
+      }
+      return true;
+    };
+    ok = qk();
+    int i = 0;
+    for (Walk w = walk(); ok && w.more(); w.next()) {
+      const int tiles = w.tiles(), keys = w.keys();
+      for (int t = 0; t < tiles; ++t, ++i) {
+        const int n = 2 * i + 1;
+        const uint32_t vt = base + (n % C::kStages) * C::kStage;
+        if (!(ok = qk())) break;
+        if (!(ok = wait(full(n), phase(n)))) break;
+        // keys past the request's length hold whatever their page holds, and 0 * NaN is not 0
+        const int from = keys - t * kTile;
+        if (from < kTile && (from & (kGroup - 1)) != 0) {
+          const int rows = kGroup - (from & (kGroup - 1));
+          for (int e = lane; e < rows * (D / 16); e += 32)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + TL::chunk_at(from + e / (D / 16), e % (D / 16))), "r"(0) : "memory");
+          tc::fence_async_smem();
+          __syncwarp();
+        }
+        if (!(ok = wait(b_p, i & 1))) break;
+        tc::fence_after_sync();
+        if (lane == 0) {
+#pragma unroll
+          for (int hf = 0; hf < C::kHalves; ++hf)
+#pragma unroll
+            for (int ks = 0; ks < kTile / 32; ++ks)
+              // (d = 64: rows 64 .. 127 of the product are not used; the leading offset only keeps them in the ring)
+              mma_f8_ss(tmem + C::kO + hf * C::kNP, dv + (n % C::kStages) * (C::kStage >> 4) + ((hf * TL::kHalf + ks * 32 * TL::kRow) >> 4),
+                        dp + ks * (512 >> 4), ipv, (t > 0) | ks);
+          tc::mma_commit(b_pv + 8 * (i & 1));
+          tc::mma_commit(empty(n));
+        }
         __syncwarp();
       }
-      const int4 e = my_info[next & 63];
-      if (e.y > 0) {
-        const int s = issued % C::kStages;
-        if (lane == 0) {
-          const uint32_t dst = my_ring + s * C::kStage, bar = my_bars + s * 8;
-          mbar_arrive_expect_tx(bar, C::kStage);
-#pragma unroll
-          for (int x = 0; x < D; x += 128) {
-            tma_rows(dst + x * kGroup, &kmap, x, e.x, bar);
-            tma_rows(dst + kGroup * D + x * kGroup, &vmap, x, e.x, bar);
-          }
-        }
-        ++issued;
-      }
-      ++next;
     }
-  };
-
-  for (int k = 0; k < mine; ++k) {
-    fetch(k * C::kSlots);
-    const int f = blockIdx.x + k * gridDim.x;
-    const Unit u = find_unit(pre, p.nb, HC, p.chunks, f, lens, cap);
-    const int head0 = u.h * G + u.chunk * 16;             // the unit's first query head
-    const int heads = min(p.heads, G - u.chunk * 16);
-
-    // queries: B fragments of Q^T, scaled per head to [1, 2)
-    uint32_t qf[NT][D / 16][2];
-    float qexp[NT];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int hd = nt * 8 + r;
-      const uint16_t* qp = a.q + static_cast<int64_t>(p.b0 + u.b) * a.q_stride + static_cast<int64_t>(head0 + hd) * D;
-      uint4 raw[D / 64][2];
-      uint32_t top = 0;
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          raw[c][x] = hd < heads ? *reinterpret_cast<const uint4*>(qp + (j + 4 * c) * 16 + x * 8) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {raw[c][x].x, raw[c][x].y, raw[c][x].z, raw[c][x].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+  } else if (warp == 6) {
+    // ---- queries: rows of Q, high parts then low parts, one unit ahead
+    bool ok = true;
+    int k = 0;
+    for (Walk w = walk(); w.more() && ok; w.next(), ++k) {
+      const int head0 = first_head(w), heads = unit_heads(w);
+      const uint16_t* qp = a.q + static_cast<int64_t>(p.b0 + w.b) * a.q_stride + static_cast<int64_t>(head0) * D;
+      ok = __all_sync(0xFFFFFFFFu, wait(b_qempty + 8 * (k & 1), ((k >> 1) & 1) ^ 1));
+      if (!ok) break;
+      const uint32_t qt = s_q + (k & 1) * C::kQ;
+      constexpr int kPer = D / 16;          // 16-element chunks of a head, one to a lane
+      constexpr int kAtOnce = 32 / kPer;    // heads at a time
+#pragma unroll 1
+      for (int h0 = 0; h0 < C::kNQ / 2; h0 += kAtOnce) {
+        const int hd = h0 + lane / kPer, c = lane % kPer;
+        uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (hd < heads) {
+          raw[0] = *reinterpret_cast<const uint4*>(qp + hd * D + c * 16);
+          raw[1] = *reinterpret_cast<const uint4*>(qp + hd * D + c * 16 + 8);
         }
-      }
-      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-      top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-      const int ex = min(max(static_cast<int>(top >> 7), 1), 254) - 127;  // exponent of the largest element
-      // a subnormal or non-finite largest element only loses the exact scaling, not its value
-      const float down = __int_as_float((min(max(127 - ex, 1), 254)) << 23);
-      qexp[nt] = 1.0f / down;
+        const uint32_t x[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+        uint32_t top = 0;
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        const uint32_t w[8] = {raw[c][0].x, raw[c][0].y, raw[c][0].z, raw[c][0].w,
-                               raw[c][1].x, raw[c][1].y, raw[c][1].z, raw[c][1].w};
+        for (int i = 0; i < 8; ++i) top = max(top, max(x[i] & 0x7FFFu, (x[i] >> 16) & 0x7FFFu));
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          qf[nt][c * 4 + i / 2][i & 1] = pack_f16(bf2f_(w[i] & 0xFFFFu) * down, bf2f_(w[i] >> 16) * down);
-      }
-    }
-    // the factor of heads 2j, 2j + 1
-    float hf[NT][2], m[NT][2], l[NT][2];
-    float acc[NT][D / 16][4];
-    float vs_ref = 0.0f;
+        for (int o = 1; o < kPer; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        const int e = min(max(static_cast<int>(top >> 7), 1), 254);  // 127 + exponent of the largest
+        const int down = min(max(127 + 7 - (e - 127), 1), 254);      // * 2^(7 - exponent)
+        const float sc = __int_as_float(down << 23);
+        const float put = a.scale < 0.0f ? -sc : sc;                 // the factor is kept positive
+        uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+        for (int i = 0; i < 4; ++i) {
+          float f[4], g[4];
+          f[0] = __uint_as_float(x[2 * i] << 16) * put;
+          f[1] = __uint_as_float(x[2 * i] & 0xFFFF0000u) * put;
+          f[2] = __uint_as_float(x[2 * i + 1] << 16) * put;
+          f[3] = __uint_as_float(x[2 * i + 1] & 0xFFFF0000u) * put;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        hf[nt][x] = __shfl_sync(0xFFFFFFFFu, qexp[nt], (2 * j + x) * 4) * a.scale * kLog2e;
-        m[nt][x] = -INFINITY;
-        l[nt][x] = 0.0f;
-      }
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) acc[nt][i][x] = 0.0f;
-    }
-
-    for (int i = 0; i < C::kSlots; ++i) {
-      const int at = k * C::kSlots + i;
-      fetch(at);
-      const int4 e = my_info[at & 63];
-      const int valid = e.y;
-      if (valid == 0) continue;
-      const int st = consumed % C::kStages;
-      if (ok && !mbar_wait_bounded(my_bars + st * 8, (consumed / C::kStages) & 1)) ok = false;
-      if (!__all_sync(0xFFFFFFFFu, ok)) {
-        ok = false;
-        break;
-      }
-      const uint32_t kt = my_ring + st * C::kStage, vt = kt + kGroup * D;
-      float s[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) s[nt][x] = 0.0f;
-      const int key = group_key(r);
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        const uint4 ka = lds128(kt + tile_at<D>(key, j + 4 * c));
-        const uint4 kb = lds128(kt + tile_at<D>(key + 8, j + 4 * c));
-        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          uint32_t a0, a1, a2, a3;
-          to_f16(wa[x], a0, a2);
-          to_f16(wb[x], a1, a3);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], a0, a1, a2, a3, qf[nt][c * 4 + x][0], qf[nt][c * 4 + x][1]);
-        }
-      }
-      const float ks = __int_as_float(e.z), vs = __int_as_float(e.w);
-      bool above = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          s[nt][x] *= hf[nt][x & 1] * ks;
-          if (key + (x & 2) * 4 >= valid) s[nt][x] = -INFINITY;
-          above |= s[nt][x] > m[nt][x & 1] + 8.0f;
-        }
-      if (__any_sync(0xFFFFFFFFu, above)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            float t = fmaxf(s[nt][x], s[nt][x + 2]);
-            t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 4));
-            t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 8));
-            t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 16));
-            t = t > m[nt][x] + 8.0f ? t : m[nt][x];  // by the head alone, whatever the others do
-            const float corr = t == -INFINITY ? 1.0f : ex2(m[nt][x] - t);
-            m[nt][x] = t;
-            l[nt][x] *= corr;
-#pragma unroll
-            for (int q = 0; q < D / 16; ++q) {
-              acc[nt][q][x] *= corr;
-              acc[nt][q][x + 2] *= corr;
-            }
+          for (int z = 0; z < 4; ++z) {
+            g[z] = __uint_as_float(__float_as_uint(f[z]) & 0xFFF00000u);  // sign, exponent, 3 bits
+            f[z] -= g[z];
           }
-      }
-      if (vs > vs_ref * 16.0f) {
-        const float down = vs_ref / vs;
-        vs_ref = vs;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int q = 0; q < D / 16; ++q)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) acc[nt][q][x] *= down;
-      }
-      const float rel = vs_ref > 0.0f ? __fdividef(vs, vs_ref) : 0.0f;
-      uint32_t pb[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float pr[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          pr[x] = ex2(s[nt][x] - m[nt][x & 1]);
-          l[nt][x & 1] += pr[x];
-          pr[x] *= rel;
+          hi[i] = e4m3x4(g[0], g[1], g[2], g[3]);
+          lo[i] = e4m3x4(f[0], f[1], f[2], f[3]);
         }
-        pb[nt][0] = transpose8x8(pack_f16(pr[0], pr[1]));
-        pb[nt][1] = transpose8x8(pack_f16(pr[2], pr[3]));
-      }
-      // values: keys past the last one hold whatever the page holds, and 0 * NaN is not 0
-      const int ke = 2 * j, ko = (2 * j) ^ 5;
-      const bool cut = valid < kGroup;
-      if (D >= 128) {
-#pragma unroll
-        for (int hh = 0; hh < D / 128; ++hh) {
-          uint4 v[4];
-          v[0] = lds128(vt + tile_at<D>(ke, hh * 8 + r));
-          v[1] = lds128(vt + tile_at<D>(ko, hh * 8 + r));
-          v[2] = lds128(vt + tile_at<D>(ke + 8, hh * 8 + r));
-          v[3] = lds128(vt + tile_at<D>(ko + 8, hh * 8 + r));
-          if (cut) {
-            const uint4 z = make_uint4(0, 0, 0, 0);
-            if (ke >= valid) v[0] = z;
-            if (ko >= valid) v[1] = z;
-            if (ke + 8 >= valid) v[2] = z;
-            if (ko + 8 >= valid) v[3] = z;
-          }
-          const uint32_t w[4][4] = {{v[0].x, v[0].y, v[0].z, v[0].w}, {v[1].x, v[1].y, v[1].z, v[1].w},
-                                    {v[2].x, v[2].y, v[2].z, v[2].w}, {v[3].x, v[3].y, v[3].z, v[3].w}};
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              uint32_t a0, a1, a2, a3;
-              to_f16(__byte_perm(w[0][x], w[1][x], y ? 0x7362 : 0x5140), a0, a1);
-              to_f16(__byte_perm(w[2][x], w[3][x], y ? 0x7362 : 0x5140), a2, a3);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16816(acc[nt][hh * 8 + x * 2 + y], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-            }
-        }
-      } else {
-        uint2 v[4];
-        const uint32_t sub = (r & 1) * 8;
-        v[0] = lds64(vt + tile_at<D>(ke, r >> 1) + sub);
-        v[1] = lds64(vt + tile_at<D>(ko, r >> 1) + sub);
-        v[2] = lds64(vt + tile_at<D>(ke + 8, r >> 1) + sub);
-        v[3] = lds64(vt + tile_at<D>(ko + 8, r >> 1) + sub);
-        if (cut) {
-          const uint2 z = make_uint2(0, 0);
-          if (ke >= valid) v[0] = z;
-          if (ko >= valid) v[1] = z;
-          if (ke + 8 >= valid) v[2] = z;
-          if (ko + 8 >= valid) v[3] = z;
-        }
-        const uint32_t w[4][2] = {{v[0].x, v[0].y}, {v[1].x, v[1].y}, {v[2].x, v[2].y}, {v[3].x, v[3].y}};
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            uint32_t a0, a1, a2, a3;
-            to_f16(__byte_perm(w[0][x], w[1][x], y ? 0x7362 : 0x5140), a0, a1);
-            to_f16(__byte_perm(w[2][x], w[3][x], y ? 0x7362 : 0x5140), a2, a3);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816(acc[nt][x * 2 + y], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-          }
-      }
-      __syncwarp();  // the stage is free: its next copy may start
-      ++consumed;
-    }
-
-    // join the CTA's warps
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float t = l[nt][x];
-        t += __shfl_xor_sync(0xFFFFFFFFu, t, 4);
-        t += __shfl_xor_sync(0xFFFFFFFFu, t, 8);
-        t += __shfl_xor_sync(0xFFFFFFFFu, t, 16);
-        if (r == 0) {
-          s_m[warp * 8 * NT + nt * 8 + 2 * j + x] = m[nt][x];
-          s_l[warp * 8 * NT + nt * 8 + 2 * j + x] = t;
-        }
-      }
-    if (lane == 0) s_vs[warp] = vs_ref;
-    constexpr int DPT = D >= 128 ? 16 : 8;  // consecutive d of one lane in each 128 (or 64) of D
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float* o = join + (warp * 8 + 2 * j + x) * C::kHeadStride + r * DPT;
-#pragma unroll
-        for (int q = 0; q < D / 16; q += 2) {
-          const int at = (q / (DPT / 2)) * 128 + (q % (DPT / 2)) * 2;
-          *reinterpret_cast<float4*>(o + at) = make_float4(acc[nt][q][x], acc[nt][q][x + 2], acc[nt][q + 1][x], acc[nt][q + 1][x + 2]);
-        }
-      }
-      __syncthreads();
-      for (int e = tid; e < 8 * D / 4; e += C::kThreads) {
-        const int hd = e / (D / 4), d4 = e % (D / 4) * 4;
-        if (nt * 8 + hd >= heads) continue;
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) top = fmaxf(top, s_m[w * 8 * NT + nt * 8 + hd]);
-        float sum = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const float mw = s_m[w * 8 * NT + nt * 8 + hd];
-          const float lw = s_l[w * 8 * NT + nt * 8 + hd];
-          // a warp without keys has m = -inf, l = 0; with only NaN scores m = -inf, l = NaN
-          const float c = mw == -INFINITY ? (lw == 0.0f ? 0.0f : 1.0f) : ex2(mw - top);
-          sum += lw * c;
-          const float cv = c * s_vs[w];
-          const float4 v = *reinterpret_cast<const float4*>(join + (w * 8 + hd) * C::kHeadStride + d4);
-          o.x += v.x * cv;
-          o.y += v.y * cv;
-          o.z += v.z * cv;
-          o.w += v.w * cv;
-        }
-        const int head = nt * 8 + hd;
-        if (u.count == 1) {
-          const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-          uint2 st;
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(st.x) : "f"(o.y * inv), "f"(o.x * inv));
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(st.y) : "f"(o.w * inv), "f"(o.z * inv));
-          *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(p.b0 + u.b) * a.Hq + head0 + head) * D + d4) = st;
+        // row of the operand: high part of head hd, low part HP rows on; rows past 2 HP stay zero
+        if (hd < HP) {
+          const uint32_t at = TQ::chunk_at(hd, c), al = TQ::chunk_at(HP + hd, c);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(qt + at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(qt + al), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
+          // a query that is not finite would saturate in 8 bits: its head is NaN through its factor
+          if (c == 0)
+            s_factor[(k % C::kFactorRing) * 16 + hd] =
+                top < 0x7F80u ? fabsf(a.scale) * kLog2e * __int_as_float((254 - down) << 23) : __int_as_float(0x7FC00000);
         } else {
-          const int64_t at = static_cast<int64_t>(f) * p.heads + head;
-          *reinterpret_cast<float4*>(p.part + at * D + d4) = o;
-          if (d4 == 0) p.ml[at] = make_float2(top, sum);
+          const uint32_t z0 = TQ::chunk_at(HP + hd, c);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(qt + z0), "r"(0) : "memory");
+          const uint32_t z1 = TQ::chunk_at(C::kNQ / 2 + hd, c);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(qt + z1), "r"(0) : "memory");
         }
       }
-      __syncthreads();
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_factor + 8 * (k % C::kFactorRing));
+      mbar_arrive(b_qfull + 8 * (k & 1));
+    }
+  } else {
+    // ---- softmax: thread = key of the tile; at a unit's end thread = row of O^T
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t pt = s_p + tid * 16;
+    // A warp whose wait runs out (`ok` false) keeps meeting the others at the barriers until the four of them
+    // leave together.
+    bool ok = true, left = false;
+    int i = 0, k = 0;
+    for (Walk u = walk(); u.more() && !left; u.next(), ++k) {
+      const int tiles = u.tiles(), keys = u.keys();
+      float m[HP], l[HP], fac[HP];
+      float vs_ref = 0.0f;
+      ok = __all_sync(0xFFFFFFFFu, ok && wait(b_factor + 8 * (k % C::kFactorRing), (k / C::kFactorRing) & 1));
+#pragma unroll
+      for (int h = 0; h < HP; ++h) {
+        m[h] = -INFINITY;
+        l[h] = 0.0f;
+        fac[h] = s_factor[(k % C::kFactorRing) * 16 + h];
+      }
+      for (int t = 0; t < tiles; ++t, ++i) {
+        if (i % C::kBatch == 0 || t == 0) ok = ok && wait(b_info + 8 * ((i / C::kBatch) % C::kBatches), (i / C::kInfoRing) & 1);
+        ok = __all_sync(0xFFFFFFFFu, ok && wait(b_s + 8 * (i & 1), (i >> 1) & 1));
+        float x[HP];
+        float2 own = make_float2(-1.0f, 0.0f);
+        float vmax = 0.0f;
+        bool above = false;
+        if (ok) {
+          tc::fence_after_sync();
+          float s[C::kNQ];
+          tmem_load(tmem + C::kNQ * (i & 1) + lanes, s);
+          const float2* sc = s_scale + (i % C::kInfoRing) * kGroups;
+          own = sc[tid / kGroup];
+#pragma unroll
+          for (int g = 0; g < kGroups; ++g) vmax = fmaxf(vmax, sc[g].y);
+          __syncwarp();  // the batch's last tile: its lookups have been read
+          if (i % C::kBatch == C::kBatch - 1 && lane == 0) mbar_arrive(b_infoe + 8 * ((i / C::kBatch) % C::kBatches));
+          const bool hidden = t * kTile + tid >= keys || own.x < 0.0f;
+#pragma unroll
+          for (int h = 0; h < HP; ++h) {
+            x[h] = hidden ? -INFINITY : (s[h] + s[HP + h]) * (own.x * fac[h]);
+            above |= x[h] > m[h] + kRise;
+          }
+        }
+        const bool grow_v = vmax > 2.0f * vs_ref;
+        if (any_of_128(above || grow_v || !ok)) {
+          if (any_of_128(!ok)) {
+            left = true;
+            break;
+          }
+#pragma unroll
+          for (int h = 0; h < HP; ++h) {
+            const float w = warp_max(x[h]);
+            if (lane == 0) s_red[warp * 16 + h] = w;
+          }
+          sync_128();
+          float corr[HP];
+          const float vcorr = grow_v ? __fdividef(vs_ref, vmax) : 1.0f;
+          if (grow_v) vs_ref = vmax;
+#pragma unroll
+          for (int h = 0; h < HP; ++h) {
+            const float top = fmaxf(fmaxf(s_red[h], s_red[16 + h]), fmaxf(s_red[32 + h], s_red[48 + h]));
+            const float to = top > m[h] + kRise ? top : m[h];  // by the head alone, whatever the others do
+            corr[h] = to == -INFINITY ? 1.0f : ex2(m[h] - to);
+            m[h] = to;
+            l[h] *= corr[h];
+            corr[h] *= vcorr;
+          }
+          if (t > 0) {
+            ok = __all_sync(0xFFFFFFFFu, wait(b_pv + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1));
+            if (ok) {
+              tc::fence_after_sync();
+#pragma unroll 1
+              for (int c = 0; c < C::kHalves * C::kNP; c += 16) {
+                float o[16];
+                const uint32_t at = tmem + C::kO + c + lanes;
+                tc::tmem_ld16(at, o);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] *= corr[e % HP];
+                tc::tmem_st16(at, o);
+              }
+              tc::tmem_wait_st();
+            }
+          }
+        }
+        const float rel = vs_ref > 0.0f ? __fdividef(own.y, vs_ref) : 0.0f;
+        uint32_t part[4][HP / 2];
+#pragma unroll
+        for (int h = 0; h < HP; h += 2) {
+          float a0 = ex2(m[h] == -INFINITY ? x[h] : x[h] - m[h] - 0.2f);
+          float a1 = ex2(m[h + 1] == -INFINITY ? x[h + 1] : x[h + 1] - m[h + 1] - 0.2f);
+          l[h] += a0;
+          l[h + 1] += a1;
+          a0 *= rel;
+          a1 *= rel;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) part[y][h / 2] = split_off(a0, a1);
+        }
+        // the tile before has to be done with P (it shares the buffer)
+        ok = __all_sync(0xFFFFFFFFu, ok && (i == 0 || wait(b_pv + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1)));
+        auto word = [&](int y, int w) { return part[y][2 * w] | (part[y][2 * w + 1] << 16); };
+        auto put = [&](int block, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(pt + block * kTile * 16), "r"(w0), "r"(w1), "r"(w2), "r"(w3) : "memory");
+        };
+        if constexpr (HP == 4) {
+          put(0, word(0, 0), word(1, 0), word(2, 0), word(3, 0));
+        } else if constexpr (HP == 8) {
+          put(0, word(0, 0), word(0, 1), word(1, 0), word(1, 1));
+          put(1, word(2, 0), word(2, 1), word(3, 0), word(3, 1));
+        } else {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) put(y, word(y, 0), word(y, 1), word(y, 2), word(y, 3));
+        }
+        tc::fence_async_smem();
+        tc::fence_before_sync();
+        mbar_arrive(b_p);
+      }
+      if (left) break;
+      // the unit's sums, then its rows of O^T
+#pragma unroll
+      for (int h = 0; h < HP; ++h) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], o);
+        if (lane == 0) s_red[warp * 16 + h] = l[h];
+      }
+      if (any_of_128(!ok)) break;
+#pragma unroll
+      for (int h = 0; h < HP; ++h) l[h] = (s_red[h] + s_red[16 + h]) + (s_red[32 + h] + s_red[48 + h]);
+      ok = __all_sync(0xFFFFFFFFu, wait(b_pv + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1));
+      if (!ok) continue;  // to meet the others
+      tc::fence_after_sync();
+      const int head0 = first_head(u), heads = unit_heads(u);
+      const int64_t f = ((static_cast<int64_t>(u.b) * a.H + u.h) * p.chunks + u.chunk) * p.each + u.index;
+      const bool alone = u.count == 1;
+      uint16_t* op = a.out + (static_cast<int64_t>(p.b0 + u.b) * a.Hq + head0) * D + tid;
+      float* pp = p.part + f * p.heads * D + tid;
+#pragma unroll
+      for (int h = 0; h < HP; ++h) {
+        if (!alone && tid == h && h < heads) p.ml[f * p.heads + h] = make_float2(m[h], l[h]);
+        // fac: what a head's sums are multiplied with
+        fac[h] = !alone ? vs_ref : l[h] > 0.0f || l[h] != l[h] ? __fdividef(vs_ref, l[h]) : 0.0f;
+      }
+#pragma unroll 1
+      for (int hf = 0; hf < C::kHalves; ++hf) {
+        float o[C::kNP];
+        tmem_load(tmem + C::kO + hf * C::kNP + lanes, o);
+        if (D >= 128 || tid < D) {
+#pragma unroll
+          for (int h = 0; h < HP; ++h) {
+            const float sum = (o[h] + (o[HP + h] + (o[2 * HP + h] + o[3 * HP + h] * 0.0625f) * 0.0625f) * 0.0625f) * fac[h];
+            if (h < heads) {
+              if (alone) {
+                asm volatile("{.reg .b16 x; cvt.rn.bf16.f32 x, %1; st.global.b16 [%0], x;}" ::"l"(op + h * D + hf * 128), "f"(fac[h] == 0.0f ? 0.0f : sum) : "memory");
+              } else {
+                pp[h * D + hf * 128] = sum;
+              }
+            }
+          }
+        }
+        __syncwarp();
+      }
+      tc::fence_before_sync();
     }
   }
-  if (!ok && lane == 0) {
-    // a copy that did not come: leave once those in flight have landed
-    for (; consumed < issued; ++consumed)
-      mbar_wait_bounded(my_bars + (consumed % C::kStages) * 8, (consumed / C::kStages) & 1);
-    if (a.err) atomicOr(a.err, GDN_DEVERR_TIMEOUT);
+  tc::fence_before_sync();
+  __syncthreads();
+  if (s_fail) {  // a wait ran out: leave only once what is in flight has landed
+    if (tid == 0 && a.err) atomicOr(a.err, GDN_DEVERR_TIMEOUT);
+    if (warp == 5)
+      for (int i = max(0, copies - C::kStages); i < copies; ++i) mbar_wait_bounded(full(i), phase(i));
+    if (warp == 4 && lane == 0) {
+      tc::mma_commit(b_drain);
+      mbar_wait_bounded(b_drain, 0);
+    }
+    __syncthreads();
+  }
+  if (warp == 4) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, C::kColumns);
   }
 }
 
-// Joins the units of one request, kv head and query head in unit order; an empty request gets zeros.
-template <int D>
-__global__ void __launch_bounds__(128) attn_decode_join_kernel(const __grid_constant__ DecodeParams p) {
-  constexpr int kLanes = D / 4, kRows = 128 / kLanes;
+// Joins the units of one request, kv head and query head in unit order (4 kLanes of its d per CTA); an
+// empty request gets zeros.
+template <int D, int kLanes>
+__global__ void __launch_bounds__(256) attn_decode_join_kernel(const __grid_constant__ DecodeParams p) {
+  constexpr int kRows = 256 / kLanes;
   __shared__ float4 s_o[kRows][kLanes];
-  __shared__ float s_sum[kRows], s_top[4];
+  __shared__ float s_sum[kRows], s_top[8];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const AttnArgs& a = p.a;
   const int HC = a.H * p.chunks, G = a.Hq / a.H;
   const int b = blockIdx.x / HC, hc = blockIdx.x % HC, head = blockIdx.y;
   const int qh = (hc / p.chunks) * G + (hc % p.chunks) * 16 + head;
   if ((hc % p.chunks) * 16 + head >= G) return;
-  const int first = p.pre[b], n = p.pre[b + 1] - first;
+  const int n = units_of(min(max(a.lens[p.b0 + b], 0), a.max_blocks * a.bs));
   if (n == 1) return;
-  const int tid = threadIdx.x, d4 = tid % kLanes, row = tid / kLanes;
-  const int64_t f = static_cast<int64_t>(first) * HC + static_cast<int64_t>(hc) * n;
+  const int tid = threadIdx.x, d4 = tid % kLanes + blockIdx.z * kLanes, row = tid / kLanes;
+  const int64_t f = (static_cast<int64_t>(b) * HC + hc) * p.each;
   const float2* ml = p.ml + f * p.heads + head;
   const float* part = p.part + (f * p.heads + head) * D;
   float top = -INFINITY;
-  for (int i = tid; i < n; i += 128) top = fmaxf(top, ml[static_cast<int64_t>(i) * p.heads].x);
+  for (int i = tid; i < n; i += 256) top = fmaxf(top, ml[static_cast<int64_t>(i) * p.heads].x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   if ((tid & 31) == 0) s_top[tid >> 5] = top;
   __syncthreads();
-  top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+  top = s_top[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) top = fmaxf(top, s_top[i]);
   float sum = 0.0f;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
   for (int i = row; i < n; i += kRows) {
     const float2 e = ml[static_cast<int64_t>(i) * p.heads];
+    // a unit without keys has m = -inf, l = 0; with only NaN scores m = -inf, l = NaN
     const float c = e.x == -INFINITY ? (e.y == 0.0f ? 0.0f : 1.0f) : ex2(e.x - top);
     const float4 v = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(i) * p.heads * D + d4 * 4);
     sum += e.y * c;
@@ -622,13 +793,13 @@ __global__ void __launch_bounds__(128) attn_decode_join_kernel(const __grid_cons
     o.z += v.z * c;
     o.w += v.w * c;
   }
-  s_o[row][d4] = o;
-  if (d4 == 0) s_sum[row] = sum;
+  s_o[row][tid % kLanes] = o;
+  if (tid % kLanes == 0) s_sum[row] = sum;
   __syncthreads();
   if (row != 0) return;
 #pragma unroll
   for (int i = 1; i < kRows; ++i) {
-    const float4 v = s_o[i][d4];
+    const float4 v = s_o[i][tid];
     sum += s_sum[i];
     o.x += v.x;
     o.y += v.y;
@@ -643,46 +814,59 @@ __global__ void __launch_bounds__(128) attn_decode_join_kernel(const __grid_cons
 }
 
 struct DecodeLayout {
-  size_t pre, ml, part, total;
+  size_t part, total;
 };
 DecodeLayout decode_layout(int nb, int max_blocks, int Hq, int H, int d, int bs) {
   const int G = Hq / H, heads = G < 16 ? G : 16, chunks = (G + 15) / 16;
   const size_t units = static_cast<size_t>(nb) * H * chunks * most_units(static_cast<int64_t>(max_blocks) * bs);
   DecodeLayout L;
-  L.pre = 0;
-  L.ml = (static_cast<size_t>(nb + 1) * 4 + 255) & ~static_cast<size_t>(255);
-  L.part = (L.ml + units * heads * 8 + 255) & ~static_cast<size_t>(255);
+  L.part = (units * heads * 8 + 255) & ~static_cast<size_t>(255);
   L.total = L.part + units * heads * d * 4;
   return L;
 }
 
-template <int D, int NT, int NW>
-cudaError_t launch_decode_d(DecodeParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t s) {
-  using C = DecodeCfg<D, NT, NW>;
-  auto kern = attn_decode_kernel<D, NT, NW>;
-  const int smem = C::kAlign + C::kFixed + (p.nb + 1) * 4;
+template <int D, int HP>
+cudaError_t launch_decode_d(DecodeParams& p, const CacheMaps& maps, cudaStream_t s) {
+  using C = DecodeCfg<D, HP>;
+  auto kern = attn_decode_kernel<D, HP>;
+  const int smem = C::kSmem + 4 * (p.nb + p.nb / kCoarse + 2);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  int per_sm = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, C::kThreads, smem);
+  // CTAs of an SM by its shared memory, registers and tensor memory (the occupancy query answers 1 for
+  // kernels that allocate tensor memory)
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, kern);
   if (e != cudaSuccess) return e;
-  if (per_sm < 1) return cudaErrorInvalidConfiguration;
-  const int64_t most = static_cast<int64_t>(p.nb) * p.a.H * p.chunks *
-                       most_units(static_cast<int64_t>(p.a.max_blocks) * p.a.bs);
+  int per_sm = kSmemPerSm / (smem + static_cast<int>(fa.sharedSizeBytes) + 1024);
+  const int by_regs = 65536 / (((fa.numRegs + 7) & ~7) * kThreads), by_tmem = 512 / C::kColumns;
+  if (per_sm > by_regs) per_sm = by_regs;
+  if (per_sm > by_tmem) per_sm = by_tmem;
+  if (per_sm < 1) per_sm = 1;
+  const int64_t most = static_cast<int64_t>(p.nb) * p.a.H * p.chunks * p.each;
   const int grid = static_cast<int>(most < static_cast<int64_t>(per_sm) * sm_count() ? most : per_sm * sm_count());
-  kern<<<grid, C::kThreads, smem, s>>>(p, kmap, vmap);
+  kern<<<grid, kThreads, smem, s>>>(p, maps);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  // Many units to join: few d per CTA, more units at a time
+  const bool narrow = D > 64 && p.each > 32;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.nb * p.a.H * p.chunks, p.heads, 1);
-  cfg.blockDim = dim3(128, 1, 1);
+  cfg.gridDim = dim3(p.nb * p.a.H * p.chunks, p.heads, narrow ? D / 64 : 1);
+  cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<D>, p);
+  return narrow ? cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<D, 16>, p)
+                : cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<D, D / 4>, p);
+}
+
+template <int D>
+cudaError_t launch_decode_h(DecodeParams& p, const CacheMaps& maps, cudaStream_t s) {
+  return p.heads <= 4   ? launch_decode_d<D, 4>(p, maps, s)
+         : p.heads <= 8 ? launch_decode_d<D, 8>(p, maps, s)
+                        : launch_decode_d<D, 16>(p, maps, s);
 }
 
 }  // namespace
@@ -692,28 +876,26 @@ size_t attn_decode_workspace(int B, int max_blocks, int Hq, int H, int d, int bs
 }
 
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s) {
-  CUtensorMap kmap, vmap;
-  const int64_t rows = static_cast<int64_t>(a.num_blocks) * a.H * a.bs;
-  cudaError_t e = encode_cache_map(&kmap, a.k_cache, rows, a.d, kGroup);
-  if (e == cudaSuccess) e = encode_cache_map(&vmap, a.v_cache, rows, a.d, kGroup);
+  CacheMaps maps;
+  cudaError_t e = encode_cache_maps(&maps, a);
   if (e != cudaSuccess) return e;
   const int G = a.Hq / a.H;
   DecodeParams p;
   p.a = a;
   p.heads = G < 16 ? G : 16;
   p.chunks = (G + 15) / 16;
-  for (int b0 = 0; b0 < a.B; b0 += kBatchPerLaunch) {
+  p.each = static_cast<int>(most_units(static_cast<int64_t>(a.max_blocks) * a.bs));
+  const int launches = (a.B + kBatchPerLaunch - 1) / kBatchPerLaunch, per = (a.B + launches - 1) / launches;
+  for (int b0 = 0; b0 < a.B; b0 += per) {
     p.b0 = b0;
-    p.nb = a.B - b0 < kBatchPerLaunch ? a.B - b0 : kBatchPerLaunch;
+    p.nb = a.B - b0 < per ? a.B - b0 : per;
     const DecodeLayout L = decode_layout(p.nb, a.max_blocks, a.Hq, a.H, a.d, a.bs);
     char* ws = static_cast<char*>(a.workspace);
-    p.pre = reinterpret_cast<int32_t*>(ws + L.pre);
-    p.ml = reinterpret_cast<float2*>(ws + L.ml);
+    p.ml = reinterpret_cast<float2*>(ws);
     p.part = reinterpret_cast<float*>(ws + L.part);
-    const bool wide = p.heads > 8;
-    if (a.d == 64) e = wide ? launch_decode_d<64, 2, 8>(p, kmap, vmap, s) : launch_decode_d<64, 1, 8>(p, kmap, vmap, s);
-    else if (a.d == 128) e = wide ? launch_decode_d<128, 2, 8>(p, kmap, vmap, s) : launch_decode_d<128, 1, 8>(p, kmap, vmap, s);
-    else e = wide ? launch_decode_d<256, 2, 4>(p, kmap, vmap, s) : launch_decode_d<256, 1, 4>(p, kmap, vmap, s);
+    e = a.d == 64    ? launch_decode_h<64>(p, maps, s)
+        : a.d == 128 ? launch_decode_h<128>(p, maps, s)
+                     : launch_decode_h<256>(p, maps, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

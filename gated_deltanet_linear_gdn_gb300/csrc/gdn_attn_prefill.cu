@@ -16,42 +16,39 @@
 // bound is the dense bf16 rate, with half the shared-memory traffic for K and V.
 //
 // Scales. A block of keys has one ks: it enters the exponent, exp2(s * ks * factor - m). Its vs
-// enters as p * (vs / vs_ref), vs_ref the largest vs seen (within 1.75); the row sum takes p
-// without it. The running maximum m moves when a score passes it by 2^4, so that 16 p <= 256
+// enters there, too, as log2(vs / vs_ref), vs_ref the largest vs seen (within 1.75); the row sum takes it
+// back by group of 16. The running maximum m moves when a score passes it by 2^4, so that 16 p <= 256
 // fits e4m3; the accumulator is rescaled only then.
 //
 // One CTA per unit: 256 rows (two 128-row tiles) for d <= 128, 128 rows for d = 256, where two
 // score buffers take turns instead of two row tiles (tensor memory: 2 x 128 columns of scores,
-// 256 columns of output). Warps: one warpgroup of softmax per row tile (thread = row), one warp
-// issuing MMAs, one fetching pages by TMA. p overwrites the scores it came from in tensor memory
-// and is the A operand of the second product there.
+// 256 columns of output). Warps: two warpgroups of softmax for each row tile (two threads share a row, 64
+// columns each, and exchange their maxima), one warp issuing MMAs, one looking up pages and scales four
+// tiles at a time, one copying keys and one values, so that neither waits for the other's ring. p overwrites the scores it came from in tensor memory and is
+// the A operand of the second product there.
 //
 // A plan kernel turns the lengths into a list of units, the longest first. A request with few
 // rows over a long cache is also cut along the keys, by a rule on its own sizes alone
 // (kv_splits), and a third kernel joins the fp32 partial sums in order: results do not depend on
 // the rest of the batch.
-#include "gdn_cache.cuh"
+#include <type_traits>
+
+#include "gdn_attn.cuh"
 #include "gdn_internal.h"
-#include "gdn_ptx.cuh"
-#include "gdn_tc.cuh"
 
 namespace gdn {
 
 namespace {
 
-constexpr int kTile = 128;             // keys of a tile
-constexpr int kGroup = 16;             // keys of one TMA box: the smallest block
-constexpr int kGroups = kTile / kGroup;
 constexpr int kPlanThreads = 1024;
 constexpr int kBatchPerLaunch = 2048;
 constexpr int kBuckets = 256;
-constexpr float kLog2e = 1.4426950408889634f;
 // key splits: up to this many units for a request that has fewer than kFewUnits
 constexpr int kFewUnits = 76, kSplitUnits = 228, kMaxSplits = 32, kMinSplitTiles = 8;
 
-struct PrefillUnit {
+struct __align__(16) PrefillUnit {
   int b, h, row0, tile0, tile1, slot;  // slot: partial sums' place, or -1: the unit is the whole
-  int splits, pad;
+  int splits, first, n, len, pad0, pad1;  // the request's first row of q, its tokens, its cached length
 };
 
 struct PrefillParams {
@@ -177,7 +174,10 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     d.tile1 = min(d.tile0 + each, tiles);
     d.slot = s > 1 ? s_slot[lo] + rem : -1;
     d.splits = s;
-    d.pad = 0;
+    d.first = first;
+    d.n = n;
+    d.len = len;
+    d.pad0 = d.pad1 = 0;
     return d;
   };
   for (int u = tid; u < carry; u += kPlanThreads) {
@@ -213,138 +213,24 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
   }
 }
 
-// ------------------------------------------------------------------------------------ helpers
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  uint32_t r;
-  asm("{.reg .b16 x, y; cvt.rn.satfinite.e4m3x2.f32 x, %2, %1; cvt.rn.satfinite.e4m3x2.f32 y, %4, %3; mov.b32 %0, {x, y};}"
-      : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
-  return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(r)
-      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
-        "l"(*reinterpret_cast<unsigned long long*>(&c)));
-  return *reinterpret_cast<float2*>(&r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(r)
-      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
-  return *reinterpret_cast<float2*>(&r);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  unsigned long long r;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(r)
-      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
-  return *reinterpret_cast<float2*>(&r);
-}
-
-// The 4 leading significant bits, to nearest: v * 2^20 absorbs the rest (T. J. Dekker, "A
-// floating-point technique for extending the available precision", 1971).
-__device__ __forceinline__ float2 top_bits(float2 v) {
-  const float2 t = mul2(v, make_float2(1048577.0f, 1048577.0f));
-  const float2 minus = make_float2(-1.0f, -1.0f);
-  return fma2(fma2(v, minus, t), minus, t);
-}
-
-__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int row, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
-          "r"(dst), "l"(map), "r"(x), "r"(row), "r"(bar)
-      : "memory");
-}
-
-#define GDN_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : GDN_R8(r, 0), GDN_R8(r, 8), GDN_R8(r, 16), GDN_R8(r, 24)
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-#undef GDN_R8
-
-// The factor of a score in the exponent. Never zero, so that a masked score (-inf) stays -inf: a
-// smaller one moves no exponent (scores are below 2^26).
-__device__ __forceinline__ float exponent_scale(float ks, float factor) { return fmaxf(fabsf(ks) * factor, 1e-37f); }
-
-// 8-bit MMAs (kind::f8f6f4, e4m3 x e4m3, fp32 accumulators, 32 elements of K per instruction).
-__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc)
-      : "memory");
-}
-// Instruction descriptor: fp32 D, e4m3 A and B, B optionally MN-major.
-__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, bool b_mn) {
-  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-// Operand tiles are rows of min(d, 128) bytes in the hardware swizzle that TMA writes (128-byte
-// rows: 16-byte chunk ^ row mod 8; 64-byte rows: chunk ^ (row / 2) mod 4), 8 rows to an atom;
-// d = 256 has two such tiles side by side.
-//   K-major (Q, K): the stride offset is the next 8 rows; a K step of 32 is 32 bytes on.
-//   MN-major (V, rows are K): the stride offset is the next 8 K rows, the leading offset the next
-//   128 bytes of N; a K step of 32 is 32 rows on.
-template <int D>
-struct Tile {
-  static constexpr int kRow = D < 128 ? D : 128;
-  static constexpr int kHalf = kTile * kRow;           // one 128-row tile of kRow bytes
-  static constexpr int kBytes = kTile * D;
-  static __device__ __forceinline__ uint64_t desc(uint32_t addr, uint32_t lbo) {
-    uint64_t d = tc::smem_desc(addr, lbo, 8 * kRow);
-    d |= static_cast<uint64_t>(D < 128 ? 4 : 2) << 61;  // 64-byte / 128-byte swizzle
-    return d;
-  }
-  static __device__ __forceinline__ uint64_t k_step(uint32_t tile, int ks) {
-    constexpr int per = kRow / 32;
-    return desc(tile + (ks / per) * kHalf + (ks % per) * 32, 16);
-  }
-  static __device__ __forceinline__ uint64_t mn_step(uint32_t tile, int ks) { return desc(tile + ks * 32 * kRow, kHalf); }
-  static __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
-    if (D < 128) return row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
-    return (chunk >> 3) * kHalf + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
-  }
-};
-
 template <int D>
 struct PrefillCfg {
   static constexpr int kTilesM = D == 256 ? 1 : 2;       // row tiles of a unit
+  static constexpr int kSplitC = 4 / kTilesM;            // softmax warpgroups that share a row tile, by columns
   static constexpr int kRows = kTilesM * 128;
-  static constexpr int kSoftWarps = 4 * kTilesM;
-  static constexpr int kThreads = 32 * (kSoftWarps + 2);
-  static constexpr int kStages = D == 256 ? 2 : 3;
+  static constexpr int kSoftWarps = 4 * kTilesM * kSplitC;
+  static constexpr int kThreads = 32 * (kSoftWarps + 4); // and warps for MMAs, lookups, copies of K, copies of V
+  static constexpr int kStages = D == 256 ? 2 : 3;       // key tiles in the ring, and value tiles
+  static constexpr int kBatch = 4, kBatches = 4, kInfoRing = kBatch * kBatches;  // tiles looked up at a time; kept
   static constexpr int kQ = kTilesM * 2 * Tile<D>::kBytes;  // hi and lo of each row tile
   static constexpr int kKV = kStages * 2 * Tile<D>::kBytes;
-  static constexpr int kScales = kStages * kGroups * 2 * 4;
-  static constexpr int kSmem = 1024 + kQ + kKV + kScales + 256;
+  static constexpr int kAtScale = kQ + kKV;                 // [kInfoRing][kGroups] (ks, log2 vs)
+  static constexpr int kAtRow = kAtScale + kInfoRing * kGroups * 8;
+  static constexpr int kAtTop = kAtRow + kInfoRing * kGroups * 4;  // [kInfoRing] the tile's largest log2 vs
+  static constexpr int kAtMax = kAtTop + kInfoRing * 4;  // [2][kSplitC][kRows]
+  static constexpr int kAtFactor = kAtMax + 2 * kSplitC * kRows * 4;  // [kRows]
+  static constexpr int kAtBars = kAtFactor + kRows * 4;
+  static constexpr int kSmem = 1024 + kAtBars + 8 * (4 * kStages + 2 * kBatches + 8);
   // tensor memory columns
   static constexpr int kS = 0;         // two score buffers of 128
   static constexpr int kO = 256;       // output, D columns per row tile
@@ -352,44 +238,43 @@ struct PrefillCfg {
 
 template <int D>
 __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
-    attn_prefill_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CUtensorMap kmap,
-                        const __grid_constant__ CUtensorMap vmap) {
+    attn_prefill_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CacheMaps maps) {
   using C = PrefillCfg<D>;
   using TL = Tile<D>;
+  constexpr int NC = kTile / C::kSplitC;  // columns (keys) of a softmax thread
+  constexpr int NG = NC / kGroup;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + (-smem_addr(smem_raw) & 1023u);
   const uint32_t s_q = smem_addr(smem), s_k = s_q + C::kQ, s_v = s_k + C::kStages * TL::kBytes;
-  float* s_scale = reinterpret_cast<float*>(smem + C::kQ + C::kKV);  // [stage][group][ks, vs]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kQ + C::kKV + C::kScales);
-  const uint32_t bar = smem_addr(bars);
-  // barriers
+  float2* s_scale = reinterpret_cast<float2*>(smem + C::kAtScale);
+  int32_t* s_row = reinterpret_cast<int32_t*>(smem + C::kAtRow);
+  float* s_top = reinterpret_cast<float*>(smem + C::kAtTop);
+  float* s_max = reinterpret_cast<float*>(smem + C::kAtMax);
+  float* s_factor = reinterpret_cast<float*>(smem + C::kAtFactor);
+  const uint32_t bar = s_q + C::kAtBars;
   const uint32_t b_kfull = bar, b_kempty = bar + 8 * C::kStages, b_vfull = bar + 16 * C::kStages,
-                 b_vempty = bar + 24 * C::kStages, b_s = bar + 32 * C::kStages, b_p = b_s + 16, b_pv = b_p + 16,
-                 b_q = b_pv + 16, b_drain = b_q + 8;
-  static_assert(8 * (4 * C::kStages + 8) <= 256, "barriers fit");
+                 b_vempty = bar + 24 * C::kStages, b_info = bar + 32 * C::kStages, b_infoe = b_info + 8 * C::kBatches,
+                 b_s = b_infoe + 8 * C::kBatches, b_p = b_s + 16, b_pv = b_p + 16, b_q = b_pv + 16, b_drain = b_q + 8;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_fail;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const AttnArgs& a = p.a;
+  if (tid < 4) prefetch_map(tid == 0 ? &maps.k_page : tid == 1 ? &maps.v_page : tid == 2 ? &maps.k_group : &maps.v_group);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (static_cast<int>(blockIdx.x) >= *reinterpret_cast<volatile int32_t*>(p.counts)) return;
   const PrefillUnit u = p.units[blockIdx.x];
-  int first, n, len;
-  request(p, u.b, first, n, len);
+  const int first = u.first, n = u.n, len = u.len;
   const int G = a.Hq / a.H;
+  const int rows_all = n * G;  // (below 2^31: the caller's tokens x heads are)
   const int tiles = u.tile1 - u.tile0;
 
   if (tid == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(b_kfull + 8 * i, 1);
-      mbar_init(b_kempty + 8 * i, 1);
-      mbar_init(b_vfull + 8 * i, 1);
-      mbar_init(b_vempty + 8 * i, 1);
-    }
+    for (int i = 0; i < 4 * C::kStages + C::kBatches; ++i) mbar_init(bar + 8 * i, 1);
+    for (int i = 0; i < C::kBatches; ++i) mbar_init(b_infoe + 8 * i, C::kSoftWarps + 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_s + 8 * i, 1);
-      mbar_init(b_p + 8 * i, 128);
+      mbar_init(b_p + 8 * i, 32 * C::kSoftWarps / C::kTilesM);
       mbar_init(b_pv + 8 * i, 1);
     }
     mbar_init(b_q, 32 * C::kSoftWarps);
@@ -406,360 +291,434 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = s_tmem;
 
-  // A bounded wait that also gives up once another role has.
-  auto wait = [&](uint32_t b, int parity) -> bool {
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(b, parity)) return true;
-    const uint64_t t0 = global_ns();
-    while (!s_fail) {
-      if (mbar_try_wait_sleep(b, parity, 20000u)) return true;
-      if (global_ns() - t0 > 1000000000ull) s_fail = 1;
-    }
-    return false;
-  };
+  auto wait = [&](uint32_t b, int parity) { return wait_or_fail(b, parity, &s_fail); };
+  // the score buffer of row tile t and key tile j, and which use of it that is
+  auto buffer = [](int t, int j) { return C::kTilesM == 2 ? t : j & 1; };
+  auto use = [](int j) { return C::kTilesM == 2 ? j & 1 : (j >> 1) & 1; };
 
-  const uint32_t kv_bytes = TL::kBytes;
+  int copies = 0;  // of a copying warp
   if (warp == C::kSoftWarps + 1) {
-    // ---- pages: lane g < 8 fetches the 16-key group g of each tile
-    const int total_rows = a.num_blocks * a.H * a.bs;  // past the map: zeros
-    int done = 0;
+    // ---- lookups: lane = (tile of the batch, 16-key group)
     bool ok = true;
-    for (int j = 0; j < tiles && ok; ++j) {
-      const int st = j % C::kStages, ph = (j / C::kStages) & 1;
-      int row = total_rows;
-      float ks = -1.0f, vs = 0.0f;
-      if (lane < kGroups) {
-        const int pos = (u.tile0 + j) * kTile + lane * kGroup;
-        if (pos < len) {
-          const int page = a.block_table[static_cast<int64_t>(p.b0 + u.b) * a.max_blocks + pos / a.bs];
-          if (page >= 0 && page < a.num_blocks) {
-            row = (page * a.H + u.h) * a.bs + pos % a.bs;
-            ks = a.k_scale[static_cast<int64_t>(page) * a.H + u.h];
-            vs = a.v_scale[static_cast<int64_t>(page) * a.H + u.h];
-          } else if (a.err) {
-            atomicOr(a.err, GDN_DEVERR_BLOCK_RANGE);
-          }
+    const int shift = 31 - __clz(a.bs);
+    for (int j0 = 0; j0 < tiles && ok; j0 += C::kBatch) {
+      const int j = j0 + lane / kGroups, pos = (u.tile0 + j) * kTile + (lane % kGroups) * kGroup;
+      int row = a.num_blocks * a.H * a.bs;           // past the cache: zeros
+      float2 sc = make_float2(-1.0f, -INFINITY);     // no key, or a page that is none: not seen
+      if (j < tiles && pos < len) {
+        const int page = a.block_table[static_cast<int64_t>(p.b0 + u.b) * a.max_blocks + (pos >> shift)];
+        if (page >= 0 && page < a.num_blocks) {
+          const int64_t at = static_cast<int64_t>(page) * a.H + u.h;
+          sc = make_float2(a.k_scale[at], a.v_scale[at]);
+          row = (static_cast<int>(at) << shift) + (pos & (a.bs - 1));
+        } else if (a.err) {
+          atomicOr(a.err, GDN_DEVERR_BLOCK_RANGE);
         }
       }
-      ok = wait(b_kempty + 8 * st, ph ^ 1);
-      if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
-      if (lane == 0) mbar_arrive_expect_tx(b_kfull + 8 * st, kv_bytes);
-      __syncwarp();
-      if (lane < kGroups)
+      if (sc.x >= 0.0f) asm("lg2.approx.f32 %0, %0;" : "+f"(sc.y));
+      const int slot = (j0 / C::kBatch) % C::kBatches;
+      ok = __all_sync(0xFFFFFFFFu, wait(b_infoe + 8 * slot, ((j0 / C::kInfoRing) & 1) ^ 1));
+      if (!ok) break;
+      float top = sc.y;
 #pragma unroll
-        for (int x = 0; x < D; x += 128)
-          tma_rows(s_k + st * TL::kBytes + (x / 128) * TL::kHalf + lane * kGroup * TL::kRow, &kmap, x, row, b_kfull + 8 * st);
-      ok = wait(b_vempty + 8 * st, ph ^ 1);
-      if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; done = 2 * j + 1; break; }
-      if (lane < kGroups) {
-        s_scale[(st * kGroups + lane) * 2] = ks;
-        s_scale[(st * kGroups + lane) * 2 + 1] = vs;
-      }
+      for (int o = 1; o < kGroups; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      s_scale[slot * 32 + lane] = sc;
+      s_row[slot * 32 + lane] = row;
+      if (lane % kGroups == 0) s_top[slot * C::kBatch + lane / kGroups] = top;
       __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(b_vfull + 8 * st, kv_bytes);
-      __syncwarp();
-      if (lane < kGroups)
-#pragma unroll
-        for (int x = 0; x < D; x += 128)
-          tma_rows(s_v + st * TL::kBytes + (x / 128) * TL::kHalf + lane * kGroup * TL::kRow, &vmap, x, row, b_vfull + 8 * st);
-      done = 2 * j + 2;
+      if (lane == 0) mbar_arrive(b_info + 8 * slot);
     }
-    if (s_fail) {  // leave only once every copy has landed
-      for (int i = max(0, done - 2 * C::kStages); i < done; ++i)
-        mbar_wait_bounded(((i & 1) ? b_vfull : b_kfull) + 8 * ((i / 2) % C::kStages), ((i / 2) / C::kStages) & 1);
+  } else if (warp >= C::kSoftWarps + 2) {
+    // ---- copies of keys, copies of values: lane g < 8 has the 16-key group g of each tile
+    const bool is_v = warp == C::kSoftWarps + 3;
+    const CUtensorMap* by_page = is_v ? &maps.v_page : &maps.k_page;
+    const CUtensorMap* by_group = is_v ? &maps.v_group : &maps.k_group;
+    const uint32_t b_full = is_v ? b_vfull : b_kfull, b_empty = is_v ? b_vempty : b_kempty, to = is_v ? s_v : s_k;
+    const bool head = ((lane * kGroup) & (a.bs - 1)) == 0;  // the group starts a page
+    bool ok = true;
+    for (int j = 0; j < tiles && ok; ++j) {
+      const int st = j % C::kStages, slot = (j / C::kBatch) % C::kBatches;
+      if (j % C::kBatch == 0) ok = wait(b_info + 8 * slot, (j / C::kInfoRing) & 1);
+      ok = __all_sync(0xFFFFFFFFu, ok && wait(b_empty + 8 * st, ((j / C::kStages) & 1) ^ 1));
+      if (!ok) break;
+      const int row = s_row[(j % C::kInfoRing) * kGroups + lane % kGroups];
+      __syncwarp();
+      if (is_v && j % C::kBatch == C::kBatch - 1 && lane == 0) mbar_arrive(b_infoe + 8 * slot);
+      // a page of which every token is the request's goes in one box
+      const bool whole = ((lane * kGroup) & -a.bs) + a.bs <= len - (u.tile0 + j) * kTile;
+      if (lane == 0) mbar_arrive_expect_tx(b_full + 8 * st, TL::kBytes);
+      __syncwarp();
+      if (lane < kGroups && (head || !whole))
+#pragma unroll
+        for (int x = 0; x < D; x += 128)
+          tma_rows(to + st * TL::kBytes + (x / 128) * TL::kHalf + lane * kGroup * TL::kRow, whole ? by_page : by_group, x, row, b_full + 8 * st);
+      copies = j + 1;
     }
   } else if (warp == C::kSoftWarps) {
     // ---- MMAs
-    constexpr uint32_t iqk = idesc_f8(128, kTile, false), ipv = idesc_f8(128, D, true);
+    constexpr uint32_t iqk = idesc_f8(128, kTile, false, false), ipv = idesc_f8(128, D, false, true);
     bool ok = tiles == 0 || wait(b_q, 0);
     tc::fence_after_sync();
+    // descriptors but for their start address (bits 0 .. 13, in 16 bytes), which each MMA adds: the issuing
+    // warp shares its scheduler with softmax warps, and a few instructions an MMA are what it gets
+    const uint64_t dk = TL::desc(s_k, 16), dq = TL::desc(s_q, 16), dv = TL::desc(s_v, TL::kHalf);
+    auto k_off = [](int ks) { return static_cast<uint64_t>((ks / (TL::kRow / 32)) * TL::kHalf + (ks % (TL::kRow / 32)) * 32) >> 4; };
     auto qk = [&](int j, int t) {  // scores of row tile t, key tile j
       if (lane == 0) {
-        const uint32_t d = tmem + C::kS + 128 * (C::kTilesM == 2 ? t : j & 1);
-        const uint32_t kt = s_k + (j % C::kStages) * TL::kBytes;
+        const uint32_t d = tmem + C::kS + 128 * buffer(t, j);
+        const uint64_t kt = dk + (j % C::kStages) * (TL::kBytes >> 4), qt = dq + t * 2 * (TL::kBytes >> 4);
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int ks = 0; ks < D / 32; ++ks)
-            mma_f8_ss(d, TL::k_step(s_q + (t * 2 + part) * TL::kBytes, ks), TL::k_step(kt, ks), iqk, part | ks);
-        tc::mma_commit(b_s + 8 * (C::kTilesM == 2 ? t : j & 1));
+            mma_f8_ss(d, qt + part * (TL::kBytes >> 4) + k_off(ks), kt + k_off(ks), iqk, part | ks);
+        tc::mma_commit(b_s + 8 * buffer(t, j));
         if (t == C::kTilesM - 1) tc::mma_commit(b_kempty + 8 * (j % C::kStages));
       }
       __syncwarp();
     };
     auto pv = [&](int j, int t) {
       if (lane == 0) {
-        const uint32_t pa = tmem + C::kS + 128 * (C::kTilesM == 2 ? t : j & 1);
-        const uint32_t vt = s_v + (j % C::kStages) * TL::kBytes;
+        const uint32_t pa = tmem + C::kS + 128 * buffer(t, j);
+        const uint64_t vt = dv + (j % C::kStages) * (TL::kBytes >> 4);
 #pragma unroll
         for (int ks = 0; ks < kTile / 32; ++ks)
 #pragma unroll
           for (int part = 0; part < 2; ++part)
-            mma_f8_ts(tmem + C::kO + t * D, pa + ks * 32 + part * 8, TL::mn_step(vt, ks), ipv, (j > 0) | (ks | part));
-        tc::mma_commit(b_pv + 8 * t);
+            mma_f8_ts(tmem + C::kO + t * D, pa + ks * 32 + part * 8, vt + ks * (32 * TL::kRow >> 4), ipv, (j > 0) | (ks | part));
+        tc::mma_commit(b_pv + 8 * buffer(t, j));
         if (t == C::kTilesM - 1) tc::mma_commit(b_vempty + 8 * (j % C::kStages));
       }
       __syncwarp();
     };
     // V rows past the request's length hold whatever their page holds: 0 * NaN is not 0
     auto clear_tail = [&](int j) {
-      const int at = (u.tile0 + j) * kTile;
-      const int from = len - at;
+      const int from = len - (u.tile0 + j) * kTile;
       if (from >= kTile || (from & (kGroup - 1)) == 0) return;
       const int rows = kGroup - (from & (kGroup - 1));
       const uint32_t vt = s_v + (j % C::kStages) * TL::kBytes;
-      for (int i = lane; i < rows * (D / 16); i += 32) {
-        const int row = from + i / (D / 16), c = i % (D / 16);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + TL::chunk_at(row, c)), "r"(0) : "memory");
-      }
+      for (int i = lane; i < rows * (D / 16); i += 32)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vt + TL::chunk_at(from + i / (D / 16), i % (D / 16))), "r"(0) : "memory");
       tc::fence_async_smem();
       __syncwarp();
     };
-    for (int j = 0; ok && j < tiles; ++j) {
-      const int st = j % C::kStages, ph = (j / C::kStages) & 1;
-      const int nst = (j + 1) % C::kStages, nph = ((j + 1) / C::kStages) & 1;
-      if (j == 0) {
-        ok = wait(b_kfull + 8 * st, ph);
-        if (!ok) break;
-#pragma unroll
-        for (int t = 0; t < C::kTilesM; ++t) qk(0, t);
+    // step by step: scores of row tile t of key tile i, and (two row tiles) after the products of tile
+    // i - 1 or (one row tile, two buffers) before them
+#pragma unroll 1
+    for (int i = 0; ok && i <= tiles; ++i) {
+      const int j = i - 1;
+      if (i < tiles && !(ok = wait(b_kfull + 8 * (i % C::kStages), (i / C::kStages) & 1))) break;
+      if (j >= 0) {
+        if (C::kTilesM == 1 && i < tiles) qk(i, 0);
+        if (!(ok = wait(b_vfull + 8 * (j % C::kStages), (j / C::kStages) & 1))) break;
+        clear_tail(j);
+      } else if (C::kTilesM == 1 && tiles > 0) {
+        qk(0, 0);
       }
-      if (C::kTilesM == 1 && j + 1 < tiles) {
-        if (!(ok = wait(b_kfull + 8 * nst, nph))) break;
-        qk(j + 1, 0);
-      }
-#pragma unroll
+#pragma unroll 1
       for (int t = 0; t < C::kTilesM; ++t) {
-        const int x = C::kTilesM == 2 ? t : j & 1;
-        const int use = C::kTilesM == 2 ? j : j >> 1;
-        if (!(ok = wait(b_p + 8 * x, use & 1))) break;
-        if (t == 0) {
-          if (!(ok = wait(b_vfull + 8 * st, ph))) break;
-          clear_tail(j);
+        if (j >= 0) {
+          if (!(ok = wait(b_p + 8 * buffer(t, j), use(j)))) break;
+          tc::fence_after_sync();
+          pv(j, t);
         }
-        tc::fence_after_sync();
-        pv(j, t);
-        if (C::kTilesM == 2 && j + 1 < tiles) {
-          if (t == 0 && !(ok = wait(b_kfull + 8 * nst, nph))) break;
-          qk(j + 1, t);
-        }
+        if (C::kTilesM == 2 && i < tiles) qk(i, t);
       }
-    }
-    if (s_fail) {  // MMAs in flight read shared memory and write tensor memory: wait for them
-      if (lane == 0) {
-        tc::mma_commit(b_drain);
-        mbar_wait_bounded(b_drain, 0);
-      }
-      __syncwarp();
     }
   } else {
-    // ---- softmax: thread = row
-    const int t = warp / 4;                       // row tile
-    const int r = tid & 127;                      // row of the tile
-    const int row = u.row0 + t * 128 + r;         // (token, head) row of the request
-    const int64_t rows_all = static_cast<int64_t>(n) * G;
-    const bool live = row < rows_all;
-    const int token = live ? row / G : 0;
-    const int head = u.h * G + (live ? row % G : 0);
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    // query row: scaled to [128, 256) by a power of two and split
-    float factor;
-    bool finite;
+    // ---- queries: a warp takes 8 or 16 rows, a lane 8 elements of one; each row is scaled to [128, 256) by a
+    // power of two and split
     {
-      const uint16_t* qp = a.q + static_cast<int64_t>(first + token) * a.q_stride + static_cast<int64_t>(head) * D;
-      uint32_t top = 0;
-      for (int c = 0; live && c < D / 8; ++c) {
-        const uint4 w = *reinterpret_cast<const uint4*>(qp + c * 8);
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+      constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes of a row, rows at a time
+      const float sign = a.scale < 0.0f ? -1.0f : 1.0f;     // the factor is kept positive
+      constexpr int kPer = C::kRows / C::kSoftWarps;         // rows of a warp
+      constexpr int kLoads = kPer / kAtOnce < 4 ? kPer / kAtOnce : 4;  // in flight
+#pragma unroll 1
+      for (int i0 = 0; i0 < kPer / kAtOnce; i0 += kLoads) {
+      uint4 raw[kLoads];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, max(x[i] & 0x7FFFu, (x[i] >> 16) & 0x7FFFu));
+      for (int i = 0; i < kLoads; ++i) {
+        const int rr = warp * kPer + (i0 + i) * kAtOnce + lane / kLanes;  // row of the unit
+        const int row = u.row0 + rr, token = row / G;
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (row < rows_all)
+          raw[i] = *reinterpret_cast<const uint4*>(a.q + (first + token) * a.q_stride +
+                                                   (u.h * G + row - token * G) * D + (lane % kLanes) * 8);
       }
-      const int e = min(max(static_cast<int>(top >> 7), 1), 254);       // 127 + exponent of the largest
-      const int down = min(max(127 + 7 - (e - 127), 1), 254);           // * 2^(7 - exponent)
-      const float sc = __int_as_float(down << 23);
-      // kept positive: the sign of `scale` goes to the query
-      factor = fabsf(a.scale) * kLog2e / sc;
-      const float put = a.scale < 0.0f ? -sc : sc;
-      const uint32_t qh = s_q + (t * 2) * TL::kBytes, ql = qh + TL::kBytes;
-      for (int c = 0; c < D / 16; ++c) {
-        uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int rr = warp * kPer + (i0 + i) * kAtOnce + lane / kLanes;
+        const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        uint32_t top = 0;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) top = max(top, max(x[y] & 0x7FFFu, (x[y] >> 16) & 0x7FFFu));
+        if constexpr (kLanes == 32) {
+          top = __reduce_max_sync(0xFFFFFFFFu, top);
+        } else {
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        }
+        const int e = min(max(static_cast<int>(top >> 7), 1), 254);       // 127 + exponent of the largest
+        const int down = min(max(127 + 7 - (e - 127), 1), 254);           // * 2^(7 - exponent)
+        const float sc = __int_as_float(down << 23), put = sc * sign;
+        uint32_t hi[2], lo[2];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const uint4 w = live ? *reinterpret_cast<const uint4*>(qp + c * 16 + y * 8) : make_uint4(0, 0, 0, 0);
-          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+          float f[4], g[4];
+          f[0] = __uint_as_float(x[2 * y] << 16) * put;
+          f[1] = __uint_as_float(x[2 * y] & 0xFFFF0000u) * put;
+          f[2] = __uint_as_float(x[2 * y + 1] << 16) * put;
+          f[3] = __uint_as_float(x[2 * y + 1] & 0xFFFF0000u) * put;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float f[4], g[4];
-            f[0] = __uint_as_float(x[2 * i] << 16) * put;
-            f[1] = __uint_as_float(x[2 * i] & 0xFFFF0000u) * put;
-            f[2] = __uint_as_float(x[2 * i + 1] << 16) * put;
-            f[3] = __uint_as_float(x[2 * i + 1] & 0xFFFF0000u) * put;
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              g[z] = __uint_as_float(__float_as_uint(f[z]) & 0xFFF00000u);  // sign, exponent, 3 bits
-              f[z] -= g[z];
-            }
-            hi[y * 2 + i] = e4m3x4(g[0], g[1], g[2], g[3]);
-            lo[y * 2 + i] = e4m3x4(f[0], f[1], f[2], f[3]);
+          for (int z = 0; z < 4; ++z) {
+            g[z] = __uint_as_float(__float_as_uint(f[z]) & 0xFFF00000u);  // sign, exponent, 3 bits
+            f[z] -= g[z];
           }
+          hi[y] = e4m3x4(g[0], g[1], g[2], g[3]);
+          lo[y] = e4m3x4(f[0], f[1], f[2], f[3]);
         }
-        const uint32_t at = TL::chunk_at(r, c);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(qh + at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(ql + at), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
+        {
+          const int c = lane % kLanes;
+          const uint32_t at = s_q + (rr / 128) * 2 * TL::kBytes + TL::chunk_at(rr % 128, c >> 1) + (c & 1) * 8;
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + TL::kBytes), "r"(lo[0]), "r"(lo[1]) : "memory");
+          // a query that is not finite saturates in 8 bits: its row is NaN through its sum
+          if (c == 0) s_factor[rr] = top < 0x7F80u ? fabsf(a.scale) * kLog2e * __int_as_float((254 - down) << 23) : __int_as_float(0x7FC00000);
+        }
       }
-      finite = top < 0x7F80u;
+      }
     }
     tc::fence_async_smem();
     mbar_arrive(b_q);
 
+    // ---- softmax: kSplitC threads a row, NC of the tile's columns each
+    const int t = warp / (4 * C::kSplitC);        // row tile
+    const int half = warp / 4 % C::kSplitC;       // (which of the row's threads)
+    const int r = t * 128 + (warp & 3) * 32 + lane;  // row of the unit
+    const int row = u.row0 + r;                   // (token, head) row of the request
+    const bool live = row < rows_all;
+    const int token = live ? row / G : 0;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int team = 1 + t * 4 + (warp & 3);      // the barrier of the warps that share rows
+    bool ok = wait(b_q, 0);
+    const float given = s_factor[r];
+    const bool finite = given == given;
+    const float factor = finite ? given : 0.0f;
     const int sees = live ? min(len, len - n + token + 1) : 0;  // keys this row sees
     // keys before this one are seen by every row of the warp
     const int all_see = __reduce_min_sync(0xFFFFFFFFu, sees);
-    // a query that is not finite saturates in 8 bits: its row is NaN through its sum
-    float m = -INFINITY, l = finite || sees <= 0 ? 0.0f : __int_as_float(0x7FC00000), vs_ref = 0.0f;
-    bool ok = true;
+    float m = -INFINITY, l = finite || sees <= 0 ? 0.0f : __int_as_float(0x7FC00000), lv_ref = -INFINITY;
+    // the two warps of a row agree on when to leave; a warp whose wait runs out meets the other until then
+    bool left = false;
     for (int j = 0; j < tiles; ++j) {
-      const int x = C::kTilesM == 2 ? t : j & 1;
-      const int use = C::kTilesM == 2 ? j : j >> 1;
-      const int st = j % C::kStages;
-      // scales are written before V's copy is armed; V is awaited for them
-      ok = wait(b_vfull + 8 * st, (j / C::kStages) & 1) && wait(b_s + 8 * x, use & 1);
-      if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
-      tc::fence_after_sync();
-      const uint32_t sc = tmem + C::kS + 128 * x + lanes;
-      float s[kTile];
+      const int slot = (j / C::kBatch) % C::kBatches;
+      ok = __all_sync(0xFFFFFFFFu, ok && wait(b_info + 8 * slot, (j / C::kInfoRing) & 1) && wait(b_s + 8 * buffer(t, j), use(j)));
+      const uint32_t sc = tmem + C::kS + 128 * buffer(t, j) + half * NC + lanes;
+      const float2* scales = s_scale + (j % C::kInfoRing) * kGroups;
+      const int cut = sees - (u.tile0 + j) * kTile - half * NC;      // columns from here on are hidden
+      const bool masked = all_see < (u.tile0 + j) * kTile + (half + 1) * NC;
+      // 32 scores, -inf where they are hidden. 64 are read twice (for the maximum, for the exponentials)
+      // rather than kept: registers for four such warps on a scheduler are worth more.
+      auto scores = [&](int c, float (&s)[32]) {
+        tmem_ld32(sc + c, s);
+        tc::tmem_wait_ld();
+        if (masked) {
 #pragma unroll
-      for (int c = 0; c < kTile; c += 32) tmem_ld32(sc + c, s + c);
-      tc::tmem_wait_ld();
-      const float* scales = s_scale + st * kGroups * 2;
-      const int key0 = (u.tile0 + j) * kTile;
-      if (all_see < key0 + kTile) {
-        const int cut = sees - key0;
-#pragma unroll
-        for (int c = 0; c < kTile; ++c)
-          if (c >= cut) s[c] = -INFINITY;
-      }
-      float mx = -INFINITY, vmax = 0.0f;
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        const float ks = scales[2 * g];
-        vmax = fmaxf(vmax, scales[2 * g + 1]);
-        if (ks < 0.0f) {  // a page that is none
-#pragma unroll
-          for (int c = 0; c < kGroup; ++c) s[g * kGroup + c] = -INFINITY;
+          for (int i = 0; i < 32; ++i)
+            if (c + i >= cut) s[i] = -INFINITY;
         }
-        float t0 = s[g * kGroup];
 #pragma unroll
-        for (int c = 1; c + 1 < kGroup; c += 2) t0 = max3(t0, s[g * kGroup + c], s[g * kGroup + c + 1]);
-        t0 = fmaxf(t0, s[g * kGroup + kGroup - 1]);
-        mx = fmaxf(mx, t0 * exponent_scale(ks, factor));
+        for (int g = 0; g < 2; ++g)
+          if (scales[half * NG + c / kGroup + g].x < 0.0f) {  // a page that is none
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i) s[g * kGroup + i] = -INFINITY;
+          }
+      };
+      float mx = -INFINITY, lv_top = -INFINITY;
+      float s[32];
+      if (ok) {
+        tc::fence_after_sync();
+        lv_top = s_top[j % C::kInfoRing];
+#pragma unroll 1
+        for (int c = 0; c < NC; c += 32) {
+          scores(c, s);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            float t0 = s[g * kGroup];
+#pragma unroll
+            for (int i = 1; i + 1 < kGroup; i += 2) t0 = max3(t0, s[g * kGroup + i], s[g * kGroup + i + 1]);
+            t0 = fmaxf(t0, s[g * kGroup + kGroup - 1]);
+            mx = fmaxf(mx, t0 * exponent_scale(scales[half * NG + c / kGroup + g].x, factor));
+          }
+        }
       }
-      const bool grow_v = vmax > 1.75f * vs_ref;
+      s_max[((j & 1) * C::kSplitC + half) * C::kRows + r] = mx;
+      int gone;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, %3, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+          : "=r"(gone)
+          : "r"(static_cast<int>(!ok)), "r"(team), "n"(32 * C::kSplitC)
+          : "memory");
+      if (gone) {
+        left = true;
+        break;
+      }
+#pragma unroll
+      for (int i = 1; i < C::kSplitC; ++i) mx = fmaxf(mx, s_max[((j & 1) * C::kSplitC + (half ^ i)) * C::kRows + r]);
+      const bool grow_v = lv_top > lv_ref + 0.8f;
       if (__any_sync(0xFFFFFFFFu, mx > m + 4.0f) || grow_v) {
         const float to = mx > m + 4.0f ? mx : m;  // by the row alone, whatever its neighbours do
         float corr = to == -INFINITY ? 1.0f : ex2(m - to);
         m = to;
         l *= corr;
         if (grow_v) {
-          corr *= vs_ref / vmax;
-          vs_ref = vmax;
+          corr *= ex2(lv_ref - lv_top);
+          lv_ref = lv_top;
         }
         if (j > 0) {
-          ok = wait(b_pv + 8 * t, (j - 1) & 1);
-          if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
-          tc::fence_after_sync();
+          ok = __all_sync(0xFFFFFFFFu, wait(b_pv + 8 * buffer(t, j - 1), use(j - 1)));
+          if (ok) {
+            tc::fence_after_sync();
 #pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            float o[16];
-            tc::tmem_ld16(tmem + C::kO + t * D + lanes + c, o);
-            tc::tmem_wait_ld();
+            for (int c = half * (D / C::kSplitC); c < (half + 1) * (D / C::kSplitC); c += 32) {
+              float o[32];
+              tmem_ld32(tmem + C::kO + t * D + lanes + c, o);
+              tc::tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] *= corr;
-            tc::tmem_st16(tmem + C::kO + t * D + lanes + c, o);
+              for (int i = 0; i < 32; ++i) o[i] *= corr;
+              tmem_st32(tmem + C::kO + t * D + lanes + c, o);
+            }
           }
         }
       }
-      const float inv_vs = vs_ref > 0.0f ? 1.0f / vs_ref : 0.0f;
       const float base = m == -INFINITY ? 0.0f : 4.0f - m;
-      float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int c = 0; c < kTile; c += 32) {
-        uint32_t w[16];
+#pragma unroll 1
+      for (int c = 0; c < NC; c += 32) {
+        float w[16];
+        if (NC > 32) scores(c, s);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          const float ks = exponent_scale(scales[2 * (c / kGroup + g)], factor);
-          const float rel = scales[2 * (c / kGroup + g) + 1] * inv_vs;
-          const float2 k2 = make_float2(ks, ks), b2 = make_float2(base, base), r2 = make_float2(rel, rel);
+          // p * vs / vs_ref comes out of the exponential; the row sum takes it back by group
+          const float2 e2 = scales[half * NG + c / kGroup + g];
+          const float ks = exponent_scale(e2.x, factor), dl = fmaxf(e2.y - lv_ref, -60.0f);
+          const float2 k2 = make_float2(ks, ks), b2 = make_float2(base + dl, base + dl);
+          float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
           for (int i = 0; i < kGroup; i += 4) {
             float2 hi[2], lo[2];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const int e = c + g * kGroup + i + 2 * y;
+              const int e = g * kGroup + i + 2 * y;
               float2 v = fma2(make_float2(s[e], s[e + 1]), k2, b2);
               v.x = ex2(v.x);
               v.y = ex2(v.y);
               sum = add2(sum, v);
-              v = mul2(v, r2);
               hi[y] = top_bits(v);
-              lo[y] = add2(v, make_float2(-hi[y].x, -hi[y].y));
+              lo[y] = fma2(hi[y], make_float2(-1.0f, -1.0f), v);
             }
-            w[g * 4 + i / 4] = e4m3x4(hi[0].x, hi[0].y, hi[1].x, hi[1].y);
-            w[8 + g * 4 + i / 4] = e4m3x4(lo[0].x, lo[0].y, lo[1].x, lo[1].y);
+            w[g * 4 + i / 4] = __uint_as_float(e4m3x4(hi[0].x, hi[0].y, hi[1].x, hi[1].y));
+            w[8 + g * 4 + i / 4] = __uint_as_float(e4m3x4(lo[0].x, lo[0].y, lo[1].x, lo[1].y));
           }
+          l += (sum.x + sum.y) * ex2(-dl);
         }
-        float f[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(w[i]);
-        tc::tmem_st16(sc + c, f);
+        tc::tmem_st16(sc + c, w);
       }
-      l += sum.x + sum.y;
       tc::tmem_wait_st();
       tc::fence_before_sync();
-      mbar_arrive(b_p + 8 * x);
+      mbar_arrive(b_p + 8 * buffer(t, j));
+      if (j % C::kBatch == C::kBatch - 1 && lane == 0) mbar_arrive(b_infoe + 8 * slot);  // (the warp has met at the store)
     }
     // epilogue
-    // (with two score buffers the last two products may both be under way: a wait for the
-    // last one's parity alone could pass on the one two before)
-    if (C::kTilesM == 1 && ok && tiles > 1) ok = wait(b_pv + 8 * t, (tiles - 2) & 1);
-    if (ok && tiles > 0) ok = wait(b_pv + 8 * t, (tiles - 1) & 1);
-    if (__all_sync(0xFFFFFFFFu, ok)) {
+    if (ok && tiles > 0) ok = wait(b_pv + 8 * buffer(t, tiles - 1), use(tiles - 1));
+    ok = __all_sync(0xFFFFFFFFu, ok && !left);
+    if (!left) {  // the row's sum from its threads
+      s_max[((tiles & 1) * C::kSplitC + half) * C::kRows + r] = l;
+      asm volatile("barrier.cta.sync %0, %1;" ::"r"(team), "n"(32 * C::kSplitC) : "memory");
+      l = 0.0f;
+#pragma unroll
+      for (int i = 0; i < C::kSplitC; ++i) l += s_max[((tiles & 1) * C::kSplitC + i) * C::kRows + r];
+    }
+    if (ok) {
       tc::fence_after_sync();
       const bool whole = u.slot < 0;
+      const float vs_ref = lv_ref == -INFINITY ? 0.0f : ex2(lv_ref);
       const float inv = l > 0.0f || l != l ? vs_ref / l : 0.0f;
       const float mul = whole ? inv : vs_ref;
-      uint16_t* op = a.out + (static_cast<int64_t>(first + token) * a.Hq + head) * D;
-      const int64_t at = static_cast<int64_t>(u.slot) * C::kRows + t * 128 + r;
-      float* pp = p.part + at * D;
-      for (int c = 0; c < D; c += 16) {
-        float o[16];
-        if (tiles > 0) {
-          tc::tmem_ld16(tmem + C::kO + t * D + lanes + c, o);
-          tc::tmem_wait_ld();
-        } else {
+      const bool none = tiles == 0 || (whole && inv == 0.0f);  // zeros, whatever tensor memory holds
+      if (!whole && live && half == 0) p.ml[static_cast<int64_t>(u.slot) * C::kRows + r] = make_float2(m, l);
+      // Through the row tile's queries in shared memory (their MMAs are done), some columns at a time, so that
+      // a warp writes rows piece by piece and not 32 rows at once; 16-byte chunks c of row i at c ^ (i mod chunks)
+      const uint32_t stage = s_q + warp * (C::kQ / C::kSoftWarps);
+      constexpr int kFit = C::kQ / C::kSoftWarps / 128;  // fp32 columns of 32 rows that fit
+      constexpr int kCols = kFit < D / C::kSplitC ? kFit : D / C::kSplitC;
+      constexpr int kLoad = kCols < 32 ? 16 : 32;
+      // where the lane's row goes, in elements
+      const int64_t mine = whole ? (static_cast<int64_t>(first + token) * a.Hq + u.h * G + row - token * G) * D
+                                 : (static_cast<int64_t>(u.slot) * C::kRows + r) * D;
+#pragma unroll 1
+      for (int c = half * (D / C::kSplitC); c < (half + 1) * (D / C::kSplitC); c += kCols) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = 0.0f;
-        }
-        if (live && whole) {
-          uint32_t w[8];
+        for (int x = 0; x < kCols; x += kLoad) {
+          float o[kLoad];
+          if (tiles > 0) {
+            if constexpr (kLoad == 32) tmem_ld32(tmem + C::kO + t * D + lanes + c + x, o);
+            else tc::tmem_ld16(tmem + C::kO + t * D + lanes + c + x, o);
+            tc::tmem_wait_ld();
+          }
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(inv == 0.0f ? 0.0f : o[2 * i + 1] * mul), "f"(inv == 0.0f ? 0.0f : o[2 * i] * mul));
-          *reinterpret_cast<uint4*>(op + c) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(op + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-        } else if (live) {
+          for (int i = 0; i < kLoad; ++i) o[i] = none ? 0.0f : o[i] * mul;
+          if (whole) {
 #pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<float4*>(pp + c + i) = make_float4(o[i] * mul, o[i + 1] * mul, o[i + 2] * mul, o[i + 3] * mul);
+            for (int i = 0; i < kLoad; i += 8) {
+              uint32_t w[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[y]) : "f"(o[i + 2 * y + 1]), "f"(o[i + 2 * y]));
+              const int chunk = ((x + i) / 8) ^ (lane % (kCols / 8));
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * (kCols * 2) + chunk * 16), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < kLoad; i += 4) {
+              const int chunk = ((x + i) / 4) ^ (lane % (kCols / 4));
+              asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * (kCols * 4) + chunk * 16), "f"(o[i]), "f"(o[i + 1]), "f"(o[i + 2]), "f"(o[i + 3]) : "memory");
+            }
+          }
         }
         __syncwarp();
+        auto drain = [&](auto per_tag) {
+          constexpr int per = decltype(per_tag)::value;  // chunks of a row
+#pragma unroll
+          for (int e = 0; e < per; ++e) {
+            const int i = (e * 32 + lane) / per, chunk = lane % per;
+            const int64_t at = __shfl_sync(0xFFFFFFFFu, mine, i);
+            const bool there = __shfl_sync(0xFFFFFFFFu, static_cast<int>(live), i);
+            uint4 v;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(stage + i * per * 16 + ((chunk ^ (i % per)) << 4)));
+            if (there) {
+              if (per == kCols / 8) *reinterpret_cast<uint4*>(a.out + at + c + chunk * 8) = v;
+              else *reinterpret_cast<uint4*>(p.part + at + c + chunk * 4) = v;
+            }
+          }
+        };
+        if (whole) drain(std::integral_constant<int, kCols / 8>{});
+        else drain(std::integral_constant<int, kCols / 4>{});
+        __syncwarp();
       }
-      if (!whole && live) p.ml[at] = make_float2(m, l);
     }
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (tid == 0 && s_fail && a.err) atomicOr(a.err, GDN_DEVERR_TIMEOUT);
+  if (s_fail) {  // a wait ran out: leave only once what is in flight has landed
+    if (tid == 0 && a.err) atomicOr(a.err, GDN_DEVERR_TIMEOUT);
+    if (warp >= C::kSoftWarps + 2)
+      for (int i = max(0, copies - C::kStages); i < copies; ++i)
+        mbar_wait_bounded((warp == C::kSoftWarps + 2 ? b_kfull : b_vfull) + 8 * (i % C::kStages), (i / C::kStages) & 1);
+    if (warp == C::kSoftWarps && lane == 0) {
+      tc::mma_commit(b_drain);
+      mbar_wait_bounded(b_drain, 0);
+    }
+    __syncthreads();
+  }
   if (warp == C::kSoftWarps) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
@@ -775,8 +734,7 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(const __grid_con
   if (static_cast<int>(blockIdx.x) >= p.counts[1]) return;
   const PrefillUnit u = p.joins[blockIdx.x];
   const AttnArgs& a = p.a;
-  int first, n, len;
-  request(p, u.b, first, n, len);
+  const int first = u.first, n = u.n;
   const int G = a.Hq / a.H;
   const int d4 = threadIdx.x % kLanes;
   for (int i = threadIdx.x / kLanes; i < 16; i += kPar) {
@@ -856,15 +814,14 @@ cudaError_t launch_after(void (*kern)(KArgs...), dim3 grid, int threads, int sme
 }
 
 template <int D>
-cudaError_t launch_prefill_d(const PrefillParams& p, const PrefillLayout& L, const CUtensorMap& kmap,
-                             const CUtensorMap& vmap, cudaStream_t s) {
+cudaError_t launch_prefill_d(const PrefillParams& p, const PrefillLayout& L, const CacheMaps& maps, cudaStream_t s) {
   using C = PrefillCfg<D>;
   cudaError_t e = cudaFuncSetAttribute(attn_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   attn_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = launch_after(attn_prefill_kernel<D>, dim3(L.max_units), C::kThreads, C::kSmem, s, p, kmap, vmap);
+  e = launch_after(attn_prefill_kernel<D>, dim3(L.max_units), C::kThreads, C::kSmem, s, p, maps);
   if (e != cudaSuccess || L.max_slots == 0) return e;
   const int64_t joins = static_cast<int64_t>(p.nb) * kFewUnits;
   const int grid = static_cast<int>(joins < L.max_units ? joins : L.max_units);
@@ -878,10 +835,8 @@ size_t attn_prefill_workspace(int T, int B, int max_blocks, int Hq, int H, int d
 }
 
 cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t s) {
-  CUtensorMap kmap, vmap;
-  const int64_t rows = static_cast<int64_t>(a.num_blocks) * a.H * a.bs;
-  cudaError_t e = encode_cache_map(&kmap, a.k_cache, rows, a.d, kGroup);
-  if (e == cudaSuccess) e = encode_cache_map(&vmap, a.v_cache, rows, a.d, kGroup);
+  CacheMaps maps;
+  cudaError_t e = encode_cache_maps(&maps, a);
   if (e != cudaSuccess) return e;
   for (int b0 = 0; b0 < a.B; b0 += kBatchPerLaunch) {
     PrefillParams p;
@@ -898,9 +853,9 @@ cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t s) {
     p.joins = reinterpret_cast<PrefillUnit*>(ws + L.joins);
     p.ml = reinterpret_cast<float2*>(ws + L.ml);
     p.part = reinterpret_cast<float*>(ws + L.part);
-    e = a.d == 64    ? launch_prefill_d<64>(p, L, kmap, vmap, s)
-        : a.d == 128 ? launch_prefill_d<128>(p, L, kmap, vmap, s)
-                     : launch_prefill_d<256>(p, L, kmap, vmap, s);
+    e = a.d == 64    ? launch_prefill_d<64>(p, L, maps, s)
+        : a.d == 128 ? launch_prefill_d<128>(p, L, maps, s)
+                     : launch_prefill_d<256>(p, L, maps, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

@@ -79,9 +79,12 @@ cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s);
 size_t attn_prefill_workspace(int T, int B, int max_blocks, int Hq, int H, int d, int bs);
 cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t s);
 
-// Tensor map of one cache pool as rows of d bytes, read in boxes of `rows` rows by
-// min(d, 128) bytes that land swizzled (128-byte pattern; 64-byte for d = 64) in shared memory.
-// Encoded anew for every call; cudaErrorNotSupported if the driver lacks the entry point.
-cudaError_t encode_cache_map(CUtensorMap* map, const uint8_t* cache, int64_t total_rows, int d, int rows);
+// Tensor maps of the two pools as rows of d bytes, read in boxes of 16 rows (the smallest block) or of a
+// block's rows by min(d, 128) bytes that land swizzled (128-byte pattern; 64-byte for d = 64) in
+// shared memory. Encoded anew for every call; cudaErrorNotSupported if the driver lacks the entry point.
+struct CacheMaps {
+  CUtensorMap k_group, v_group, k_page, v_page;
+};
+cudaError_t encode_cache_maps(CacheMaps* maps, const AttnArgs& a);
 
 }  // namespace gdn

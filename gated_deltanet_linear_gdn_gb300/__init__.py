@@ -11,6 +11,7 @@ torch is used only for device memory, streams and dtypes.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -174,8 +175,13 @@ def _ptr(t):
     return ctypes.c_void_p(int(t))
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch._C._cuda_getDevice())  # current_stream() without its object
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
@@ -302,40 +308,53 @@ def gdn_mixed_step(mixed_qkv, a, b, A_log, dt_bias, conv_weight, conv_bias, conv
 
 
 # ------------------------------------------------- paged 8-bit cache and its attention
+#
+# A step makes these calls once per layer, and the smallest take a few microseconds on the GPU:
+# pointers go to the library as plain integers and shapes are checked once.
 
-def _rows(t):
-    """(pointer, elements from one token to the next) of a [tokens, heads, d] bf16 tensor whose
+_I32, _BF16, _F32 = torch.int32, torch.bfloat16, torch.float32
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _dense(t, dtype, shape, name):
+    """The address of a dense device tensor of this type and shape."""
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, not {t.dtype} "
+                         f"{tuple(t.shape)}")
+    if not (t.is_cuda and t.is_contiguous()) and t.numel():
+        raise ValueError(f"{name} must be a contiguous device tensor")
+    return t.data_ptr()
+
+
+def _tokens(t, shape, name):
+    """(address, elements from one token to the next) of a bf16 tensor [tokens, heads, d] whose
     heads are dense; the token stride is free (a slice of a wider projection)."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3:
-        raise ValueError("a bfloat16 tensor [tokens, heads, d] is expected")
-    if t.numel() == 0:
-        return None, t.shape[1] * t.shape[2]
-    if not t.is_cuda:
-        raise ValueError("device tensors expected")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-        raise ValueError("the heads of a token must be dense")
-    step = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
-    return ctypes.c_void_p(t.data_ptr()), step
+    if t.dtype is not _BF16 or t.shape != shape:
+        raise ValueError(f"{name} must be bfloat16 of shape {tuple(shape)}, not {t.dtype} "
+                         f"{tuple(t.shape)}")
+    n, heads, d = shape
+    if n == 0:
+        return 0, heads * d
+    step, of_head, of_d = t.stride()
+    if not t.is_cuda or (of_d != 1 and d > 1) or (of_head != d and heads > 1):
+        raise ValueError(f"{name} must be a device tensor with dense heads")
+    return t.data_ptr(), (step if n > 1 else max(step, heads * d))
 
 
-def _want(t, dtype, shape, name):
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    return _ptr(t)
+@functools.lru_cache(maxsize=None)
+def _cache_dims(q_heads, kv_heads, head_dim, block_size):
+    return gdn_cache_dims(q_heads, kv_heads, head_dim, block_size)
 
 
-def _cache(k_cache, v_cache, k_scale, v_scale, q_heads=None):
-    """Checked pointers of the cache, its number of blocks and its gdn_cache_dims."""
-    if k_cache.dim() != 4 or k_cache.dtype not in (torch.float8_e4m3fn, torch.uint8):
+def _cache(k_cache, v_cache, k_scale, v_scale):
+    """The cache's addresses and shape [num_blocks, Hkv, block_size, head_dim]."""
+    shape, dtype = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or dtype not in _E4M3:
         raise ValueError("the caches must be float8_e4m3fn (or its bytes) [num_blocks, Hkv, "
                          "block_size, head_dim]")
-    NB, H, bs, d = k_cache.shape
-    return ([_ptr(k_cache), _want(v_cache, k_cache.dtype, k_cache.shape, "v_cache"),
-             _want(k_scale, torch.float32, (NB, H), "k_scale"),
-             _want(v_scale, torch.float32, (NB, H), "v_scale")],
-            NB, gdn_cache_dims(H if q_heads is None else q_heads, H, d, bs))
+    return (_dense(k_cache, dtype, shape, "k_cache"), _dense(v_cache, dtype, shape, "v_cache"),
+            _dense(k_scale, _F32, shape[:2], "k_scale"),
+            _dense(v_scale, _F32, shape[:2], "v_scale")), shape
 
 
 def gdn_cache_tables(lens_old, lens_new, block_table, free_ring, pool, pool_out, cu_tokens,
@@ -343,28 +362,25 @@ def gdn_cache_tables(lens_old, lens_new, block_table, free_ring, pool, pool_out,
     """The step's block tables, slots and positions from its requests' lengths (include/gdn.h).
     block_table [B, max_blocks], free_ring [num_blocks], pool and pool_out [2] (head, free
     count): in place; writes cu_tokens [B + 1], slot_map and positions [capacity], lens [B]."""
-    i32, B = torch.int32, lens_old.shape[0]
-    T = slot_map.shape[0]
+    (B,), (T,), (N,), W = lens_old.shape, slot_map.shape, free_ring.shape, block_table.shape[-1]
     _check(lib().gdn_cache_tables(
-        _want(lens_old, i32, (B,), "lens_old"), _want(lens_new, i32, (B,), "lens_new"), B,
-        _want(block_table, i32, (B, block_table.shape[-1]), "block_table"),
-        block_table.shape[-1], _want(free_ring, i32, (free_ring.numel(),), "free_ring"),
-        free_ring.numel(), _want(pool, i32, (2,), "pool"), _want(pool_out, i32, (2,), "pool_out"),
-        int(block_size), T, _want(cu_tokens, i32, (B + 1,), "cu_tokens"),
-        _want(slot_map, i32, (T,), "slot_map"), _want(positions, i32, (T,), "positions"),
-        _want(lens, i32, (B,), "lens"), _ptr(err), _stream(stream)))
+        _dense(lens_old, _I32, (B,), "lens_old"), _dense(lens_new, _I32, (B,), "lens_new"), B,
+        _dense(block_table, _I32, (B, W), "block_table"), W,
+        _dense(free_ring, _I32, (N,), "free_ring"), N, _dense(pool, _I32, (2,), "pool"),
+        _dense(pool_out, _I32, (2,), "pool_out"), block_size, T,
+        _dense(cu_tokens, _I32, (B + 1,), "cu_tokens"), _dense(slot_map, _I32, (T,), "slot_map"),
+        _dense(positions, _I32, (T,), "positions"), _dense(lens, _I32, (B,), "lens"),
+        _ptr(err), _stream(stream)))
 
 
 def gdn_cache_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, *, err=None,
                      stream=None):
     """Writes k, v [T, Hkv, d] (bf16, any token stride) into the 8-bit cache at slot_map [T]."""
-    ptrs, NB, dims = _cache(k_cache, v_cache, k_scale, v_scale)
-    T = slot_map.shape[0]
-    if tuple(k.shape) != (T, dims.num_kv_heads, dims.head_dim) or k.shape != v.shape:
-        raise ValueError("k and v must be [tokens, Hkv, head_dim]")
-    (kp, ks), (vp, vs) = _rows(k), _rows(v)
-    _check(lib().gdn_cache_append(kp, ks, vp, vs, _want(slot_map, torch.int32, (T,), "slot_map"),
-                                  T, *ptrs, NB, dims, _ptr(err), _stream(stream)))
+    addresses, (NB, H, bs, d) = _cache(k_cache, v_cache, k_scale, v_scale)
+    (T,) = slot_map.shape
+    _check(lib().gdn_cache_append(*_tokens(k, (T, H, d), "k"), *_tokens(v, (T, H, d), "v"),
+                                  _dense(slot_map, _I32, (T,), "slot_map"), T, *addresses, NB,
+                                  _cache_dims(H, H, d, bs), _ptr(err), _stream(stream)))
 
 
 def gdn_attn_decode_workspace_size(batch, max_blocks, num_q_heads, num_kv_heads, head_dim,
@@ -378,16 +394,13 @@ def gdn_attn_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, ou
                     scale=None, err=None, stream=None):
     """Attention of one token per request over the 8-bit cache. q, out: [B, Hq, d] bf16 (q with
     any token stride); scale: head_dim ** -0.5 if None."""
-    B, Hq, d = q.shape
-    ptrs, NB, dims = _cache(k_cache, v_cache, k_scale, v_scale, Hq)
-    if d != dims.head_dim:
-        raise ValueError("q and the cache differ in head_dim")
-    qp, qs = _rows(q)
+    addresses, (NB, H, bs, d) = _cache(k_cache, v_cache, k_scale, v_scale)
+    B, Hq, W = q.shape[0], q.shape[1], block_table.shape[-1]
     _check(lib().gdn_attn_decode(
-        qp, qs, *ptrs, NB, _want(block_table, torch.int32, (B, block_table.shape[-1]), "block_table"),
-        block_table.shape[-1], _want(lens, torch.int32, (B,), "lens"), B, dims,
-        float(d ** -0.5 if scale is None else scale),
-        _want(out, torch.bfloat16, (B, Hq, d), "out"), _ptr(workspace),
+        *_tokens(q, (B, Hq, d), "q"), *addresses, NB,
+        _dense(block_table, _I32, (B, W), "block_table"), W, _dense(lens, _I32, (B,), "lens"), B,
+        _cache_dims(Hq, H, d, bs), d ** -0.5 if scale is None else scale,
+        _dense(out, _BF16, (B, Hq, d), "out"), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream)))
 
 
@@ -402,19 +415,15 @@ def gdn_attn_prefill(q, cu_tokens, k_cache, v_cache, k_scale, v_scale, block_tab
                      workspace, *, scale=None, err=None, stream=None):
     """Causal attention of packed prompt tokens over the 8-bit cache, which holds them already.
     q, out: [T, Hq, d] bf16 (q with any token stride); cu_tokens [B + 1], lens [B] int32."""
-    T, Hq, d = q.shape
-    B = lens.shape[0]
-    ptrs, NB, dims = _cache(k_cache, v_cache, k_scale, v_scale, Hq)
-    if d != dims.head_dim:
-        raise ValueError("q and the cache differ in head_dim")
-    qp, qs = _rows(q)
+    addresses, (NB, H, bs, d) = _cache(k_cache, v_cache, k_scale, v_scale)
+    T, Hq, B, W = q.shape[0], q.shape[1], lens.shape[0], block_table.shape[-1]
     _check(lib().gdn_attn_prefill(
-        qp, qs, _want(cu_tokens, torch.int32, (B + 1,), "cu_tokens"), *ptrs, NB,
-        _want(block_table, torch.int32, (B, block_table.shape[-1]), "block_table"),
-        block_table.shape[-1], _want(lens, torch.int32, (B,), "lens"), B, T, dims,
-        float(d ** -0.5 if scale is None else scale),
-        _want(out, torch.bfloat16, (T, Hq, d), "out"), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream)))
+        *_tokens(q, (T, Hq, d), "q"), _dense(cu_tokens, _I32, (B + 1,), "cu_tokens"), *addresses,
+        NB, _dense(block_table, _I32, (B, W), "block_table"), W,
+        _dense(lens, _I32, (B,), "lens"), B, T, _cache_dims(Hq, H, d, bs),
+        d ** -0.5 if scale is None else scale, _dense(out, _BF16, (T, Hq, d), "out"),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err),
+        _stream(stream)))
 
 
 class DecodeGraph:

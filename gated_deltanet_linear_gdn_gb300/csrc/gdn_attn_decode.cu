@@ -751,66 +751,98 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
   }
 }
 
-// Joins the units of one request, kv head and query head in unit order (4 kLanes of its d per CTA); an
-// empty request gets zeros.
-template <int D, int kLanes>
-__global__ void __launch_bounds__(256) attn_decode_join_kernel(const __grid_constant__ DecodeParams p) {
-  constexpr int kRows = 256 / kLanes;
-  __shared__ float4 s_o[kRows][kLanes];
-  __shared__ float s_sum[kRows], s_top[8];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const AttnArgs& a = p.a;
-  const int HC = a.H * p.chunks, G = a.Hq / a.H;
-  const int b = blockIdx.x / HC, hc = blockIdx.x % HC, head = blockIdx.y;
-  const int qh = (hc / p.chunks) * G + (hc % p.chunks) * 16 + head;
-  if ((hc % p.chunks) * 16 + head >= G) return;
-  const int n = units_of(min(max(a.lens[p.b0 + b], 0), a.max_blocks * a.bs));
-  if (n == 1) return;
-  const int tid = threadIdx.x, d4 = tid % kLanes + blockIdx.z * kLanes, row = tid / kLanes;
-  const int64_t f = (static_cast<int64_t>(b) * HC + hc) * p.each;
-  const float2* ml = p.ml + f * p.heads + head;
-  const float* part = p.part + (f * p.heads + head) * D;
-  float top = -INFINITY;
-  for (int i = tid; i < n; i += 256) top = fmaxf(top, ml[static_cast<int64_t>(i) * p.heads].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  if ((tid & 31) == 0) s_top[tid >> 5] = top;
-  __syncthreads();
-  top = s_top[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) top = fmaxf(top, s_top[i]);
-  float sum = 0.0f;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (int i = row; i < n; i += kRows) {
-    const float2 e = ml[static_cast<int64_t>(i) * p.heads];
+// Joins the units of one request, kv head and head chunk; an empty request gets zeros. A thread has four d
+// of one head. Up to kJoinRows units it takes in order; more are taken by kJoinRows threads, unit u by
+// u mod kJoinRows, whose sums are then taken in order (for few units that is the same). Either way the order
+// goes by the request's own units.
+constexpr int kJoinRows = 16;
+
+struct JoinSum {
+  float m = -INFINITY, l = 0.0f;
+  float4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+  __device__ __forceinline__ static float weight(float m, float l, float top) {
     // a unit without keys has m = -inf, l = 0; with only NaN scores m = -inf, l = NaN
-    const float c = e.x == -INFINITY ? (e.y == 0.0f ? 0.0f : 1.0f) : ex2(e.x - top);
-    const float4 v = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(i) * p.heads * D + d4 * 4);
-    sum += e.y * c;
-    o.x += v.x * c;
-    o.y += v.y * c;
-    o.z += v.z * c;
-    o.w += v.w * c;
+    return m == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : ex2(m - top);
   }
-  s_o[row][tid % kLanes] = o;
-  if (tid % kLanes == 0) s_sum[row] = sum;
-  __syncthreads();
-  if (row != 0) return;
+  __device__ __forceinline__ void add(float2 e, const float4& v) {
+    const float top = fmaxf(m, e.x), wa = weight(m, l, top), wb = weight(e.x, e.y, top);
+    m = top;
+    l = l * wa + e.y * wb;
+    o.x = o.x * wa + v.x * wb;
+    o.y = o.y * wa + v.y * wb;
+    o.z = o.z * wa + v.z * wb;
+    o.w = o.w * wa + v.w * wb;
+  }
+  // units u, u + step, ..
+  __device__ __forceinline__ void add_units(const float2* ml, const float4* part, int u, int n, int step, int heads, int d4s) {
+    constexpr int kAhead = 4;
+#pragma unroll 1
+    for (; u < n; u += kAhead * step) {
+      float2 e[kAhead];
+      float4 v[kAhead];
 #pragma unroll
-  for (int i = 1; i < kRows; ++i) {
-    const float4 v = s_o[i][tid];
-    sum += s_sum[i];
-    o.x += v.x;
-    o.y += v.y;
-    o.z += v.z;
-    o.w += v.w;
+      for (int i = 0; i < kAhead; ++i)
+        if (u + i * step < n) {
+          const int64_t at = static_cast<int64_t>(u + i * step) * heads;
+          e[i] = ml[at];
+          v[i] = part[at * d4s];
+        }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (u + i * step < n) add(e[i], v[i]);
+    }
   }
-  const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-  uint2 st;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(st.x) : "f"(o.y * inv), "f"(o.x * inv));
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(st.y) : "f"(o.w * inv), "f"(o.z * inv));
-  *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(p.b0 + b) * a.Hq + qh) * D + d4 * 4) = st;
+  __device__ __forceinline__ void store(uint16_t* out) const {
+    const float inv = l > 0.0f || l != l ? __fdividef(1.0f, l) : 0.0f;
+    uint2 st;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(st.x) : "f"(o.y * inv), "f"(o.x * inv));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(st.y) : "f"(o.w * inv), "f"(o.z * inv));
+    *reinterpret_cast<uint2*>(out) = st;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) attn_decode_join_kernel(const __grid_constant__ DecodeParams p) {
+  constexpr int kLanes = D / 4;
+  __shared__ float4 s_o[kJoinRows][16];
+  __shared__ float2 s_ml[kJoinRows];
+  const AttnArgs& a = p.a;
+  const int HC = a.H * p.chunks, G = a.Hq / a.H, tid = threadIdx.x;
+  const int b = blockIdx.x / HC, hc = blockIdx.x - b * HC, h = hc / p.chunks, chunk = hc - h * p.chunks;
+  const int heads = min(p.heads, G - chunk * 16);
+  const int n = units_of(min(max(a.lens[p.b0 + b], 0), a.max_blocks * a.bs));
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (by every CTA: this kernel's end stands for the call's)
+  if (n == 1 || (n <= kJoinRows && blockIdx.y > 0)) return;
+  const int64_t f = static_cast<int64_t>(blockIdx.x) * p.each * p.heads;
+  const float2* ml = p.ml + f;
+  const float4* part = reinterpret_cast<const float4*>(p.part + f * D);
+  uint16_t* out = a.out + (static_cast<int64_t>(p.b0 + b) * a.Hq + h * G + chunk * 16) * D;
+  if (n <= kJoinRows) {
+#pragma unroll 1
+    for (int i = tid; i < heads * kLanes; i += 256) {
+      JoinSum sum;
+      const int head = i / kLanes;
+      sum.add_units(ml + head, part + i, 0, n, 1, p.heads, kLanes);
+      sum.store(out + i * 4);
+    }
+    return;
+  }
+  const int row = tid / 16, lane = tid % 16;
+#pragma unroll 1
+  for (int i0 = blockIdx.y * 16; i0 < heads * kLanes; i0 += gridDim.y * 16) {  // 16 lanes of one head
+    JoinSum sum;
+    const int head = i0 / kLanes;
+    sum.add_units(ml + head, part + i0 + lane, row, n, kJoinRows, p.heads, kLanes);
+    s_o[row][lane] = sum.o;
+    if (lane == 0) s_ml[row] = make_float2(sum.m, sum.l);
+    __syncthreads();
+    if (row == 0) {
+#pragma unroll 1
+      for (int i = 1; i < kJoinRows; ++i) sum.add(s_ml[i], s_o[i][lane]);
+      sum.store(out + (i0 + lane) * 4);
+    }
+    __syncthreads();
+  }
 }
 
 struct DecodeLayout {
@@ -847,10 +879,9 @@ cudaError_t launch_decode_d(DecodeParams& p, const CacheMaps& maps, cudaStream_t
   kern<<<grid, kThreads, smem, s>>>(p, maps);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // Many units to join: few d per CTA, more units at a time
-  const bool narrow = D > 64 && p.each > 32;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.nb * p.a.H * p.chunks, p.heads, narrow ? D / 64 : 1);
+  // where requests may have many units, CTAs enough for all their heads and d
+  cfg.gridDim = dim3(p.nb * p.a.H * p.chunks, p.each > kJoinRows ? p.heads * D / 64 : 1, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -858,8 +889,7 @@ cudaError_t launch_decode_d(DecodeParams& p, const CacheMaps& maps, cudaStream_t
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return narrow ? cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<D, 16>, p)
-                : cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<D, D / 4>, p);
+  return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<D>, p);
 }
 
 template <int D>

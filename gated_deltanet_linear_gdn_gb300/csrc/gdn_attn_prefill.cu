@@ -213,6 +213,217 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
   }
 }
 
+// ---- what the two kernels share
+
+// Looks up the pages and scales of a unit's tiles, four at a time: lane = (tile of the batch, 16-key group).
+template <typename C>
+__device__ __forceinline__ void look_up(const PrefillParams& p, const PrefillUnit& u, int tiles, float2* s_scale, int32_t* s_row,
+                                        float* s_top, uint32_t b_info, uint32_t b_infoe, volatile int* fail) {
+  const AttnArgs& a = p.a;
+  const int lane = threadIdx.x & 31, shift = 31 - __clz(a.bs);
+  bool ok = true;
+#pragma unroll 1
+  for (int j0 = 0; j0 < tiles && ok; j0 += C::kBatch) {
+    const int j = j0 + lane / kGroups, pos = (u.tile0 + j) * kTile + (lane % kGroups) * kGroup;
+    int row = a.num_blocks * a.H * a.bs;           // past the cache: zeros
+    float2 sc = make_float2(-1.0f, -INFINITY);     // no key, or a page that is none: not seen
+    if (j < tiles && pos < u.len) {
+      const int page = a.block_table[static_cast<int64_t>(p.b0 + u.b) * a.max_blocks + (pos >> shift)];
+      if (page >= 0 && page < a.num_blocks) {
+        const int64_t at = static_cast<int64_t>(page) * a.H + u.h;
+        sc = make_float2(a.k_scale[at], a.v_scale[at]);
+        row = (static_cast<int>(at) << shift) + (pos & (a.bs - 1));
+      } else if (a.err) {
+        atomicOr(a.err, GDN_DEVERR_BLOCK_RANGE);
+      }
+    }
+    if (sc.x >= 0.0f) asm("lg2.approx.f32 %0, %0;" : "+f"(sc.y));
+    const int slot = (j0 / C::kBatch) % C::kBatches;
+    ok = __all_sync(0xFFFFFFFFu, wait_or_fail(b_infoe + 8 * slot, ((j0 / C::kInfoRing) & 1) ^ 1, fail));
+    if (!ok) break;
+    float top = sc.y;
+#pragma unroll
+    for (int o = 1; o < kGroups; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    s_scale[slot * 32 + lane] = sc;
+    s_row[slot * 32 + lane] = row;
+    if (lane % kGroups == 0) s_top[slot * C::kBatch + lane / kGroups] = top;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b_info + 8 * slot);
+  }
+}
+
+// Copies the key or the value tiles of a unit into a ring of kStages: lane g < 8 has the 16-key group g of each
+// tile. `release`: the lookup ring's barriers that this warp answers for, or 0. Returns the copies started.
+template <int D, typename C, int kStages>
+__device__ __forceinline__ int copy_tiles(const AttnArgs& a, const PrefillUnit& u, int tiles, const CUtensorMap* by_page,
+                                          const CUtensorMap* by_group, uint32_t to, const int32_t* s_row, uint32_t b_full,
+                                          uint32_t b_empty, uint32_t b_info, uint32_t release, volatile int* fail) {
+  using TL = Tile<D>;
+  const int lane = threadIdx.x & 31;
+  const bool head = ((lane * kGroup) & (a.bs - 1)) == 0;  // the group starts a page
+  bool ok = true;
+  int copies = 0;
+#pragma unroll 1
+  for (int j = 0; j < tiles; ++j) {
+    const int st = j % kStages, slot = (j / C::kBatch) % C::kBatches;
+    if (j % C::kBatch == 0) ok = wait_or_fail(b_info + 8 * slot, (j / C::kInfoRing) & 1, fail);
+    ok = __all_sync(0xFFFFFFFFu, ok && wait_or_fail(b_empty + 8 * st, ((j / kStages) & 1) ^ 1, fail));
+    if (!ok) break;
+    const int row = s_row[(j % C::kInfoRing) * kGroups + lane % kGroups];
+    __syncwarp();
+    if (release && j % C::kBatch == C::kBatch - 1 && lane == 0) mbar_arrive(release + 8 * slot);
+    // a page of which every token is the request's goes in one box
+    const bool whole = ((lane * kGroup) & -a.bs) + a.bs <= u.len - (u.tile0 + j) * kTile;
+    if (lane == 0) mbar_arrive_expect_tx(b_full + 8 * st, TL::kBytes);
+    __syncwarp();
+    if (lane < kGroups && (head || !whole))
+#pragma unroll
+      for (int x = 0; x < D; x += 128)
+        tma_rows(to + st * TL::kBytes + (x / 128) * TL::kHalf + lane * kGroup * TL::kRow, whole ? by_page : by_group, x, row, b_full + 8 * st);
+    copies = j + 1;
+  }
+  return copies;
+}
+
+// Queries of a unit's rows: a warp takes kRows / kWarps rows, a lane 8 elements of one; each row is scaled to
+// [128, 256) by a power of two and split into two e4m3 parts.
+template <int D, int kRows, int kWarps>
+__device__ __forceinline__ void split_queries(const AttnArgs& a, const PrefillUnit& u, int G, int rows_all, uint32_t s_q, float* s_factor) {
+  using TL = Tile<D>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, first = u.first;
+  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes of a row, rows at a time
+  const float sign = a.scale < 0.0f ? -1.0f : 1.0f;     // the factor is kept positive
+  constexpr int kPer = kRows / kWarps;         // rows of a warp
+  constexpr int kLoads = kPer / kAtOnce < 4 ? kPer / kAtOnce : 4;  // in flight
+#pragma unroll 1
+  for (int i0 = 0; i0 < kPer / kAtOnce; i0 += kLoads) {
+  uint4 raw[kLoads];
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int rr = warp * kPer + (i0 + i) * kAtOnce + lane / kLanes;  // row of the unit
+    const int row = u.row0 + rr, token = row / G;
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (row < rows_all)
+      raw[i] = *reinterpret_cast<const uint4*>(a.q + (first + token) * a.q_stride +
+                                               (u.h * G + row - token * G) * D + (lane % kLanes) * 8);
+  }
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int rr = warp * kPer + (i0 + i) * kAtOnce + lane / kLanes;
+    const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+    uint32_t top = 0;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) top = max(top, max(x[y] & 0x7FFFu, (x[y] >> 16) & 0x7FFFu));
+    if constexpr (kLanes == 32) {
+      top = __reduce_max_sync(0xFFFFFFFFu, top);
+    } else {
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    }
+    const int e = min(max(static_cast<int>(top >> 7), 1), 254);       // 127 + exponent of the largest
+    const int down = min(max(127 + 7 - (e - 127), 1), 254);           // * 2^(7 - exponent)
+    const float sc = __int_as_float(down << 23), put = sc * sign;
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      float f[4], g[4];
+      f[0] = __uint_as_float(x[2 * y] << 16) * put;
+      f[1] = __uint_as_float(x[2 * y] & 0xFFFF0000u) * put;
+      f[2] = __uint_as_float(x[2 * y + 1] << 16) * put;
+      f[3] = __uint_as_float(x[2 * y + 1] & 0xFFFF0000u) * put;
+#pragma unroll
+      for (int z = 0; z < 4; ++z) {
+        g[z] = __uint_as_float(__float_as_uint(f[z]) & 0xFFF00000u);  // sign, exponent, 3 bits
+        f[z] -= g[z];
+      }
+      hi[y] = e4m3x4(g[0], g[1], g[2], g[3]);
+      lo[y] = e4m3x4(f[0], f[1], f[2], f[3]);
+    }
+    {
+      const int c = lane % kLanes;
+      const uint32_t at = s_q + (rr / 128) * 2 * TL::kBytes + TL::chunk_at(rr % 128, c >> 1) + (c & 1) * 8;
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + TL::kBytes), "r"(lo[0]), "r"(lo[1]) : "memory");
+      // a query that is not finite saturates in 8 bits: its row is NaN through its sum
+      if (c == 0) s_factor[rr] = top < 0x7F80u ? fabsf(a.scale) * kLog2e * __int_as_float((254 - down) << 23) : __int_as_float(0x7FC00000);
+    }
+  }
+  }
+}
+
+// Writes kWide columns from c0 of a unit's rows, thread = row: the result, or the partial sums of a unit that is
+// one of several. Through shared memory that the row tile's queries had (kBytes a warp), some columns at a
+// time, so that a warp writes rows piece by piece and not 32 rows at once; 16-byte chunk c of row i at
+// c ^ (i mod chunks).
+template <int D, int kWide, int kBytes>
+__device__ __forceinline__ void store_rows(const PrefillParams& p, const PrefillUnit& u, int rows, int r, bool live, int token, int head,
+                                           int G, int tiles, float l, float lv_ref, uint32_t taddr, int c0, uint32_t stage) {
+  const AttnArgs& a = p.a;
+  const int lane = threadIdx.x & 31;
+  const bool whole = u.slot < 0;
+  const float vs_ref = lv_ref == -INFINITY ? 0.0f : ex2(lv_ref);
+  const float inv = l > 0.0f || l != l ? __fdividef(vs_ref, l) : 0.0f;
+  const float mul = whole ? inv : vs_ref;
+  const bool none = tiles == 0 || (whole && inv == 0.0f);  // zeros, whatever tensor memory holds
+  constexpr int kFit = kBytes / 128;                       // fp32 columns of 32 rows that fit
+  constexpr int kCols = kFit < kWide ? kFit : kWide;
+  constexpr int kLoad = kCols < 32 ? 16 : 32;
+  // where the lane's row goes, in elements
+  const int64_t mine = whole ? (static_cast<int64_t>(u.first + token) * a.Hq + u.h * G + head) * D
+                             : (static_cast<int64_t>(u.slot) * rows + r) * D;
+#pragma unroll 1
+  for (int c = c0; c < c0 + kWide; c += kCols) {
+#pragma unroll 1
+    for (int x = 0; x < kCols; x += kLoad) {
+      float o[kLoad];
+      if (tiles > 0) {
+        if constexpr (kLoad == 32) tmem_ld32(taddr + c + x, o);
+        else tc::tmem_ld16(taddr + c + x, o);
+        tc::tmem_wait_ld();
+      }
+#pragma unroll
+      for (int i = 0; i < kLoad; ++i) o[i] = none ? 0.0f : o[i] * mul;
+      if (whole) {
+#pragma unroll
+        for (int i = 0; i < kLoad; i += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[y]) : "f"(o[i + 2 * y + 1]), "f"(o[i + 2 * y]));
+          const int chunk = ((x + i) / 8) ^ (lane % (kCols / 8));
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * (kCols * 2) + chunk * 16), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kLoad; i += 4) {
+          const int chunk = ((x + i) / 4) ^ (lane % (kCols / 4));
+          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * (kCols * 4) + chunk * 16), "f"(o[i]), "f"(o[i + 1]), "f"(o[i + 2]), "f"(o[i + 3]) : "memory");
+        }
+      }
+    }
+    __syncwarp();
+    auto drain = [&](auto per_tag) {
+      constexpr int per = decltype(per_tag)::value;  // chunks of a row
+#pragma unroll 4
+      for (int e = 0; e < per; ++e) {
+        const int i = (e * 32 + lane) / per, chunk = lane % per;
+        const int64_t at = __shfl_sync(0xFFFFFFFFu, mine, i);
+        const bool there = __shfl_sync(0xFFFFFFFFu, static_cast<int>(live), i);
+        uint4 v;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(stage + i * per * 16 + ((chunk ^ (i % per)) << 4)));
+        if (there) {
+          if (per == kCols / 8) *reinterpret_cast<uint4*>(a.out + at + c + chunk * 8) = v;
+          else *reinterpret_cast<uint4*>(p.part + at + c + chunk * 4) = v;
+        }
+      }
+    };
+    if (whole) drain(std::integral_constant<int, kCols / 8>{});
+    else drain(std::integral_constant<int, kCols / 4>{});
+    __syncwarp();
+  }
+}
+
+// ------------------------------------------------------------------------------- head_dim 256
+
 template <int D>
 struct PrefillCfg {
   static constexpr int kTilesM = D == 256 ? 1 : 2;       // row tiles of a unit
@@ -264,7 +475,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (static_cast<int>(blockIdx.x) >= *reinterpret_cast<volatile int32_t*>(p.counts)) return;
   const PrefillUnit u = p.units[blockIdx.x];
-  const int first = u.first, n = u.n, len = u.len;
+  const int n = u.n, len = u.len;
   const int G = a.Hq / a.H;
   const int rows_all = n * G;  // (below 2^31: the caller's tokens x heads are)
   const int tiles = u.tile1 - u.tile0;
@@ -298,62 +509,11 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
 
   int copies = 0;  // of a copying warp
   if (warp == C::kSoftWarps + 1) {
-    // ---- lookups: lane = (tile of the batch, 16-key group)
-    bool ok = true;
-    const int shift = 31 - __clz(a.bs);
-    for (int j0 = 0; j0 < tiles && ok; j0 += C::kBatch) {
-      const int j = j0 + lane / kGroups, pos = (u.tile0 + j) * kTile + (lane % kGroups) * kGroup;
-      int row = a.num_blocks * a.H * a.bs;           // past the cache: zeros
-      float2 sc = make_float2(-1.0f, -INFINITY);     // no key, or a page that is none: not seen
-      if (j < tiles && pos < len) {
-        const int page = a.block_table[static_cast<int64_t>(p.b0 + u.b) * a.max_blocks + (pos >> shift)];
-        if (page >= 0 && page < a.num_blocks) {
-          const int64_t at = static_cast<int64_t>(page) * a.H + u.h;
-          sc = make_float2(a.k_scale[at], a.v_scale[at]);
-          row = (static_cast<int>(at) << shift) + (pos & (a.bs - 1));
-        } else if (a.err) {
-          atomicOr(a.err, GDN_DEVERR_BLOCK_RANGE);
-        }
-      }
-      if (sc.x >= 0.0f) asm("lg2.approx.f32 %0, %0;" : "+f"(sc.y));
-      const int slot = (j0 / C::kBatch) % C::kBatches;
-      ok = __all_sync(0xFFFFFFFFu, wait(b_infoe + 8 * slot, ((j0 / C::kInfoRing) & 1) ^ 1));
-      if (!ok) break;
-      float top = sc.y;
-#pragma unroll
-      for (int o = 1; o < kGroups; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      s_scale[slot * 32 + lane] = sc;
-      s_row[slot * 32 + lane] = row;
-      if (lane % kGroups == 0) s_top[slot * C::kBatch + lane / kGroups] = top;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(b_info + 8 * slot);
-    }
+    look_up<C>(p, u, tiles, s_scale, s_row, s_top, b_info, b_infoe, &s_fail);
   } else if (warp >= C::kSoftWarps + 2) {
-    // ---- copies of keys, copies of values: lane g < 8 has the 16-key group g of each tile
     const bool is_v = warp == C::kSoftWarps + 3;
-    const CUtensorMap* by_page = is_v ? &maps.v_page : &maps.k_page;
-    const CUtensorMap* by_group = is_v ? &maps.v_group : &maps.k_group;
-    const uint32_t b_full = is_v ? b_vfull : b_kfull, b_empty = is_v ? b_vempty : b_kempty, to = is_v ? s_v : s_k;
-    const bool head = ((lane * kGroup) & (a.bs - 1)) == 0;  // the group starts a page
-    bool ok = true;
-    for (int j = 0; j < tiles && ok; ++j) {
-      const int st = j % C::kStages, slot = (j / C::kBatch) % C::kBatches;
-      if (j % C::kBatch == 0) ok = wait(b_info + 8 * slot, (j / C::kInfoRing) & 1);
-      ok = __all_sync(0xFFFFFFFFu, ok && wait(b_empty + 8 * st, ((j / C::kStages) & 1) ^ 1));
-      if (!ok) break;
-      const int row = s_row[(j % C::kInfoRing) * kGroups + lane % kGroups];
-      __syncwarp();
-      if (is_v && j % C::kBatch == C::kBatch - 1 && lane == 0) mbar_arrive(b_infoe + 8 * slot);
-      // a page of which every token is the request's goes in one box
-      const bool whole = ((lane * kGroup) & -a.bs) + a.bs <= len - (u.tile0 + j) * kTile;
-      if (lane == 0) mbar_arrive_expect_tx(b_full + 8 * st, TL::kBytes);
-      __syncwarp();
-      if (lane < kGroups && (head || !whole))
-#pragma unroll
-        for (int x = 0; x < D; x += 128)
-          tma_rows(to + st * TL::kBytes + (x / 128) * TL::kHalf + lane * kGroup * TL::kRow, whole ? by_page : by_group, x, row, b_full + 8 * st);
-      copies = j + 1;
-    }
+    copies = is_v ? copy_tiles<D, C, C::kStages>(a, u, tiles, &maps.v_page, &maps.v_group, s_v, s_row, b_vfull, b_vempty, b_info, b_infoe, &s_fail)
+                  : copy_tiles<D, C, C::kStages>(a, u, tiles, &maps.k_page, &maps.k_group, s_k, s_row, b_kfull, b_kempty, b_info, 0, &s_fail);
   } else if (warp == C::kSoftWarps) {
     // ---- MMAs
     constexpr uint32_t iqk = idesc_f8(128, kTile, false, false), ipv = idesc_f8(128, D, false, true);
@@ -426,68 +586,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
       }
     }
   } else {
-    // ---- queries: a warp takes 8 or 16 rows, a lane 8 elements of one; each row is scaled to [128, 256) by a
-    // power of two and split
-    {
-      constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes of a row, rows at a time
-      const float sign = a.scale < 0.0f ? -1.0f : 1.0f;     // the factor is kept positive
-      constexpr int kPer = C::kRows / C::kSoftWarps;         // rows of a warp
-      constexpr int kLoads = kPer / kAtOnce < 4 ? kPer / kAtOnce : 4;  // in flight
-#pragma unroll 1
-      for (int i0 = 0; i0 < kPer / kAtOnce; i0 += kLoads) {
-      uint4 raw[kLoads];
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int rr = warp * kPer + (i0 + i) * kAtOnce + lane / kLanes;  // row of the unit
-        const int row = u.row0 + rr, token = row / G;
-        raw[i] = make_uint4(0, 0, 0, 0);
-        if (row < rows_all)
-          raw[i] = *reinterpret_cast<const uint4*>(a.q + (first + token) * a.q_stride +
-                                                   (u.h * G + row - token * G) * D + (lane % kLanes) * 8);
-      }
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int rr = warp * kPer + (i0 + i) * kAtOnce + lane / kLanes;
-        const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-        uint32_t top = 0;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) top = max(top, max(x[y] & 0x7FFFu, (x[y] >> 16) & 0x7FFFu));
-        if constexpr (kLanes == 32) {
-          top = __reduce_max_sync(0xFFFFFFFFu, top);
-        } else {
-#pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        }
-        const int e = min(max(static_cast<int>(top >> 7), 1), 254);       // 127 + exponent of the largest
-        const int down = min(max(127 + 7 - (e - 127), 1), 254);           // * 2^(7 - exponent)
-        const float sc = __int_as_float(down << 23), put = sc * sign;
-        uint32_t hi[2], lo[2];
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          float f[4], g[4];
-          f[0] = __uint_as_float(x[2 * y] << 16) * put;
-          f[1] = __uint_as_float(x[2 * y] & 0xFFFF0000u) * put;
-          f[2] = __uint_as_float(x[2 * y + 1] << 16) * put;
-          f[3] = __uint_as_float(x[2 * y + 1] & 0xFFFF0000u) * put;
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            g[z] = __uint_as_float(__float_as_uint(f[z]) & 0xFFF00000u);  // sign, exponent, 3 bits
-            f[z] -= g[z];
-          }
-          hi[y] = e4m3x4(g[0], g[1], g[2], g[3]);
-          lo[y] = e4m3x4(f[0], f[1], f[2], f[3]);
-        }
-        {
-          const int c = lane % kLanes;
-          const uint32_t at = s_q + (rr / 128) * 2 * TL::kBytes + TL::chunk_at(rr % 128, c >> 1) + (c & 1) * 8;
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + TL::kBytes), "r"(lo[0]), "r"(lo[1]) : "memory");
-          // a query that is not finite saturates in 8 bits: its row is NaN through its sum
-          if (c == 0) s_factor[rr] = top < 0x7F80u ? fabsf(a.scale) * kLog2e * __int_as_float((254 - down) << 23) : __int_as_float(0x7FC00000);
-        }
-      }
-      }
-    }
+    split_queries<D, C::kRows, C::kSoftWarps>(a, u, G, rows_all, s_q, s_factor);
     tc::fence_async_smem();
     mbar_arrive(b_q);
 
@@ -640,70 +739,10 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
     }
     if (ok) {
       tc::fence_after_sync();
-      const bool whole = u.slot < 0;
-      const float vs_ref = lv_ref == -INFINITY ? 0.0f : ex2(lv_ref);
-      const float inv = l > 0.0f || l != l ? vs_ref / l : 0.0f;
-      const float mul = whole ? inv : vs_ref;
-      const bool none = tiles == 0 || (whole && inv == 0.0f);  // zeros, whatever tensor memory holds
-      if (!whole && live && half == 0) p.ml[static_cast<int64_t>(u.slot) * C::kRows + r] = make_float2(m, l);
-      // Through the row tile's queries in shared memory (their MMAs are done), some columns at a time, so that
-      // a warp writes rows piece by piece and not 32 rows at once; 16-byte chunks c of row i at c ^ (i mod chunks)
-      const uint32_t stage = s_q + warp * (C::kQ / C::kSoftWarps);
-      constexpr int kFit = C::kQ / C::kSoftWarps / 128;  // fp32 columns of 32 rows that fit
-      constexpr int kCols = kFit < D / C::kSplitC ? kFit : D / C::kSplitC;
-      constexpr int kLoad = kCols < 32 ? 16 : 32;
-      // where the lane's row goes, in elements
-      const int64_t mine = whole ? (static_cast<int64_t>(first + token) * a.Hq + u.h * G + row - token * G) * D
-                                 : (static_cast<int64_t>(u.slot) * C::kRows + r) * D;
-#pragma unroll 1
-      for (int c = half * (D / C::kSplitC); c < (half + 1) * (D / C::kSplitC); c += kCols) {
-#pragma unroll
-        for (int x = 0; x < kCols; x += kLoad) {
-          float o[kLoad];
-          if (tiles > 0) {
-            if constexpr (kLoad == 32) tmem_ld32(tmem + C::kO + t * D + lanes + c + x, o);
-            else tc::tmem_ld16(tmem + C::kO + t * D + lanes + c + x, o);
-            tc::tmem_wait_ld();
-          }
-#pragma unroll
-          for (int i = 0; i < kLoad; ++i) o[i] = none ? 0.0f : o[i] * mul;
-          if (whole) {
-#pragma unroll
-            for (int i = 0; i < kLoad; i += 8) {
-              uint32_t w[4];
-#pragma unroll
-              for (int y = 0; y < 4; ++y) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[y]) : "f"(o[i + 2 * y + 1]), "f"(o[i + 2 * y]));
-              const int chunk = ((x + i) / 8) ^ (lane % (kCols / 8));
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * (kCols * 2) + chunk * 16), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < kLoad; i += 4) {
-              const int chunk = ((x + i) / 4) ^ (lane % (kCols / 4));
-              asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * (kCols * 4) + chunk * 16), "f"(o[i]), "f"(o[i + 1]), "f"(o[i + 2]), "f"(o[i + 3]) : "memory");
-            }
-          }
-        }
-        __syncwarp();
-        auto drain = [&](auto per_tag) {
-          constexpr int per = decltype(per_tag)::value;  // chunks of a row
-#pragma unroll
-          for (int e = 0; e < per; ++e) {
-            const int i = (e * 32 + lane) / per, chunk = lane % per;
-            const int64_t at = __shfl_sync(0xFFFFFFFFu, mine, i);
-            const bool there = __shfl_sync(0xFFFFFFFFu, static_cast<int>(live), i);
-            uint4 v;
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(stage + i * per * 16 + ((chunk ^ (i % per)) << 4)));
-            if (there) {
-              if (per == kCols / 8) *reinterpret_cast<uint4*>(a.out + at + c + chunk * 8) = v;
-              else *reinterpret_cast<uint4*>(p.part + at + c + chunk * 4) = v;
-            }
-          }
-        };
-        if (whole) drain(std::integral_constant<int, kCols / 8>{});
-        else drain(std::integral_constant<int, kCols / 4>{});
-        __syncwarp();
-      }
+      if (u.slot >= 0 && live && half == 0) p.ml[static_cast<int64_t>(u.slot) * C::kRows + r] = make_float2(m, l);
+      store_rows<D, D / C::kSplitC, C::kQ / C::kSoftWarps>(p, u, C::kRows, r, live, token, row - token * G, G, tiles, l, lv_ref,
+                                                           tmem + C::kO + t * D + lanes, half * (D / C::kSplitC),
+                                                           s_q + warp * (C::kQ / C::kSoftWarps));
     }
   }
   tc::fence_before_sync();
@@ -720,6 +759,311 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
     __syncthreads();
   }
   if (warp == C::kSoftWarps) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------------- head_dim 64 and 128
+//
+// Here a key costs half the MMA time and the same softmax, so the softmax decides. Its probabilities are f16
+// (one conversion for two of them instead of six operations for the two e4m3 parts) and a warpgroup converts each
+// tile of V to f16 once for the 256 rows that use it; e4m3 values are exact in f16. A thread has a row. Scores are
+// read once: the probabilities are computed with the maximum as it stands, and again only if the tile's
+// own passes it by 2^8 (f16 has the range), which after the first tile almost never happens.
+template <int D>
+struct NarrowCfg {
+  static constexpr int kRows = 256;
+  static constexpr int kSoftWarps = 8, kConvWarps = 4;
+  static constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 4);  // and warps for MMAs, lookups, copies of K and V
+  static constexpr int kStagesK = 3, kStagesV = 2;
+  static constexpr int kBatch = 4, kBatches = 4, kInfoRing = kBatch * kBatches;
+  using TL = Tile<D>;
+  using TV = Tile<2 * D>;                                 // V in f16: rows of 2 D bytes
+  static constexpr int kQ = 2 * 2 * TL::kBytes;           // hi and lo of two row tiles
+  static constexpr int kAtK = kQ;
+  static constexpr int kAtV = kAtK + kStagesK * TL::kBytes;
+  static constexpr int kAtV16 = kAtV + kStagesV * TL::kBytes;
+  static constexpr int kAtScale = kAtV16 + kStagesV * TV::kBytes;  // [kInfoRing][kGroups] (ks, log2 vs)
+  static constexpr int kAtRow = kAtScale + kInfoRing * kGroups * 8;
+  static constexpr int kAtTop = kAtRow + kInfoRing * kGroups * 4;  // [kInfoRing] the tile's largest log2 vs
+  static constexpr int kAtFactor = kAtTop + kInfoRing * 4;         // [kRows]
+  static constexpr int kAtBars = kAtFactor + kRows * 4;
+  static constexpr int kBars = 2 * kStagesK + 4 * kStagesV + 2 * kBatches + 8;
+  static constexpr int kSmem = 1024 + kAtBars + 8 * kBars;
+  static constexpr int kS = 0, kO = 256;                  // tensor memory: scores of two row tiles, then output
+};
+
+template <int D>
+__global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
+    attn_prefill_narrow_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CacheMaps maps) {
+  using C = NarrowCfg<D>;
+  using TL = typename C::TL;
+  using TV = typename C::TV;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + (-smem_addr(smem_raw) & 1023u);
+  const uint32_t s_q = smem_addr(smem), s_k = s_q + C::kAtK, s_v = s_q + C::kAtV, s_v16 = s_q + C::kAtV16;
+  float2* s_scale = reinterpret_cast<float2*>(smem + C::kAtScale);
+  int32_t* s_row = reinterpret_cast<int32_t*>(smem + C::kAtRow);
+  float* s_top = reinterpret_cast<float*>(smem + C::kAtTop);
+  float* s_factor = reinterpret_cast<float*>(smem + C::kAtFactor);
+  const uint32_t b_kfull = s_q + C::kAtBars, b_kempty = b_kfull + 8 * C::kStagesK, b_vfull = b_kempty + 8 * C::kStagesK,
+                 b_wfull = b_vfull + 8 * C::kStagesV, b_vempty = b_wfull + 8 * C::kStagesV, b_wempty = b_vempty + 8 * C::kStagesV,
+                 b_info = b_wempty + 8 * C::kStagesV, b_infoe = b_info + 8 * C::kBatches, b_s = b_infoe + 8 * C::kBatches,
+                 b_p = b_s + 16, b_pv = b_p + 16, b_q = b_pv + 16, b_drain = b_q + 8;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_fail;
+  constexpr int kMma = C::kSoftWarps + C::kConvWarps, kLook = kMma + 1, kCopyK = kMma + 2, kCopyV = kMma + 3;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const AttnArgs& a = p.a;
+  if (tid < 4) prefetch_map(tid == 0 ? &maps.k_page : tid == 1 ? &maps.v_page : tid == 2 ? &maps.k_group : &maps.v_group);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (static_cast<int>(blockIdx.x) >= *reinterpret_cast<volatile int32_t*>(p.counts)) return;
+  const PrefillUnit u = p.units[blockIdx.x];
+  const int n = u.n, len = u.len;
+  const int G = a.Hq / a.H;
+  const int rows_all = n * G;  // (below 2^31: the caller's tokens x heads are)
+  const int tiles = u.tile1 - u.tile0;
+
+  if (tid < C::kBars) {
+    // who arrives: a copy, a commit or one lane, but for what threads and warps release themselves
+    const uint32_t b = b_kfull + 8 * tid;
+    mbar_init(b, b >= b_wfull && b < b_wempty ? 32 * C::kConvWarps
+                 : b >= b_infoe && b < b_s    ? C::kSoftWarps + 1
+                 : b >= b_p && b < b_pv       ? 128
+                 : b == b_q                   ? 32 * C::kSoftWarps
+                                              : 1);
+  }
+  if (tid == 0) s_fail = 0;
+  fence_mbar_init();
+  if (warp == kMma) {
+    tc::tmem_alloc(&s_tmem, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = s_tmem;
+  auto wait = [&](uint32_t b, int parity) { return wait_or_fail(b, parity, &s_fail); };
+
+  int copies = 0;  // of a copying warp
+  if (warp == kLook) {
+    look_up<C>(p, u, tiles, s_scale, s_row, s_top, b_info, b_infoe, &s_fail);
+  } else if (warp == kCopyK) {
+    copies = copy_tiles<D, C, C::kStagesK>(a, u, tiles, &maps.k_page, &maps.k_group, s_k, s_row, b_kfull, b_kempty, b_info, 0, &s_fail);
+  } else if (warp == kCopyV) {
+    copies = copy_tiles<D, C, C::kStagesV>(a, u, tiles, &maps.v_page, &maps.v_group, s_v, s_row, b_vfull, b_vempty, b_info, b_infoe, &s_fail);
+  } else if (warp == kMma) {
+    // ---- MMAs; descriptors but for their start address, which each MMA adds
+    constexpr uint32_t iqk = idesc_f8(128, kTile, false, false);
+    constexpr uint32_t ipv = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | (8u << 24);  // f16 x f16 (MN-major) -> fp32
+    const uint64_t dk = TL::desc(s_k, 16), dq = TL::desc(s_q, 16), dv = TV::desc(s_v16, TV::kHalf);
+    auto qk = [&](int j, int t) {
+      if (lane == 0) {
+        const uint64_t kt = dk + (j % C::kStagesK) * (TL::kBytes >> 4), qt = dq + t * 2 * (TL::kBytes >> 4);
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int ks = 0; ks < D / 32; ++ks)
+            mma_f8_ss(tmem + C::kS + 128 * t, qt + part * (TL::kBytes >> 4) + ks * 2, kt + ks * 2, iqk, part | ks);
+        tc::mma_commit(b_s + 8 * t);
+        if (t == 1) tc::mma_commit(b_kempty + 8 * (j % C::kStagesK));
+      }
+      __syncwarp();
+    };
+    auto pv = [&](int j, int t) {
+      if (lane == 0) {
+        const uint32_t pa = tmem + C::kS + 128 * t;
+        const uint64_t vt = dv + (j % C::kStagesV) * (TV::kBytes >> 4);
+#pragma unroll
+        for (int ks = 0; ks < kTile / 16; ++ks)
+          tc::mma_bf16_ts(tmem + C::kO + t * D, pa + (ks >> 1) * 32 + (ks & 1) * 8, vt + ks * (16 * TV::kRow >> 4), ipv, (j > 0) | ks);
+        tc::mma_commit(b_pv + 8 * t);
+        if (t == 1) tc::mma_commit(b_wempty + 8 * (j % C::kStagesV));
+      }
+      __syncwarp();
+    };
+    bool ok = tiles == 0 || wait(b_q, 0);
+    tc::fence_after_sync();
+#pragma unroll 1
+    for (int i = 0; ok && i <= tiles; ++i) {
+      const int j = i - 1;
+#pragma unroll 1
+      for (int t = 0; t < 2; ++t) {
+        if (j >= 0) {
+          if (t == 0 && !(ok = wait(b_wfull + 8 * (j % C::kStagesV), (j / C::kStagesV) & 1))) break;
+          if (!(ok = wait(b_p + 8 * t, j & 1))) break;
+          tc::fence_after_sync();
+          pv(j, t);
+        }
+        if (i < tiles) {
+          if (t == 0 && !(ok = wait(b_kfull + 8 * (i % C::kStagesK), (i / C::kStagesK) & 1))) break;
+          qk(i, t);
+        }
+      }
+    }
+  } else if (warp >= C::kSoftWarps) {
+    // ---- V to f16: 16-byte chunks of a tile to the threads in turn; keys past the request's length, which hold
+    // whatever their page holds, become zero (0 * NaN is not 0)
+    const int me = tid - 32 * C::kSoftWarps;
+    constexpr int kChunks = D / 16;  // of a key
+    bool ok = true;
+#pragma unroll 1
+    for (int j = 0; j < tiles && ok; ++j) {
+      const int st = j % C::kStagesV, ph = (j / C::kStagesV) & 1;
+      ok = wait(b_vfull + 8 * st, ph) && wait(b_wempty + 8 * st, ph ^ 1);
+      if (!ok) break;
+      const int keys = len - (u.tile0 + j) * kTile;
+      const uint32_t from = s_v + st * TL::kBytes, to = s_v16 + st * TV::kBytes;
+#pragma unroll 4
+      for (int i = me; i < kTile * kChunks; i += 32 * C::kConvWarps) {
+        const int key = i / kChunks, c = i % kChunks;
+        uint32_t x[4], y[8];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(from + TL::chunk_at(key, c)));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (key >= keys) x[e] = 0;
+          asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %2; cvt.rn.f16x2.e4m3x2 %0, lo; cvt.rn.f16x2.e4m3x2 %1, hi;}" : "=r"(y[2 * e]), "=r"(y[2 * e + 1]) : "r"(x[e]));
+        }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + TV::chunk_at(key, 2 * c)), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + TV::chunk_at(key, 2 * c + 1)), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7]) : "memory");
+      }
+      tc::fence_async_smem();
+      mbar_arrive(b_wfull + 8 * st);
+      mbar_arrive(b_vempty + 8 * st);
+    }
+  } else {
+    split_queries<D, C::kRows, C::kSoftWarps>(a, u, G, rows_all, s_q, s_factor);
+    tc::fence_async_smem();
+    mbar_arrive(b_q);
+
+    // ---- softmax: thread = row
+    const int t = warp / 4, r = tid;              // row tile; row of the unit
+    const int row = u.row0 + r;                   // (token, head) row of the request
+    const bool live = row < rows_all;
+    const int token = live ? row / G : 0;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    bool ok = wait(b_q, 0);
+    const float given = s_factor[r];
+    const bool finite = given == given;
+    const float factor = finite ? given : 0.0f;
+    const int sees = live ? min(len, len - n + token + 1) : 0;  // keys this row sees
+    const int all_see = __reduce_min_sync(0xFFFFFFFFu, sees);   // keys before this one are seen by every row of the warp
+    // a query that is not finite saturates in 8 bits: its row is NaN through its sum
+    float m = -INFINITY, l = finite || sees <= 0 ? 0.0f : __int_as_float(0x7FC00000), lv_ref = -INFINITY;
+    const uint32_t sc = tmem + C::kS + 128 * t + lanes;
+#pragma unroll 1
+    for (int j = 0; j < tiles; ++j) {
+      const int slot = (j / C::kBatch) % C::kBatches;
+      if (j % C::kBatch == 0) ok = ok && wait(b_info + 8 * slot, (j / C::kInfoRing) & 1);
+      ok = __all_sync(0xFFFFFFFFu, ok && wait(b_s + 8 * t, j & 1));
+      if (!ok) break;
+      tc::fence_after_sync();
+      const float2* scales = s_scale + (j % C::kInfoRing) * kGroups;
+      const int cut = sees - (u.tile0 + j) * kTile;      // columns from here on are hidden
+      const bool masked = all_see < (u.tile0 + j + 1) * kTile;
+      const float lv_top = s_top[j % C::kInfoRing];
+      uint32_t w[kTile / 2];
+      float sum;
+#pragma unroll 1
+      for (int round = 0;; ++round) {
+        const float base = m == -INFINITY ? 0.0f : -m;
+        float mx = -INFINITY;
+        sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < kTile; c += 32) {
+          float s[32];
+          tmem_ld32(sc + c, s);
+          tc::tmem_wait_ld();
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c + i >= cut) s[i] = -INFINITY;
+          }
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const float2 e2 = scales[c / kGroup + g];
+            if (e2.x < 0.0f) {  // a page that is none
+#pragma unroll
+              for (int i = 0; i < kGroup; ++i) s[g * kGroup + i] = -INFINITY;
+            }
+            // p * vs / vs_ref comes out of the exponential; the row sum takes it back by group
+            const float ks = exponent_scale(e2.x, factor), dl = fmaxf(e2.y - lv_ref, -60.0f);
+            float t0 = s[g * kGroup];
+#pragma unroll
+            for (int i = 1; i + 1 < kGroup; i += 2) t0 = max3(t0, s[g * kGroup + i], s[g * kGroup + i + 1]);
+            mx = fmaxf(mx, fmaxf(t0, s[g * kGroup + kGroup - 1]) * ks);
+            const float2 k2 = make_float2(ks, ks), b2 = make_float2(base + dl, base + dl);
+            float2 part = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < kGroup; i += 2) {
+              float2 v = fma2(make_float2(s[g * kGroup + i], s[g * kGroup + i + 1]), k2, b2);
+              v.x = ex2(v.x);
+              v.y = ex2(v.y);
+              part = add2(part, v);
+              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[(c + g * kGroup + i) / 2]) : "f"(v.y), "f"(v.x));
+            }
+            sum = fmaf(part.x + part.y, ex2(-dl), sum);
+          }
+        }
+        if (round) break;
+        const bool grow_v = lv_top > lv_ref + 3.0f;
+        if (!__any_sync(0xFFFFFFFFu, mx > m + 8.0f) && !grow_v) break;
+        const float to = mx > m + 8.0f ? mx : m;  // by the row alone, whatever its neighbours do
+        float corr = to == -INFINITY ? 1.0f : ex2(m - to);
+        m = to;
+        l *= corr;
+        if (grow_v) {
+          corr *= ex2(lv_ref - lv_top);
+          lv_ref = lv_top;
+        }
+        if (j > 0) {
+          ok = __all_sync(0xFFFFFFFFu, wait(b_pv + 8 * t, (j - 1) & 1));
+          if (!ok) break;
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            float o[16];
+            tc::tmem_ld16(tmem + C::kO + t * D + lanes + c, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] *= corr;
+            tc::tmem_st16(tmem + C::kO + t * D + lanes + c, o);
+          }
+        }
+      }
+      if (!ok) break;
+      l += sum;
+#pragma unroll
+      for (int c = 0; c < kTile; c += 32) tmem_st16u(sc + c, w + c / 2);
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      mbar_arrive(b_p + 8 * t);
+      if (j % C::kBatch == C::kBatch - 1 && lane == 0) mbar_arrive(b_infoe + 8 * slot);  // (the warp has met at the store)
+    }
+    if (ok && tiles > 0) ok = wait(b_pv + 8 * t, (tiles - 1) & 1);
+    if (__all_sync(0xFFFFFFFFu, ok)) {
+      tc::fence_after_sync();
+      if (u.slot >= 0 && live) p.ml[static_cast<int64_t>(u.slot) * C::kRows + r] = make_float2(m, l);
+      store_rows<D, D, C::kQ / C::kSoftWarps>(p, u, C::kRows, r, live, token, row - token * G, G, tiles, l, lv_ref,
+                                              tmem + C::kO + t * D + lanes, 0, s_q + warp * (C::kQ / C::kSoftWarps));
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (s_fail) {  // a wait ran out: leave only once what is in flight has landed
+    if (tid == 0 && a.err) atomicOr(a.err, GDN_DEVERR_TIMEOUT);
+    const int stages = warp == kCopyK ? C::kStagesK : C::kStagesV;
+    for (int i = max(0, copies - stages); i < copies; ++i)
+      mbar_wait_bounded((warp == kCopyK ? b_kfull : b_vfull) + 8 * (i % stages), (i / stages) & 1);
+    if (warp == kMma && lane == 0) {
+      tc::mma_commit(b_drain);
+      mbar_wait_bounded(b_drain, 0);
+    }
+    __syncthreads();
+  }
+  if (warp == kMma) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);
   }
@@ -815,13 +1159,17 @@ cudaError_t launch_after(void (*kern)(KArgs...), dim3 grid, int threads, int sme
 
 template <int D>
 cudaError_t launch_prefill_d(const PrefillParams& p, const PrefillLayout& L, const CacheMaps& maps, cudaStream_t s) {
-  using C = PrefillCfg<D>;
-  cudaError_t e = cudaFuncSetAttribute(attn_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  using C = std::conditional_t<D == 256, PrefillCfg<256>, NarrowCfg<D == 256 ? 128 : D>>;
+  auto kern = [] {
+    if constexpr (D == 256) return attn_prefill_kernel<D>;
+    else return attn_prefill_narrow_kernel<D>;
+  }();
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   attn_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = launch_after(attn_prefill_kernel<D>, dim3(L.max_units), C::kThreads, C::kSmem, s, p, maps);
+  e = launch_after(kern, dim3(L.max_units), C::kThreads, C::kSmem, s, p, maps);
   if (e != cudaSuccess || L.max_slots == 0) return e;
   const int64_t joins = static_cast<int64_t>(p.nb) * kFewUnits;
   const int grid = static_cast<int>(joins < L.max_units ? joins : L.max_units);

@@ -43,8 +43,10 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kBatchPerLaunch = 2048;
 constexpr int kBuckets = 256;
-// key splits: up to this many units for a request that has fewer than kFewUnits
-constexpr int kFewUnits = 76, kSplitUnits = 228, kMaxSplits = 32, kMinSplitTiles = 8;
+// key splits: a request with fewer than few_units(d) row tiles x heads gets up to three times as many (head_dim 256:
+// half, as its partial sums are twice as large)
+constexpr int kMaxSplits = 32, kMinSplitTiles = 8;
+__host__ __device__ __forceinline__ constexpr int few_units(int d) { return d == 256 ? 76 : 152; }
 
 struct __align__(16) PrefillUnit {
   int b, h, row0, tile0, tile1, slot;  // slot: partial sums' place, or -1: the unit is the whole
@@ -65,11 +67,11 @@ struct PrefillParams {
 
 // How many pieces the key tiles of a request are cut into: the fewest rounds of an assumed 152
 // CTAs, counted in tiles with a constant cost per piece.
-__host__ __device__ __forceinline__ int kv_splits(int units, int tiles) {
-  if (units >= kFewUnits || tiles < 2 * kMinSplitTiles) return 1;
+__host__ __device__ __forceinline__ int kv_splits(int units, int tiles, int d) {
+  if (units >= few_units(d) || tiles < 2 * kMinSplitTiles) return 1;
   int best = 1, cost = 0x7fffffff;
-  for (int s = 1; s <= kMaxSplits && s * kMinSplitTiles <= tiles && s * units <= kSplitUnits; ++s) {
-    const int c = ((units * s + 151) / 152) * ((tiles + s - 1) / s + 4);
+  for (int s = 1; s <= kMaxSplits && s * kMinSplitTiles <= tiles && s * units <= 3 * few_units(d); ++s) {
+    const int c = ((units * s + 151) / 152) * ((tiles + s - 1) / s + 8);
     if (c < cost) {
       cost = c;
       best = s;
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
       request(p, b, first, n, len);
       if (n != a.cu_tokens[p.b0 + b + 1] - a.cu_tokens[p.b0 + b] || len != a.lens[p.b0 + b]) flags = GDN_DEVERR_SEQLENS;
       const int qt = static_cast<int>((static_cast<int64_t>(n) * G + p.rows - 1) / p.rows) * a.H;
-      const int s = kv_splits(qt, (len + kTile - 1) / kTile);
+      const int s = kv_splits(qt, (len + kTile - 1) / kTile, a.d);
       units = qt * s;
       slots = s > 1 ? units : 0;
     }
@@ -217,11 +219,12 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
 
 // Looks up the pages and scales of a unit's tiles, four at a time: lane = (tile of the batch, 16-key group).
 template <typename C>
-__device__ __forceinline__ void look_up(const PrefillParams& p, const PrefillUnit& u, int tiles, float2* s_scale, int32_t* s_row,
-                                        float* s_top, uint32_t b_info, uint32_t b_infoe, volatile int* fail) {
+__device__ __forceinline__ void look_up(const PrefillParams& p, const PrefillUnit& u, int tiles, unsigned char* scales, int32_t* s_row,
+                                        void* refs, uint32_t b_info, uint32_t b_infoe, volatile int* fail) {
   const AttnArgs& a = p.a;
   const int lane = threadIdx.x & 31, shift = 31 - __clz(a.bs);
   bool ok = true;
+  float ref = -INFINITY;
 #pragma unroll 1
   for (int j0 = 0; j0 < tiles && ok; j0 += C::kBatch) {
     const int j = j0 + lane / kGroups, pos = (u.tile0 + j) * kTile + (lane % kGroups) * kGroup;
@@ -244,9 +247,24 @@ __device__ __forceinline__ void look_up(const PrefillParams& p, const PrefillUni
     float top = sc.y;
 #pragma unroll
     for (int o = 1; o < kGroups; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    s_scale[slot * 32 + lane] = sc;
     s_row[slot * 32 + lane] = row;
-    if (lane % kGroups == 0) s_top[slot * C::kBatch + lane / kGroups] = top;
+    if constexpr (C::kRefs) {
+      // the power of two that the values' scales are taken by: it follows a tile's largest once that passes it by 2^3
+      float before = ref, after = ref;
+#pragma unroll
+      for (int i = 0; i < C::kBatch; ++i) {
+        const float t = __shfl_sync(0xFFFFFFFFu, top, i * kGroups);
+        const float next = t > ref + 3.0f ? t : ref;
+        if (lane / kGroups == i) before = ref, after = next;
+        ref = next;
+      }
+      const float none = sc.x < 0.0f ? -INFINITY : 0.0f, dl = fmaxf(sc.y - after, -60.0f);
+      reinterpret_cast<float4*>(scales)[slot * 32 + lane] = make_float4(sc.x, dl + none, ex2(-dl), none);
+      if (lane % kGroups == 0) static_cast<float2*>(refs)[slot * C::kBatch + lane / kGroups] = make_float2(before, after);
+    } else {
+      reinterpret_cast<float2*>(scales)[slot * 32 + lane] = sc;
+      if (lane % kGroups == 0) static_cast<float*>(refs)[slot * C::kBatch + lane / kGroups] = top;
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(b_info + 8 * slot);
   }
@@ -432,6 +450,7 @@ struct PrefillCfg {
   static constexpr int kSoftWarps = 4 * kTilesM * kSplitC;
   static constexpr int kThreads = 32 * (kSoftWarps + 4); // and warps for MMAs, lookups, copies of K, copies of V
   static constexpr int kStages = D == 256 ? 2 : 3;       // key tiles in the ring, and value tiles
+  static constexpr bool kRefs = false;
   static constexpr int kBatch = 4, kBatches = 4, kInfoRing = kBatch * kBatches;  // tiles looked up at a time; kept
   static constexpr int kQ = kTilesM * 2 * Tile<D>::kBytes;  // hi and lo of each row tile
   static constexpr int kKV = kStages * 2 * Tile<D>::kBytes;
@@ -509,7 +528,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
 
   int copies = 0;  // of a copying warp
   if (warp == C::kSoftWarps + 1) {
-    look_up<C>(p, u, tiles, s_scale, s_row, s_top, b_info, b_infoe, &s_fail);
+    look_up<C>(p, u, tiles, smem + C::kAtScale, s_row, s_top, b_info, b_infoe, &s_fail);
   } else if (warp >= C::kSoftWarps + 2) {
     const bool is_v = warp == C::kSoftWarps + 3;
     copies = is_v ? copy_tiles<D, C, C::kStages>(a, u, tiles, &maps.v_page, &maps.v_group, s_v, s_row, b_vfull, b_vempty, b_info, b_infoe, &s_fail)
@@ -623,14 +642,19 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
         tc::tmem_wait_ld();
         if (masked) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
+          for (int i = 0; i < 32; ++i) {
             if (c + i >= cut) s[i] = -INFINITY;
+            asm volatile("" : "+f"(s[i]));  // kept behind the branch: as selects these cost every tile
+          }
         }
 #pragma unroll
         for (int g = 0; g < 2; ++g)
           if (scales[half * NG + c / kGroup + g].x < 0.0f) {  // a page that is none
 #pragma unroll
-            for (int i = 0; i < kGroup; ++i) s[g * kGroup + i] = -INFINITY;
+            for (int i = 0; i < kGroup; ++i) {
+              s[g * kGroup + i] = -INFINITY;
+              asm volatile("" : "+f"(s[g * kGroup + i]));
+            }
           }
       };
       float mx = -INFINITY, lv_top = -INFINITY;
@@ -773,25 +797,27 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
 // own passes it by 2^8 (f16 has the range), which after the first tile almost never happens.
 template <int D>
 struct NarrowCfg {
-  static constexpr int kRows = 256;
+  static constexpr int kRows = 128;
   static constexpr int kSoftWarps = 8, kConvWarps = 4;
-  static constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 4);  // and warps for MMAs, lookups, copies of K and V
-  static constexpr int kStagesK = 3, kStagesV = 2;
+  static constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 5);  // and warps for Q K, P V, lookups, copies of K and V
+  static constexpr int kStagesK = 4, kStagesV = 3, kStagesW = 2, kScores = 3;  // W: V in f16
+  static constexpr bool kRefs = true;
   static constexpr int kBatch = 4, kBatches = 4, kInfoRing = kBatch * kBatches;
   using TL = Tile<D>;
   using TV = Tile<2 * D>;                                 // V in f16: rows of 2 D bytes
-  static constexpr int kQ = 2 * 2 * TL::kBytes;           // hi and lo of two row tiles
+  static constexpr int kQ = 2 * TL::kBytes;               // hi and lo
   static constexpr int kAtK = kQ;
   static constexpr int kAtV = kAtK + kStagesK * TL::kBytes;
   static constexpr int kAtV16 = kAtV + kStagesV * TL::kBytes;
-  static constexpr int kAtScale = kAtV16 + kStagesV * TV::kBytes;  // [kInfoRing][kGroups] (ks, log2 vs)
-  static constexpr int kAtRow = kAtScale + kInfoRing * kGroups * 8;
-  static constexpr int kAtTop = kAtRow + kInfoRing * kGroups * 4;  // [kInfoRing] the tile's largest log2 vs
-  static constexpr int kAtFactor = kAtTop + kInfoRing * 4;         // [kRows]
-  static constexpr int kAtBars = kAtFactor + kRows * 4;
-  static constexpr int kBars = 2 * kStagesK + 4 * kStagesV + 2 * kBatches + 8;
+  static constexpr int kAtScale = kAtV16 + kStagesW * TV::kBytes;  // [kInfoRing][kGroups]
+  static constexpr int kAtRow = kAtScale + kInfoRing * kGroups * 16;
+  static constexpr int kAtTop = kAtRow + kInfoRing * kGroups * 4;  // [kInfoRing]
+  static constexpr int kAtFactor = kAtTop + kInfoRing * 8;         // [kRows]
+  static constexpr int kAtMax = kAtFactor + kRows * 4;             // [3][kRows]: reference, two sums
+  static constexpr int kAtBars = kAtMax + 3 * kRows * 4;
+  static constexpr int kBars = 2 * kStagesK + 2 * kStagesV + kStagesW + 2 * kBatches + 3 * kScores + 3 + kSoftWarps;
   static constexpr int kSmem = 1024 + kAtBars + 8 * kBars;
-  static constexpr int kS = 0, kO = 256;                  // tensor memory: scores of two row tiles, then output
+  static constexpr int kO = 128 * kScores;                // tensor memory: scores of three tiles, then output
 };
 
 template <int D>
@@ -803,17 +829,18 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + (-smem_addr(smem_raw) & 1023u);
   const uint32_t s_q = smem_addr(smem), s_k = s_q + C::kAtK, s_v = s_q + C::kAtV, s_v16 = s_q + C::kAtV16;
-  float2* s_scale = reinterpret_cast<float2*>(smem + C::kAtScale);
+  const float4* s_scale = reinterpret_cast<float4*>(smem + C::kAtScale);
   int32_t* s_row = reinterpret_cast<int32_t*>(smem + C::kAtRow);
-  float* s_top = reinterpret_cast<float*>(smem + C::kAtTop);
+  float2* s_ref = reinterpret_cast<float2*>(smem + C::kAtTop);
   float* s_factor = reinterpret_cast<float*>(smem + C::kAtFactor);
+  float* s_max = reinterpret_cast<float*>(smem + C::kAtMax);
   const uint32_t b_kfull = s_q + C::kAtBars, b_kempty = b_kfull + 8 * C::kStagesK, b_vfull = b_kempty + 8 * C::kStagesK,
-                 b_wfull = b_vfull + 8 * C::kStagesV, b_vempty = b_wfull + 8 * C::kStagesV, b_wempty = b_vempty + 8 * C::kStagesV,
-                 b_info = b_wempty + 8 * C::kStagesV, b_infoe = b_info + 8 * C::kBatches, b_s = b_infoe + 8 * C::kBatches,
-                 b_p = b_s + 16, b_pv = b_p + 16, b_q = b_pv + 16, b_drain = b_q + 8;
+                 b_vempty = b_vfull + 8 * C::kStagesV, b_wfull = b_vempty + 8 * C::kStagesV, b_info = b_wfull + 8 * C::kStagesW,
+                 b_infoe = b_info + 8 * C::kBatches, b_s = b_infoe + 8 * C::kBatches, b_pv = b_s + 8 * C::kScores,
+                 b_p = b_pv + 8 * C::kScores, b_q = b_p + 8 * C::kScores, b_drain = b_q + 8, b_turn = b_drain + 16;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_fail;
-  constexpr int kMma = C::kSoftWarps + C::kConvWarps, kLook = kMma + 1, kCopyK = kMma + 2, kCopyV = kMma + 3;
+  constexpr int kMma = C::kSoftWarps + C::kConvWarps, kLook = kMma + 2, kCopyK = kMma + 3, kCopyV = kMma + 4;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const AttnArgs& a = p.a;
@@ -829,11 +856,11 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
   if (tid < C::kBars) {
     // who arrives: a copy, a commit or one lane, but for what threads and warps release themselves
     const uint32_t b = b_kfull + 8 * tid;
-    mbar_init(b, b >= b_wfull && b < b_wempty ? 32 * C::kConvWarps
-                 : b >= b_infoe && b < b_s    ? C::kSoftWarps + 1
-                 : b >= b_p && b < b_pv       ? 128
-                 : b == b_q                   ? 32 * C::kSoftWarps
-                                              : 1);
+    mbar_init(b, b >= b_vempty && b < b_info ? 32 * C::kConvWarps
+                 : b >= b_infoe && b < b_s ? C::kSoftWarps + 1
+                 : b >= b_p && b < b_q     ? C::kSoftWarps / 2
+                 : b == b_q                ? 32 * C::kSoftWarps
+                                           : 1);
   }
   if (tid == 0) s_fail = 0;
   fence_mbar_init();
@@ -849,60 +876,52 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
 
   int copies = 0;  // of a copying warp
   if (warp == kLook) {
-    look_up<C>(p, u, tiles, s_scale, s_row, s_top, b_info, b_infoe, &s_fail);
+    look_up<C>(p, u, tiles, smem + C::kAtScale, s_row, s_ref, b_info, b_infoe, &s_fail);
   } else if (warp == kCopyK) {
     copies = copy_tiles<D, C, C::kStagesK>(a, u, tiles, &maps.k_page, &maps.k_group, s_k, s_row, b_kfull, b_kempty, b_info, 0, &s_fail);
   } else if (warp == kCopyV) {
     copies = copy_tiles<D, C, C::kStagesV>(a, u, tiles, &maps.v_page, &maps.v_group, s_v, s_row, b_vfull, b_vempty, b_info, b_infoe, &s_fail);
-  } else if (warp == kMma) {
-    // ---- MMAs; descriptors but for their start address, which each MMA adds
+  } else if (warp >= kMma) {
+    // ---- MMAs: a thread for Q K and one for P V, so that the waits and commits of one pass under the products of
+    // the other. Scores of tile i go where those of i - 3 were, once their probabilities have been multiplied.
+    // Descriptors but for their start address, which each MMA adds.
     constexpr uint32_t iqk = idesc_f8(128, kTile, false, false);
     constexpr uint32_t ipv = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | (8u << 24);  // f16 x f16 (MN-major) -> fp32
     const uint64_t dk = TL::desc(s_k, 16), dq = TL::desc(s_q, 16), dv = TV::desc(s_v16, TV::kHalf);
-    auto qk = [&](int j, int t) {
-      if (lane == 0) {
-        const uint64_t kt = dk + (j % C::kStagesK) * (TL::kBytes >> 4), qt = dq + t * 2 * (TL::kBytes >> 4);
+    if (lane == 0 && warp == kMma) {
+      bool ok = tiles == 0 || wait(b_q, 0);
+      int st = 0, ph = 0, buf = 0, sph = 1;
+#pragma unroll 1
+      for (int i = 0; ok && i < tiles; ++i) {
+        if (!wait(b_kfull + 8 * st, ph) || !wait(b_pv + 8 * buf, sph)) break;
+        tc::fence_after_sync();
+        const uint64_t kt = dk + st * (TL::kBytes >> 4);
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int ks = 0; ks < D / 32; ++ks)
-            mma_f8_ss(tmem + C::kS + 128 * t, qt + part * (TL::kBytes >> 4) + ks * 2, kt + ks * 2, iqk, part | ks);
-        tc::mma_commit(b_s + 8 * t);
-        if (t == 1) tc::mma_commit(b_kempty + 8 * (j % C::kStagesK));
+            mma_f8_ss(tmem + 128 * buf, dq + part * (TL::kBytes >> 4) + ks * 2, kt + ks * 2, iqk, part | ks);
+        tc::mma_commit(b_s + 8 * buf);
+        tc::mma_commit(b_kempty + 8 * st);
+        if (++st == C::kStagesK) st = 0, ph ^= 1;
+        if (++buf == C::kScores) buf = 0, sph ^= 1;
       }
-      __syncwarp();
-    };
-    auto pv = [&](int j, int t) {
-      if (lane == 0) {
-        const uint32_t pa = tmem + C::kS + 128 * t;
-        const uint64_t vt = dv + (j % C::kStagesV) * (TV::kBytes >> 4);
+    } else if (lane == 0) {
+      int buf = 0, sph = 0;
+#pragma unroll 1
+      for (int j = 0; j < tiles; ++j) {
+        if (!wait(b_wfull + 8 * (j & 1), (j >> 1) & 1) || !wait(b_p + 8 * buf, sph)) break;
+        tc::fence_after_sync();
+        const uint32_t pa = tmem + 128 * buf;
+        const uint64_t vt = dv + (j & 1) * (TV::kBytes >> 4);
 #pragma unroll
         for (int ks = 0; ks < kTile / 16; ++ks)
-          tc::mma_bf16_ts(tmem + C::kO + t * D, pa + (ks >> 1) * 32 + (ks & 1) * 8, vt + ks * (16 * TV::kRow >> 4), ipv, (j > 0) | ks);
-        tc::mma_commit(b_pv + 8 * t);
-        if (t == 1) tc::mma_commit(b_wempty + 8 * (j % C::kStagesV));
-      }
-      __syncwarp();
-    };
-    bool ok = tiles == 0 || wait(b_q, 0);
-    tc::fence_after_sync();
-#pragma unroll 1
-    for (int i = 0; ok && i <= tiles; ++i) {
-      const int j = i - 1;
-#pragma unroll 1
-      for (int t = 0; t < 2; ++t) {
-        if (j >= 0) {
-          if (t == 0 && !(ok = wait(b_wfull + 8 * (j % C::kStagesV), (j / C::kStagesV) & 1))) break;
-          if (!(ok = wait(b_p + 8 * t, j & 1))) break;
-          tc::fence_after_sync();
-          pv(j, t);
-        }
-        if (i < tiles) {
-          if (t == 0 && !(ok = wait(b_kfull + 8 * (i % C::kStagesK), (i / C::kStagesK) & 1))) break;
-          qk(i, t);
-        }
+          tc::mma_bf16_ts(tmem + C::kO, pa + (ks >> 1) * 32 + (ks & 1) * 8, vt + ks * (16 * TV::kRow >> 4), ipv, (j > 0) | ks);
+        tc::mma_commit(b_pv + 8 * buf);
+        if (++buf == C::kScores) buf = 0, sph ^= 1;
       }
     }
+    __syncwarp();
   } else if (warp >= C::kSoftWarps) {
     // ---- V to f16: 16-byte chunks of a tile to the threads in turn; keys past the request's length, which hold
     // whatever their page holds, become zero (0 * NaN is not 0)
@@ -911,14 +930,14 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
     bool ok = true;
 #pragma unroll 1
     for (int j = 0; j < tiles && ok; ++j) {
-      const int st = j % C::kStagesV, ph = (j / C::kStagesV) & 1;
-      ok = wait(b_vfull + 8 * st, ph) && wait(b_wempty + 8 * st, ph ^ 1);
+      const int st = j % C::kStagesV;
+      ok = wait(b_vfull + 8 * st, (j / C::kStagesV) & 1) && (j < 2 || wait(b_pv + 8 * ((j - 2) % C::kScores), ((j - 2) / C::kScores) & 1));
       if (!ok) break;
       const int keys = len - (u.tile0 + j) * kTile;
-      const uint32_t from = s_v + st * TL::kBytes, to = s_v16 + st * TV::kBytes;
+      const uint32_t from = s_v + st * TL::kBytes, to = s_v16 + (j & 1) * TV::kBytes;
 #pragma unroll 4
       for (int i = me; i < kTile * kChunks; i += 32 * C::kConvWarps) {
-        const int key = i / kChunks, c = i % kChunks;
+        const int key = i / (8 * kChunks) * 8 + i % 8, c = i / 8 % kChunks;  // (8 keys at a time: no bank twice)
         uint32_t x[4], y[8];
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(from + TL::chunk_at(key, c)));
 #pragma unroll
@@ -930,7 +949,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + TV::chunk_at(key, 2 * c + 1)), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7]) : "memory");
       }
       tc::fence_async_smem();
-      mbar_arrive(b_wfull + 8 * st);
+      mbar_arrive(b_wfull + 8 * (j & 1));
       mbar_arrive(b_vempty + 8 * st);
     }
   } else {
@@ -938,12 +957,13 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
     tc::fence_async_smem();
     mbar_arrive(b_q);
 
-    // ---- softmax: thread = row
-    const int t = warp / 4, r = tid;              // row tile; row of the unit
-    const int row = u.row0 + r;                   // (token, head) row of the request
+    // ---- softmax: thread = row; the two warpgroups take the tiles in turn. The reference that both subtract, m, is
+    // what the tile before left: warps w and w + 4, which have the same rows, hand it on.
+    const int own = warp / 4, pair = warp & 3, r = pair * 32 + lane;  // r: row of the unit
+    const int row = u.row0 + r;                                      // (token, head) row of the request
     const bool live = row < rows_all;
     const int token = live ? row / G : 0;
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t lanes = static_cast<uint32_t>(pair * 32) << 16;
     bool ok = wait(b_q, 0);
     const float given = s_factor[r];
     const bool finite = given == given;
@@ -951,103 +971,132 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
     const int sees = live ? min(len, len - n + token + 1) : 0;  // keys this row sees
     const int all_see = __reduce_min_sync(0xFFFFFFFFu, sees);   // keys before this one are seen by every row of the warp
     // a query that is not finite saturates in 8 bits: its row is NaN through its sum
-    float m = -INFINITY, l = finite || sees <= 0 ? 0.0f : __int_as_float(0x7FC00000), lv_ref = -INFINITY;
-    const uint32_t sc = tmem + C::kS + 128 * t + lanes;
+    float m = -INFINITY, l = finite || sees <= 0 ? 0.0f : __int_as_float(0x7FC00000);
+    const uint32_t turn = b_turn + 8 * (4 * own + pair), turn_of = b_turn + 8 * (4 * (own ^ 1) + pair);
+    // whether any thread of the two warps says so
+    auto vote = [&](bool x) {
+      uint32_t any;
+      asm volatile("{.reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, %2, 64, p; selp.u32 %0, 1, 0, q;}"
+                   : "=r"(any) : "r"(static_cast<uint32_t>(x)), "r"(1 + pair) : "memory");
+      return any != 0;
+    };
+    int buf = own, sph = 0;
 #pragma unroll 1
-    for (int j = 0; j < tiles; ++j) {
+    for (int j = own; j < tiles; j += 2) {
       const int slot = (j / C::kBatch) % C::kBatches;
-      if (j % C::kBatch == 0) ok = ok && wait(b_info + 8 * slot, (j / C::kInfoRing) & 1);
-      ok = __all_sync(0xFFFFFFFFu, ok && wait(b_s + 8 * t, j & 1));
+      if (j % C::kBatch < 2) ok = ok && wait(b_info + 8 * slot, (j / C::kInfoRing) & 1);
+      ok = ok && wait(b_s + 8 * buf, sph);
+      ok = __all_sync(0xFFFFFFFFu, ok);
       if (!ok) break;
       tc::fence_after_sync();
-      const float2* scales = s_scale + (j % C::kInfoRing) * kGroups;
-      const int cut = sees - (u.tile0 + j) * kTile;      // columns from here on are hidden
+      const uint32_t sc = tmem + 128 * buf + lanes;
+      const float4* scales = s_scale + (j % C::kInfoRing) * kGroups;
+      const int cut = sees - (u.tile0 + j) * kTile;  // columns from here on are hidden
       const bool masked = all_see < (u.tile0 + j + 1) * kTile;
-      const float lv_top = s_top[j % C::kInfoRing];
-      uint32_t w[kTile / 2];
-      float sum;
-#pragma unroll 1
-      for (int round = 0;; ++round) {
-        const float base = m == -INFINITY ? 0.0f : -m;
-        float mx = -INFINITY;
-        sum = 0.0f;
+      const float2 refs = s_ref[j % C::kInfoRing];   // the values' power of two before this tile and with it
+      // the largest exponent of the tile; a page that is none has rows of zeros: its exponents become -infinity by what
+      // is added
+      auto hide = [&](float (&s)[32], int c) {
+        if (masked) {
 #pragma unroll
-        for (int c = 0; c < kTile; c += 32) {
-          float s[32];
-          tmem_ld32(sc + c, s);
-          tc::tmem_wait_ld();
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c + i >= cut) s[i] = -INFINITY;
-          }
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const float2 e2 = scales[c / kGroup + g];
-            if (e2.x < 0.0f) {  // a page that is none
-#pragma unroll
-              for (int i = 0; i < kGroup; ++i) s[g * kGroup + i] = -INFINITY;
-            }
-            // p * vs / vs_ref comes out of the exponential; the row sum takes it back by group
-            const float ks = exponent_scale(e2.x, factor), dl = fmaxf(e2.y - lv_ref, -60.0f);
-            float t0 = s[g * kGroup];
-#pragma unroll
-            for (int i = 1; i + 1 < kGroup; i += 2) t0 = max3(t0, s[g * kGroup + i], s[g * kGroup + i + 1]);
-            mx = fmaxf(mx, fmaxf(t0, s[g * kGroup + kGroup - 1]) * ks);
-            const float2 k2 = make_float2(ks, ks), b2 = make_float2(base + dl, base + dl);
-            float2 part = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int i = 0; i < kGroup; i += 2) {
-              float2 v = fma2(make_float2(s[g * kGroup + i], s[g * kGroup + i + 1]), k2, b2);
-              v.x = ex2(v.x);
-              v.y = ex2(v.y);
-              part = add2(part, v);
-              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[(c + g * kGroup + i) / 2]) : "f"(v.y), "f"(v.x));
-            }
-            sum = fmaf(part.x + part.y, ex2(-dl), sum);
+          for (int i = 0; i < 32; ++i) {
+            if (c + i >= cut) s[i] = -INFINITY;
+            asm volatile("" : "+f"(s[i]));  // kept behind the branch: as selects these cost every tile
           }
         }
-        if (round) break;
-        const bool grow_v = lv_top > lv_ref + 3.0f;
-        if (!__any_sync(0xFFFFFFFFu, mx > m + 8.0f) && !grow_v) break;
-        const float to = mx > m + 8.0f ? mx : m;  // by the row alone, whatever its neighbours do
-        float corr = to == -INFINITY ? 1.0f : ex2(m - to);
-        m = to;
-        l *= corr;
-        if (grow_v) {
-          corr *= ex2(lv_ref - lv_top);
-          lv_ref = lv_top;
-        }
-        if (j > 0) {
-          ok = __all_sync(0xFFFFFFFFu, wait(b_pv + 8 * t, (j - 1) & 1));
-          if (!ok) break;
-          tc::fence_after_sync();
+      };
+      float mx = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            float o[16];
-            tc::tmem_ld16(tmem + C::kO + t * D + lanes + c, o);
-            tc::tmem_wait_ld();
+      for (int c = 0; c < kTile; c += 32) {
+        float s[32];
+        tmem_ld32(sc + c, s);
+        tc::tmem_wait_ld();
+        hide(s, c);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] *= corr;
-            tc::tmem_st16(tmem + C::kO + t * D + lanes + c, o);
-          }
+        for (int g = 0; g < 2; ++g) {
+          const float4 e = scales[c / kGroup + g];
+          float t0 = s[g * kGroup];
+#pragma unroll
+          for (int i = 1; i + 1 < kGroup; i += 2) t0 = max3(t0, s[g * kGroup + i], s[g * kGroup + i + 1]);
+          mx = fmaxf(mx, fmaf(fmaxf(t0, s[g * kGroup + kGroup - 1]), exponent_scale(e.x, factor), e.w));
         }
       }
+      if (j > 0) ok = __all_sync(0xFFFFFFFFu, wait(turn_of, ((j - 1) >> 1) & 1));
       if (!ok) break;
-      l += sum;
+      // the reference follows the row's maximum once that passes it by 2^8 (f16 has the range): by the row alone,
+      // whatever its neighbours do
+      const float was = j > 0 ? s_max[r] : -INFINITY, to = mx > was + 8.0f ? mx : was;
+      const bool grown = refs.x != refs.y;
+      const bool scaled = j > 0 && (__any_sync(0xFFFFFFFFu, to != was) || grown);
+      s_max[r] = to;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(turn);
+      if (to != m) l *= ex2(m - to);
+      m = to;
+      if (scaled) {
+        ok = __all_sync(0xFFFFFFFFu, wait(b_pv + 8 * ((j - 1) % C::kScores), ((j - 1) / C::kScores) & 1));
+        if (!ok) break;
+        tc::fence_after_sync();
+        const float corr = (to != was ? ex2(was - to) : 1.0f) * (grown ? ex2(refs.x - refs.y) : 1.0f);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          float o[16];
+          tc::tmem_ld16(tmem + C::kO + lanes + c, o);
+          tc::tmem_wait_ld();
 #pragma unroll
-      for (int c = 0; c < kTile; c += 32) tmem_st16u(sc + c, w + c / 2);
+          for (int i = 0; i < 16; ++i) o[i] *= corr;
+          tc::tmem_st16(tmem + C::kO + lanes + c, o);
+        }
+      }
+      // the probabilities: p * vs / vs_ref comes out of the exponential; the row sum takes it back by group
+      const float base = m == -INFINITY ? 0.0f : -m;
+#pragma unroll 1
+      for (int c = 0; c < kTile; c += 32) {
+        float cur[32];
+        tmem_ld32(sc + c, cur);
+        tc::tmem_wait_ld();
+        hide(cur, c);
+        uint32_t w[16];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const float4 e = scales[c / kGroup + g];
+          const float ks = exponent_scale(e.x, factor), add = base + e.y;
+          const float2 k2 = make_float2(ks, ks), b2 = make_float2(add, add);
+          float2 part = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int i = 0; i < kGroup; i += 2) {
+            float2 v = fma2(make_float2(cur[g * kGroup + i], cur[g * kGroup + i + 1]), k2, b2);
+            v.x = ex2(v.x);
+            v.y = ex2(v.y);
+            part = add2(part, v);
+            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[(g * kGroup + i) / 2]) : "f"(v.y), "f"(v.x));
+          }
+          l = fmaf(part.x + part.y, e.z, l);
+        }
+        tmem_st16u(sc + c, w);
+      }
       tc::tmem_wait_st();
       tc::fence_before_sync();
-      mbar_arrive(b_p + 8 * t);
-      if (j % C::kBatch == C::kBatch - 1 && lane == 0) mbar_arrive(b_infoe + 8 * slot);  // (the warp has met at the store)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_p + 8 * buf);
+      if (j % C::kBatch >= 2 && lane == 0) mbar_arrive(b_infoe + 8 * slot);
+      buf += 2;
+      if (buf >= C::kScores) buf -= C::kScores, sph ^= 1;
     }
-    if (ok && tiles > 0) ok = wait(b_pv + 8 * t, (tiles - 1) & 1);
-    if (__all_sync(0xFFFFFFFFu, ok)) {
-      tc::fence_after_sync();
-      if (u.slot >= 0 && live) p.ml[static_cast<int64_t>(u.slot) * C::kRows + r] = make_float2(m, l);
-      store_rows<D, D, C::kQ / C::kSoftWarps>(p, u, C::kRows, r, live, token, row - token * G, G, tiles, l, lv_ref,
-                                              tmem + C::kO + t * D + lanes, 0, s_q + warp * (C::kQ / C::kSoftWarps));
+    // the last two products in order: a barrier's parity tells a product only from the one before on it
+#pragma unroll 1
+    for (int j = max(0, tiles - 2); j < tiles; ++j) ok = ok && wait(b_pv + 8 * (j % C::kScores), (j / C::kScores) & 1);
+    if (!vote(!ok)) {
+      const float last = tiles > 0 ? s_max[r] : -INFINITY;
+      const float2 refs = tiles > 0 ? s_ref[(tiles - 1) % C::kInfoRing] : make_float2(0.0f, -INFINITY);
+      s_max[(1 + own) * C::kRows + r] = m == last ? l : l * ex2(m - last);
+      if (!vote(!ok)) {
+        tc::fence_after_sync();
+        l = s_max[C::kRows + r] + s_max[2 * C::kRows + r];
+        if (u.slot >= 0 && live && own == 0) p.ml[static_cast<int64_t>(u.slot) * C::kRows + r] = make_float2(last, l);
+        store_rows<D, D / 2, C::kQ / C::kSoftWarps>(p, u, C::kRows, r, live, token, row - token * G, G, tiles, l, refs.y,
+                                                    tmem + C::kO + lanes, own * (D / 2), s_q + warp * (C::kQ / C::kSoftWarps));
+      }
     }
   }
   tc::fence_before_sync();
@@ -1057,9 +1106,9 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
     const int stages = warp == kCopyK ? C::kStagesK : C::kStagesV;
     for (int i = max(0, copies - stages); i < copies; ++i)
       mbar_wait_bounded((warp == kCopyK ? b_kfull : b_vfull) + 8 * (i % stages), (i / stages) & 1);
-    if (warp == kMma && lane == 0) {
-      tc::mma_commit(b_drain);
-      mbar_wait_bounded(b_drain, 0);
+    if (warp >= kMma && warp < kLook && lane == 0) {
+      tc::mma_commit(b_drain + 8 * (warp - kMma));
+      mbar_wait_bounded(b_drain + 8 * (warp - kMma), 0);
     }
     __syncthreads();
   }
@@ -1110,24 +1159,24 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(const __grid_con
   }
 }
 
-int unit_rows(int d) { return d == 256 ? 128 : 256; }
+constexpr int kUnitRows = 128;
 
 struct PrefillLayout {
   size_t units, joins, ml, part, total;
   int max_units, max_slots;
 };
-// max_slots: a request has fewer than kFewUnits row tiles x heads to be split, and at most
-// kSplitUnits units then.
+// max_slots: a request has fewer than few_units(d) row tiles x heads to be split, and at most three times
+// that then.
 PrefillLayout prefill_layout(int T, int B, int max_blocks, int Hq, int H, int d, int bs) {
-  const int rows = unit_rows(d), G = Hq / H;
+  const int rows = kUnitRows, G = Hq / H;
   const int64_t tiles = (static_cast<int64_t>(max_blocks) * bs + kTile - 1) / kTile;
   const int64_t row_tiles = H * ((static_cast<int64_t>(T) * G + rows - 1) / rows + B);
   int64_t splits = tiles / kMinSplitTiles;
   if (splits > kMaxSplits) splits = kMaxSplits;
   int64_t slots = 0;
-  if (splits > 1 && H < kFewUnits) {
+  if (splits > 1 && H < few_units(d)) {
     slots = row_tiles * splits;
-    const int64_t most = static_cast<int64_t>(B) * kSplitUnits;
+    const int64_t most = static_cast<int64_t>(B) * 3 * few_units(d);
     if (slots > most) slots = most;
   }
   PrefillLayout L;
@@ -1171,7 +1220,7 @@ cudaError_t launch_prefill_d(const PrefillParams& p, const PrefillLayout& L, con
   if (e != cudaSuccess) return e;
   e = launch_after(kern, dim3(L.max_units), C::kThreads, C::kSmem, s, p, maps);
   if (e != cudaSuccess || L.max_slots == 0) return e;
-  const int64_t joins = static_cast<int64_t>(p.nb) * kFewUnits;
+  const int64_t joins = static_cast<int64_t>(p.nb) * few_units(D);
   const int grid = static_cast<int>(joins < L.max_units ? joins : L.max_units);
   return launch_after(attn_prefill_join_kernel<D>, dim3(grid, C::kRows / 16), 256, 0, s, p);
 }
@@ -1191,7 +1240,7 @@ cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t s) {
     p.a = a;
     p.b0 = b0;
     p.nb = a.B - b0 < kBatchPerLaunch ? a.B - b0 : kBatchPerLaunch;
-    p.rows = unit_rows(a.d);
+    p.rows = kUnitRows;
     const PrefillLayout L = prefill_layout(a.T, p.nb, a.max_blocks, a.Hq, a.H, a.d, a.bs);
     p.max_units = L.max_units;
     p.max_slots = L.max_slots;

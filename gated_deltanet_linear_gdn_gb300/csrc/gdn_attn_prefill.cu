@@ -45,6 +45,7 @@ constexpr int kBatchPerLaunch = 2048;
 constexpr int kBuckets = 256;
 // key splits: a request with fewer than few_units(d) row tiles x heads gets up to three times as many (head_dim 256:
 // half, as its partial sums are twice as large)
+constexpr int kUnitRows = 128;  // (token, head) rows of a unit
 constexpr int kMaxSplits = 32, kMinSplitTiles = 8;
 __host__ __device__ __forceinline__ constexpr int few_units(int d) { return d == 256 ? 76 : 152; }
 
@@ -56,7 +57,6 @@ struct __align__(16) PrefillUnit {
 struct PrefillParams {
   AttnArgs a;
   int b0, nb;
-  int rows;                 // rows of a unit
   int max_units, max_slots;
   int32_t* counts;          // [0] units, [1] split tiles
   PrefillUnit* units;       // [max_units]
@@ -70,6 +70,7 @@ struct PrefillParams {
 __host__ __device__ __forceinline__ int kv_splits(int units, int tiles, int d) {
   if (units >= few_units(d) || tiles < 2 * kMinSplitTiles) return 1;
   int best = 1, cost = 0x7fffffff;
+#pragma unroll 1
   for (int s = 1; s <= kMaxSplits && s * kMinSplitTiles <= tiles && s * units <= 3 * few_units(d); ++s) {
     const int c = ((units * s + 151) / 152) * ((tiles + s - 1) / s + 8);
     if (c < cost) {
@@ -87,6 +88,8 @@ __device__ __forceinline__ void request(const PrefillParams& p, int b, int& firs
   len = min(max(p.a.lens[p.b0 + b], 0), cap);
   if (first < 0 || n < 0 || first + static_cast<int64_t>(n) > p.a.T) n = 0;
 }
+// Row tiles of a request; its rows are fewer than 2^31.
+__device__ __forceinline__ int row_tiles(int n, int G) { return static_cast<int>((static_cast<uint32_t>(n) * G + kUnitRows - 1) / kUnitRows); }
 // Key tiles that rows row0 .. row0 + rows - 1 of a request see.
 __device__ __forceinline__ int tiles_of(int row0, int rows, int n, int len, int G) {
   const int last = min((row0 + rows - 1) / G, n - 1);  // the unit's last token
@@ -105,6 +108,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
   int flags = 0, carry = 0, carry_slot = 0;
   if (tid < kBuckets) s_count[tid] = 0;
   if (tid == 0) s_joins = 0;
+#pragma unroll 1
   for (int base = 0; base < p.nb; base += kPlanThreads) {
     const int b = base + tid;
     int units = 0, slots = 0;
@@ -112,7 +116,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
       int first, n, len;
       request(p, b, first, n, len);
       if (n != a.cu_tokens[p.b0 + b + 1] - a.cu_tokens[p.b0 + b] || len != a.lens[p.b0 + b]) flags = GDN_DEVERR_SEQLENS;
-      const int qt = static_cast<int>((static_cast<int64_t>(n) * G + p.rows - 1) / p.rows) * a.H;
+      const int qt = row_tiles(n, G) * a.H;
       const int s = kv_splits(qt, (len + kTile - 1) / kTile, a.d);
       units = qt * s;
       slots = s > 1 ? units : 0;
@@ -132,6 +136,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     }
     __syncthreads();
     int bv = carry, bw = carry_slot;
+#pragma unroll 4
     for (int i = 0; i < kPlanThreads / 32; ++i) {
       if (i < warp) {
         bv += s_warp[0][i];
@@ -156,6 +161,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
   // unit u of the list before it is ordered
   auto describe = [&](int u) {
     int lo = 0, hi = p.nb - 1;
+#pragma unroll 1
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (s_first[mid] <= u) lo = mid; else hi = mid - 1;
@@ -164,13 +170,13 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     request(p, lo, first, n, len);
     PrefillUnit d;
     d.b = lo;
-    const int qt = static_cast<int>((static_cast<int64_t>(n) * G + p.rows - 1) / p.rows);
+    const int qt = row_tiles(n, G);
     const int s = (s_first[lo + 1] - s_first[lo]) / (qt * a.H);
     const int rem = u - s_first[lo];
     const int piece = rem % s, tile = rem / s;
     d.h = tile % a.H;
-    d.row0 = (tile / a.H) * p.rows;
-    const int tiles = tiles_of(d.row0, p.rows, n, len, G);
+    d.row0 = (tile / a.H) * kUnitRows;
+    const int tiles = tiles_of(d.row0, kUnitRows, n, len, G);
     const int each = (tiles + s - 1) / s;
     d.tile0 = min(piece * each, tiles);
     d.tile1 = min(d.tile0 + each, tiles);
@@ -182,33 +188,37 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
     d.pad0 = d.pad1 = 0;
     return d;
   };
-  for (int u = tid; u < carry; u += kPlanThreads) {
-    const PrefillUnit d = describe(u);
-    atomicAdd(&s_count[kBuckets - 1 - min(d.tile1 - d.tile0, kBuckets - 1)], 1);
-  }
-  __syncthreads();
-  if (warp == 0) {  // bucket counts to first places
-    int before = 0;
-    for (int i = lane; i < kBuckets; i += 32) {
-      const int own = s_count[i];
-      int v = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xFFFFFFFFu, v, o);
-        if (lane >= o) v += x;
+  // counts, then places (a loop, so that the code is fetched once)
+#pragma unroll 1
+  for (int place = 0; place < 2; ++place) {
+#pragma unroll 1
+    for (int u = tid; u < carry; u += kPlanThreads) {
+      const PrefillUnit d = describe(u);
+      // (the order within a bucket is free: it decides when a unit runs, not what it computes)
+      const int at = atomicAdd(&s_count[kBuckets - 1 - min(d.tile1 - d.tile0, kBuckets - 1)], 1);
+      if (place) {
+        p.units[at] = d;
+        if (d.splits > 1 && (d.slot - s_slot[d.b]) % d.splits == 0) p.joins[atomicAdd(&s_joins, 1)] = d;
       }
-      s_count[i] = before + v - own;
-      before += __shfl_sync(0xFFFFFFFFu, v, 31);
     }
+    __syncthreads();
+    if (warp == 0 && !place) {  // bucket counts to first places
+      int before = 0;
+#pragma unroll 1
+      for (int i = lane; i < kBuckets; i += 32) {
+        const int own = s_count[i];
+        int v = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xFFFFFFFFu, v, o);
+          if (lane >= o) v += x;
+        }
+        s_count[i] = before + v - own;
+        before += __shfl_sync(0xFFFFFFFFu, v, 31);
+      }
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  for (int u = tid; u < carry; u += kPlanThreads) {
-    const PrefillUnit d = describe(u);
-    // (the order within a bucket is free: it decides when a unit runs, not what it computes)
-    p.units[atomicAdd(&s_count[kBuckets - 1 - min(d.tile1 - d.tile0, kBuckets - 1)], 1)] = d;
-    if (d.splits > 1 && (d.slot - s_slot[d.b]) % d.splits == 0) p.joins[atomicAdd(&s_joins, 1)] = d;
-  }
-  __syncthreads();
   if (tid == 0) {
     p.counts[0] = carry;
     p.counts[1] = s_joins;
@@ -1134,12 +1144,12 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(const __grid_con
     const int r = blockIdx.y * 16 + i, row = u.row0 + r;
     if (row >= static_cast<int64_t>(n) * G) break;
     float top = -INFINITY;
-    for (int s = 0; s < u.splits; ++s) top = fmaxf(top, p.ml[static_cast<int64_t>(u.slot + s) * p.rows + r].x);
+    for (int s = 0; s < u.splits; ++s) top = fmaxf(top, p.ml[static_cast<int64_t>(u.slot + s) * kUnitRows + r].x);
     float sum = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
     for (int s = 0; s < u.splits; ++s) {
-      const int64_t at = static_cast<int64_t>(u.slot + s) * p.rows + r;
+      const int64_t at = static_cast<int64_t>(u.slot + s) * kUnitRows + r;
       const float2 e = p.ml[at];
       const float c = e.x == -INFINITY ? (e.y == 0.0f ? 0.0f : 1.0f) : ex2(e.x - top);
       const float4 v = *reinterpret_cast<const float4*>(p.part + at * D + d4 * 4);
@@ -1158,8 +1168,6 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(const __grid_con
     *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(first + row / G) * a.Hq + u.h * G + row % G) * D + d4 * 4) = st;
   }
 }
-
-constexpr int kUnitRows = 128;
 
 struct PrefillLayout {
   size_t units, joins, ml, part, total;
@@ -1240,7 +1248,6 @@ cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t s) {
     p.a = a;
     p.b0 = b0;
     p.nb = a.B - b0 < kBatchPerLaunch ? a.B - b0 : kBatchPerLaunch;
-    p.rows = kUnitRows;
     const PrefillLayout L = prefill_layout(a.T, p.nb, a.max_blocks, a.Hq, a.H, a.d, a.bs);
     p.max_units = L.max_units;
     p.max_slots = L.max_slots;

@@ -157,11 +157,6 @@ struct Tile {
     d |= static_cast<uint64_t>(D < 128 ? 4 : 2) << 61;  // 64-byte / 128-byte swizzle
     return d;
   }
-  static __device__ __forceinline__ uint64_t k_step(uint32_t tile, int ks) {
-    constexpr int per = kRow / 32;
-    return desc(tile + (ks / per) * kHalf + (ks % per) * 32, 16);
-  }
-  static __device__ __forceinline__ uint64_t mn_step(uint32_t tile, int ks) { return desc(tile + ks * 32 * kRow, kHalf); }
   static __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
     if (D < 128) return row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
     return (chunk >> 3) * kHalf + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);

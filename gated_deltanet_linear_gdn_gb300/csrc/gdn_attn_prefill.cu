@@ -6,26 +6,21 @@
 // rows of the product are the pairs (token, query head of the group), token-major, so a 128-row
 // tile uses each key tile for all G heads.
 //
-// Both products run on 8-bit operands, straight from the pages: no conversion of K or V, no
-// pass through registers. The other operand is split into two e4m3 parts,
+// S = Q K^T runs on 8-bit operands straight from the pages. A query is split into two e4m3 parts,
 //   q = q_hi + q_lo (a row scaled by a power of two so that max |q| lies in [128, 256)),
-//   p = p_hi + p_lo (p_hi: p to 4 significant bits, p_lo = e4m3(p - p_hi)),
-// and multiplied in two MMAs into the same fp32 accumulator. Four and four significant bits: q is
-// a bf16 value (8 bits), so its split is exact down to 2^-18 of the row's largest element, and p
-// keeps 8 bits, as a bf16 p would. Two 8-bit MMAs cost what one 16-bit MMA costs, so the
-// bound is the dense bf16 rate, with half the shared-memory traffic for K and V.
+// multiplied in two MMAs into the same fp32 accumulator: q is a bf16 value (8 significant bits), so the split is
+// exact down to 2^-18 of the row's largest element. Two 8-bit MMAs cost what one 16-bit MMA costs, so the
+// bound is the dense bf16 rate. P V differs by head_dim, see the two kernels below; p overwrites the scores it
+// came from in tensor memory and is the A operand of the second product there.
 //
 // Scales. A block of keys has one ks: it enters the exponent, exp2(s * ks * factor - m). Its vs
-// enters there, too, as log2(vs / vs_ref), vs_ref the largest vs seen (within 1.75); the row sum takes it
-// back by group of 16. The running maximum m moves when a score passes it by 2^4, so that 16 p <= 256
-// fits e4m3; the accumulator is rescaled only then.
+// enters there, too, as log2(vs / vs_ref), vs_ref the largest vs seen (within a factor); the row sum takes it
+// back by group of 16. The running maximum m moves only when a score passes it by a power of two that the type of
+// p has room for; the accumulator is rescaled only then.
 //
-// One CTA per unit: 256 rows (two 128-row tiles) for d <= 128, 128 rows for d = 256, where two
-// score buffers take turns instead of two row tiles (tensor memory: 2 x 128 columns of scores,
-// 256 columns of output). Warps: two warpgroups of softmax for each row tile (two threads share a row, 64
-// columns each, and exchange their maxima), one warp issuing MMAs, one looking up pages and scales four
-// tiles at a time, one copying keys and one values, so that neither waits for the other's ring. p overwrites the scores it came from in tensor memory and is
-// the A operand of the second product there.
+// One CTA per unit of 128 rows: its queries stay in shared memory, its output in tensor memory. Loops over
+// the columns of a tile are kept rolled: a CTA fetches every role's code, and unrolled loops waited for instructions
+// (rolling the softmax's from 128 to 32 columns: 470 -> 368 us for 300 tokens at 60,000, head_dim 128).
 //
 // A plan kernel turns the lengths into a list of units, the longest first. A request with few
 // rows over a long cache is also cut along the keys, by a rule on its own sizes alone
@@ -325,57 +320,57 @@ __device__ __forceinline__ void split_queries(const AttnArgs& a, const PrefillUn
   constexpr int kLoads = kPer / kAtOnce < 4 ? kPer / kAtOnce : 4;  // in flight
 #pragma unroll 1
   for (int i0 = 0; i0 < kPer / kAtOnce; i0 += kLoads) {
-  uint4 raw[kLoads];
+    uint4 raw[kLoads];
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int rr = warp * kPer + (i0 + i) * kAtOnce + lane / kLanes;  // row of the unit
-    const int row = u.row0 + rr, token = row / G;
-    raw[i] = make_uint4(0, 0, 0, 0);
-    if (row < rows_all)
-      raw[i] = *reinterpret_cast<const uint4*>(a.q + (first + token) * a.q_stride +
-                                               (u.h * G + row - token * G) * D + (lane % kLanes) * 8);
-  }
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
-    const int rr = warp * kPer + (i0 + i) * kAtOnce + lane / kLanes;
-    const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-    uint32_t top = 0;
-#pragma unroll
-    for (int y = 0; y < 4; ++y) top = max(top, max(x[y] & 0x7FFFu, (x[y] >> 16) & 0x7FFFu));
-    if constexpr (kLanes == 32) {
-      top = __reduce_max_sync(0xFFFFFFFFu, top);
-    } else {
-#pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    for (int i = 0; i < kLoads; ++i) {
+      const int rr = warp * kPer + (i0 + i) * kAtOnce + lane / kLanes;  // row of the unit
+      const int row = u.row0 + rr, token = row / G;
+      raw[i] = make_uint4(0, 0, 0, 0);
+      if (row < rows_all)
+        raw[i] = *reinterpret_cast<const uint4*>(a.q + (first + token) * a.q_stride +
+                                                 (u.h * G + row - token * G) * D + (lane % kLanes) * 8);
     }
-    const int e = min(max(static_cast<int>(top >> 7), 1), 254);       // 127 + exponent of the largest
-    const int down = min(max(127 + 7 - (e - 127), 1), 254);           // * 2^(7 - exponent)
-    const float sc = __int_as_float(down << 23), put = sc * sign;
-    uint32_t hi[2], lo[2];
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      float f[4], g[4];
-      f[0] = __uint_as_float(x[2 * y] << 16) * put;
-      f[1] = __uint_as_float(x[2 * y] & 0xFFFF0000u) * put;
-      f[2] = __uint_as_float(x[2 * y + 1] << 16) * put;
-      f[3] = __uint_as_float(x[2 * y + 1] & 0xFFFF0000u) * put;
+    for (int i = 0; i < kLoads; ++i) {
+      const int rr = warp * kPer + (i0 + i) * kAtOnce + lane / kLanes;
+      const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+      uint32_t top = 0;
 #pragma unroll
-      for (int z = 0; z < 4; ++z) {
-        g[z] = __uint_as_float(__float_as_uint(f[z]) & 0xFFF00000u);  // sign, exponent, 3 bits
-        f[z] -= g[z];
+      for (int y = 0; y < 4; ++y) top = max(top, max(x[y] & 0x7FFFu, (x[y] >> 16) & 0x7FFFu));
+      if constexpr (kLanes == 32) {
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+      } else {
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
       }
-      hi[y] = e4m3x4(g[0], g[1], g[2], g[3]);
-      lo[y] = e4m3x4(f[0], f[1], f[2], f[3]);
+      const int e = min(max(static_cast<int>(top >> 7), 1), 254);       // 127 + exponent of the largest
+      const int down = min(max(127 + 7 - (e - 127), 1), 254);           // * 2^(7 - exponent)
+      const float sc = __int_as_float(down << 23), put = sc * sign;
+      uint32_t hi[2], lo[2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float f[4], g[4];
+        f[0] = __uint_as_float(x[2 * y] << 16) * put;
+        f[1] = __uint_as_float(x[2 * y] & 0xFFFF0000u) * put;
+        f[2] = __uint_as_float(x[2 * y + 1] << 16) * put;
+        f[3] = __uint_as_float(x[2 * y + 1] & 0xFFFF0000u) * put;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          g[z] = __uint_as_float(__float_as_uint(f[z]) & 0xFFF00000u);  // sign, exponent, 3 bits
+          f[z] -= g[z];
+        }
+        hi[y] = e4m3x4(g[0], g[1], g[2], g[3]);
+        lo[y] = e4m3x4(f[0], f[1], f[2], f[3]);
+      }
+      {
+        const int c = lane % kLanes;
+        const uint32_t at = s_q + TL::chunk_at(rr, c >> 1) + (c & 1) * 8;
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + TL::kBytes), "r"(lo[0]), "r"(lo[1]) : "memory");
+        // a query that is not finite saturates in 8 bits: its row is NaN through its sum
+        if (c == 0) s_factor[rr] = top < 0x7F80u ? fabsf(a.scale) * kLog2e * __int_as_float((254 - down) << 23) : __int_as_float(0x7FC00000);
+      }
     }
-    {
-      const int c = lane % kLanes;
-      const uint32_t at = s_q + (rr / 128) * 2 * TL::kBytes + TL::chunk_at(rr % 128, c >> 1) + (c & 1) * 8;
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(hi[0]), "r"(hi[1]) : "memory");
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + TL::kBytes), "r"(lo[0]), "r"(lo[1]) : "memory");
-      // a query that is not finite saturates in 8 bits: its row is NaN through its sum
-      if (c == 0) s_factor[rr] = top < 0x7F80u ? fabsf(a.scale) * kLog2e * __int_as_float((254 - down) << 23) : __int_as_float(0x7FC00000);
-    }
-  }
   }
 }
 
@@ -451,18 +446,23 @@ __device__ __forceinline__ void store_rows(const PrefillParams& p, const Prefill
 }
 
 // ------------------------------------------------------------------------------- head_dim 256
-
-template <int D>
-struct PrefillCfg {
-  static constexpr int kTilesM = D == 256 ? 1 : 2;       // row tiles of a unit
-  static constexpr int kSplitC = 4 / kTilesM;            // softmax warpgroups that share a row tile, by columns
-  static constexpr int kRows = kTilesM * 128;
-  static constexpr int kSoftWarps = 4 * kTilesM * kSplitC;
+//
+// Both products on 8-bit operands, no conversion of V: p = p_hi + p_lo, p_hi to 4 significant bits and p_lo =
+// e4m3(p - p_hi), 8 bits in all, as a bf16 p would keep. m moves when a score passes it by 2^4, so that 16 p <= 256
+// fits e4m3. Sixteen softmax warps, four threads a row with 32 columns each (they exchange their maxima), two
+// score buffers (2 x 128 columns of tensor memory, 256 of output), a warp that issues MMAs: the 2,090 cycles of products a
+// tile hide most of the softmax. 4,096 tokens (16 / 2 heads): 129 us, 57% of the bf16 rate with the masked half
+// of the diagonal counted out. With f16 probabilities, as below, V alone would take 128 KB of shared memory.
+struct WideCfg {
+  static constexpr int D = 256;
+  static constexpr int kSplitC = 4;                      // softmax warpgroups that share the rows, by columns
+  static constexpr int kRows = kUnitRows;
+  static constexpr int kSoftWarps = 4 * kSplitC;
   static constexpr int kThreads = 32 * (kSoftWarps + 4); // and warps for MMAs, lookups, copies of K, copies of V
-  static constexpr int kStages = D == 256 ? 2 : 3;       // key tiles in the ring, and value tiles
+  static constexpr int kStages = 2;                      // key tiles in the ring, and value tiles
   static constexpr bool kRefs = false;
   static constexpr int kBatch = 4, kBatches = 4, kInfoRing = kBatch * kBatches;  // tiles looked up at a time; kept
-  static constexpr int kQ = kTilesM * 2 * Tile<D>::kBytes;  // hi and lo of each row tile
+  static constexpr int kQ = 2 * Tile<D>::kBytes;         // hi and lo
   static constexpr int kKV = kStages * 2 * Tile<D>::kBytes;
   static constexpr int kAtScale = kQ + kKV;                 // [kInfoRing][kGroups] (ks, log2 vs)
   static constexpr int kAtRow = kAtScale + kInfoRing * kGroups * 8;
@@ -473,13 +473,13 @@ struct PrefillCfg {
   static constexpr int kSmem = 1024 + kAtBars + 8 * (4 * kStages + 2 * kBatches + 8);
   // tensor memory columns
   static constexpr int kS = 0;         // two score buffers of 128
-  static constexpr int kO = 256;       // output, D columns per row tile
+  static constexpr int kO = 256;       // output, D columns
 };
 
-template <int D>
-__global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
-    attn_prefill_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CacheMaps maps) {
-  using C = PrefillCfg<D>;
+__global__ void __launch_bounds__(WideCfg::kThreads, 1)
+    attn_prefill_wide_kernel(const __grid_constant__ PrefillParams p, const __grid_constant__ CacheMaps maps) {
+  using C = WideCfg;
+  constexpr int D = C::D;
   using TL = Tile<D>;
   constexpr int NC = kTile / C::kSplitC;  // columns (keys) of a softmax thread
   constexpr int NG = NC / kGroup;
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
     for (int i = 0; i < C::kBatches; ++i) mbar_init(b_infoe + 8 * i, C::kSoftWarps + 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_s + 8 * i, 1);
-      mbar_init(b_p + 8 * i, 32 * C::kSoftWarps / C::kTilesM);
+      mbar_init(b_p + 8 * i, 32 * C::kSoftWarps);
       mbar_init(b_pv + 8 * i, 1);
     }
     mbar_init(b_q, 32 * C::kSoftWarps);
@@ -532,9 +532,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
   const uint32_t tmem = s_tmem;
 
   auto wait = [&](uint32_t b, int parity) { return wait_or_fail(b, parity, &s_fail); };
-  // the score buffer of row tile t and key tile j, and which use of it that is
-  auto buffer = [](int t, int j) { return C::kTilesM == 2 ? t : j & 1; };
-  auto use = [](int j) { return C::kTilesM == 2 ? j & 1 : (j >> 1) & 1; };
+  auto use = [](int j) { return (j >> 1) & 1; };  // of score buffer j & 1, its barriers' parity
 
   int copies = 0;  // of a copying warp
   if (warp == C::kSoftWarps + 1) {
@@ -552,31 +550,31 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
     // warp shares its scheduler with softmax warps, and a few instructions an MMA are what it gets
     const uint64_t dk = TL::desc(s_k, 16), dq = TL::desc(s_q, 16), dv = TL::desc(s_v, TL::kHalf);
     auto k_off = [](int ks) { return static_cast<uint64_t>((ks / (TL::kRow / 32)) * TL::kHalf + (ks % (TL::kRow / 32)) * 32) >> 4; };
-    auto qk = [&](int j, int t) {  // scores of row tile t, key tile j
+    auto qk = [&](int j) {  // scores of key tile j
       if (lane == 0) {
-        const uint32_t d = tmem + C::kS + 128 * buffer(t, j);
-        const uint64_t kt = dk + (j % C::kStages) * (TL::kBytes >> 4), qt = dq + t * 2 * (TL::kBytes >> 4);
+        const uint32_t d = tmem + C::kS + 128 * (j & 1);
+        const uint64_t kt = dk + (j % C::kStages) * (TL::kBytes >> 4);
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int ks = 0; ks < D / 32; ++ks)
-            mma_f8_ss(d, qt + part * (TL::kBytes >> 4) + k_off(ks), kt + k_off(ks), iqk, part | ks);
-        tc::mma_commit(b_s + 8 * buffer(t, j));
-        if (t == C::kTilesM - 1) tc::mma_commit(b_kempty + 8 * (j % C::kStages));
+            mma_f8_ss(d, dq + part * (TL::kBytes >> 4) + k_off(ks), kt + k_off(ks), iqk, part | ks);
+        tc::mma_commit(b_s + 8 * (j & 1));
+        tc::mma_commit(b_kempty + 8 * (j % C::kStages));
       }
       __syncwarp();
     };
-    auto pv = [&](int j, int t) {
+    auto pv = [&](int j) {
       if (lane == 0) {
-        const uint32_t pa = tmem + C::kS + 128 * buffer(t, j);
+        const uint32_t pa = tmem + C::kS + 128 * (j & 1);
         const uint64_t vt = dv + (j % C::kStages) * (TL::kBytes >> 4);
 #pragma unroll
         for (int ks = 0; ks < kTile / 32; ++ks)
 #pragma unroll
           for (int part = 0; part < 2; ++part)
-            mma_f8_ts(tmem + C::kO + t * D, pa + ks * 32 + part * 8, vt + ks * (32 * TL::kRow >> 4), ipv, (j > 0) | (ks | part));
-        tc::mma_commit(b_pv + 8 * buffer(t, j));
-        if (t == C::kTilesM - 1) tc::mma_commit(b_vempty + 8 * (j % C::kStages));
+            mma_f8_ts(tmem + C::kO, pa + ks * 32 + part * 8, vt + ks * (32 * TL::kRow >> 4), ipv, (j > 0) | (ks | part));
+        tc::mma_commit(b_pv + 8 * (j & 1));
+        tc::mma_commit(b_vempty + 8 * (j % C::kStages));
       }
       __syncwarp();
     };
@@ -591,27 +589,20 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
       tc::fence_async_smem();
       __syncwarp();
     };
-    // step by step: scores of row tile t of key tile i, and (two row tiles) after the products of tile
-    // i - 1 or (one row tile, two buffers) before them
+    // step by step: scores of tile i, then the products of tile i - 1
 #pragma unroll 1
     for (int i = 0; ok && i <= tiles; ++i) {
       const int j = i - 1;
-      if (i < tiles && !(ok = wait(b_kfull + 8 * (i % C::kStages), (i / C::kStages) & 1))) break;
+      if (i < tiles) {
+        if (!(ok = wait(b_kfull + 8 * (i % C::kStages), (i / C::kStages) & 1))) break;
+        qk(i);
+      }
       if (j >= 0) {
-        if (C::kTilesM == 1 && i < tiles) qk(i, 0);
         if (!(ok = wait(b_vfull + 8 * (j % C::kStages), (j / C::kStages) & 1))) break;
         clear_tail(j);
-      } else if (C::kTilesM == 1 && tiles > 0) {
-        qk(0, 0);
-      }
-#pragma unroll 1
-      for (int t = 0; t < C::kTilesM; ++t) {
-        if (j >= 0) {
-          if (!(ok = wait(b_p + 8 * buffer(t, j), use(j)))) break;
-          tc::fence_after_sync();
-          pv(j, t);
-        }
-        if (C::kTilesM == 2 && i < tiles) qk(i, t);
+        if (!(ok = wait(b_p + 8 * (j & 1), use(j)))) break;
+        tc::fence_after_sync();
+        pv(j);
       }
     }
   } else {
@@ -620,14 +611,13 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
     mbar_arrive(b_q);
 
     // ---- softmax: kSplitC threads a row, NC of the tile's columns each
-    const int t = warp / (4 * C::kSplitC);        // row tile
-    const int half = warp / 4 % C::kSplitC;       // (which of the row's threads)
-    const int r = t * 128 + (warp & 3) * 32 + lane;  // row of the unit
+    const int half = warp / 4;                    // which of the row's threads
+    const int r = (warp & 3) * 32 + lane;         // row of the unit
     const int row = u.row0 + r;                   // (token, head) row of the request
     const bool live = row < rows_all;
     const int token = live ? row / G : 0;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int team = 1 + t * 4 + (warp & 3);      // the barrier of the warps that share rows
+    const int team = 1 + (warp & 3);              // the barrier of the warps that share rows
     bool ok = wait(b_q, 0);
     const float given = s_factor[r];
     const bool finite = given == given;
@@ -640,8 +630,8 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
     bool left = false;
     for (int j = 0; j < tiles; ++j) {
       const int slot = (j / C::kBatch) % C::kBatches;
-      ok = __all_sync(0xFFFFFFFFu, ok && wait(b_info + 8 * slot, (j / C::kInfoRing) & 1) && wait(b_s + 8 * buffer(t, j), use(j)));
-      const uint32_t sc = tmem + C::kS + 128 * buffer(t, j) + half * NC + lanes;
+      ok = __all_sync(0xFFFFFFFFu, ok && wait(b_info + 8 * slot, (j / C::kInfoRing) & 1) && wait(b_s + 8 * (j & 1), use(j)));
+      const uint32_t sc = tmem + C::kS + 128 * (j & 1) + half * NC + lanes;
       const float2* scales = s_scale + (j % C::kInfoRing) * kGroups;
       const int cut = sees - (u.tile0 + j) * kTile - half * NC;      // columns from here on are hidden
       const bool masked = all_see < (u.tile0 + j) * kTile + (half + 1) * NC;
@@ -709,17 +699,17 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
           lv_ref = lv_top;
         }
         if (j > 0) {
-          ok = __all_sync(0xFFFFFFFFu, wait(b_pv + 8 * buffer(t, j - 1), use(j - 1)));
+          ok = __all_sync(0xFFFFFFFFu, wait(b_pv + 8 * ((j - 1) & 1), use(j - 1)));
           if (ok) {
             tc::fence_after_sync();
 #pragma unroll 1
             for (int c = half * (D / C::kSplitC); c < (half + 1) * (D / C::kSplitC); c += 32) {
               float o[32];
-              tmem_ld32(tmem + C::kO + t * D + lanes + c, o);
+              tmem_ld32(tmem + C::kO + lanes + c, o);
               tc::tmem_wait_ld();
 #pragma unroll
               for (int i = 0; i < 32; ++i) o[i] *= corr;
-              tmem_st32(tmem + C::kO + t * D + lanes + c, o);
+              tmem_st32(tmem + C::kO + lanes + c, o);
             }
           }
         }
@@ -758,11 +748,11 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
-      mbar_arrive(b_p + 8 * buffer(t, j));
+      mbar_arrive(b_p + 8 * (j & 1));
       if (j % C::kBatch == C::kBatch - 1 && lane == 0) mbar_arrive(b_infoe + 8 * slot);  // (the warp has met at the store)
     }
     // epilogue
-    if (ok && tiles > 0) ok = wait(b_pv + 8 * buffer(t, tiles - 1), use(tiles - 1));
+    if (ok && tiles > 0) ok = wait(b_pv + 8 * ((tiles - 1) & 1), use(tiles - 1));
     ok = __all_sync(0xFFFFFFFFu, ok && !left);
     if (!left) {  // the row's sum from its threads
       s_max[((tiles & 1) * C::kSplitC + half) * C::kRows + r] = l;
@@ -775,7 +765,7 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
       tc::fence_after_sync();
       if (u.slot >= 0 && live && half == 0) p.ml[static_cast<int64_t>(u.slot) * C::kRows + r] = make_float2(m, l);
       store_rows<D, D / C::kSplitC, C::kQ / C::kSoftWarps>(p, u, C::kRows, r, live, token, row - token * G, G, tiles, l, lv_ref,
-                                                           tmem + C::kO + t * D + lanes, half * (D / C::kSplitC),
+                                                           tmem + C::kO + lanes, half * (D / C::kSplitC),
                                                            s_q + warp * (C::kQ / C::kSoftWarps));
     }
   }
@@ -800,11 +790,21 @@ __global__ void __launch_bounds__(PrefillCfg<D>::kThreads, 1)
 
 // ------------------------------------------------------------------------- head_dim 64 and 128
 //
-// Here a key costs half the MMA time and the same softmax, so the softmax decides. Its probabilities are f16
-// (one conversion for two of them instead of six operations for the two e4m3 parts) and a warpgroup converts each
-// tile of V to f16 once for the 256 rows that use it; e4m3 values are exact in f16. A thread has a row. Scores are
-// read once: the probabilities are computed with the maximum as it stands, and again only if the tile's
-// own passes it by 2^8 (f16 has the range), which after the first tile almost never happens.
+// Here a key costs half the MMA time and the same softmax, so the softmax and shared memory decide. Probabilities
+// are f16 (11 significant bits, 2^-24 of the reference; one conversion for two of them instead of six operations for
+// two e4m3 parts), and a warpgroup converts each tile of V to f16; e4m3 values are exact in f16. m moves when a score
+// passes it by 2^8, the reference for vs when one passes it by 2^3 (f16 has the range).
+//
+// Scores of three tiles are in tensor memory (3 x 128 columns, and D of output): Q K of the next tiles runs under
+// the softmax. Two warpgroups take the tiles in turn, thread = row, and hand m on; Q K and P V are issued by a thread
+// each, so that the waits of one pass under the products of the other. Per tile and 128 rows, the products take
+// about 1,110 cycles of the tensor pipe, and nearly as many of shared memory: Q, K and V in f16 as operands, V read
+// and written by the conversion, the copies; together 1,400. Measured about 2,050: 300 tokens at 60,000 (32 / 8
+// heads of 128) 368 us, against 198 for the same program without the arithmetic of softmax and conversion, and 301
+// with one MMA a product and no conversion.
+// Not kept: 256 rows (two row tiles, one score buffer each: 402 us, each tile's chain of softmax and products
+// exposed); sixteen softmax warps (385: a vote between the two threads of a row); p computed before its tile's
+// maximum is known and again where that passes (420: twice the registers and code).
 template <int D>
 struct NarrowCfg {
   static constexpr int kRows = 128;
@@ -1216,9 +1216,9 @@ cudaError_t launch_after(void (*kern)(KArgs...), dim3 grid, int threads, int sme
 
 template <int D>
 cudaError_t launch_prefill_d(const PrefillParams& p, const PrefillLayout& L, const CacheMaps& maps, cudaStream_t s) {
-  using C = std::conditional_t<D == 256, PrefillCfg<256>, NarrowCfg<D == 256 ? 128 : D>>;
+  using C = std::conditional_t<D == 256, WideCfg, NarrowCfg<D == 256 ? 128 : D>>;
   auto kern = [] {
-    if constexpr (D == 256) return attn_prefill_kernel<D>;
+    if constexpr (D == 256) return attn_prefill_wide_kernel;
     else return attn_prefill_narrow_kernel<D>;
   }();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);

@@ -415,7 +415,9 @@ typedef struct {
  *   lens_old, lens_new [batch] int32;  block_table [batch, max_blocks] int32, in place
  *   free_ring  [num_blocks] int32, in place: a ring of block ids
  *   pool       [2] int32: the ring's head (0 .. num_blocks - 1) and how many blocks are free
- *   pool_out   [2] int32: the same after the call; may be `pool` itself
+ *   pool_out   [2] int32: the same after the call; may be `pool` itself (with pool_out and lens
+ *              in place the call runs on one thread-block cluster; with both apart, which a long
+ *              step is faster for, on as many CTAs as its tokens fill)
  *   total_tokens  the size of slot_map and positions; entries past the step's new tokens are
  *              filled with -1 (a padded step), and a step with more sets GDN_DEVERR_SEQLENS
  *   cu_tokens  [batch + 1] int32;  slot_map, positions [total_tokens] int32 (NULL if 0)
@@ -462,8 +464,9 @@ gdn_status gdn_cache_append(const void* k, int64_t k_stride, const void* v, int6
  *   out[b, h] = sum_j softmax_j(scale * q[b, h] . k_j) v_j
  * A request of length 0 (or with no readable block) gives zeros. A length outside [0, max_blocks *
  * block_size] sets GDN_DEVERR_SEQLENS and is clamped. What lies in a block past the request's
- * length is never used, NaN bytes included. Softmax statistics and sums are fp32; the
- * probabilities are rounded to f16 for the product with V.
+ * length is never used, NaN bytes included. Softmax statistics and sums are fp32. Queries are
+ * exact to 2^-18 of a head's largest element; the probabilities keep 16 significant bits, and
+ * 2^-22 of the largest, for the product with V.
  *
  *   q          [batch] rows of Hq * head_dim bf16, q_stride elements apart (16-byte aligned, a
  *              multiple of 8)
@@ -486,8 +489,8 @@ gdn_status gdn_attn_decode(const void* q, int64_t q_stride, const void* k_cache,
  * are rows cu_tokens[b] .. cu_tokens[b + 1] of q; their keys and values are in the cache already
  * (append first) as the last of its lens[b] tokens. With n new tokens, token i attends to
  * positions 0 .. lens[b] - n + i; a token that sees nothing (lens[b] < n: its row was refused)
- * gives zeros. Otherwise as gdn_attn_decode: the probabilities keep 8 significant bits for
- * the product with V (two e4m3 parts), queries are exact to 2^-18 of a row's largest element. A NaN
+ * gives zeros. Otherwise as gdn_attn_decode, but for the probabilities: for the product with V
+ * they are f16 for head_dim 64 and 128 and keep 8 significant bits (two e4m3 parts) for 256. A NaN
  * among a request's values reaches the rows that do not see it, too, if they share a 128-token tile.
  *
  *   q          [total_tokens] rows of Hq * head_dim bf16, q_stride elements apart

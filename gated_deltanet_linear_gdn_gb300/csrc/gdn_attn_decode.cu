@@ -22,7 +22,7 @@
 // only a unit's first tile stops for them: 0.87 p vs / vs_ref <= 448, the largest e4m3.
 //
 // Split. A (request, kv head) is cut into units of 256, 512 or 1,024 keys by its OWN length
-// (unit_keys), never by the batch: a row's result depends on its own inputs alone, bit for bit, as
+// (unit_shift), never by the batch: a row's result depends on its own inputs alone, bit for bit, as
 // for every other call of the library. A persistent grid walks the units. A request of one unit is
 // finished here, a longer one leaves fp32 partial sums (with their maximum and sum) that a second,
 // programmatically dependent kernel joins in unit order.
@@ -85,17 +85,20 @@ constexpr int kThreads = 32 * 8;
 constexpr int kSmemPerSm = 228 * 1024;  // 1 KB of it taken by each resident CTA
 constexpr float kRise = 8.0f;          // log2 of what a score may pass the running maximum by
 
-// log2 of the keys of one unit of a request of `len` keys, and its units.
-__host__ __device__ __forceinline__ int unit_shift(int len) { return len <= 2048 ? 8 : len <= 8192 ? 9 : 10; }
+// log2 of the keys of one unit of a request of `len` keys, and its units. Small units shorten the chain of tiles
+// that a small batch waits for, and cost a large one partial sums (d = 256, 8 query heads a kv head: 8 KB a unit next
+// to 128 KB of cache for 256 keys). Units of 256 and 512 keys at length 4,097, one request: 13.5 and 17.9 us; up
+// to 8,192, 256 requests: 410 and 350 us. So 256 up to 24 units, then 512 up to 24, then 1,024.
+constexpr int kFewUnits = 24;
+__host__ __device__ __forceinline__ int unit_shift(int len) { return len <= kFewUnits << 8 ? 8 : len <= kFewUnits << 9 ? 9 : 10; }
 __host__ __device__ __forceinline__ int units_of(int len) {
   const int s = unit_shift(len);
   return (len + (1 << s) - 1) >> s;
 }
 // The most units that any length up to `cap` has.
 int64_t most_units(int64_t cap) {
-  if (cap <= 2048) return (cap + 255) / 256;
-  if (cap <= 4096) return 8;
-  return cap <= 8192 ? (cap + 511) / 512 : cap <= 16384 ? 16 : (cap + kMaxUnitKeys - 1) / kMaxUnitKeys;
+  if (cap <= kFewUnits << 8) return (cap + 255) / 256;
+  return cap <= kFewUnits << 10 ? kFewUnits : (cap + kMaxUnitKeys - 1) / kMaxUnitKeys;
 }
 
 struct DecodeParams {
@@ -276,22 +279,14 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cap = a.max_blocks * a.bs;
 
+  int len = tid < p.nb ? a.lens[p.b0 + tid] : 0;  // (on its way under the set-up)
   if (tid < 4) prefetch_map(tid == 0 ? &maps.k_page : tid == 1 ? &maps.v_page : tid == 2 ? &maps.k_group : &maps.v_group);
-  if (tid == 0) {
-    for (int i = 0; i < 2 * C::kStages + 2 * C::kBatches + C::kFactorRing; ++i)
-      mbar_init(b_full + 8 * i, b_full + 8 * i >= b_infoe && b_full + 8 * i < b_factor ? 4 : 1);
-    mbar_init(b_s, 1);
-    mbar_init(b_s + 8, 1);
-    mbar_init(b_p, 128);
-    mbar_init(b_pv, 1);
-    mbar_init(b_pv + 8, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(b_qfull + 8 * i, 32);
-      mbar_init(b_qempty + 8 * i, 1);
-    }
-    mbar_init(b_drain, 1);
-    s_fail = 0;
+  if (tid < C::kBars) {
+    // who arrives: a copy, a commit or one lane, but for what warps and threads release themselves
+    const uint32_t bar = b_full + 8 * tid;
+    mbar_init(bar, bar >= b_infoe && bar < b_factor ? 4 : bar == b_p ? 128 : bar >= b_qfull && bar < b_qempty ? 32 : 1);
   }
+  if (tid == 0) s_fail = 0;
   fence_mbar_init();
   if (warp == 4) {
     tc::tmem_alloc(&s_tmem, C::kColumns);
@@ -302,9 +297,8 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
     int carry = 0, flags = 0;
     for (int at = 0; at < p.nb; at += kThreads) {
       const int b = at + tid;
-      int len = 0;
+      if (at > 0) len = b < p.nb ? a.lens[p.b0 + b] : 0;
       if (b < p.nb) {
-        len = a.lens[p.b0 + b];
         if (len < 0 || len > cap) flags = GDN_DEVERR_SEQLENS;
         len = min(max(len, 0), cap);
         lens[b] = len;
@@ -503,8 +497,13 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
       }
     }
   } else if (warp == 6) {
-    // ---- queries: rows of Q, high parts then low parts, one unit ahead
+    // ---- queries: rows of Q, high parts then low parts, one unit ahead; rows past 2 HP stay zero
     bool ok = true;
+    for (int e = 2 * HP * (D / 16) + lane; e < 2 * C::kNQ * (D / 16); e += 32) {
+      const int buffer = e / (C::kNQ * (D / 16)), i = e - buffer * (C::kNQ * (D / 16)), row = i / (D / 16);
+      if (row >= 2 * HP)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(s_q + buffer * C::kQ + TQ::chunk_at(row, i % (D / 16))), "r"(0) : "memory");
+    }
     int k = 0;
     for (Walk w = walk(); w.more() && ok; w.next(), ++k) {
       const int head0 = first_head(w), heads = unit_heads(w);
@@ -514,54 +513,64 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
       const uint32_t qt = s_q + (k & 1) * C::kQ;
       constexpr int kPer = D / 16;          // 16-element chunks of a head, one to a lane
       constexpr int kAtOnce = 32 / kPer;    // heads at a time
+      constexpr int kGroupsOf = (HP + kAtOnce - 1) / kAtOnce, kLoads = kGroupsOf < 4 ? kGroupsOf : 4;  // groups of heads; in flight
 #pragma unroll 1
-      for (int h0 = 0; h0 < C::kNQ / 2; h0 += kAtOnce) {
-        const int hd = h0 + lane / kPer, c = lane % kPer;
-        uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-        if (hd < heads) {
-          raw[0] = *reinterpret_cast<const uint4*>(qp + hd * D + c * 16);
-          raw[1] = *reinterpret_cast<const uint4*>(qp + hd * D + c * 16 + 8);
-        }
-        const uint32_t x[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
-        uint32_t top = 0;
+      for (int g0 = 0; g0 < kGroupsOf * kAtOnce; g0 += kLoads * kAtOnce) {
+        uint4 all[kLoads][2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, max(x[i] & 0x7FFFu, (x[i] >> 16) & 0x7FFFu));
-#pragma unroll
-        for (int o = 1; o < kPer; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-        const int e = min(max(static_cast<int>(top >> 7), 1), 254);  // 127 + exponent of the largest
-        const int down = min(max(127 + 7 - (e - 127), 1), 254);      // * 2^(7 - exponent)
-        const float sc = __int_as_float(down << 23);
-        const float put = a.scale < 0.0f ? -sc : sc;                 // the factor is kept positive
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float f[4], g[4];
-          f[0] = __uint_as_float(x[2 * i] << 16) * put;
-          f[1] = __uint_as_float(x[2 * i] & 0xFFFF0000u) * put;
-          f[2] = __uint_as_float(x[2 * i + 1] << 16) * put;
-          f[3] = __uint_as_float(x[2 * i + 1] & 0xFFFF0000u) * put;
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            g[z] = __uint_as_float(__float_as_uint(f[z]) & 0xFFF00000u);  // sign, exponent, 3 bits
-            f[z] -= g[z];
+        for (int i = 0; i < kLoads; ++i) {
+          const int hd = g0 + i * kAtOnce + lane / kPer, c = lane % kPer;
+          all[i][0] = all[i][1] = make_uint4(0, 0, 0, 0);
+          if (hd < heads) {
+            all[i][0] = *reinterpret_cast<const uint4*>(qp + hd * D + c * 16);
+            all[i][1] = *reinterpret_cast<const uint4*>(qp + hd * D + c * 16 + 8);
           }
-          hi[i] = e4m3x4(g[0], g[1], g[2], g[3]);
-          lo[i] = e4m3x4(f[0], f[1], f[2], f[3]);
         }
-        // row of the operand: high part of head hd, low part HP rows on; rows past 2 HP stay zero
-        if (hd < HP) {
-          const uint32_t at = TQ::chunk_at(hd, c), al = TQ::chunk_at(HP + hd, c);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(qt + at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(qt + al), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
-          // a query that is not finite would saturate in 8 bits: its head is NaN through its factor
-          if (c == 0)
-            s_factor[(k % C::kFactorRing) * 16 + hd] =
-                top < 0x7F80u ? fabsf(a.scale) * kLog2e * __int_as_float((254 - down) << 23) : __int_as_float(0x7FC00000);
-        } else {
-          const uint32_t z0 = TQ::chunk_at(HP + hd, c);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(qt + z0), "r"(0) : "memory");
-          const uint32_t z1 = TQ::chunk_at(C::kNQ / 2 + hd, c);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(qt + z1), "r"(0) : "memory");
+#pragma unroll 1
+        for (int i0 = 0; i0 < kLoads; ++i0) {
+          const int hd = g0 + i0 * kAtOnce + lane / kPer, c = lane % kPer;
+          const uint4 raw[2] = {all[0][0], all[0][1]};
+#pragma unroll
+          for (int i = 0; i + 1 < kLoads; ++i) {
+            all[i][0] = all[i + 1][0];
+            all[i][1] = all[i + 1][1];
+          }
+          const uint32_t x[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+          uint32_t top = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top = max(top, max(x[i] & 0x7FFFu, (x[i] >> 16) & 0x7FFFu));
+#pragma unroll
+          for (int o = 1; o < kPer; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+          const int e = min(max(static_cast<int>(top >> 7), 1), 254);  // 127 + exponent of the largest
+          const int down = min(max(127 + 7 - (e - 127), 1), 254);      // * 2^(7 - exponent)
+          const float sc = __int_as_float(down << 23);
+          const float put = a.scale < 0.0f ? -sc : sc;                 // the factor is kept positive
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float f[4], g[4];
+            f[0] = __uint_as_float(x[2 * i] << 16) * put;
+            f[1] = __uint_as_float(x[2 * i] & 0xFFFF0000u) * put;
+            f[2] = __uint_as_float(x[2 * i + 1] << 16) * put;
+            f[3] = __uint_as_float(x[2 * i + 1] & 0xFFFF0000u) * put;
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              g[z] = __uint_as_float(__float_as_uint(f[z]) & 0xFFF00000u);  // sign, exponent, 3 bits
+              f[z] -= g[z];
+            }
+            hi[i] = e4m3x4(g[0], g[1], g[2], g[3]);
+            lo[i] = e4m3x4(f[0], f[1], f[2], f[3]);
+          }
+          // row of the operand: high part of head hd, low part HP rows on
+          if (hd < HP) {
+            const uint32_t at = TQ::chunk_at(hd, c), al = TQ::chunk_at(HP + hd, c);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(qt + at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(qt + al), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
+            // a query that is not finite would saturate in 8 bits: its head is NaN through its factor
+            if (c == 0)
+              s_factor[(k % C::kFactorRing) * 16 + hd] =
+                  top < 0x7F80u ? fabsf(a.scale) * kLog2e * __int_as_float((254 - down) << 23) : __int_as_float(0x7FC00000);
+          }
         }
       }
       tc::fence_async_smem();

@@ -70,6 +70,9 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// Before a barrier is made anew: nothing may be on its way to it.
+__device__ __forceinline__ void mbar_inval(uint32_t bar) { asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar) : "memory"); }
+
 // Waits for a barrier's phase, giving up after about a second or as soon as another role of the CTA has
 // (`fail`, in shared memory). False: the caller stops.
 // Kept small: a kernel holds some twenty of them, and its first pass through its code is paced by

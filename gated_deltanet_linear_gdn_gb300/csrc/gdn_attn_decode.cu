@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
   __shared__ volatile int s_fail;
 
   const AttnArgs& a = p.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // (known to be the same in a warp)
   const int cap = a.max_blocks * a.bs;
 
   int len = tid < p.nb ? a.lens[p.b0 + tid] : 0;  // (on its way under the set-up)

@@ -53,7 +53,7 @@ struct PrefillParams {
   AttnArgs a;
   int b0, nb;
   int max_units, max_slots;
-  int32_t* counts;          // [0] units, [1] split tiles
+  int32_t* counts;          // [0] units, [1] split tiles, [2] units taken after the grid's first
   PrefillUnit* units;       // [max_units]
   PrefillUnit* joins;       // [max_units]: the first split of each split row tile
   float2* ml;               // [max_slots][rows] (maximum, sum)
@@ -61,7 +61,9 @@ struct PrefillParams {
 };
 
 // How many pieces the key tiles of a request are cut into: the fewest rounds of an assumed 152
-// CTAs, counted in tiles with a constant cost per piece.
+// CTAs, counted in tiles with a constant cost per piece (a prologue and an epilogue take about 8 tiles). 300 tokens at
+// 60,000 (80 units of 470 tiles): 368 us in 5 pieces, 686 whole; 8 ragged prompts, none of them alone on the GPU: 346
+// and 321, the price of results that do not depend on the batch.
 __host__ __device__ __forceinline__ int kv_splits(int units, int tiles, int d) {
   if (units >= few_units(d) || tiles < 2 * kMinSplitTiles) return 1;
   int best = 1, cost = 0x7fffffff;
@@ -217,6 +219,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
   if (tid == 0) {
     p.counts[0] = carry;
     p.counts[1] = s_joins;
+    p.counts[2] = 0;
   }
 }
 
@@ -451,7 +454,7 @@ __device__ __forceinline__ void store_rows(const PrefillParams& p, const Prefill
 // e4m3(p - p_hi), 8 bits in all, as a bf16 p would keep. m moves when a score passes it by 2^4, so that 16 p <= 256
 // fits e4m3. Sixteen softmax warps, four threads a row with 32 columns each (they exchange their maxima), two
 // score buffers (2 x 128 columns of tensor memory, 256 of output), a warp that issues MMAs: the 2,090 cycles of products a
-// tile hide most of the softmax. 4,096 tokens (16 / 2 heads): 129 us, 57% of the bf16 rate with the masked half
+// tile hide most of the softmax. 4,096 tokens (16 / 2 heads): 122 us, 60% of the bf16 rate with the masked half
 // of the diagonal counted out. With f16 probabilities, as below, V alone would take 128 KB of shared memory.
 struct WideCfg {
   static constexpr int D = 256;
@@ -498,7 +501,7 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_fail;
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // (known to be the same in a warp)
   const AttnArgs& a = p.a;
   if (tid < 4) prefetch_map(tid == 0 ? &maps.k_page : tid == 1 ? &maps.v_page : tid == 2 ? &maps.k_group : &maps.v_group);
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -797,13 +800,15 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
 //
 // Scores of three tiles are in tensor memory (3 x 128 columns, and D of output): Q K of the next tiles runs under
 // the softmax. Two warpgroups take the tiles in turn, thread = row, and hand m on; Q K and P V are issued by a thread
-// each, so that the waits of one pass under the products of the other. Per tile and 128 rows, the products take
+// each, so that the waits of one pass under the products of the other. A CTA takes units as they come (the list holds up
+// to three times the units that a call has, and a CTA that only finds the list at its end costs as long as any start:
+// 8 ragged prompts 312 us, and 337 with a CTA per place of the list; for head_dim 256 the loop around a unit cost
+// more registers than there are). Per tile and 128 rows, the products take
 // about 1,110 cycles of the tensor pipe, and nearly as many of shared memory: Q, K and V in f16 as operands, V read
-// and written by the conversion, the copies; together 1,400. Measured about 2,050: 300 tokens at 60,000 (32 / 8
-// heads of 128) 368 us, against 198 for the same program without the arithmetic of softmax and conversion, and 301
-// with one MMA a product and no conversion.
-// Not kept: 256 rows (two row tiles, one score buffer each: 402 us, each tile's chain of softmax and products
-// exposed); sixteen softmax warps (385: a vote between the two threads of a row); p computed before its tile's
+// and written by the conversion, the copies; together 1,400. Measured about 1,950: 300 tokens at 60,000 (32 / 8
+// heads of 128) 366 us, against 198 for the same program without the arithmetic of softmax and conversion, and 301
+// with one MMA a product and no conversion (then 371). Not kept: 256 rows (two row tiles, one score buffer each: 402
+// us, each tile's chain of softmax and products exposed); sixteen softmax warps (385: a vote between the two threads of a row); p computed before its tile's
 // maximum is known and again where that passes (420: twice the registers and code).
 template <int D>
 struct NarrowCfg {
@@ -837,294 +842,312 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
   using TL = typename C::TL;
   using TV = typename C::TV;
   extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = smem_raw + (-smem_addr(smem_raw) & 1023u);
-  const uint32_t s_q = smem_addr(smem), s_k = s_q + C::kAtK, s_v = s_q + C::kAtV, s_v16 = s_q + C::kAtV16;
-  const float4* s_scale = reinterpret_cast<float4*>(smem + C::kAtScale);
-  int32_t* s_row = reinterpret_cast<int32_t*>(smem + C::kAtRow);
-  float2* s_ref = reinterpret_cast<float2*>(smem + C::kAtTop);
-  float* s_factor = reinterpret_cast<float*>(smem + C::kAtFactor);
-  float* s_max = reinterpret_cast<float*>(smem + C::kAtMax);
-  const uint32_t b_kfull = s_q + C::kAtBars, b_kempty = b_kfull + 8 * C::kStagesK, b_vfull = b_kempty + 8 * C::kStagesK,
-                 b_vempty = b_vfull + 8 * C::kStagesV, b_wfull = b_vempty + 8 * C::kStagesV, b_info = b_wfull + 8 * C::kStagesW,
-                 b_infoe = b_info + 8 * C::kBatches, b_s = b_infoe + 8 * C::kBatches, b_pv = b_s + 8 * C::kScores,
-                 b_p = b_pv + 8 * C::kScores, b_q = b_p + 8 * C::kScores, b_drain = b_q + 8, b_turn = b_drain + 16;
   __shared__ uint32_t s_tmem;
-  __shared__ volatile int s_fail;
+  __shared__ PrefillUnit s_unit;
+  __shared__ volatile int s_fail, s_next;
   constexpr int kMma = C::kSoftWarps + C::kConvWarps, kLook = kMma + 2, kCopyK = kMma + 3, kCopyV = kMma + 4;
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);  // (known to be the same in a warp)
   const AttnArgs& a = p.a;
   if (tid < 4) prefetch_map(tid == 0 ? &maps.k_page : tid == 1 ? &maps.v_page : tid == 2 ? &maps.k_group : &maps.v_group);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (static_cast<int>(blockIdx.x) >= *reinterpret_cast<volatile int32_t*>(p.counts)) return;
-  const PrefillUnit u = p.units[blockIdx.x];
-  const int n = u.n, len = u.len;
+  const int units = *reinterpret_cast<volatile int32_t*>(p.counts);
+  if (static_cast<int>(blockIdx.x) >= units) return;
   const int G = a.Hq / a.H;
-  const int rows_all = n * G;  // (below 2^31: the caller's tokens x heads are)
-  const int tiles = u.tile1 - u.tile0;
-
-  if (tid < C::kBars) {
-    // who arrives: a copy, a commit or one lane, but for what threads and warps release themselves
-    const uint32_t b = b_kfull + 8 * tid;
-    mbar_init(b, b >= b_vempty && b < b_info ? 32 * C::kConvWarps
-                 : b >= b_infoe && b < b_s ? C::kSoftWarps + 1
-                 : b >= b_p && b < b_q     ? C::kSoftWarps / 2
-                 : b == b_q                ? 32 * C::kSoftWarps
-                                           : 1);
-  }
   if (tid == 0) s_fail = 0;
-  fence_mbar_init();
   if (warp == kMma) {
     tc::tmem_alloc(&s_tmem, 512);
     tc::tmem_relinquish();
   }
-  tc::fence_before_sync();
-  __syncthreads();
-  tc::fence_after_sync();
-  const uint32_t tmem = s_tmem;
   auto wait = [&](uint32_t b, int parity) { return wait_or_fail(b, parity, &s_fail); };
 
-  int copies = 0;  // of a copying warp
-  if (warp == kLook) {
-    look_up<C>(p, u, tiles, smem + C::kAtScale, s_row, s_ref, b_info, b_infoe, &s_fail);
-  } else if (warp == kCopyK) {
-    copies = copy_tiles<D, C, C::kStagesK>(a, u, tiles, &maps.k_page, &maps.k_group, s_k, s_row, b_kfull, b_kempty, b_info, 0, &s_fail);
-  } else if (warp == kCopyV) {
-    copies = copy_tiles<D, C, C::kStagesV>(a, u, tiles, &maps.v_page, &maps.v_group, s_v, s_row, b_vfull, b_vempty, b_info, b_infoe, &s_fail);
-  } else if (warp >= kMma) {
-    // ---- MMAs: a thread for Q K and one for P V, so that the waits and commits of one pass under the products of
-    // the other. Scores of tile i go where those of i - 3 were, once their probabilities have been multiplied.
-    // Descriptors but for their start address, which each MMA adds.
-    constexpr uint32_t iqk = idesc_f8(128, kTile, false, false);
-    constexpr uint32_t ipv = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | (8u << 24);  // f16 x f16 (MN-major) -> fp32
-    const uint64_t dk = TL::desc(s_k, 16), dq = TL::desc(s_q, 16), dv = TV::desc(s_v16, TV::kHalf);
-    if (lane == 0 && warp == kMma) {
-      bool ok = tiles == 0 || wait(b_q, 0);
-      int st = 0, ph = 0, buf = 0, sph = 1;
 #pragma unroll 1
-      for (int i = 0; ok && i < tiles; ++i) {
-        if (!wait(b_kfull + 8 * st, ph) || !wait(b_pv + 8 * buf, sph)) break;
-        tc::fence_after_sync();
-        const uint64_t kt = dk + st * (TL::kBytes >> 4);
-#pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int ks = 0; ks < D / 32; ++ks)
-            mma_f8_ss(tmem + 128 * buf, dq + part * (TL::kBytes >> 4) + ks * 2, kt + ks * 2, iqk, part | ks);
-        tc::mma_commit(b_s + 8 * buf);
-        tc::mma_commit(b_kempty + 8 * st);
-        if (++st == C::kStagesK) st = 0, ph ^= 1;
-        if (++buf == C::kScores) buf = 0, sph ^= 1;
-      }
-    } else if (lane == 0) {
-      int buf = 0, sph = 0;
-#pragma unroll 1
-      for (int j = 0; j < tiles; ++j) {
-        if (!wait(b_wfull + 8 * (j & 1), (j >> 1) & 1) || !wait(b_p + 8 * buf, sph)) break;
-        tc::fence_after_sync();
-        const uint32_t pa = tmem + 128 * buf;
-        const uint64_t vt = dv + (j & 1) * (TV::kBytes >> 4);
-#pragma unroll
-        for (int ks = 0; ks < kTile / 16; ++ks)
-          tc::mma_bf16_ts(tmem + C::kO, pa + (ks >> 1) * 32 + (ks & 1) * 8, vt + ks * (16 * TV::kRow >> 4), ipv, (j > 0) | ks);
-        tc::mma_commit(b_pv + 8 * buf);
-        if (++buf == C::kScores) buf = 0, sph ^= 1;
-      }
+  for (int next = blockIdx.x;; next = s_next) {
+    uint32_t slack = -smem_addr(smem_raw) & 1023u;
+    asm volatile("" : "+r"(slack));  // (addresses are worked out per unit: kept from one to the next they cost spills)
+    unsigned char* smem = smem_raw + slack;
+    const uint32_t s_q = smem_addr(smem), s_k = s_q + C::kAtK, s_v = s_q + C::kAtV, s_v16 = s_q + C::kAtV16;
+    const float4* s_scale = reinterpret_cast<float4*>(smem + C::kAtScale);
+    int32_t* s_row = reinterpret_cast<int32_t*>(smem + C::kAtRow);
+    float2* s_ref = reinterpret_cast<float2*>(smem + C::kAtTop);
+    float* s_factor = reinterpret_cast<float*>(smem + C::kAtFactor);
+    float* s_max = reinterpret_cast<float*>(smem + C::kAtMax);
+    const uint32_t b_kfull = s_q + C::kAtBars, b_kempty = b_kfull + 8 * C::kStagesK, b_vfull = b_kempty + 8 * C::kStagesK,
+                   b_vempty = b_vfull + 8 * C::kStagesV, b_wfull = b_vempty + 8 * C::kStagesV, b_info = b_wfull + 8 * C::kStagesW,
+                   b_infoe = b_info + 8 * C::kBatches, b_s = b_infoe + 8 * C::kBatches, b_pv = b_s + 8 * C::kScores,
+                   b_p = b_pv + 8 * C::kScores, b_q = b_p + 8 * C::kScores, b_drain = b_q + 8, b_turn = b_drain + 16;
+    if (tid < static_cast<int>(sizeof(PrefillUnit) / 4)) reinterpret_cast<int*>(&s_unit)[tid] = reinterpret_cast<const int*>(p.units + next)[tid];
+    if (tid < C::kBars) {
+      // who arrives: a copy, a commit or one lane, but for what threads and warps release themselves
+      const uint32_t b = b_kfull + 8 * tid;
+      if (next != static_cast<int>(blockIdx.x)) mbar_inval(b);
+      mbar_init(b, b >= b_vempty && b < b_info ? 32 * C::kConvWarps
+                   : b >= b_infoe && b < b_s   ? C::kSoftWarps + 1
+                   : b >= b_p && b < b_q       ? C::kSoftWarps / 2
+                   : b == b_q                  ? 32 * C::kSoftWarps
+                                               : 1);
     }
-    __syncwarp();
-  } else if (warp >= C::kSoftWarps) {
-    // ---- V to f16: 16-byte chunks of a tile to the threads in turn; keys past the request's length, which hold
-    // whatever their page holds, become zero (0 * NaN is not 0)
-    const int me = tid - 32 * C::kSoftWarps;
-    constexpr int kChunks = D / 16;  // of a key
-    bool ok = true;
-#pragma unroll 1
-    for (int j = 0; j < tiles && ok; ++j) {
-      const int st = j % C::kStagesV;
-      ok = wait(b_vfull + 8 * st, (j / C::kStagesV) & 1) && (j < 2 || wait(b_pv + 8 * ((j - 2) % C::kScores), ((j - 2) / C::kScores) & 1));
-      if (!ok) break;
-      const int keys = len - (u.tile0 + j) * kTile;
-      const uint32_t from = s_v + st * TL::kBytes, to = s_v16 + (j & 1) * TV::kBytes;
-#pragma unroll 4
-      for (int i = me; i < kTile * kChunks; i += 32 * C::kConvWarps) {
-        const int key = i / (8 * kChunks) * 8 + i % 8, c = i / 8 % kChunks;  // (8 keys at a time: no bank twice)
-        uint32_t x[4], y[8];
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(from + TL::chunk_at(key, c)));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (key >= keys) x[e] = 0;
-          asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %2; cvt.rn.f16x2.e4m3x2 %0, lo; cvt.rn.f16x2.e4m3x2 %1, hi;}" : "=r"(y[2 * e]), "=r"(y[2 * e + 1]) : "r"(x[e]));
-        }
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + TV::chunk_at(key, 2 * c)), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + TV::chunk_at(key, 2 * c + 1)), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7]) : "memory");
-      }
-      tc::fence_async_smem();
-      mbar_arrive(b_wfull + 8 * (j & 1));
-      mbar_arrive(b_vempty + 8 * st);
-    }
-  } else {
-    split_queries<D, C::kRows, C::kSoftWarps>(a, u, G, rows_all, s_q, s_factor);
-    tc::fence_async_smem();
-    mbar_arrive(b_q);
+    fence_mbar_init();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = s_tmem;
+    const PrefillUnit& u = s_unit;
+    const int n = u.n, len = u.len;
+    const int rows_all = n * G;  // (below 2^31: the caller's tokens x heads are)
+    const int tiles = u.tile1 - u.tile0;
+    // the CTA's next unit, on its way under this one (its readers are past the barrier above)
+    if (tid == 32 * kLook) s_next = gridDim.x + atomicAdd(p.counts + 2, 1);
 
-    // ---- softmax: thread = row; the two warpgroups take the tiles in turn. The reference that both subtract, m, is
-    // what the tile before left: warps w and w + 4, which have the same rows, hand it on.
-    const int own = warp / 4, pair = warp & 3, r = pair * 32 + lane;  // r: row of the unit
-    const int row = u.row0 + r;                                      // (token, head) row of the request
-    const bool live = row < rows_all;
-    const int token = live ? row / G : 0;
-    const uint32_t lanes = static_cast<uint32_t>(pair * 32) << 16;
-    bool ok = wait(b_q, 0);
-    const float given = s_factor[r];
-    const bool finite = given == given;
-    const float factor = finite ? given : 0.0f;
-    const int sees = live ? min(len, len - n + token + 1) : 0;  // keys this row sees
-    const int all_see = __reduce_min_sync(0xFFFFFFFFu, sees);   // keys before this one are seen by every row of the warp
-    // a query that is not finite saturates in 8 bits: its row is NaN through its sum
-    float m = -INFINITY, l = finite || sees <= 0 ? 0.0f : __int_as_float(0x7FC00000);
-    const uint32_t turn = b_turn + 8 * (4 * own + pair), turn_of = b_turn + 8 * (4 * (own ^ 1) + pair);
-    // whether any thread of the two warps says so
-    auto vote = [&](bool x) {
-      uint32_t any;
-      asm volatile("{.reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, %2, 64, p; selp.u32 %0, 1, 0, q;}"
-                   : "=r"(any) : "r"(static_cast<uint32_t>(x)), "r"(1 + pair) : "memory");
-      return any != 0;
-    };
-    int buf = own, sph = 0;
+    int copies = 0;  // of a copying warp
+    if (warp == kLook) {
+      look_up<C>(p, u, tiles, smem + C::kAtScale, s_row, s_ref, b_info, b_infoe, &s_fail);
+    } else if (warp == kCopyK) {
+      copies = copy_tiles<D, C, C::kStagesK>(a, u, tiles, &maps.k_page, &maps.k_group, s_k, s_row, b_kfull, b_kempty, b_info, 0, &s_fail);
+    } else if (warp == kCopyV) {
+      copies = copy_tiles<D, C, C::kStagesV>(a, u, tiles, &maps.v_page, &maps.v_group, s_v, s_row, b_vfull, b_vempty, b_info, b_infoe, &s_fail);
+    } else if (warp >= kMma) {
+      // ---- MMAs: a thread for Q K and one for P V, so that the waits and commits of one pass under the products of
+      // the other. Scores of tile i go where those of i - 3 were, once their probabilities have been multiplied.
+      // Descriptors but for their start address, which each MMA adds.
+      constexpr uint32_t iqk = idesc_f8(128, kTile, false, false);
+      constexpr uint32_t ipv = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(D >> 3) << 17) | (8u << 24);  // f16 x f16 (MN-major) -> fp32
+      const uint64_t dk = TL::desc(s_k, 16), dq = TL::desc(s_q, 16), dv = TV::desc(s_v16, TV::kHalf);
+      if (lane == 0 && warp == kMma) {
+        bool ok = tiles == 0 || wait(b_q, 0);
+        int st = 0, ph = 0, buf = 0, sph = 1;
 #pragma unroll 1
-    for (int j = own; j < tiles; j += 2) {
-      const int slot = (j / C::kBatch) % C::kBatches;
-      if (j % C::kBatch < 2) ok = ok && wait(b_info + 8 * slot, (j / C::kInfoRing) & 1);
-      ok = ok && wait(b_s + 8 * buf, sph);
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      if (!ok) break;
-      tc::fence_after_sync();
-      const uint32_t sc = tmem + 128 * buf + lanes;
-      const float4* scales = s_scale + (j % C::kInfoRing) * kGroups;
-      const int cut = sees - (u.tile0 + j) * kTile;  // columns from here on are hidden
-      const bool masked = all_see < (u.tile0 + j + 1) * kTile;
-      const float2 refs = s_ref[j % C::kInfoRing];   // the values' power of two before this tile and with it
-      // the largest exponent of the tile; a page that is none has rows of zeros: its exponents become -infinity by what
-      // is added
-      auto hide = [&](float (&s)[32], int c) {
-        if (masked) {
+        for (int i = 0; ok && i < tiles; ++i) {
+          if (!wait(b_kfull + 8 * st, ph) || !wait(b_pv + 8 * buf, sph)) break;
+          tc::fence_after_sync();
+          const uint64_t kt = dk + st * (TL::kBytes >> 4);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (c + i >= cut) s[i] = -INFINITY;
-            asm volatile("" : "+f"(s[i]));  // kept behind the branch: as selects these cost every tile
-          }
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int ks = 0; ks < D / 32; ++ks)
+              mma_f8_ss(tmem + 128 * buf, dq + part * (TL::kBytes >> 4) + ks * 2, kt + ks * 2, iqk, part | ks);
+          tc::mma_commit(b_s + 8 * buf);
+          tc::mma_commit(b_kempty + 8 * st);
+          if (++st == C::kStagesK) st = 0, ph ^= 1;
+          if (++buf == C::kScores) buf = 0, sph ^= 1;
         }
-      };
-      float mx = -INFINITY;
+        // the barriers are made anew for the next unit: no commit may be on its way
 #pragma unroll 1
-      for (int c = 0; c < kTile; c += 32) {
-        float s[32];
-        tmem_ld32(sc + c, s);
-        tc::tmem_wait_ld();
-        hide(s, c);
+        for (int i = max(0, tiles - C::kStagesK); i < tiles && !s_fail; ++i) wait(b_kempty + 8 * (i % C::kStagesK), (i / C::kStagesK) & 1);
+      } else if (lane == 0) {
+        int buf = 0, sph = 0;
+#pragma unroll 1
+        for (int j = 0; j < tiles; ++j) {
+          if (!wait(b_wfull + 8 * (j & 1), (j >> 1) & 1) || !wait(b_p + 8 * buf, sph)) break;
+          tc::fence_after_sync();
+          const uint32_t pa = tmem + 128 * buf;
+          const uint64_t vt = dv + (j & 1) * (TV::kBytes >> 4);
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const float4 e = scales[c / kGroup + g];
-          float t0 = s[g * kGroup];
-#pragma unroll
-          for (int i = 1; i + 1 < kGroup; i += 2) t0 = max3(t0, s[g * kGroup + i], s[g * kGroup + i + 1]);
-          mx = fmaxf(mx, fmaf(fmaxf(t0, s[g * kGroup + kGroup - 1]), exponent_scale(e.x, factor), e.w));
+          for (int ks = 0; ks < kTile / 16; ++ks)
+            tc::mma_bf16_ts(tmem + C::kO, pa + (ks >> 1) * 32 + (ks & 1) * 8, vt + ks * (16 * TV::kRow >> 4), ipv, (j > 0) | ks);
+          tc::mma_commit(b_pv + 8 * buf);
+          if (++buf == C::kScores) buf = 0, sph ^= 1;
         }
+#pragma unroll 1
+        for (int j = max(0, tiles - C::kScores); j < tiles && !s_fail; ++j) wait(b_pv + 8 * (j % C::kScores), (j / C::kScores) & 1);
       }
-      if (j > 0) ok = __all_sync(0xFFFFFFFFu, wait(turn_of, ((j - 1) >> 1) & 1));
-      if (!ok) break;
-      // the reference follows the row's maximum once that passes it by 2^8 (f16 has the range): by the row alone,
-      // whatever its neighbours do
-      const float was = j > 0 ? s_max[r] : -INFINITY, to = mx > was + 8.0f ? mx : was;
-      const bool grown = refs.x != refs.y;
-      const bool scaled = j > 0 && (__any_sync(0xFFFFFFFFu, to != was) || grown);
-      s_max[r] = to;
       __syncwarp();
-      if (lane == 0) mbar_arrive(turn);
-      if (to != m) l *= ex2(m - to);
-      m = to;
-      if (scaled) {
-        ok = __all_sync(0xFFFFFFFFu, wait(b_pv + 8 * ((j - 1) % C::kScores), ((j - 1) / C::kScores) & 1));
+    } else if (warp >= C::kSoftWarps) {
+      // ---- V to f16: 16-byte chunks of a tile to the threads in turn; keys past the request's length, which hold
+      // whatever their page holds, become zero (0 * NaN is not 0)
+      const int me = tid - 32 * C::kSoftWarps;
+      constexpr int kChunks = D / 16;  // of a key
+      bool ok = true;
+#pragma unroll 1
+      for (int j = 0; j < tiles && ok; ++j) {
+        const int st = j % C::kStagesV;
+        ok = wait(b_vfull + 8 * st, (j / C::kStagesV) & 1) && (j < 2 || wait(b_pv + 8 * ((j - 2) % C::kScores), ((j - 2) / C::kScores) & 1));
+        if (!ok) break;
+        const int keys = len - (u.tile0 + j) * kTile;
+        const uint32_t from = s_v + st * TL::kBytes, to = s_v16 + (j & 1) * TV::kBytes;
+#pragma unroll 4
+        for (int i = me; i < kTile * kChunks; i += 32 * C::kConvWarps) {
+          const int key = i / (8 * kChunks) * 8 + i % 8, c = i / 8 % kChunks;  // (8 keys at a time: no bank twice)
+          uint32_t x[4], y[8];
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(from + TL::chunk_at(key, c)));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (key >= keys) x[e] = 0;
+            asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %2; cvt.rn.f16x2.e4m3x2 %0, lo; cvt.rn.f16x2.e4m3x2 %1, hi;}" : "=r"(y[2 * e]), "=r"(y[2 * e + 1]) : "r"(x[e]));
+          }
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + TV::chunk_at(key, 2 * c)), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + TV::chunk_at(key, 2 * c + 1)), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7]) : "memory");
+        }
+        tc::fence_async_smem();
+        mbar_arrive(b_wfull + 8 * (j & 1));
+        mbar_arrive(b_vempty + 8 * st);
+      }
+    } else {
+      split_queries<D, C::kRows, C::kSoftWarps>(a, u, G, rows_all, s_q, s_factor);
+      tc::fence_async_smem();
+      mbar_arrive(b_q);
+
+      // ---- softmax: thread = row; the two warpgroups take the tiles in turn. The reference that both subtract, m, is
+      // what the tile before left: warps w and w + 4, which have the same rows, hand it on.
+      const int own = warp / 4, pair = warp & 3, r = pair * 32 + lane;  // r: row of the unit
+      int sees = 0;                       // keys this row, a (token, head) pair of the request, sees
+      if (u.row0 + r < rows_all) sees = min(len, len - n + (u.row0 + r) / G + 1);
+      const uint32_t lanes = static_cast<uint32_t>(pair * 32) << 16;
+      bool ok = wait(b_q, 0);
+      const float given = s_factor[r];
+      const bool finite = given == given;
+      const float factor = finite ? given : 0.0f;
+      const int all_see = __reduce_min_sync(0xFFFFFFFFu, sees);   // keys before this one are seen by every row of the warp
+      // a query that is not finite saturates in 8 bits: its row is NaN through its sum
+      float m = -INFINITY, l = finite || sees <= 0 ? 0.0f : __int_as_float(0x7FC00000);
+      const uint32_t turn = b_turn + 8 * (4 * own + pair), turn_of = b_turn + 8 * (4 * (own ^ 1) + pair);
+      // whether any thread of the two warps says so
+      auto vote = [&](bool x) {
+        uint32_t any;
+        asm volatile("{.reg .pred p, q; setp.ne.u32 p, %1, 0; barrier.cta.red.or.pred q, %2, 64, p; selp.u32 %0, 1, 0, q;}"
+                     : "=r"(any) : "r"(static_cast<uint32_t>(x)), "r"(1 + pair) : "memory");
+        return any != 0;
+      };
+      int buf = own, sph = 0;
+#pragma unroll 1
+      for (int j = own; j < tiles; j += 2) {
+        const int slot = (j / C::kBatch) % C::kBatches;
+        if (j % C::kBatch < 2) ok = ok && wait(b_info + 8 * slot, (j / C::kInfoRing) & 1);
+        ok = ok && wait(b_s + 8 * buf, sph);
+        ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         tc::fence_after_sync();
-        const float corr = (to != was ? ex2(was - to) : 1.0f) * (grown ? ex2(refs.x - refs.y) : 1.0f);
-#pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          float o[16];
-          tc::tmem_ld16(tmem + C::kO + lanes + c, o);
-          tc::tmem_wait_ld();
+        const uint32_t sc = tmem + 128 * buf + lanes;
+        const float4* scales = s_scale + (j % C::kInfoRing) * kGroups;
+        const int cut = sees - (u.tile0 + j) * kTile;  // columns from here on are hidden
+        const bool masked = all_see < (u.tile0 + j + 1) * kTile;
+        const float2 refs = s_ref[j % C::kInfoRing];   // the values' power of two before this tile and with it
+        // the largest exponent of the tile; a page that is none has rows of zeros: its exponents become -infinity by what
+        // is added
+        auto hide = [&](float (&s)[32], int c) {
+          if (masked) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] *= corr;
-          tc::tmem_st16(tmem + C::kO + lanes + c, o);
-        }
-      }
-      // the probabilities: p * vs / vs_ref comes out of the exponential; the row sum takes it back by group
-      const float base = m == -INFINITY ? 0.0f : -m;
-#pragma unroll 1
-      for (int c = 0; c < kTile; c += 32) {
-        float cur[32];
-        tmem_ld32(sc + c, cur);
-        tc::tmem_wait_ld();
-        hide(cur, c);
-        uint32_t w[16];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const float4 e = scales[c / kGroup + g];
-          const float ks = exponent_scale(e.x, factor), add = base + e.y;
-          const float2 k2 = make_float2(ks, ks), b2 = make_float2(add, add);
-          float2 part = make_float2(0.0f, 0.0f);
-#pragma unroll
-          for (int i = 0; i < kGroup; i += 2) {
-            float2 v = fma2(make_float2(cur[g * kGroup + i], cur[g * kGroup + i + 1]), k2, b2);
-            v.x = ex2(v.x);
-            v.y = ex2(v.y);
-            part = add2(part, v);
-            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[(g * kGroup + i) / 2]) : "f"(v.y), "f"(v.x));
+            for (int i = 0; i < 32; ++i) {
+              if (c + i >= cut) s[i] = -INFINITY;
+              asm volatile("" : "+f"(s[i]));  // kept behind the branch: as selects these cost every tile
+            }
           }
-          l = fmaf(part.x + part.y, e.z, l);
-        }
-        tmem_st16u(sc + c, w);
-      }
-      tc::tmem_wait_st();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(b_p + 8 * buf);
-      if (j % C::kBatch >= 2 && lane == 0) mbar_arrive(b_infoe + 8 * slot);
-      buf += 2;
-      if (buf >= C::kScores) buf -= C::kScores, sph ^= 1;
-    }
-    // the last two products in order: a barrier's parity tells a product only from the one before on it
+        };
+        float mx = -INFINITY;
 #pragma unroll 1
-    for (int j = max(0, tiles - 2); j < tiles; ++j) ok = ok && wait(b_pv + 8 * (j % C::kScores), (j / C::kScores) & 1);
-    if (!vote(!ok)) {
-      const float last = tiles > 0 ? s_max[r] : -INFINITY;
-      const float2 refs = tiles > 0 ? s_ref[(tiles - 1) % C::kInfoRing] : make_float2(0.0f, -INFINITY);
-      s_max[(1 + own) * C::kRows + r] = m == last ? l : l * ex2(m - last);
+        for (int c = 0; c < kTile; c += 32) {
+          float s[32];
+          tmem_ld32(sc + c, s);
+          tc::tmem_wait_ld();
+          hide(s, c);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const float4 e = scales[c / kGroup + g];
+            float t0 = s[g * kGroup];
+#pragma unroll
+            for (int i = 1; i + 1 < kGroup; i += 2) t0 = max3(t0, s[g * kGroup + i], s[g * kGroup + i + 1]);
+            mx = fmaxf(mx, fmaf(fmaxf(t0, s[g * kGroup + kGroup - 1]), exponent_scale(e.x, factor), e.w));
+          }
+        }
+        if (j > 0) ok = __all_sync(0xFFFFFFFFu, wait(turn_of, ((j - 1) >> 1) & 1));
+        if (!ok) break;
+        // the reference follows the row's maximum once that passes it by 2^8 (f16 has the range): by the row alone,
+        // whatever its neighbours do
+        const float was = j > 0 ? s_max[r] : -INFINITY, to = mx > was + 8.0f ? mx : was;
+        const bool grown = refs.x != refs.y;
+        const bool scaled = j > 0 && (__any_sync(0xFFFFFFFFu, to != was) || grown);
+        s_max[r] = to;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(turn);
+        if (to != m) l *= ex2(m - to);
+        m = to;
+        if (scaled) {
+          ok = __all_sync(0xFFFFFFFFu, wait(b_pv + 8 * ((j - 1) % C::kScores), ((j - 1) / C::kScores) & 1));
+          if (!ok) break;
+          tc::fence_after_sync();
+          const float corr = (to != was ? ex2(was - to) : 1.0f) * (grown ? ex2(refs.x - refs.y) : 1.0f);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            float o[16];
+            tc::tmem_ld16(tmem + C::kO + lanes + c, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] *= corr;
+            tc::tmem_st16(tmem + C::kO + lanes + c, o);
+          }
+        }
+        // the probabilities: p * vs / vs_ref comes out of the exponential; the row sum takes it back by group
+        const float base = m == -INFINITY ? 0.0f : -m;
+#pragma unroll 1
+        for (int c = 0; c < kTile; c += 32) {
+          float cur[32];
+          tmem_ld32(sc + c, cur);
+          tc::tmem_wait_ld();
+          hide(cur, c);
+          uint32_t w[16];
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const float4 e = scales[c / kGroup + g];
+            const float ks = exponent_scale(e.x, factor), add = base + e.y;
+            const float2 k2 = make_float2(ks, ks), b2 = make_float2(add, add);
+            float2 part = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < kGroup; i += 2) {
+              float2 v = fma2(make_float2(cur[g * kGroup + i], cur[g * kGroup + i + 1]), k2, b2);
+              v.x = ex2(v.x);
+              v.y = ex2(v.y);
+              part = add2(part, v);
+              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[(g * kGroup + i) / 2]) : "f"(v.y), "f"(v.x));
+            }
+            l = fmaf(part.x + part.y, e.z, l);
+          }
+          tmem_st16u(sc + c, w);
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_p + 8 * buf);
+        if (j % C::kBatch >= 2 && lane == 0) mbar_arrive(b_infoe + 8 * slot);
+        buf += 2;
+        if (buf >= C::kScores) buf -= C::kScores, sph ^= 1;
+      }
+      // the last two products in order: a barrier's parity tells a product only from the one before on it
+#pragma unroll 1
+      for (int j = max(0, tiles - 2); j < tiles; ++j) ok = ok && wait(b_pv + 8 * (j % C::kScores), (j / C::kScores) & 1);
       if (!vote(!ok)) {
-        tc::fence_after_sync();
-        l = s_max[C::kRows + r] + s_max[2 * C::kRows + r];
-        if (u.slot >= 0 && live && own == 0) p.ml[static_cast<int64_t>(u.slot) * C::kRows + r] = make_float2(last, l);
-        store_rows<D, D / 2, C::kQ / C::kSoftWarps>(p, u, C::kRows, r, live, token, row - token * G, G, tiles, l, refs.y,
-                                                    tmem + C::kO + lanes, own * (D / 2), s_q + warp * (C::kQ / C::kSoftWarps));
+        const float last = tiles > 0 ? s_max[r] : -INFINITY;
+        const float2 refs = tiles > 0 ? s_ref[(tiles - 1) % C::kInfoRing] : make_float2(0.0f, -INFINITY);
+        s_max[(1 + own) * C::kRows + r] = m == last ? l : l * ex2(m - last);
+        if (!vote(!ok)) {
+          tc::fence_after_sync();
+          l = s_max[C::kRows + r] + s_max[2 * C::kRows + r];
+          const int row = u.row0 + r, token = row / G;
+          const bool live = row < rows_all;
+          if (u.slot >= 0 && live && own == 0) p.ml[static_cast<int64_t>(u.slot) * C::kRows + r] = make_float2(last, l);
+          store_rows<D, D / 2, C::kQ / C::kSoftWarps>(p, u, C::kRows, r, live, token, row - token * G, G, tiles, l, refs.y,
+                                                      tmem + C::kO + lanes, own * (D / 2), s_q + warp * (C::kQ / C::kSoftWarps));
+        }
       }
     }
-  }
-  tc::fence_before_sync();
-  __syncthreads();
-  if (s_fail) {  // a wait ran out: leave only once what is in flight has landed
-    if (tid == 0 && a.err) atomicOr(a.err, GDN_DEVERR_TIMEOUT);
-    const int stages = warp == kCopyK ? C::kStagesK : C::kStagesV;
-    for (int i = max(0, copies - stages); i < copies; ++i)
-      mbar_wait_bounded((warp == kCopyK ? b_kfull : b_vfull) + 8 * (i % stages), (i / stages) & 1);
-    if (warp >= kMma && warp < kLook && lane == 0) {
-      tc::mma_commit(b_drain + 8 * (warp - kMma));
-      mbar_wait_bounded(b_drain + 8 * (warp - kMma), 0);
-    }
+    tc::fence_before_sync();
     __syncthreads();
+    if (s_fail) {  // a wait ran out: leave only once what is in flight has landed
+      if (tid == 0 && a.err) atomicOr(a.err, GDN_DEVERR_TIMEOUT);
+      const int stages = warp == kCopyK ? C::kStagesK : C::kStagesV;
+      for (int i = max(0, copies - stages); i < copies; ++i)
+        mbar_wait_bounded((warp == kCopyK ? b_kfull : b_vfull) + 8 * (i % stages), (i / stages) & 1);
+      if (warp >= kMma && warp < kLook && lane == 0) {
+        tc::mma_commit(b_drain + 8 * (warp - kMma));
+        mbar_wait_bounded(b_drain + 8 * (warp - kMma), 0);
+      }
+      __syncthreads();
+      break;
+    }
+    if (s_next >= units) break;
   }
   if (warp == kMma) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 512);
+    tc::tmem_dealloc(s_tmem, 512);
   }
 }
 
@@ -1226,11 +1249,13 @@ cudaError_t launch_prefill_d(const PrefillParams& p, const PrefillLayout& L, con
   attn_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = launch_after(kern, dim3(L.max_units), C::kThreads, C::kSmem, s, p, maps);
+  // head_dim 256: a CTA for each place of the list; otherwise one an SM, which takes units as they come
+  const int grid = D == 256 || L.max_units < sm_count() ? L.max_units : sm_count();
+  e = launch_after(kern, dim3(grid), C::kThreads, C::kSmem, s, p, maps);
   if (e != cudaSuccess || L.max_slots == 0) return e;
   const int64_t joins = static_cast<int64_t>(p.nb) * few_units(D);
-  const int grid = static_cast<int>(joins < L.max_units ? joins : L.max_units);
-  return launch_after(attn_prefill_join_kernel<D>, dim3(grid, C::kRows / 16), 256, 0, s, p);
+  const int join_grid = static_cast<int>(joins < L.max_units ? joins : L.max_units);
+  return launch_after(attn_prefill_join_kernel<D>, dim3(join_grid, C::kRows / 16), 256, 0, s, p);
 }
 
 }  // namespace

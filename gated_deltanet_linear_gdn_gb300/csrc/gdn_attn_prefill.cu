@@ -63,7 +63,9 @@ struct PrefillParams {
 // How many pieces the key tiles of a request are cut into: the fewest rounds of an assumed 152
 // CTAs, counted in tiles with a constant cost per piece (a prologue and an epilogue take about 8 tiles). 300 tokens at
 // 60,000 (80 units of 470 tiles): 368 us in 5 pieces, 686 whole; 8 ragged prompts, none of them alone on the GPU: 346
-// and 321, the price of results that do not depend on the batch.
+// and 321, the price of results that do not depend on the batch. Pieces of unequal length that fill 152 CTAs evenly
+// (cuts at multiples of one length over all row tiles, end to end) took 481: row tiles no longer read the same keys at the
+// same time.
 __host__ __device__ __forceinline__ int kv_splits(int units, int tiles, int d) {
   if (units >= few_units(d) || tiles < 2 * kMinSplitTiles) return 1;
   int best = 1, cost = 0x7fffffff;

@@ -27,7 +27,7 @@
 // finished here, a longer one leaves fp32 partial sums (with their maximum and sum) that a second,
 // programmatically dependent kernel joins in unit order.
 //
-// Measured: 256 requests of up to 8,192 tokens (16 / 2 heads of 256) 349 us, 5.7 TB/s, where the same copies without
+// Measured: 256 requests of up to 8,192 tokens (16 / 2 heads of 256) 347 us, 5.7 TB/s, where the same copies without
 // the products take 297; 2 of 131,071 56 us; one of 4,097 13.1 us, a chain of set-up (2,000 cycles), two lookups (1,600), copy,
 // two tiles (2,300 each), stores and the join.
 //

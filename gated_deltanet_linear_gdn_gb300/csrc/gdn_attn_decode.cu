@@ -143,7 +143,8 @@ struct DecodeCfg {
   static constexpr int kAtFactor = kAtKeys + kInfoRing * 4;
   static constexpr int kAtRed = kAtFactor + kFactorRing * 16 * 4;
   static constexpr int kBars = 2 * kStages + 2 * kBatches + kFactorRing + 11;
-  static constexpr int kAtBars = kAtRed + 4 * 16 * 4;
+  static constexpr int kAtSum = kAtRed + 4 * 16 * 4;
+  static constexpr int kAtBars = kAtSum + 4 * 16 * 4;
   static constexpr int kAtPre = kAtBars + kBars * 8;             // then lens[nb], tsum[nb / kCoarse + 2]
   static constexpr int kSmem = 1024 + kAtPre;
   static_assert(kAtBars % 8 == 0 && kQ % 1024 == 0, "alignment");
@@ -269,7 +270,10 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
   int32_t* s_row = reinterpret_cast<int32_t*>(smem + C::kAtRow);    // [tile % kInfoRing][group] row of the cache
   int32_t* s_keys = reinterpret_cast<int32_t*>(smem + C::kAtKeys);  // [tile % kInfoRing] keys of the tile, 0: no more
   float* s_factor = reinterpret_cast<float*>(smem + C::kAtFactor);  // [unit % kFactorRing][16]
-  float* s_red = reinterpret_cast<float*>(smem + C::kAtRed);        // [warp][16]
+  // [warp][16], a tile's maxima and a unit's sums: apart, as no barrier lies between the reads of the last tile's
+  // maxima and the writes of the sums
+  float* s_red = reinterpret_cast<float*>(smem + C::kAtRed);
+  float* s_sum = reinterpret_cast<float*>(smem + C::kAtSum);
   int32_t* lens = reinterpret_cast<int32_t*>(smem + C::kAtPre);
   int32_t* tsum = lens + p.nb;
   const uint32_t b_full = base + C::kAtBars, b_empty = b_full + 8 * C::kStages, b_info = b_empty + 8 * C::kStages,
@@ -705,11 +709,11 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
       for (int h = 0; h < HP; ++h) {
 #pragma unroll
         for (int o = 16; o; o >>= 1) l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], o);
-        if (lane == 0) s_red[warp * 16 + h] = l[h];
+        if (lane == 0) s_sum[warp * 16 + h] = l[h];
       }
       if (any_of_128(!ok)) break;
 #pragma unroll
-      for (int h = 0; h < HP; ++h) l[h] = (s_red[h] + s_red[16 + h]) + (s_red[32 + h] + s_red[48 + h]);
+      for (int h = 0; h < HP; ++h) l[h] = (s_sum[h] + s_sum[16 + h]) + (s_sum[32 + h] + s_sum[48 + h]);
       ok = __all_sync(0xFFFFFFFFu, wait(b_pv + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1));
       if (!ok) continue;  // to meet the others
       tc::fence_after_sync();

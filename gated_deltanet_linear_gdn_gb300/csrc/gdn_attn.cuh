@@ -52,12 +52,23 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return *reinterpret_cast<float2*>(&r);
 }
 
-// The 4 leading significant bits, to nearest: v * 2^20 absorbs the rest (T. J. Dekker, "A
-// floating-point technique for extending the available precision", 1971).
-__device__ __forceinline__ float2 top_bits(float2 v) {
-  const float2 t = mul2(v, make_float2(1048577.0f, 1048577.0f));
-  const float2 minus = make_float2(-1.0f, -1.0f);
-  return fma2(fma2(v, minus, t), minus, t);
+// Four f16 values (none above 57,344) as sums of three e5m2 values each. An f16's upper byte is an e5m2 value: the first two
+// parts are that byte rounded (half of its last place added to the magnitude, which carries as it should), and what they
+// leave is exact in f16; the third is rounded to nearest. Exact from 2^-6 on, below that to 2^-17. NaN stays NaN through
+// the third part.
+__device__ __forceinline__ void split_e5m2(const uint32_t (&h)[2], uint32_t (&part)[3]) {
+  uint32_t hi[2], mid[2], lo[2];
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    uint32_t r;
+    hi[y] = (h[y] + 0x00800080u) & 0xFF00FF00u;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h[y]), "r"(hi[y]));
+    mid[y] = (r + 0x00800080u) & 0xFF00FF00u;
+    asm("{.reg .b16 x; sub.rn.f16x2 %0, %1, %2; cvt.rn.satfinite.e5m2x2.f16x2 x, %0; mov.b32 %0, {x, 0};}" : "=&r"(lo[y]) : "r"(r), "r"(mid[y]));
+  }
+  part[0] = __byte_perm(hi[0], hi[1], 0x7531);
+  part[1] = __byte_perm(mid[0], mid[1], 0x7531);
+  part[2] = __byte_perm(lo[0], lo[1], 0x5410);
 }
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
@@ -113,6 +124,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
 }
 #undef GDN_F8
 
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+               "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
                "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
@@ -143,6 +159,8 @@ __device__ __forceinline__ void mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint
 __host__ __device__ constexpr uint32_t idesc_f8(int M, int N, bool a_mn, bool b_mn) {
   return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
+
+constexpr uint32_t kIdescE5m2A = 1u << 7;  // A in e5m2 instead (the two types of this kind are free of each other)
 
 // Operand tiles are rows of min(d, 128) bytes in the hardware swizzle that TMA writes (128-byte
 // rows: 16-byte chunk ^ row mod 8; 64-byte rows: chunk ^ (row / 2) mod 4), 8 rows to an atom;

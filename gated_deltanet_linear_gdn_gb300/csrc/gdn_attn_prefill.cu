@@ -452,11 +452,13 @@ __device__ __forceinline__ void store_rows(const PrefillParams& p, const Prefill
 
 // ------------------------------------------------------------------------------- head_dim 256
 //
-// Both products on 8-bit operands, no conversion of V: p = p_hi + p_lo, p_hi to 4 significant bits and p_lo =
-// e4m3(p - p_hi), 8 bits in all, as a bf16 p would keep. m moves when a score passes it by 2^4, so that 16 p <= 256
-// fits e4m3. Sixteen softmax warps, four threads a row with 32 columns each (they exchange their maxima), two
-// score buffers (2 x 128 columns of tensor memory, 256 of output), a warp that issues MMAs: the 2,090 cycles of products a
-// tile hide most of the softmax. 4,096 tokens (16 / 2 heads): 122 us, 60% of the bf16 rate with the masked half
+// Both products on 8-bit operands, no conversion of V: p, rounded to f16, is the sum of three e5m2 values (split_e5m2),
+// each of the part that the ones before leave: 11 significant bits. e5m2 has f16's exponents, so all three have the factor 1 and
+// one accumulator, down to 2^-17: m moves when a score passes it by 2^4 and stands for 2^11, so a key is rounded to 2^-28 of
+// the row's largest whatever stands between. (Two e4m3 parts, a quarter fewer products and 123 us where this takes 138, end at 2^-14 of it:
+// 5,000 keys 10 nats below one of no value came out 14 to 26% small.) Sixteen softmax warps, four threads a row with 32 columns each (they exchange their maxima), two
+// score buffers (2 x 128 columns of tensor memory, 256 of output), a warp that issues MMAs: the 2,610 cycles of products a
+// tile hide most of the softmax. 4,096 tokens (16 / 2 heads): 138 us, 53% of the bf16 rate with the masked half
 // of the diagonal counted out. With f16 probabilities, as below, V alone would take 128 KB of shared memory.
 struct WideCfg {
   static constexpr int D = 256;
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
                   : copy_tiles<D, C, C::kStages>(a, u, tiles, &maps.k_page, &maps.k_group, s_k, s_row, b_kfull, b_kempty, b_info, 0, &s_fail);
   } else if (warp == C::kSoftWarps) {
     // ---- MMAs
-    constexpr uint32_t iqk = idesc_f8(128, kTile, false, false), ipv = idesc_f8(128, D, false, true);
+    constexpr uint32_t iqk = idesc_f8(128, kTile, false, false), ipv = idesc_f8(128, D, false, true) | kIdescE5m2A;
     bool ok = tiles == 0 || wait(b_q, 0);
     tc::fence_after_sync();
     // descriptors but for their start address (bits 0 .. 13, in 16 bytes), which each MMA adds: the issuing
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
 #pragma unroll
         for (int ks = 0; ks < kTile / 32; ++ks)
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
+          for (int part = 0; part < 3; ++part)
             mma_f8_ts(tmem + C::kO, pa + ks * 32 + part * 8, vt + ks * (32 * TL::kRow >> 4), ipv, (j > 0) | (ks | part));
         tc::mma_commit(b_pv + 8 * (j & 1));
         tc::mma_commit(b_vempty + 8 * (j % C::kStages));
@@ -719,10 +721,10 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
           }
         }
       }
-      const float base = m == -INFINITY ? 0.0f : 4.0f - m;
+      const float base = m == -INFINITY ? 0.0f : 11.0f - m;
 #pragma unroll 1
       for (int c = 0; c < NC; c += 32) {
-        float w[16];
+        float w[24];  // high, middle and low parts of four keys each
         if (NC > 32) scores(c, s);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
@@ -733,7 +735,7 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
           float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
           for (int i = 0; i < kGroup; i += 4) {
-            float2 hi[2], lo[2];
+            uint32_t h[2];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               const int e = g * kGroup + i + 2 * y;
@@ -741,15 +743,18 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
               v.x = ex2(v.x);
               v.y = ex2(v.y);
               sum = add2(sum, v);
-              hi[y] = top_bits(v);
-              lo[y] = fma2(hi[y], make_float2(-1.0f, -1.0f), v);
+              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[y]) : "f"(v.y), "f"(v.x));
             }
-            w[g * 4 + i / 4] = __uint_as_float(e4m3x4(hi[0].x, hi[0].y, hi[1].x, hi[1].y));
-            w[8 + g * 4 + i / 4] = __uint_as_float(e4m3x4(lo[0].x, lo[0].y, lo[1].x, lo[1].y));
+            uint32_t part[3];
+            split_e5m2(h, part);
+#pragma unroll
+            for (int y = 0; y < 3; ++y) w[y * 8 + g * 4 + i / 4] = __uint_as_float(part[y]);
           }
           l += (sum.x + sum.y) * ex2(-dl);
         }
-        tc::tmem_st16(sc + c, w);
+        tmem_st8(sc + c, w);
+        tmem_st8(sc + c + 8, w + 8);
+        tmem_st8(sc + c + 16, w + 16);
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();

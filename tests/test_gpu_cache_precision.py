@@ -1,0 +1,155 @@
+"""What attention over the 8-bit cache keeps of a softmax that is not flat: one key far above the others, blocks of
+values whose scales differ by many powers of two, values that a row does not see. Against plain 64-bit attention,
+element by element, within what the kernels say they round (include/gdn.h): a probability to `bits` significant bits
+and to `floor` of the row's largest probability x scale of V, a query to 2^-18 of its row's largest element, sums in
+fp32, the result to bf16."""
+import numpy as np
+import pytest
+import torch
+
+import gated_deltanet_linear_gdn_gb300 as gdn
+
+import _cache_oracle as co
+
+pytestmark = pytest.mark.gpu
+
+# (significant bits, floor) of a probability
+KEEPS = {("prefill", 256): (11, 2.0 ** -28)}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from gated_deltanet_linear_gdn_gb300 import build
+    build.build_library()
+    assert torch.cuda.is_available()
+
+
+def i32(x):
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+class Pages:
+    """A cache of the given keys and values [n, H, d] of one request, in shuffled pages; the bytes and scales of a page
+    by its largest element."""
+
+    def __init__(self, k, v, bs, seed=0):
+        n, self.H, self.d = k.shape
+        self.n, self.bs, W = n, bs, -(-n // bs)
+        perm = torch.from_numpy(np.random.default_rng(seed).permutation(W + 2)).cuda()
+        self.table = perm[:W].to(torch.int32)[None].contiguous()
+
+        def pool(x):
+            x = torch.nn.functional.pad(x, (0, 0, 0, 0, 0, W * bs - n)).view(W, bs, self.H, self.d).transpose(1, 2)
+            s = (x.abs().amax(dim=(2, 3)) / 448).clamp(min=2.0 ** -64)
+            c = torch.full((W + 2, self.H, bs, self.d), 0x7F, dtype=torch.uint8, device="cuda")
+            c[self.table[0].long()] = (x / s[:, :, None, None]).clamp(-448, 448).to(co.F8).view(torch.uint8)
+            all_s = torch.ones(W + 2, self.H, device="cuda")
+            all_s[self.table[0].long()] = s
+            return c, all_s
+
+        (self.kc, self.ks), (self.vc, self.vs) = pool(k), pool(v)
+        self.err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def pools(self):
+        return self.kc, self.vc, self.ks, self.vs
+
+    def values(self, cache, scale):
+        lut = torch.from_numpy(co.E4M3).cuda()
+        p = self.table[0].long()
+        x = lut[cache[p].long()] * scale[p].double()[:, :, None, None]
+        return x.transpose(1, 2).reshape(-1, self.H, self.d)[:self.n]
+
+    def scale_of(self, scale):  # of each key's page, [n, H]
+        return scale[self.table[0].long()].double().repeat_interleave(self.bs, 0)[:self.n]
+
+
+def run(c, q, which):
+    """The rows of q as the last tokens of the request; `decode`: each by itself, as a batch."""
+    T, Hq, d = q.shape
+    out = torch.full_like(q, 7.0)
+    if which == "decode":
+        table = c.table.expand(T, -1).contiguous()
+        lens = i32(np.arange(c.n - T + 1, c.n + 1))
+        ws = torch.empty(gdn.gdn_attn_decode_workspace_size(T, table.shape[1], Hq, c.H, d, c.bs), dtype=torch.uint8, device="cuda")
+        gdn.gdn_attn_decode(q, *c.pools(), table, lens, out, ws, err=c.err)
+    else:
+        ws = torch.empty(gdn.gdn_attn_prefill_workspace_size(T, 1, c.table.shape[1], Hq, c.H, d, c.bs), dtype=torch.uint8, device="cuda")
+        gdn.gdn_attn_prefill(q, i32([0, T]), *c.pools(), c.table, i32([c.n]), out, ws, err=c.err)
+    torch.cuda.synchronize()
+    assert int(c.err) == 0
+    return out
+
+
+def exact(c, q, which):
+    """The result in 64 bits and the bound: see the head of this file."""
+    T, Hq, d = q.shape
+    G = Hq // c.H
+    bits, floor = KEEPS[which, d]
+    k, v = c.values(c.kc, c.ks), c.values(c.vc, c.vs)
+    vs = c.scale_of(c.vs)
+    hidden = torch.arange(c.n, device="cuda")[None, :] > (c.n - T + torch.arange(T, device="cuda"))[:, None]
+    out = torch.empty(T, Hq, d, dtype=torch.float64, device="cuda")
+    tol = torch.empty_like(out)
+    for m in range(Hq):
+        h = m // G
+        x = q[:, m].double()
+        s = (x @ k[:, h].T * d ** -0.5).masked_fill(hidden, -torch.inf)
+        p = torch.softmax(s, dim=1)
+        vh = torch.where(v[:, h].isnan(), 0.0, v[:, h])
+        o = p @ vh
+        out[:, m] = o
+        # a score: queries 2^-18 of the largest element, fp32 sums over d; twice for the key and for the maximum
+        size = x.abs().amax(dim=1, keepdim=True) * k[:, h].abs().sum(dim=1).amax() * d ** -0.5
+        e = 2 * ((2.0 ** -18 + d * 2.0 ** -24) * size + 2.0 ** -21 * (1 + torch.where(hidden, 0.0, s).abs().amax(dim=1, keepdim=True)))
+        mag = p @ vh.abs()
+        least = (p * vs[:, h]).amax(dim=1, keepdim=True) * floor * ((~hidden).double() @ (vh.abs() / vs[:, h, None]))
+        tol[:, m] = (2.0 ** -bits + e + c.n * 2.0 ** -24) * mag + least + 2.0 ** -8 * o.abs() + 1e-30
+    return out, tol
+
+
+def check(c, q, which):
+    want, tol = exact(c, q, which)
+    got = run(c, q, which).double()
+    assert bool(torch.isfinite(got).all())
+    off = (got - want).abs()
+    assert bool((off <= tol).all()), (float((off / tol).max()), float((off.norm() / want.norm())))
+
+
+def rand(seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return lambda *shape: torch.randn(*shape, device="cuda", generator=g)
+
+
+def one_key_above(which, T, Hq, H, d, gap, flat):
+    """The usual first token: `gap` nats above the rest, a value of next to nothing, so that what comes out is the sum of
+    many small probabilities; with `flat` they are all the same and their rounding does not average out."""
+    n, r = 5003, rand(gap + d)
+    u = torch.sign(r(d)) * 0.5
+    k = (0.0 if flat else 0.6) * r(n, H, d)
+    k[0] = u * (gap / (0.25 * d ** 0.5))
+    v = 1.0 + 0.3 * r(n, H, d)
+    v[0] = 0.002
+    q = (u + (0.0 if flat else 0.05) * r(T, Hq, d)).bfloat16()
+    check(Pages(k, v, 16, gap), q, which)
+
+
+def one_key_above_a_long_request(which, T, d):
+    n, r = 60000, rand(d)
+    u = torch.sign(r(d)) * 0.5
+    k = 0.4 * r(n, 1, d)
+    k[0] = u * (11 / (0.25 * d ** 0.5))
+    v = 1.0 + r(n, 1, d)
+    v[0] = 0.01
+    check(Pages(k, v, 64), (u + 0.05 * r(T, 4, d)).bfloat16(), which)
+
+
+@pytest.mark.parametrize("T", [5, 300])
+@pytest.mark.parametrize("Hq,H", [(4, 2), (16, 2)])
+@pytest.mark.parametrize("gap", [6, 10, 12, 16])
+@pytest.mark.parametrize("flat", [False, True])
+def test_prompts_256_one_key_above_the_others(T, Hq, H, gap, flat):
+    one_key_above("prefill", T, Hq, H, 256, gap, flat)
+
+
+def test_prompts_256_one_key_above_a_long_request():
+    one_key_above_a_long_request("prefill", 70, 256)

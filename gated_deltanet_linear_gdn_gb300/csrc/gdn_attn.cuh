@@ -18,6 +18,9 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// The root of exp2(x). A row's sum is multiplied with it twice: next to a scale of V of 2^90 the sum of a block of zeros (2^-64)
+// is within what fp32 holds and exp2(x) is not.
+__device__ __forceinline__ float ex2_root(float x) { return ex2(0.5f * x); }
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   uint32_t r;
   asm("{.reg .b16 x, y; cvt.rn.satfinite.e4m3x2.f32 x, %2, %1; cvt.rn.satfinite.e4m3x2.f32 y, %4, %3; mov.b32 %0, {x, y};}"
@@ -139,6 +142,10 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
 // The factor of a score in the exponent. Never zero, so that a masked score (-inf) stays -inf: a
 // smaller one moves no exponent (scores are below 2^26).
 __device__ __forceinline__ float exponent_scale(float ks, float factor) { return fmaxf(fabsf(ks) * factor, 1e-37f); }
+
+// log2 of the scales of V below which a key's part of the row's sum is computed by itself: from p * vs, as elsewhere, it
+// would be lost where the row's largest p * vs is 2^126 times as large.
+constexpr int kFarScale = -30;
 
 // 8-bit MMAs (kind::f8f6f4, e4m3 x e4m3, fp32 accumulators, 32 elements of K per instruction).
 __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t acc) {

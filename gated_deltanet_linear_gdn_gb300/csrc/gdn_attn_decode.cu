@@ -17,9 +17,12 @@
 //
 // Eight-bit queries and probabilities are split into parts, side by side in N: a query into two e4m3
 // values (scaled per head so that its largest element lies in [128, 256): exact down to 2^-18 of that),
-// a probability into four with factors 1, 1/16, 1/256, 1/4096 (16 bits, and 2^-22 of the largest). The running
-// maximum moves when a score passes it by 2^8 and the reference for vs when one passes it by 2, so that almost
-// only a unit's first tile stops for them: 0.87 p vs / vs_ref <= 448, the largest e4m3.
+// a probability into four with factors 1, 1/16, 1/256, 1/4096 (16 bits, and 2^-22 of the largest).
+//
+// Scales of V. With x the exponent of a score and e that of vs, m is the running maximum of x + e, and p = exp2(x - m)
+// goes into the sum, p vs into the product. So what a key is rounded to goes by the largest probability x scale of the row, and
+// not by a scale that weighs nothing. m moves when an x + e passes it by 2^8, so that almost only a unit's first tile
+// stops for it: p vs < 2^7.8 * 2 <= 448, the largest e4m3.
 //
 // Split. A (request, kv head) is cut into units of 256, 512 or 1,024 keys by its OWN length
 // (unit_shift), never by the batch: a row's result depends on its own inputs alone, bit for bit, as
@@ -597,7 +600,6 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
     for (Walk u = walk(); u.more() && !left; u.next(), ++k) {
       const int tiles = u.tiles(), keys = u.keys();
       float m[HP], l[HP], fac[HP];
-      float vs_ref = 0.0f;
       ok = __all_sync(0xFFFFFFFFu, ok && wait(b_factor + 8 * (k % C::kFactorRing), (k / C::kFactorRing) & 1));
 #pragma unroll
       for (int h = 0; h < HP; ++h) {
@@ -610,7 +612,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
         ok = __all_sync(0xFFFFFFFFu, ok && wait(b_s + 8 * (i & 1), (i >> 1) & 1));
         float x[HP];
         float2 own = make_float2(-1.0f, 0.0f);
-        float vmax = 0.0f;
+        float e = 0.0f;  // of vs
         bool above = false;
         if (ok) {
           tc::fence_after_sync();
@@ -618,40 +620,37 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
           tmem_load(tmem + C::kNQ * (i & 1) + lanes, s);
           const float2* sc = s_scale + (i % C::kInfoRing) * kGroups;
           own = sc[tid / kGroup];
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g) vmax = fmaxf(vmax, sc[g].y);
+          // (e from -64, the writer's least scale, so that zero is one of the scales)
+          e = static_cast<float>(max((__float_as_int(own.y) >> 23) & 255, 63) - 127);
           __syncwarp();  // the batch's last tile: its lookups have been read
           if (i % C::kBatch == C::kBatch - 1 && lane == 0) mbar_arrive(b_infoe + 8 * ((i / C::kBatch) % C::kBatches));
           const bool hidden = t * kTile + tid >= keys || own.x < 0.0f;
 #pragma unroll
           for (int h = 0; h < HP; ++h) {
             x[h] = hidden ? -INFINITY : (s[h] + s[HP + h]) * (own.x * fac[h]);
-            above |= x[h] > m[h] + kRise;
+            above |= x[h] > m[h] + (kRise - e);
           }
         }
-        const bool grow_v = vmax > 2.0f * vs_ref;
-        if (any_of_128(above || grow_v || !ok)) {
+        if (any_of_128(above || !ok)) {
           if (any_of_128(!ok)) {
             left = true;
             break;
           }
 #pragma unroll
           for (int h = 0; h < HP; ++h) {
-            const float w = warp_max(x[h]);
+            const float w = warp_max(x[h] + e);
             if (lane == 0) s_red[warp * 16 + h] = w;
           }
           sync_128();
           float corr[HP];
-          const float vcorr = grow_v ? __fdividef(vs_ref, vmax) : 1.0f;
-          if (grow_v) vs_ref = vmax;
 #pragma unroll
           for (int h = 0; h < HP; ++h) {
             const float top = fmaxf(fmaxf(s_red[h], s_red[16 + h]), fmaxf(s_red[32 + h], s_red[48 + h]));
             const float to = top > m[h] + kRise ? top : m[h];  // by the head alone, whatever the others do
-            corr[h] = to == -INFINITY ? 1.0f : ex2(m[h] - to);
+            const float root = to == -INFINITY ? 1.0f : ex2_root(m[h] - to);
             m[h] = to;
-            l[h] *= corr[h];
-            corr[h] *= vcorr;
+            l[h] = l[h] * root * root;
+            corr[h] = root * root;
           }
           if (t > 0) {
             ok = __all_sync(0xFFFFFFFFu, wait(b_pv + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1));
@@ -671,7 +670,6 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
             }
           }
         }
-        const float rel = vs_ref > 0.0f ? __fdividef(own.y, vs_ref) : 0.0f;
         uint32_t part[4][HP / 2];
 #pragma unroll
         for (int h = 0; h < HP; h += 2) {
@@ -679,8 +677,8 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
           float a1 = ex2(m[h + 1] == -INFINITY ? x[h + 1] : x[h + 1] - m[h + 1] - 0.2f);
           l[h] += a0;
           l[h + 1] += a1;
-          a0 *= rel;
-          a1 *= rel;
+          a0 *= own.y;
+          a1 *= own.y;
 #pragma unroll
           for (int y = 0; y < 4; ++y) part[y][h / 2] = split_off(a0, a1);
         }
@@ -726,7 +724,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
       for (int h = 0; h < HP; ++h) {
         if (!alone && tid == h && h < heads) p.ml[f * p.heads + h] = make_float2(m[h], l[h]);
         // fac: what a head's sums are multiplied with
-        fac[h] = !alone ? vs_ref : l[h] > 0.0f || l[h] != l[h] ? __fdividef(vs_ref, l[h]) : 0.0f;
+        fac[h] = !alone ? 1.0f : l[h] > 0.0f || l[h] != l[h] ? __fdividef(1.0f, l[h]) : 0.0f;
       }
 #pragma unroll 1
       for (int hf = 0; hf < C::kHalves; ++hf) {
@@ -777,14 +775,15 @@ constexpr int kJoinRows = 16;
 struct JoinSum {
   float m = -INFINITY, l = 0.0f;
   float4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+  // the root of a unit's weight
   __device__ __forceinline__ static float weight(float m, float l, float top) {
     // a unit without keys has m = -inf, l = 0; with only NaN scores m = -inf, l = NaN
-    return m == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : ex2(m - top);
+    return m == -INFINITY ? (l == 0.0f ? 0.0f : 1.0f) : ex2_root(m - top);
   }
   __device__ __forceinline__ void add(float2 e, const float4& v) {
-    const float top = fmaxf(m, e.x), wa = weight(m, l, top), wb = weight(e.x, e.y, top);
+    const float top = fmaxf(m, e.x), ra = weight(m, l, top), rb = weight(e.x, e.y, top), wa = ra * ra, wb = rb * rb;
     m = top;
-    l = l * wa + e.y * wb;
+    l = l * ra * ra + e.y * rb * rb;
     o.x = o.x * wa + v.x * wb;
     o.y = o.y * wa + v.y * wb;
     o.z = o.z * wa + v.z * wb;

@@ -13,10 +13,12 @@
 // bound is the dense bf16 rate. P V differs by head_dim, see the two kernels below; p overwrites the scores it
 // came from in tensor memory and is the A operand of the second product there.
 //
-// Scales. A block of keys has one ks: it enters the exponent, exp2(s * ks * factor - m). Its vs
-// enters there, too, as log2(vs / vs_ref), vs_ref the largest vs seen (within a factor); the row sum takes it
-// back by group of 16. The running maximum m moves only when a score passes it by a power of two that the type of
-// p has room for; the accumulator is rescaled only then.
+// Scales. A block of keys has one ks: it enters the exponent, and its vs as a power, too: with x = s * ks * factor and
+// y = x + log2(vs), p = exp2(y - m) goes into the product with V's bytes, and the row sum takes vs back by group of 16,
+// l = sum p / vs. m is the running maximum of y over the keys that the row sees: what a key is rounded to goes by the
+// largest probability x scale of the row itself, not by a scale that weighs nothing or that it does not see (a
+// reference of its own for vs, the largest of a tile, lost rows whole next to one). m moves only when a y passes it by a power
+// of two that the type of p has room for; the accumulator is rescaled only then.
 //
 // One CTA per unit of 128 rows: its queries stay in shared memory, its output in tensor memory. Loops over
 // the columns of a tile are kept rolled: a CTA fetches every role's code, and unrolled loops waited for instructions
@@ -227,57 +229,58 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
 
 // ---- what the two kernels share
 
-// Looks up the pages and scales of a unit's tiles, four at a time: lane = (tile of the batch, 16-key group).
+// Looks up the pages and scales of a unit's tiles, four at a time: lane = (tile of the batch, 16-key group). Of a
+// group: ks, log2 vs, 1 / vs (0 for a vs far below the usual ones), and whether its tile has one of those.
 template <typename C>
-__device__ __forceinline__ void look_up(const PrefillParams& p, const PrefillUnit& u, int tiles, unsigned char* scales, int32_t* s_row,
-                                        void* refs, uint32_t b_info, uint32_t b_infoe, volatile int* fail) {
+__device__ __forceinline__ void look_up(const PrefillParams& p, const PrefillUnit& u, int tiles, float4* scales, int32_t* s_row,
+                                        uint32_t b_info, uint32_t b_infoe, volatile int* fail) {
   const AttnArgs& a = p.a;
   const int lane = threadIdx.x & 31, shift = 31 - __clz(a.bs);
   bool ok = true;
-  float ref = -INFINITY;
 #pragma unroll 1
   for (int j0 = 0; j0 < tiles && ok; j0 += C::kBatch) {
     const int j = j0 + lane / kGroups, pos = (u.tile0 + j) * kTile + (lane % kGroups) * kGroup;
-    int row = a.num_blocks * a.H * a.bs;           // past the cache: zeros
-    float2 sc = make_float2(-1.0f, -INFINITY);     // no key, or a page that is none: not seen
+    int row = a.num_blocks * a.H * a.bs;                      // past the cache: zeros
+    float4 sc = make_float4(0.0f, -INFINITY, 0.0f, 0.0f);     // no key, or a page that is none: not seen
     if (j < tiles && pos < u.len) {
       const int page = a.block_table[static_cast<int64_t>(p.b0 + u.b) * a.max_blocks + (pos >> shift)];
       if (page >= 0 && page < a.num_blocks) {
         const int64_t at = static_cast<int64_t>(page) * a.H + u.h;
-        sc = make_float2(a.k_scale[at], a.v_scale[at]);
+        sc.x = a.k_scale[at];
+        sc.y = a.v_scale[at];
         row = (static_cast<int>(at) << shift) + (pos & (a.bs - 1));
+        // (the writer's least scale stands for smaller ones, zero among them: 1 / vs has to leave room for sums)
+        asm("lg2.approx.f32 %0, %0;" : "+f"(sc.y));
+        sc.y = fmaxf(sc.y, -64.0f);
+        sc.z = sc.y < kFarScale ? 0.0f : ex2(-sc.y);
       } else if (a.err) {
         atomicOr(a.err, GDN_DEVERR_BLOCK_RANGE);
       }
     }
-    if (sc.x >= 0.0f) asm("lg2.approx.f32 %0, %0;" : "+f"(sc.y));
+    const uint32_t far = __ballot_sync(0xFFFFFFFFu, sc.z == 0.0f && sc.y != -INFINITY);
+    sc.w = ((far >> (lane & -kGroups)) & ((1u << kGroups) - 1)) != 0 ? 1.0f : 0.0f;
     const int slot = (j0 / C::kBatch) % C::kBatches;
     ok = __all_sync(0xFFFFFFFFu, wait_or_fail(b_infoe + 8 * slot, ((j0 / C::kInfoRing) & 1) ^ 1, fail));
     if (!ok) break;
-    float top = sc.y;
-#pragma unroll
-    for (int o = 1; o < kGroups; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
     s_row[slot * 32 + lane] = row;
-    if constexpr (C::kRefs) {
-      // the power of two that the values' scales are taken by: it follows a tile's largest once that passes it by 2^3
-      float before = ref, after = ref;
-#pragma unroll
-      for (int i = 0; i < C::kBatch; ++i) {
-        const float t = __shfl_sync(0xFFFFFFFFu, top, i * kGroups);
-        const float next = t > ref + 3.0f ? t : ref;
-        if (lane / kGroups == i) before = ref, after = next;
-        ref = next;
-      }
-      const float none = sc.x < 0.0f ? -INFINITY : 0.0f, dl = fmaxf(sc.y - after, -60.0f);
-      reinterpret_cast<float4*>(scales)[slot * 32 + lane] = make_float4(sc.x, dl + none, ex2(-dl), none);
-      if (lane % kGroups == 0) static_cast<float2*>(refs)[slot * C::kBatch + lane / kGroups] = make_float2(before, after);
-    } else {
-      reinterpret_cast<float2*>(scales)[slot * 32 + lane] = sc;
-      if (lane % kGroups == 0) static_cast<float*>(refs)[slot * C::kBatch + lane / kGroups] = top;
-    }
+    scales[slot * 32 + lane] = sc;
     __syncwarp();
     if (lane == 0) mbar_arrive(b_info + 8 * slot);
   }
+}
+
+// What the keys of blocks with a far vs, among 32 scores of two groups, add to a row's sum. All but never called.
+__device__ __forceinline__ float far_sum(const float (&s)[32], const float4* scales, float factor, float base) {
+  float sum = 0.0f;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const float4 e = scales[g];
+    if (e.z != 0.0f || e.y == -INFINITY) continue;
+    const float ks = exponent_scale(e.x, factor);
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) sum += ex2(fmaf(s[g * kGroup + i], ks, base));
+  }
+  return sum;
 }
 
 // Copies the key or the value tiles of a unit into a ring of kStages: lane g < 8 has the 16-key group g of each
@@ -385,13 +388,12 @@ __device__ __forceinline__ void split_queries(const AttnArgs& a, const PrefillUn
 // c ^ (i mod chunks).
 template <int D, int kWide, int kBytes>
 __device__ __forceinline__ void store_rows(const PrefillParams& p, const PrefillUnit& u, int rows, int r, bool live, int token, int head,
-                                           int G, int tiles, float l, float lv_ref, uint32_t taddr, int c0, uint32_t stage) {
+                                           int G, int tiles, float l, uint32_t taddr, int c0, uint32_t stage) {
   const AttnArgs& a = p.a;
   const int lane = threadIdx.x & 31;
   const bool whole = u.slot < 0;
-  const float vs_ref = lv_ref == -INFINITY ? 0.0f : ex2(lv_ref);
-  const float inv = l > 0.0f || l != l ? __fdividef(vs_ref, l) : 0.0f;
-  const float mul = whole ? inv : vs_ref;
+  const float inv = l > 0.0f || l != l ? __fdividef(1.0f, l) : 0.0f;
+  const float mul = whole ? inv : 1.0f;
   const bool none = tiles == 0 || (whole && inv == 0.0f);  // zeros, whatever tensor memory holds
   constexpr int kFit = kBytes / 128;                       // fp32 columns of 32 rows that fit
   constexpr int kCols = kFit < kWide ? kFit : kWide;
@@ -455,7 +457,7 @@ __device__ __forceinline__ void store_rows(const PrefillParams& p, const Prefill
 // Both products on 8-bit operands, no conversion of V: p, rounded to f16, is the sum of three e5m2 values (split_e5m2),
 // each of the part that the ones before leave: 11 significant bits. e5m2 has f16's exponents, so all three have the factor 1 and
 // one accumulator, down to 2^-17: m moves when a score passes it by 2^4 and stands for 2^11, so a key is rounded to 2^-28 of
-// the row's largest whatever stands between. (Two e4m3 parts, a quarter fewer products and 123 us where this takes 138, end at 2^-14 of it:
+// the row's largest whatever stands between. (Two e4m3 parts, a fifth fewer products and 123 us where this takes 138, end at 2^-14 of it:
 // 5,000 keys 10 nats below one of no value came out 14 to 26% small.) Sixteen softmax warps, four threads a row with 32 columns each (they exchange their maxima), two
 // score buffers (2 x 128 columns of tensor memory, 256 of output), a warp that issues MMAs: the 2,610 cycles of products a
 // tile hide most of the softmax. 4,096 tokens (16 / 2 heads): 138 us, 53% of the bf16 rate with the masked half
@@ -467,14 +469,12 @@ struct WideCfg {
   static constexpr int kSoftWarps = 4 * kSplitC;
   static constexpr int kThreads = 32 * (kSoftWarps + 4); // and warps for MMAs, lookups, copies of K, copies of V
   static constexpr int kStages = 2;                      // key tiles in the ring, and value tiles
-  static constexpr bool kRefs = false;
   static constexpr int kBatch = 4, kBatches = 4, kInfoRing = kBatch * kBatches;  // tiles looked up at a time; kept
   static constexpr int kQ = 2 * Tile<D>::kBytes;         // hi and lo
   static constexpr int kKV = kStages * 2 * Tile<D>::kBytes;
-  static constexpr int kAtScale = kQ + kKV;                 // [kInfoRing][kGroups] (ks, log2 vs)
-  static constexpr int kAtRow = kAtScale + kInfoRing * kGroups * 8;
-  static constexpr int kAtTop = kAtRow + kInfoRing * kGroups * 4;  // [kInfoRing] the tile's largest log2 vs
-  static constexpr int kAtMax = kAtTop + kInfoRing * 4;  // [2][kSplitC][kRows]
+  static constexpr int kAtScale = kQ + kKV;                 // [kInfoRing][kGroups] (ks, log2 vs, 1 / vs)
+  static constexpr int kAtRow = kAtScale + kInfoRing * kGroups * 16;
+  static constexpr int kAtMax = kAtRow + kInfoRing * kGroups * 4;  // [2][kSplitC][kRows]
   static constexpr int kAtFactor = kAtMax + 2 * kSplitC * kRows * 4;  // [kRows]
   static constexpr int kAtBars = kAtFactor + kRows * 4;
   static constexpr int kSmem = 1024 + kAtBars + 8 * (4 * kStages + 2 * kBatches + 8);
@@ -493,9 +493,8 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + (-smem_addr(smem_raw) & 1023u);
   const uint32_t s_q = smem_addr(smem), s_k = s_q + C::kQ, s_v = s_k + C::kStages * TL::kBytes;
-  float2* s_scale = reinterpret_cast<float2*>(smem + C::kAtScale);
+  float4* s_scale = reinterpret_cast<float4*>(smem + C::kAtScale);
   int32_t* s_row = reinterpret_cast<int32_t*>(smem + C::kAtRow);
-  float* s_top = reinterpret_cast<float*>(smem + C::kAtTop);
   float* s_max = reinterpret_cast<float*>(smem + C::kAtMax);
   float* s_factor = reinterpret_cast<float*>(smem + C::kAtFactor);
   const uint32_t bar = s_q + C::kAtBars;
@@ -543,7 +542,7 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
 
   int copies = 0;  // of a copying warp
   if (warp == C::kSoftWarps + 1) {
-    look_up<C>(p, u, tiles, smem + C::kAtScale, s_row, s_top, b_info, b_infoe, &s_fail);
+    look_up<C>(p, u, tiles, s_scale, s_row, b_info, b_infoe, &s_fail);
   } else if (warp >= C::kSoftWarps + 2) {
     const bool is_v = warp == C::kSoftWarps + 3;
     copies = is_v ? copy_tiles<D, C, C::kStages>(a, u, tiles, &maps.v_page, &maps.v_group, s_v, s_row, b_vfull, b_vempty, b_info, b_infoe, &s_fail)
@@ -632,14 +631,14 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
     const int sees = live ? min(len, len - n + token + 1) : 0;  // keys this row sees
     // keys before this one are seen by every row of the warp
     const int all_see = __reduce_min_sync(0xFFFFFFFFu, sees);
-    float m = -INFINITY, l = finite || sees <= 0 ? 0.0f : __int_as_float(0x7FC00000), lv_ref = -INFINITY;
+    float m = -INFINITY, l = finite || sees <= 0 ? 0.0f : __int_as_float(0x7FC00000);
     // the two warps of a row agree on when to leave; a warp whose wait runs out meets the other until then
     bool left = false;
     for (int j = 0; j < tiles; ++j) {
       const int slot = (j / C::kBatch) % C::kBatches;
       ok = __all_sync(0xFFFFFFFFu, ok && wait(b_info + 8 * slot, (j / C::kInfoRing) & 1) && wait(b_s + 8 * (j & 1), use(j)));
       const uint32_t sc = tmem + C::kS + 128 * (j & 1) + half * NC + lanes;
-      const float2* scales = s_scale + (j % C::kInfoRing) * kGroups;
+      const float4* scales = s_scale + (j % C::kInfoRing) * kGroups;
       const int cut = sees - (u.tile0 + j) * kTile - half * NC;      // columns from here on are hidden
       const bool masked = all_see < (u.tile0 + j) * kTile + (half + 1) * NC;
       // 32 scores, -inf where they are hidden. 64 are read twice (for the maximum, for the exponentials)
@@ -654,21 +653,13 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
             asm volatile("" : "+f"(s[i]));  // kept behind the branch: as selects these cost every tile
           }
         }
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-          if (scales[half * NG + c / kGroup + g].x < 0.0f) {  // a page that is none
-#pragma unroll
-            for (int i = 0; i < kGroup; ++i) {
-              s[g * kGroup + i] = -INFINITY;
-              asm volatile("" : "+f"(s[g * kGroup + i]));
-            }
-          }
       };
-      float mx = -INFINITY, lv_top = -INFINITY;
+      // the largest exponent of the thread's columns; a page that is none has rows of zeros: its exponents become
+      // -infinity by what is added
+      float mx = -INFINITY;
       float s[32];
       if (ok) {
         tc::fence_after_sync();
-        lv_top = s_top[j % C::kInfoRing];
 #pragma unroll 1
         for (int c = 0; c < NC; c += 32) {
           scores(c, s);
@@ -678,7 +669,8 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
 #pragma unroll
             for (int i = 1; i + 1 < kGroup; i += 2) t0 = max3(t0, s[g * kGroup + i], s[g * kGroup + i + 1]);
             t0 = fmaxf(t0, s[g * kGroup + kGroup - 1]);
-            mx = fmaxf(mx, t0 * exponent_scale(scales[half * NG + c / kGroup + g].x, factor));
+            const float4 e = scales[half * NG + c / kGroup + g];
+            mx = fmaxf(mx, fmaf(t0, exponent_scale(e.x, factor), e.y));
           }
         }
       }
@@ -695,16 +687,11 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
       }
 #pragma unroll
       for (int i = 1; i < C::kSplitC; ++i) mx = fmaxf(mx, s_max[((j & 1) * C::kSplitC + (half ^ i)) * C::kRows + r]);
-      const bool grow_v = lv_top > lv_ref + 0.8f;
-      if (__any_sync(0xFFFFFFFFu, mx > m + 4.0f) || grow_v) {
+      if (__any_sync(0xFFFFFFFFu, mx > m + 4.0f)) {
         const float to = mx > m + 4.0f ? mx : m;  // by the row alone, whatever its neighbours do
-        float corr = to == -INFINITY ? 1.0f : ex2(m - to);
+        const float root = to == -INFINITY ? 1.0f : ex2_root(m - to), corr = root * root;
         m = to;
-        l *= corr;
-        if (grow_v) {
-          corr *= ex2(lv_ref - lv_top);
-          lv_ref = lv_top;
-        }
+        l = l * root * root;
         if (j > 0) {
           ok = __all_sync(0xFFFFFFFFu, wait(b_pv + 8 * ((j - 1) & 1), use(j - 1)));
           if (ok) {
@@ -726,20 +713,21 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
       for (int c = 0; c < NC; c += 32) {
         float w[24];  // high, middle and low parts of four keys each
         if (NC > 32) scores(c, s);
+        if (scales[0].w != 0.0f) l += far_sum(s, scales + half * NG + c / kGroup, factor, base);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          // p * vs / vs_ref comes out of the exponential; the row sum takes it back by group
-          const float2 e2 = scales[half * NG + c / kGroup + g];
-          const float ks = exponent_scale(e2.x, factor), dl = fmaxf(e2.y - lv_ref, -60.0f);
-          const float2 k2 = make_float2(ks, ks), b2 = make_float2(base + dl, base + dl);
+          // p * vs comes out of the exponential; the row sum takes vs back by group
+          const float4 e = scales[half * NG + c / kGroup + g];
+          const float ks = exponent_scale(e.x, factor), add = base + e.y;
+          const float2 k2 = make_float2(ks, ks), b2 = make_float2(add, add);
           float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
           for (int i = 0; i < kGroup; i += 4) {
             uint32_t h[2];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const int e = g * kGroup + i + 2 * y;
-              float2 v = fma2(make_float2(s[e], s[e + 1]), k2, b2);
+              const int at = g * kGroup + i + 2 * y;
+              float2 v = fma2(make_float2(s[at], s[at + 1]), k2, b2);
               v.x = ex2(v.x);
               v.y = ex2(v.y);
               sum = add2(sum, v);
@@ -750,7 +738,7 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
 #pragma unroll
             for (int y = 0; y < 3; ++y) w[y * 8 + g * 4 + i / 4] = __uint_as_float(part[y]);
           }
-          l += (sum.x + sum.y) * ex2(-dl);
+          l = fmaf(sum.x + sum.y, e.z, l);
         }
         tmem_st8(sc + c, w);
         tmem_st8(sc + c + 8, w + 8);
@@ -774,7 +762,7 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
     if (ok) {
       tc::fence_after_sync();
       if (u.slot >= 0 && live && half == 0) p.ml[static_cast<int64_t>(u.slot) * C::kRows + r] = make_float2(m, l);
-      store_rows<D, D / C::kSplitC, C::kQ / C::kSoftWarps>(p, u, C::kRows, r, live, token, row - token * G, G, tiles, l, lv_ref,
+      store_rows<D, D / C::kSplitC, C::kQ / C::kSoftWarps>(p, u, C::kRows, r, live, token, row - token * G, G, tiles, l,
                                                            tmem + C::kO + lanes, half * (D / C::kSplitC),
                                                            s_q + warp * (C::kQ / C::kSoftWarps));
     }
@@ -803,7 +791,7 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
 // Here a key costs half the MMA time and the same softmax, so the softmax and shared memory decide. Probabilities
 // are f16 (11 significant bits, 2^-24 of the reference; one conversion for two of them instead of six operations for
 // two e4m3 parts), and a warpgroup converts each tile of V to f16; e4m3 values are exact in f16. m moves when a score
-// passes it by 2^8, the reference for vs when one passes it by 2^3 (f16 has the range).
+// passes it by 2^8 (f16 has the range).
 //
 // Scores of three tiles are in tensor memory (3 x 128 columns, and D of output): Q K of the next tiles runs under
 // the softmax. Two warpgroups take the tiles in turn, thread = row, and hand m on; Q K and P V are issued by a thread
@@ -823,7 +811,6 @@ struct NarrowCfg {
   static constexpr int kSoftWarps = 8, kConvWarps = 4;
   static constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 5);  // and warps for Q K, P V, lookups, copies of K and V
   static constexpr int kStagesK = 4, kStagesV = 3, kStagesW = 2, kScores = 3;  // W: V in f16
-  static constexpr bool kRefs = true;
   static constexpr int kBatch = 4, kBatches = 4, kInfoRing = kBatch * kBatches;
   using TL = Tile<D>;
   using TV = Tile<2 * D>;                                 // V in f16: rows of 2 D bytes
@@ -833,8 +820,7 @@ struct NarrowCfg {
   static constexpr int kAtV16 = kAtV + kStagesV * TL::kBytes;
   static constexpr int kAtScale = kAtV16 + kStagesW * TV::kBytes;  // [kInfoRing][kGroups]
   static constexpr int kAtRow = kAtScale + kInfoRing * kGroups * 16;
-  static constexpr int kAtTop = kAtRow + kInfoRing * kGroups * 4;  // [kInfoRing]
-  static constexpr int kAtFactor = kAtTop + kInfoRing * 8;         // [kRows]
+  static constexpr int kAtFactor = kAtRow + kInfoRing * kGroups * 4;  // [kRows]
   static constexpr int kAtMax = kAtFactor + kRows * 4;             // [3][kRows]: reference, two sums
   static constexpr int kAtBars = kAtMax + 3 * kRows * 4;
   static constexpr int kBars = 2 * kStagesK + 2 * kStagesV + kStagesW + 2 * kBatches + 3 * kScores + 3 + kSoftWarps;
@@ -874,9 +860,8 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
     asm volatile("" : "+r"(slack));  // (addresses are worked out per unit: kept from one to the next they cost spills)
     unsigned char* smem = smem_raw + slack;
     const uint32_t s_q = smem_addr(smem), s_k = s_q + C::kAtK, s_v = s_q + C::kAtV, s_v16 = s_q + C::kAtV16;
-    const float4* s_scale = reinterpret_cast<float4*>(smem + C::kAtScale);
+    float4* s_scale = reinterpret_cast<float4*>(smem + C::kAtScale);
     int32_t* s_row = reinterpret_cast<int32_t*>(smem + C::kAtRow);
-    float2* s_ref = reinterpret_cast<float2*>(smem + C::kAtTop);
     float* s_factor = reinterpret_cast<float*>(smem + C::kAtFactor);
     float* s_max = reinterpret_cast<float*>(smem + C::kAtMax);
     const uint32_t b_kfull = s_q + C::kAtBars, b_kempty = b_kfull + 8 * C::kStagesK, b_vfull = b_kempty + 8 * C::kStagesK,
@@ -908,7 +893,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
 
     int copies = 0;  // of a copying warp
     if (warp == kLook) {
-      look_up<C>(p, u, tiles, smem + C::kAtScale, s_row, s_ref, b_info, b_infoe, &s_fail);
+      look_up<C>(p, u, tiles, s_scale, s_row, b_info, b_infoe, &s_fail);
     } else if (warp == kCopyK) {
       copies = copy_tiles<D, C, C::kStagesK>(a, u, tiles, &maps.k_page, &maps.k_group, s_k, s_row, b_kfull, b_kempty, b_info, 0, &s_fail);
     } else if (warp == kCopyV) {
@@ -1028,7 +1013,6 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
         const float4* scales = s_scale + (j % C::kInfoRing) * kGroups;
         const int cut = sees - (u.tile0 + j) * kTile;  // columns from here on are hidden
         const bool masked = all_see < (u.tile0 + j + 1) * kTile;
-        const float2 refs = s_ref[j % C::kInfoRing];   // the values' power of two before this tile and with it
         // the largest exponent of the tile; a page that is none has rows of zeros: its exponents become -infinity by what
         // is added
         auto hide = [&](float (&s)[32], int c) {
@@ -1053,7 +1037,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
             float t0 = s[g * kGroup];
 #pragma unroll
             for (int i = 1; i + 1 < kGroup; i += 2) t0 = max3(t0, s[g * kGroup + i], s[g * kGroup + i + 1]);
-            mx = fmaxf(mx, fmaf(fmaxf(t0, s[g * kGroup + kGroup - 1]), exponent_scale(e.x, factor), e.w));
+            mx = fmaxf(mx, fmaf(fmaxf(t0, s[g * kGroup + kGroup - 1]), exponent_scale(e.x, factor), e.y));
           }
         }
         if (j > 0) ok = __all_sync(0xFFFFFFFFu, wait(turn_of, ((j - 1) >> 1) & 1));
@@ -1061,18 +1045,20 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
         // the reference follows the row's maximum once that passes it by 2^8 (f16 has the range): by the row alone,
         // whatever its neighbours do
         const float was = j > 0 ? s_max[r] : -INFINITY, to = mx > was + 8.0f ? mx : was;
-        const bool grown = refs.x != refs.y;
-        const bool scaled = j > 0 && (__any_sync(0xFFFFFFFFu, to != was) || grown);
+        const bool scaled = j > 0 && __any_sync(0xFFFFFFFFu, to != was);
         s_max[r] = to;
         __syncwarp();
         if (lane == 0) mbar_arrive(turn);
-        if (to != m) l *= ex2(m - to);
+        if (to != m) {
+          const float root = ex2_root(m - to);
+          l = l * root * root;
+        }
         m = to;
         if (scaled) {
           ok = __all_sync(0xFFFFFFFFu, wait(b_pv + 8 * ((j - 1) % C::kScores), ((j - 1) / C::kScores) & 1));
           if (!ok) break;
           tc::fence_after_sync();
-          const float corr = (to != was ? ex2(was - to) : 1.0f) * (grown ? ex2(refs.x - refs.y) : 1.0f);
+          const float corr = to != was ? ex2(was - to) : 1.0f;
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
             float o[16];
@@ -1083,8 +1069,18 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
             tc::tmem_st16(tmem + C::kO + lanes + c, o);
           }
         }
-        // the probabilities: p * vs / vs_ref comes out of the exponential; the row sum takes it back by group
+        // the probabilities: p * vs comes out of the exponential; the row sum takes vs back by group
         const float base = m == -INFINITY ? 0.0f : -m;
+        if (scales[0].w != 0.0f) {  // (in the loop below, a branch for each group took 4% of the time)
+#pragma unroll 1
+          for (int c = 0; c < kTile; c += 32) {
+            float s[32];
+            tmem_ld32(sc + c, s);
+            tc::tmem_wait_ld();
+            hide(s, c);
+            l += far_sum(s, scales + c / kGroup, factor, base);
+          }
+        }
 #pragma unroll 1
         for (int c = 0; c < kTile; c += 32) {
           float cur[32];
@@ -1123,15 +1119,15 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
       for (int j = max(0, tiles - 2); j < tiles; ++j) ok = ok && wait(b_pv + 8 * (j % C::kScores), (j / C::kScores) & 1);
       if (!vote(!ok)) {
         const float last = tiles > 0 ? s_max[r] : -INFINITY;
-        const float2 refs = tiles > 0 ? s_ref[(tiles - 1) % C::kInfoRing] : make_float2(0.0f, -INFINITY);
-        s_max[(1 + own) * C::kRows + r] = m == last ? l : l * ex2(m - last);
+        const float root = ex2_root(m - last);
+        s_max[(1 + own) * C::kRows + r] = m == last ? l : l * root * root;
         if (!vote(!ok)) {
           tc::fence_after_sync();
           l = s_max[C::kRows + r] + s_max[2 * C::kRows + r];
           const int row = u.row0 + r, token = row / G;
           const bool live = row < rows_all;
           if (u.slot >= 0 && live && own == 0) p.ml[static_cast<int64_t>(u.slot) * C::kRows + r] = make_float2(last, l);
-          store_rows<D, D / 2, C::kQ / C::kSoftWarps>(p, u, C::kRows, r, live, token, row - token * G, G, tiles, l, refs.y,
+          store_rows<D, D / 2, C::kQ / C::kSoftWarps>(p, u, C::kRows, r, live, token, row - token * G, G, tiles, l,
                                                       tmem + C::kO + lanes, own * (D / 2), s_q + warp * (C::kQ / C::kSoftWarps));
         }
       }
@@ -1181,9 +1177,9 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(const __grid_con
     for (int s = 0; s < u.splits; ++s) {
       const int64_t at = static_cast<int64_t>(u.slot + s) * kUnitRows + r;
       const float2 e = p.ml[at];
-      const float c = e.x == -INFINITY ? (e.y == 0.0f ? 0.0f : 1.0f) : ex2(e.x - top);
+      const float root = e.x == -INFINITY ? (e.y == 0.0f ? 0.0f : 1.0f) : ex2_root(e.x - top), c = root * root;
       const float4 v = *reinterpret_cast<const float4*>(p.part + at * D + d4 * 4);
-      sum += e.y * c;
+      sum += e.y * root * root;
       if (c != 0.0f) {
         o.x += v.x * c;
         o.y += v.y * c;

@@ -383,7 +383,8 @@ void gdn_graph_destroy(gdn_graph* graph);
  *
  * Cache: k_cache and v_cache [num_blocks, Hkv, block_size, head_dim] in e4m3 (one byte, 1-4-3,
  * largest value 448), k_scale and v_scale [num_blocks, Hkv] f32: an element stands for byte *
- * scale of its block and head. Scales are positive and normal. A request's token at position p
+ * scale of its block and head. Scales are positive and normal (zero is fine for a v_scale; to the
+ * prompt call those below 2^-64, the writer's least, are 2^-64). A request's token at position p
  * lies in block block_table[b, p / block_size] at offset p % block_size; its slot is
  * block * block_size + offset.
  */
@@ -465,8 +466,8 @@ gdn_status gdn_cache_append(const void* k, int64_t k_stride, const void* v, int6
  * A request of length 0 (or with no readable block) gives zeros. A length outside [0, max_blocks *
  * block_size] sets GDN_DEVERR_SEQLENS and is clamped. What lies in a block past the request's
  * length is never used, NaN bytes included. Softmax statistics and sums are fp32. Queries are
- * exact to 2^-18 of a head's largest element; the probabilities keep 16 significant bits, and
- * 2^-22 of the largest, for the product with V.
+ * exact to 2^-18 of a head's largest element; for the product with V the probabilities keep 16
+ * significant bits, and no less than 2^-21 of the row's largest probability x v_scale.
  *
  *   q          [batch] rows of Hq * head_dim bf16, q_stride elements apart (16-byte aligned, a
  *              multiple of 8)
@@ -491,7 +492,8 @@ gdn_status gdn_attn_decode(const void* q, int64_t q_stride, const void* k_cache,
  * positions 0 .. lens[b] - n + i; a token that sees nothing (lens[b] < n: its row was refused)
  * gives zeros. Otherwise as gdn_attn_decode, but for the probabilities: for the product with V
  * they keep 11 significant bits, and for head_dim 64 and 128 (f16) 2^-25, for 256 (three e5m2
- * parts) 2^-28 of the row's largest. A NaN
+ * parts) 2^-28 of the row's largest probability x v_scale; scales of keys that a row does not see
+ * change nothing. A NaN
  * among a request's values reaches the rows that do not see it, too, if they share a 128-token tile.
  *
  *   q          [total_tokens] rows of Hq * head_dim bf16, q_stride elements apart

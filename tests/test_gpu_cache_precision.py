@@ -14,7 +14,8 @@ import _cache_oracle as co
 pytestmark = pytest.mark.gpu
 
 # (significant bits, floor) of a probability
-KEEPS = {("prefill", 256): (11, 2.0 ** -28)}
+KEEPS = {("prefill", 64): (11, 2.0 ** -25), ("prefill", 128): (11, 2.0 ** -25), ("prefill", 256): (11, 2.0 ** -28),
+         ("decode", 64): (16, 2.0 ** -21.8), ("decode", 128): (16, 2.0 ** -21.8), ("decode", 256): (16, 2.0 ** -21.8)}
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -41,7 +42,7 @@ class Pages:
         def pool(x):
             x = torch.nn.functional.pad(x, (0, 0, 0, 0, 0, W * bs - n)).view(W, bs, self.H, self.d).transpose(1, 2)
             s = (x.abs().amax(dim=(2, 3)) / 448).clamp(min=2.0 ** -64)
-            c = torch.full((W + 2, self.H, bs, self.d), 0x7F, dtype=torch.uint8, device="cuda")
+            c = torch.full((W + 2, self.H, bs, self.d), 0x7F, dtype=torch.uint8, device="cuda")  # (NaN where no page is)
             c[self.table[0].long()] = (x / s[:, :, None, None]).clamp(-448, 448).to(co.F8).view(torch.uint8)
             all_s = torch.ones(W + 2, self.H, device="cuda")
             all_s[self.table[0].long()] = s
@@ -102,7 +103,7 @@ def exact(c, q, which):
         size = x.abs().amax(dim=1, keepdim=True) * k[:, h].abs().sum(dim=1).amax() * d ** -0.5
         e = 2 * ((2.0 ** -18 + d * 2.0 ** -24) * size + 2.0 ** -21 * (1 + torch.where(hidden, 0.0, s).abs().amax(dim=1, keepdim=True)))
         mag = p @ vh.abs()
-        least = (p * vs[:, h]).amax(dim=1, keepdim=True) * floor * ((~hidden).double() @ (vh.abs() / vs[:, h, None]))
+        least = (p * vs[:, h]).amax(dim=1, keepdim=True) * floor * ((~hidden).double() @ (vh.abs() / vs[:, h, None]).nan_to_num())
         tol[:, m] = (2.0 ** -bits + e + c.n * 2.0 ** -24) * mag + least + 2.0 ** -8 * o.abs() + 1e-30
     return out, tol
 
@@ -153,3 +154,56 @@ def test_prompts_256_one_key_above_the_others(T, Hq, H, gap, flat):
 
 def test_prompts_256_one_key_above_a_long_request():
     one_key_above_a_long_request("prefill", 70, 256)
+
+
+HEADS = [(4, 2, 64), (16, 2, 64), (8, 2, 128), (16, 1, 128), (4, 2, 256), (16, 2, 256)]
+
+
+@pytest.mark.parametrize("which,T", [("decode", 3), ("prefill", 5), ("prefill", 300)])
+@pytest.mark.parametrize("Hq,H,d", HEADS)
+@pytest.mark.parametrize("power", [-20, 14, 30])
+def test_a_block_of_other_values_that_has_no_weight(which, T, Hq, H, d, power):
+    """A page whose values are 2^power times the others', 50 nats below them: it decides nothing."""
+    n, r = 2100, rand(power + 100)
+    u = torch.sign(r(d)) * 0.5
+    k, v = 0.5 * r(n, H, d), 1.0 + r(n, H, d)
+    k[640:656] -= u * (50 / (0.25 * d ** 0.5))
+    v[640:656] *= 2.0 ** power
+    check(Pages(k, v, 16), (u + 0.05 * r(T, Hq, d)).bfloat16(), which)
+
+
+@pytest.mark.parametrize("which,T", [("decode", 3), ("prefill", 5), ("prefill", 300)])
+@pytest.mark.parametrize("Hq,H,d", HEADS)
+def test_weight_on_a_block_of_small_values(which, T, Hq, H, d):
+    """The other way round: most of the probability on a page whose values are 2^-18 of the others'."""
+    n, r = 1500, rand(d)
+    u = torch.sign(r(d)) * 0.5
+    k, v = 0.5 * r(n, H, d), 1.0 + r(n, H, d)
+    k[320:336] += u * (9 / (0.25 * d ** 0.5))
+    v[320:336] *= 2.0 ** -18
+    check(Pages(k, v, 16), (u + 0.05 * r(T, Hq, d)).bfloat16(), which)
+
+
+@pytest.mark.parametrize("which,T", [("decode", 1), ("prefill", 40)])
+@pytest.mark.parametrize("Hq,H,d", HEADS)
+@pytest.mark.parametrize("power", [0, -40, 100])
+def test_blocks_of_zeros(which, T, Hq, H, d, power):
+    """Pages of zeros, whose scale is the writer's least (2^-64), and some of scale 0, between pages of any size: their
+    keys count in the sum."""
+    n, r = 700, rand(power + d)
+    k, v = r(n, H, d), (1.0 + r(n, H, d)) * 2.0 ** power
+    v[0:64] = v[200:300] = v[500:560] = 0.0
+    c = Pages(k, v, 16)
+    c.vs[c.table[0, 14:16].long()] = 0.0
+    check(c, r(T, Hq, d).bfloat16(), which)
+
+
+@pytest.mark.parametrize("Hq,H,d", [(4, 2, 64), (8, 2, 128), (16, 2, 256)])
+@pytest.mark.parametrize("old", [0, 100, 5000])
+def test_later_tokens_of_any_size(Hq, H, d, old):
+    """What a row does not see: tokens after it, their pages' scales of any size."""
+    T, r = 200, rand(old + d)
+    k, v = r(old + T, H, d), 1.0 + r(old + T, H, d)
+    first = -(-(old + 90) // 16) * 16
+    v[first:] *= 2.0 ** 25
+    check(Pages(k, v, 16), r(T, Hq, d).bfloat16(), "prefill")

@@ -789,9 +789,9 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
 // ------------------------------------------------------------------------- head_dim 64 and 128
 //
 // Here a key costs half the MMA time and the same softmax, so the softmax and shared memory decide. Probabilities
-// are f16 (11 significant bits, 2^-24 of the reference; one conversion for two of them instead of six operations for
+// are f16 (11 significant bits; m stands for 2^7, so a key is rounded to 2^-32 of the row's largest; one conversion for two of them instead of six operations for
 // two e4m3 parts), and a warpgroup converts each tile of V to f16; e4m3 values are exact in f16. m moves when a score
-// passes it by 2^8 (f16 has the range).
+// passes it by 2^8: p <= 2^15.
 //
 // Scores of three tiles are in tensor memory (3 x 128 columns, and D of output): Q K of the next tiles runs under
 // the softmax. Two warpgroups take the tiles in turn, thread = row, and hand m on; Q K and P V are issued by a thread
@@ -1070,7 +1070,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
           }
         }
         // the probabilities: p * vs comes out of the exponential; the row sum takes vs back by group
-        const float base = m == -INFINITY ? 0.0f : -m;
+        const float base = m == -INFINITY ? 0.0f : 7.0f - m;
         if (scales[0].w != 0.0f) {  // (in the loop below, a branch for each group took 4% of the time)
 #pragma unroll 1
           for (int c = 0; c < kTile; c += 32) {

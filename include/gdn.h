@@ -491,7 +491,7 @@ gdn_status gdn_attn_decode(const void* q, int64_t q_stride, const void* k_cache,
  * (append first) as the last of its lens[b] tokens. With n new tokens, token i attends to
  * positions 0 .. lens[b] - n + i; a token that sees nothing (lens[b] < n: its row was refused)
  * gives zeros. Otherwise as gdn_attn_decode, but for the probabilities: for the product with V
- * they keep 11 significant bits, and for head_dim 64 and 128 (f16) 2^-25, for 256 (three e5m2
+ * they keep 11 significant bits, and for head_dim 64 and 128 (f16) 2^-32, for 256 (three e5m2
  * parts) 2^-28 of the row's largest probability x v_scale; scales of keys that a row does not see
  * change nothing. A NaN
  * among a request's values reaches the rows that do not see it, too, if they share a 128-token tile.

@@ -14,7 +14,7 @@ import _cache_oracle as co
 pytestmark = pytest.mark.gpu
 
 # (significant bits, floor) of a probability
-KEEPS = {("prefill", 64): (11, 2.0 ** -25), ("prefill", 128): (11, 2.0 ** -25), ("prefill", 256): (11, 2.0 ** -28),
+KEEPS = {("prefill", 64): (11, 2.0 ** -32), ("prefill", 128): (11, 2.0 ** -32), ("prefill", 256): (11, 2.0 ** -28),
          ("decode", 64): (16, 2.0 ** -21.8), ("decode", 128): (16, 2.0 ** -21.8), ("decode", 256): (16, 2.0 ** -21.8)}
 
 
@@ -207,3 +207,16 @@ def test_later_tokens_of_any_size(Hq, H, d, old):
     first = -(-(old + 90) // 16) * 16
     v[first:] *= 2.0 ** 25
     check(Pages(k, v, 16), r(T, Hq, d).bfloat16(), "prefill")
+
+
+@pytest.mark.parametrize("T", [5, 300])
+@pytest.mark.parametrize("Hq,H,d", HEADS[:4])
+@pytest.mark.parametrize("gap", [6, 10, 16, 18])
+@pytest.mark.parametrize("flat", [False, True])
+def test_prompts_64_128_one_key_above_the_others(T, Hq, H, d, gap, flat):
+    one_key_above("prefill", T, Hq, H, d, gap, flat)
+
+
+@pytest.mark.parametrize("which,T,d", [("prefill", 70, 64), ("prefill", 70, 128)])
+def test_one_key_above_a_long_request(which, T, d):
+    one_key_above_a_long_request(which, T, d)

@@ -17,12 +17,13 @@
 //
 // Eight-bit queries and probabilities are split into parts, side by side in N: a query into two e4m3
 // values (scaled per head so that its largest element lies in [128, 256): exact down to 2^-18 of that),
-// a probability into four with factors 1, 1/16, 1/256, 1/4096 (16 bits, and 2^-22 of the largest).
+// a probability into four with factors 1, 1/32, 1/32^2, 1/32^3 (16 bits, and 2^-26 of the largest).
 //
 // Scales of V. With x the exponent of a score and e that of vs, m is the running maximum of x + e, and p = exp2(x - m)
 // goes into the sum, p vs into the product. So what a key is rounded to goes by the largest probability x scale of the row, and
-// not by a scale that weighs nothing. m moves when an x + e passes it by 2^8, so that almost only a unit's first tile
-// stops for it: p vs < 2^7.8 * 2 <= 448, the largest e4m3.
+// not by a scale that weighs nothing. m stands for 2^1.8 and moves when an x + e passes it by 2^5, so that almost only a
+// unit's first tile stops for it: p vs < 2^6.8 * 2 < 256, so that what a part leaves is at most 8, and 256 times 1 / 32 of it. (With
+// 2^8 above 2^-0.2 and factors of 1/16, keys below 2^-22 of the largest were lost.)
 //
 // Split. A (request, kv head) is cut into units of 256, 512 or 1,024 keys by its OWN length
 // (unit_shift), never by the batch: a row's result depends on its own inputs alone, bit for bit, as
@@ -90,7 +91,8 @@ constexpr int kBatchPerLaunch = 384;   // requests of one launch (their lengths 
 constexpr int kCoarse = 16;            // requests between two kept tile sums
 constexpr int kThreads = 32 * 8;
 constexpr int kSmemPerSm = 228 * 1024;  // 1 KB of it taken by each resident CTA
-constexpr float kRise = 8.0f;          // log2 of what a score may pass the running maximum by
+constexpr float kRise = 5.0f;          // log2 of what a score may pass the running maximum by
+constexpr float kTop = 1.8f;           // log2 of what the running maximum stands for
 
 // log2 of the keys of one unit of a request of `len` keys, and its units. Small units shorten the chain of tiles
 // that a small batch waits for, and cost a large one partial sums (d = 256, 8 query heads a kv head: 8 KB a unit next
@@ -237,15 +239,15 @@ __device__ __forceinline__ float warp_max(float x) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(x));
   return r;
 }
-// two values to e4m3 (RNE); the values that the bytes stand for are taken off and the rest is scaled by 16
+// two values to e4m3 (RNE); the values that the bytes stand for are taken off and the rest is scaled by 32
 __device__ __forceinline__ uint32_t split_off(float& a, float& b) {
   uint32_t r, w;
   asm("{.reg .b16 x; cvt.rn.satfinite.e4m3x2.f32 x, %3, %2; cvt.rn.f16x2.e4m3x2 %1, x; mov.b32 %0, {x, 0};}"
       : "=r"(r), "=r"(w) : "f"(a), "f"(b));
   float fa, fb;
   asm("{.reg .b16 x, y; mov.b32 {x, y}, %2; cvt.f32.f16 %0, x; cvt.f32.f16 %1, y;}" : "=f"(fa), "=f"(fb) : "r"(w));
-  a = (a - fa) * 16.0f;
-  b = (b - fb) * 16.0f;
+  a = (a - fa) * 32.0f;
+  b = (b - fb) * 32.0f;
   return r;
 }
 template <int N>
@@ -673,8 +675,8 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
         uint32_t part[4][HP / 2];
 #pragma unroll
         for (int h = 0; h < HP; h += 2) {
-          float a0 = ex2(m[h] == -INFINITY ? x[h] : x[h] - m[h] - 0.2f);
-          float a1 = ex2(m[h + 1] == -INFINITY ? x[h + 1] : x[h + 1] - m[h + 1] - 0.2f);
+          float a0 = ex2(m[h] == -INFINITY ? x[h] : x[h] - m[h] + kTop);
+          float a1 = ex2(m[h + 1] == -INFINITY ? x[h + 1] : x[h + 1] - m[h + 1] + kTop);
           l[h] += a0;
           l[h + 1] += a1;
           a0 *= own.y;
@@ -733,7 +735,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
         if (D >= 128 || tid < D) {
 #pragma unroll
           for (int h = 0; h < HP; ++h) {
-            const float sum = (o[h] + (o[HP + h] + (o[2 * HP + h] + o[3 * HP + h] * 0.0625f) * 0.0625f) * 0.0625f) * fac[h];
+            const float sum = (o[h] + (o[HP + h] + (o[2 * HP + h] + o[3 * HP + h] * 0.03125f) * 0.03125f) * 0.03125f) * fac[h];
             if (h < heads) {
               if (alone) {
                 asm volatile("{.reg .b16 x; cvt.rn.bf16.f32 x, %1; st.global.b16 [%0], x;}" ::"l"(op + h * D + hf * 128), "f"(fac[h] == 0.0f ? 0.0f : sum) : "memory");

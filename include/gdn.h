@@ -467,7 +467,7 @@ gdn_status gdn_cache_append(const void* k, int64_t k_stride, const void* v, int6
  * block_size] sets GDN_DEVERR_SEQLENS and is clamped. What lies in a block past the request's
  * length is never used, NaN bytes included. Softmax statistics and sums are fp32. Queries are
  * exact to 2^-18 of a head's largest element; for the product with V the probabilities keep 16
- * significant bits, and no less than 2^-21 of the row's largest probability x v_scale.
+ * significant bits, and no less than 2^-26 of the row's largest probability x v_scale.
  *
  *   q          [batch] rows of Hq * head_dim bf16, q_stride elements apart (16-byte aligned, a
  *              multiple of 8)

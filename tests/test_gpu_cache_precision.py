@@ -15,7 +15,7 @@ pytestmark = pytest.mark.gpu
 
 # (significant bits, floor) of a probability
 KEEPS = {("prefill", 64): (11, 2.0 ** -32), ("prefill", 128): (11, 2.0 ** -32), ("prefill", 256): (11, 2.0 ** -28),
-         ("decode", 64): (16, 2.0 ** -21.8), ("decode", 128): (16, 2.0 ** -21.8), ("decode", 256): (16, 2.0 ** -21.8)}
+         ("decode", 64): (16, 2.0 ** -26), ("decode", 128): (16, 2.0 ** -26), ("decode", 256): (16, 2.0 ** -26)}
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -121,10 +121,10 @@ def rand(seed):
     return lambda *shape: torch.randn(*shape, device="cuda", generator=g)
 
 
-def one_key_above(which, T, Hq, H, d, gap, flat):
+def one_key_above(which, T, Hq, H, d, gap, flat, n=5003):
     """The usual first token: `gap` nats above the rest, a value of next to nothing, so that what comes out is the sum of
     many small probabilities; with `flat` they are all the same and their rounding does not average out."""
-    n, r = 5003, rand(gap + d)
+    r = rand(gap + d)
     u = torch.sign(r(d)) * 0.5
     k = (0.0 if flat else 0.6) * r(n, H, d)
     k[0] = u * (gap / (0.25 * d ** 0.5))
@@ -217,6 +217,14 @@ def test_prompts_64_128_one_key_above_the_others(T, Hq, H, d, gap, flat):
     one_key_above("prefill", T, Hq, H, d, gap, flat)
 
 
-@pytest.mark.parametrize("which,T,d", [("prefill", 70, 64), ("prefill", 70, 128)])
+@pytest.mark.parametrize("Hq,H,d", HEADS)
+@pytest.mark.parametrize("gap", [6, 10, 14, 16])
+@pytest.mark.parametrize("flat", [False, True])
+def test_single_tokens_one_key_above_the_others(Hq, H, d, gap, flat):
+    one_key_above("decode", 3, Hq, H, d, gap, flat)
+    one_key_above("decode", 3, Hq, H, d, gap, flat, n=250)   # (all that is looked at together)
+
+
+@pytest.mark.parametrize("which,T,d", [("decode", 2, 64), ("decode", 2, 128), ("decode", 2, 256), ("prefill", 70, 64), ("prefill", 70, 128)])
 def test_one_key_above_a_long_request(which, T, d):
     one_key_above_a_long_request(which, T, d)

@@ -316,6 +316,42 @@ __device__ __forceinline__ int copy_tiles(const AttnArgs& a, const PrefillUnit& 
   return copies;
 }
 
+// 0 * NaN is not 0: a NaN in V would reach the rows of the tile that do not see its key. So in a tile that some row sees
+// only in part, the keys that not every row sees (from `all_see` on) get zeros for their NaN, and s_nan[0 .. D) has the first key
+// with one in each column, for the rows that do see it (s_nan[D]: whether there is any). One tile or two of a unit. Not
+// inlined: in the loop of the converting warps it took 4% of the time (300 tokens at 60,000), so 1%.
+template <int D, int kThreads>
+__device__ __noinline__ void clear_nan(uint32_t tile, int key0, int len, int all_see, int me, int32_t* s_nan) {
+  constexpr int kChunks = D / 16;  // of a key
+#pragma unroll 1
+  for (int i = me; i < kTile * kChunks; i += kThreads) {
+    const int key = i / (8 * kChunks) * 8 + i % 8, c = i / 8 % kChunks;
+    if (key0 + key < all_see || key0 + key >= len) continue;
+    const uint32_t at = tile + Tile<D>::chunk_at(key, c);
+    uint32_t x[4], any = 0;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) any |= ((x[e] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // (NaN: all seven bits)
+    if (any == 0) continue;
+#pragma unroll 1
+    for (int e = 0; e < 16; ++e) {
+      uint32_t byte;
+      asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(at + e));
+      if ((byte & 0x7F) != 0x7F) continue;
+      asm volatile("st.shared.u8 [%0], %1;" ::"r"(at + e), "r"(0) : "memory");
+      atomicMin(s_nan + c * 16 + e, key0 + key);
+      s_nan[D] = 1;
+    }
+  }
+}
+// The keys that every row of a unit sees: what its first token sees.
+__device__ __forceinline__ int seen_by_all(const PrefillUnit& u, int G) { return min(max(u.len - u.n + u.row0 / G + 1, 0), u.len); }
+// The unit's first tile that some row sees only in part.
+__device__ __forceinline__ int first_partial(const PrefillUnit& u, int G) {
+  const int seen = seen_by_all(u, G);
+  return seen < u.len ? seen / kTile - u.tile0 : 0x7FFFFFFF;
+}
+
 // Queries of a unit's rows: a warp takes kRows / kWarps rows, a lane 8 elements of one; each row is scaled to
 // [128, 256) by a power of two and split into two e4m3 parts.
 template <int D, int kRows, int kWarps>
@@ -388,7 +424,7 @@ __device__ __forceinline__ void split_queries(const AttnArgs& a, const PrefillUn
 // c ^ (i mod chunks).
 template <int D, int kWide, int kBytes>
 __device__ __forceinline__ void store_rows(const PrefillParams& p, const PrefillUnit& u, int rows, int r, bool live, int token, int head,
-                                           int G, int tiles, float l, uint32_t taddr, int c0, uint32_t stage) {
+                                           int G, int tiles, float l, uint32_t taddr, int c0, uint32_t stage, const int32_t* s_nan) {
   const AttnArgs& a = p.a;
   const int lane = threadIdx.x & 31;
   const bool whole = u.slot < 0;
@@ -413,6 +449,12 @@ __device__ __forceinline__ void store_rows(const PrefillParams& p, const Prefill
       }
 #pragma unroll
       for (int i = 0; i < kLoad; ++i) o[i] = none ? 0.0f : o[i] * mul;
+      if (s_nan[D] != 0) {  // see clear_nan
+        const int sees = live ? min(u.len, u.len - u.n + token + 1) : 0;
+#pragma unroll
+        for (int i = 0; i < kLoad; ++i)
+          if (s_nan[c + x + i] < sees) o[i] = __int_as_float(0x7FC00000);
+      }
       if (whole) {
 #pragma unroll
         for (int i = 0; i < kLoad; i += 8) {
@@ -476,7 +518,8 @@ struct WideCfg {
   static constexpr int kAtRow = kAtScale + kInfoRing * kGroups * 16;
   static constexpr int kAtMax = kAtRow + kInfoRing * kGroups * 4;  // [2][kSplitC][kRows]
   static constexpr int kAtFactor = kAtMax + 2 * kSplitC * kRows * 4;  // [kRows]
-  static constexpr int kAtBars = kAtFactor + kRows * 4;
+  static constexpr int kAtNan = kAtFactor + kRows * 4;   // [D + 1], see clear_nan
+  static constexpr int kAtBars = kAtNan + (D + 2) * 4;
   static constexpr int kSmem = 1024 + kAtBars + 8 * (4 * kStages + 2 * kBatches + 8);
   // tensor memory columns
   static constexpr int kS = 0;         // two score buffers of 128
@@ -497,6 +540,7 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
   int32_t* s_row = reinterpret_cast<int32_t*>(smem + C::kAtRow);
   float* s_max = reinterpret_cast<float*>(smem + C::kAtMax);
   float* s_factor = reinterpret_cast<float*>(smem + C::kAtFactor);
+  int32_t* s_nan = reinterpret_cast<int32_t*>(smem + C::kAtNan);
   const uint32_t bar = s_q + C::kAtBars;
   const uint32_t b_kfull = bar, b_kempty = bar + 8 * C::kStages, b_vfull = bar + 16 * C::kStages,
                  b_vempty = bar + 24 * C::kStages, b_info = bar + 32 * C::kStages, b_infoe = b_info + 8 * C::kBatches,
@@ -515,6 +559,7 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
   const int rows_all = n * G;  // (below 2^31: the caller's tokens x heads are)
   const int tiles = u.tile1 - u.tile0;
 
+  if (tid <= D) s_nan[tid] = tid < D ? 0x7FFFFFFF : 0;
   if (tid == 0) {
     for (int i = 0; i < 4 * C::kStages + C::kBatches; ++i) mbar_init(bar + 8 * i, 1);
     for (int i = 0; i < C::kBatches; ++i) mbar_init(b_infoe + 8 * i, C::kSoftWarps + 1);
@@ -631,6 +676,7 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
     const int sees = live ? min(len, len - n + token + 1) : 0;  // keys this row sees
     // keys before this one are seen by every row of the warp
     const int all_see = __reduce_min_sync(0xFFFFFFFFu, sees);
+    const int partial = first_partial(u, G);
     float m = -INFINITY, l = finite || sees <= 0 ? 0.0f : __int_as_float(0x7FC00000);
     // the two warps of a row agree on when to leave; a warp whose wait runs out meets the other until then
     bool left = false;
@@ -746,6 +792,11 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
       }
       tc::tmem_wait_st();
       tc::fence_before_sync();
+      if (j >= partial) {
+        ok = ok && wait(b_vfull + 8 * (j % C::kStages), (j / C::kStages) & 1);
+        if (ok) clear_nan<D, 32 * C::kSoftWarps>(s_v + (j % C::kStages) * TL::kBytes, (u.tile0 + j) * kTile, len, seen_by_all(u, G), tid, s_nan);
+        tc::fence_async_smem();
+      }
       mbar_arrive(b_p + 8 * (j & 1));
       if (j % C::kBatch == C::kBatch - 1 && lane == 0) mbar_arrive(b_infoe + 8 * slot);  // (the warp has met at the store)
     }
@@ -764,7 +815,7 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
       if (u.slot >= 0 && live && half == 0) p.ml[static_cast<int64_t>(u.slot) * C::kRows + r] = make_float2(m, l);
       store_rows<D, D / C::kSplitC, C::kQ / C::kSoftWarps>(p, u, C::kRows, r, live, token, row - token * G, G, tiles, l,
                                                            tmem + C::kO + lanes, half * (D / C::kSplitC),
-                                                           s_q + warp * (C::kQ / C::kSoftWarps));
+                                                           s_q + warp * (C::kQ / C::kSoftWarps), s_nan);
     }
   }
   tc::fence_before_sync();
@@ -822,7 +873,8 @@ struct NarrowCfg {
   static constexpr int kAtRow = kAtScale + kInfoRing * kGroups * 16;
   static constexpr int kAtFactor = kAtRow + kInfoRing * kGroups * 4;  // [kRows]
   static constexpr int kAtMax = kAtFactor + kRows * 4;             // [3][kRows]: reference, two sums
-  static constexpr int kAtBars = kAtMax + 3 * kRows * 4;
+  static constexpr int kAtNan = kAtMax + 3 * kRows * 4;            // [D + 1], see clear_nan
+  static constexpr int kAtBars = kAtNan + (D + 2) * 4;
   static constexpr int kBars = 2 * kStagesK + 2 * kStagesV + kStagesW + 2 * kBatches + 3 * kScores + 3 + kSoftWarps;
   static constexpr int kSmem = 1024 + kAtBars + 8 * kBars;
   static constexpr int kO = 128 * kScores;                // tensor memory: scores of three tiles, then output
@@ -864,11 +916,13 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
     int32_t* s_row = reinterpret_cast<int32_t*>(smem + C::kAtRow);
     float* s_factor = reinterpret_cast<float*>(smem + C::kAtFactor);
     float* s_max = reinterpret_cast<float*>(smem + C::kAtMax);
+    int32_t* s_nan = reinterpret_cast<int32_t*>(smem + C::kAtNan);
     const uint32_t b_kfull = s_q + C::kAtBars, b_kempty = b_kfull + 8 * C::kStagesK, b_vfull = b_kempty + 8 * C::kStagesK,
                    b_vempty = b_vfull + 8 * C::kStagesV, b_wfull = b_vempty + 8 * C::kStagesV, b_info = b_wfull + 8 * C::kStagesW,
                    b_infoe = b_info + 8 * C::kBatches, b_s = b_infoe + 8 * C::kBatches, b_pv = b_s + 8 * C::kScores,
                    b_p = b_pv + 8 * C::kScores, b_q = b_p + 8 * C::kScores, b_drain = b_q + 8, b_turn = b_drain + 16;
     if (tid < static_cast<int>(sizeof(PrefillUnit) / 4)) reinterpret_cast<int*>(&s_unit)[tid] = reinterpret_cast<const int*>(p.units + next)[tid];
+    if (tid <= D) s_nan[tid] = tid < D ? 0x7FFFFFFF : 0;
     if (tid < C::kBars) {
       // who arrives: a copy, a commit or one lane, but for what threads and warps release themselves
       const uint32_t b = b_kfull + 8 * tid;
@@ -949,6 +1003,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
       // whatever their page holds, become zero (0 * NaN is not 0)
       const int me = tid - 32 * C::kSoftWarps;
       constexpr int kChunks = D / 16;  // of a key
+      const int partial = first_partial(u, G);
       bool ok = true;
 #pragma unroll 1
       for (int j = 0; j < tiles && ok; ++j) {
@@ -956,6 +1011,9 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
         ok = wait(b_vfull + 8 * st, (j / C::kStagesV) & 1) && (j < 2 || wait(b_pv + 8 * ((j - 2) % C::kScores), ((j - 2) / C::kScores) & 1));
         if (!ok) break;
         const int keys = len - (u.tile0 + j) * kTile;
+        // (a thread clears the chunks that it converts)
+        if (j >= partial)
+          clear_nan<D, 32 * C::kConvWarps>(s_v + st * TL::kBytes, (u.tile0 + j) * kTile, len, seen_by_all(u, G), me, s_nan);
         const uint32_t from = s_v + st * TL::kBytes, to = s_v16 + (j & 1) * TV::kBytes;
 #pragma unroll 4
         for (int i = me; i < kTile * kChunks; i += 32 * C::kConvWarps) {
@@ -1128,7 +1186,7 @@ __global__ void __launch_bounds__(NarrowCfg<D>::kThreads, 1)
           const bool live = row < rows_all;
           if (u.slot >= 0 && live && own == 0) p.ml[static_cast<int64_t>(u.slot) * C::kRows + r] = make_float2(last, l);
           store_rows<D, D / 2, C::kQ / C::kSoftWarps>(p, u, C::kRows, r, live, token, row - token * G, G, tiles, l,
-                                                      tmem + C::kO + lanes, own * (D / 2), s_q + warp * (C::kQ / C::kSoftWarps));
+                                                      tmem + C::kO + lanes, own * (D / 2), s_q + warp * (C::kQ / C::kSoftWarps), s_nan);
         }
       }
     }
@@ -1180,7 +1238,7 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(const __grid_con
       const float root = e.x == -INFINITY ? (e.y == 0.0f ? 0.0f : 1.0f) : ex2_root(e.x - top), c = root * root;
       const float4 v = *reinterpret_cast<const float4*>(p.part + at * D + d4 * 4);
       sum += e.y * root * root;
-      if (c != 0.0f) {
+      if (e.x != -INFINITY || e.y != 0.0f) {  // (c may be 0 next to a NaN)
         o.x += v.x * c;
         o.y += v.y * c;
         o.z += v.z * c;

@@ -493,8 +493,7 @@ gdn_status gdn_attn_decode(const void* q, int64_t q_stride, const void* k_cache,
  * gives zeros. Otherwise as gdn_attn_decode, but for the probabilities: for the product with V
  * they keep 11 significant bits, and for head_dim 64 and 128 (f16) 2^-32, for 256 (three e5m2
  * parts) 2^-28 of the row's largest probability x v_scale; scales of keys that a row does not see
- * change nothing. A NaN
- * among a request's values reaches the rows that do not see it, too, if they share a 128-token tile.
+ * change nothing, and NaN among their keys or values does not either.
  *
  *   q          [total_tokens] rows of Hq * head_dim bf16, q_stride elements apart
  *   cu_tokens  [num_seqs + 1] int32, non-decreasing, at most total_tokens; rows of q outside it

@@ -228,3 +228,32 @@ def test_single_tokens_one_key_above_the_others(Hq, H, d, gap, flat):
 @pytest.mark.parametrize("which,T,d", [("decode", 2, 64), ("decode", 2, 128), ("decode", 2, 256), ("prefill", 70, 64), ("prefill", 70, 128)])
 def test_one_key_above_a_long_request(which, T, d):
     one_key_above_a_long_request(which, T, d)
+
+
+@pytest.mark.parametrize("Hq,H,d", HEADS)
+@pytest.mark.parametrize("old,T", [(0, 5), (0, 300), (90, 129), (5000, 64), (20000, 40)])
+def test_nan_in_a_value_stays_with_the_rows_that_see_it(Hq, H, d, old, T):
+    """NaN among the values of tokens, a column or all of them: in the columns of the rows that see it, and nowhere else;
+    NaN keys of tokens that a row does not see do nothing."""
+    n, r = old + T, rand(old + T + d)
+    c = Pages(r(n, H, d), r(n, H, d), 16)
+    q = r(T, Hq, d).bfloat16()
+    put = [(n - 1, 0, slice(None)), (n - 1 - T // 2, H - 1, slice(3, 4)), (old + T // 4, 0, slice(d - 1, d)), (old, H - 1, slice(17, 20))]
+    if old:
+        put.append((old // 2, 0, slice(5, 6)))
+    at = lambda pos: (int(c.table[0, pos // 16]), pos % 16)  # noqa: E731
+    for pos, h, cols in put:
+        c.vc[at(pos)[0], h, at(pos)[1], cols] = 0
+    want = run(c, q, "prefill").clone()
+    for pos, h, cols in put:
+        c.vc[at(pos)[0], h, at(pos)[1], cols] = 0xFF if pos % 2 else 0x7F
+        want[max(pos - old, 0):, h * (Hq // H):(h + 1) * (Hq // H), cols] = float("nan")
+    got = run(c, q, "prefill")
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got.nan_to_num(), want.nan_to_num())
+
+    if T > 8:  # keys
+        c.kc[at(n - 3)[0], :, at(n - 3)[1]] = 0x7F
+        got = run(c, q, "prefill")
+        assert torch.equal(got[:-3].isnan(), want[:-3].isnan()) and torch.equal(got[:-3].nan_to_num(), want[:-3].nan_to_num())
+        assert bool(got[-3:].isnan().all())

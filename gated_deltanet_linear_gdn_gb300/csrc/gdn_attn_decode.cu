@@ -890,8 +890,10 @@ template <int D, int HP>
 cudaError_t launch_decode_d(DecodeParams& p, const CacheMaps& maps, cudaStream_t s) {
   using C = DecodeCfg<D, HP>;
   auto kern = attn_decode_kernel<D, HP>;
-  const int smem = C::kSmem + 4 * (p.nb + p.nb / kCoarse + 2);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto smem_of = [](int nb) { return C::kSmem + 4 * (nb + nb / kCoarse + 2); };
+  const int smem = smem_of(p.nb);
+  // the same for every call: the limit is the kernel's, whichever thread sets it last
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(kBatchPerLaunch));
   if (e != cudaSuccess) return e;
   // CTAs of an SM by its shared memory, registers and tensor memory (the occupancy query answers 1 for
   // kernels that allocate tensor memory)

@@ -418,10 +418,11 @@ __global__ void __launch_bounds__(kAppThreads, 4) cache_append_kernel(AppendArgs
 }  // namespace
 
 cudaError_t launch_cache_tables(const TablesArgs& a, cudaStream_t s) {
-  const size_t smem = (static_cast<size_t>(a.B) * 5 + 1) * sizeof(int32_t);
-  if (smem > 48 * 1024) {
+  auto smem_of = [](int B) { return (static_cast<size_t>(B) * 5 + 1) * sizeof(int32_t); };
+  const size_t smem = smem_of(a.B);
+  if (smem > 48 * 1024) {  // the same for every such call: the limit is the kernel's, whichever thread sets it last
     cudaError_t e = cudaFuncSetAttribute(cache_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+                                         static_cast<int>(smem_of(kMaxTableBatch)));
     if (e != cudaSuccess) return e;
   }
   const bool in_place = a.pool_out == a.pool || a.lens == a.lens_old || a.lens == a.lens_new;

@@ -64,3 +64,26 @@ def test_first_call_of_a_thread():
     assert call() == gdn.GDN_OK
     torch.cuda.synchronize()
     assert together([call], 3) == [{gdn.GDN_OK}]
+
+
+def test_decode_batches_of_different_sizes():
+    keep = []
+    calls = [decode_call(B, keep) for B in (1, 250, 20)]
+    torch.cuda.synchronize()
+    assert together(calls, 6000) == [{gdn.GDN_OK}] * 3
+
+
+def test_tables_of_different_sizes():
+    L, bs, keep = gdn.lib(), 16, []
+
+    def call(B):
+        z = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+        old, new, table, ring, pool, out, cu, lens = z(B), z(B), z((B, 1)), z(8), z(2), z(2), z(B + 1), z(B)
+        stream = torch.cuda.Stream()
+        keep.extend([old, new, table, ring, pool, out, cu, lens, stream])
+        args = (p(old), p(new), B, p(table), 1, p(ring), 8, p(pool), p(out), bs, 0, p(cu), None, None, p(lens), None,
+                ctypes.c_void_p(stream.cuda_stream))
+        return lambda: L.gdn_cache_tables(*args)
+
+    torch.cuda.synchronize()
+    assert together([call(2600), call(8192), call(4000)], 6000) == [{gdn.GDN_OK}] * 3

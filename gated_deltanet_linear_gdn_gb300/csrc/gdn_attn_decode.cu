@@ -98,7 +98,9 @@ cudaError_t encode_cache_maps(CacheMaps* maps, const AttnArgs& a) {
 namespace {
 
 constexpr int kMaxUnitKeys = 1024;
-constexpr int kBatchPerLaunch = 384;   // requests of one launch (their lengths stay in shared memory)
+// Requests of one launch. Their lengths stay in shared memory, next to what two CTAs an SM leave of it (static_assert below):
+// with 384, batches of 330 to 384 ran one CTA an SM (384 requests of 2,000 tokens, 16 / 2 heads of 256: 205 us, and 167 in two launches).
+constexpr int kBatchPerLaunch = 320;
 constexpr int kCoarse = 16;            // requests between two kept tile sums
 constexpr int kThreads = 32 * 8;
 constexpr int kSmemPerSm = 228 * 1024;  // 1 KB of it taken by each resident CTA
@@ -163,7 +165,10 @@ struct DecodeCfg {
   static constexpr int kAtBars = kAtSum + 4 * 16 * 4;
   static constexpr int kAtPre = kAtBars + kBars * 8;             // then lens[nb], tsum[nb / kCoarse + 2]
   static constexpr int kSmem = 1024 + kAtPre;
+  static constexpr int smem_of(int nb) { return kSmem + 4 * (nb + nb / kCoarse + 2); }
   static_assert(kAtBars % 8 == 0 && kQ % 1024 == 0, "alignment");
+  // (128: what the kernel declares itself)
+  static_assert(HP == 16 || 2 * (smem_of(kBatchPerLaunch) + 128 + 1024) <= kSmemPerSm, "two CTAs an SM");
 };
 
 // The units of one CTA, in order: those whose first tile lies in its equal share of the launch's tiles (all
@@ -890,10 +895,9 @@ template <int D, int HP>
 cudaError_t launch_decode_d(DecodeParams& p, const CacheMaps& maps, cudaStream_t s) {
   using C = DecodeCfg<D, HP>;
   auto kern = attn_decode_kernel<D, HP>;
-  auto smem_of = [](int nb) { return C::kSmem + 4 * (nb + nb / kCoarse + 2); };
-  const int smem = smem_of(p.nb);
+  const int smem = C::smem_of(p.nb);
   // the same for every call: the limit is the kernel's, whichever thread sets it last
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(kBatchPerLaunch));
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem_of(kBatchPerLaunch));
   if (e != cudaSuccess) return e;
   // CTAs of an SM by its shared memory, registers and tensor memory (the occupancy query answers 1 for
   // kernels that allocate tensor memory)

@@ -936,8 +936,17 @@ cudaError_t launch_decode_h(DecodeParams& p, const CacheMaps& maps, cudaStream_t
 
 }  // namespace
 
+int attn_decode_batch(int max_blocks, int Hq, int H, int bs) {
+  // shares of a launch are counted in 32 bits, in tiles of all its requests, kv heads and head chunks (requests may have pages
+  // in common, so the cache's size is no bound)
+  const int64_t each = (static_cast<int64_t>(max_blocks) * bs + kTile - 1) / kTile * H * ((Hq / H + 15) / 16);
+  const int64_t most = 0x7fffffffLL / each;
+  return static_cast<int>(most < kBatchPerLaunch ? most : kBatchPerLaunch);
+}
+
 size_t attn_decode_workspace(int B, int max_blocks, int Hq, int H, int d, int bs) {
-  return decode_layout(B < kBatchPerLaunch ? B : kBatchPerLaunch, max_blocks, Hq, H, d, bs).total;
+  const int most = attn_decode_batch(max_blocks, Hq, H, bs);
+  return decode_layout(B < most ? B : most, max_blocks, Hq, H, d, bs).total;
 }
 
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s) {
@@ -950,7 +959,8 @@ cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s) {
   p.heads = G < 16 ? G : 16;
   p.chunks = (G + 15) / 16;
   p.each = static_cast<int>(most_units(static_cast<int64_t>(a.max_blocks) * a.bs));
-  const int launches = (a.B + kBatchPerLaunch - 1) / kBatchPerLaunch, per = (a.B + launches - 1) / launches;
+  const int most = attn_decode_batch(a.max_blocks, a.Hq, a.H, a.bs);  // (not 0: the caller has checked)
+  const int launches = (a.B + most - 1) / most, per = (a.B + launches - 1) / launches;
   for (int b0 = 0; b0 < a.B; b0 += per) {
     p.b0 = b0;
     p.nb = a.B - b0 < per ? a.B - b0 : per;

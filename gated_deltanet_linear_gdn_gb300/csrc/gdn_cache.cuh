@@ -74,6 +74,8 @@ cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t s);
 // The largest batch of one gdn_cache_tables call (its per-row sums stay in shared memory).
 constexpr int kMaxTableBatch = 8192;
 
+// Requests of one launch; 0 if a single one of that many blocks is too long for its heads.
+int attn_decode_batch(int max_blocks, int Hq, int H, int bs);
 size_t attn_decode_workspace(int B, int max_blocks, int Hq, int H, int d, int bs);
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s);
 size_t attn_prefill_workspace(int T, int B, int max_blocks, int Hq, int H, int d, int bs);

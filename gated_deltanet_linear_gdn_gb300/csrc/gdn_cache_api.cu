@@ -116,6 +116,7 @@ gdn_status gdn_cache_append(const void* k, int64_t k_stride, const void* v, int6
 
 size_t gdn_attn_decode_workspace_size(int32_t batch, int32_t max_blocks, gdn_cache_dims dims) {
   if (batch <= 0 || max_blocks <= 0 || check_cache(dims, 1, true) != GDN_OK) return 0;
+  if (gdn::attn_decode_batch(max_blocks, dims.num_q_heads, dims.num_kv_heads, dims.block_size) == 0) return 0;
   return gdn::attn_decode_workspace(batch, max_blocks, dims.num_q_heads, dims.num_kv_heads, dims.head_dim,
                                     dims.block_size);
 }
@@ -131,6 +132,7 @@ gdn_status gdn_attn_decode(const void* q, int64_t q_stride, const void* k_cache,
   const gdn_status st = check_attn(q, q_stride, k_cache, v_cache, k_scale, v_scale, num_blocks, block_table,
                                    max_blocks, lens, batch, dims, scale, out, workspace, err, a);
   if (st != GDN_OK) return st;
+  if (gdn::attn_decode_batch(max_blocks, dims.num_q_heads, dims.num_kv_heads, dims.block_size) == 0) return GDN_ERR_UNSUPPORTED;
   if (workspace_bytes < gdn_attn_decode_workspace_size(batch, max_blocks, dims)) return GDN_ERR_INVALID_ARG;
   return from_cuda(gdn::launch_attn_decode(a, static_cast<cudaStream_t>(stream)));
 }

@@ -475,6 +475,7 @@ gdn_status gdn_cache_append(const void* k, int64_t k_stride, const void* v, int6
  *   out        [batch, Hq, head_dim] bf16, 16-byte aligned
  *   workspace  device scratch of >= gdn_attn_decode_workspace_size bytes, 256-byte aligned; its
  *              contents on entry do not matter
+ * Supported: batch <= 65535, max_blocks * block_size / 128 * Hkv * ceil(Hq / Hkv / 16) < 2^31.
  * batch == 0 is a no-op.
  */
 size_t gdn_attn_decode_workspace_size(int32_t batch, int32_t max_blocks, gdn_cache_dims dims);
@@ -501,7 +502,7 @@ gdn_status gdn_attn_decode(const void* q, int64_t q_stride, const void* k_cache,
  *              range is not within total_tokens sets GDN_DEVERR_SEQLENS and counts as empty
  *   out        [total_tokens, Hq, head_dim] bf16, 16-byte aligned
  *   workspace  device scratch of >= gdn_attn_prefill_workspace_size bytes, 256-byte aligned
- * num_seqs == 0 or total_tokens == 0 is a no-op.
+ * Supported: num_seqs <= 65535, total_tokens * Hq < 2^31 - 65536. num_seqs == 0 or total_tokens == 0 is a no-op.
  */
 size_t gdn_attn_prefill_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_t max_blocks,
                                        gdn_cache_dims dims);

@@ -1,0 +1,38 @@
+"""Sizes at the top of what 32-bit indices hold, through the C ABI, without a GPU: refused before any CUDA call, or split
+into launches that stay below (seen in the workspace's size)."""
+import ctypes
+
+import pytest
+
+import gated_deltanet_linear_gdn_gb300 as gdn
+from gated_deltanet_linear_gdn_gb300 import build
+
+P = ctypes.c_void_p
+FAKE = P(0x10000)  # never dereferenced: every call below fails its checks first
+INV, UNS = gdn.GDN_ERR_INVALID_ARG, gdn.GDN_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build_library()
+    return gdn.lib()
+
+
+def decode(L, B, W, q, kv, d=64, bs=128, size=1 << 62):
+    dims = gdn.gdn_cache_dims(q, kv, d, bs)
+    return L.gdn_attn_decode(FAKE, 1024 * d, FAKE, FAKE, FAKE, FAKE, 10, FAKE, W, FAKE, B, dims, 0.1, FAKE, FAKE, size, None, None)
+
+
+def test_decode_tiles_of_a_launch(L):
+    """Tiles of 128 keys x kv heads x groups of 16 query heads, over a launch's requests, are counted in 32 bits."""
+    size = gdn.gdn_attn_decode_workspace_size
+    # one request of 2^24 blocks of 128 for 1,024 kv heads: 2^34 tiles
+    assert decode(L, 1, (1 << 24) - 20, 1024, 1024) == UNS and size(1, (1 << 24) - 20, 1024, 1024, 64, 128) == 0
+    # 2^21 tiles a head: 1,023 fit, and 1,024 don't
+    assert decode(L, 1, 1 << 21, 1024, 1024) == UNS
+    assert decode(L, 1, 1 << 21, 1023, 1023, size=100) == INV        # (supported: the workspace is too small)
+    # 2^16 tiles, 128 heads: 2^23 a request, 255 of them in a launch
+    assert size(255, 1 << 16, 128, 128, 64, 128) == size(256, 1 << 16, 128, 128, 64, 128) == size(9999, 1 << 16, 128, 128, 64, 128)
+    assert size(254, 1 << 16, 128, 128, 64, 128) < size(255, 1 << 16, 128, 128, 64, 128)
+    # ordinary sizes take as many requests a launch as before
+    assert size(319, 1 << 10, 32, 8, 128, 64) < size(320, 1 << 10, 32, 8, 128, 64) == size(321, 1 << 10, 32, 8, 128, 64)

@@ -4,6 +4,9 @@
 
 namespace {
 
+// Tokens of a call of the tables or the writer: kernels step past the last one in 32 bits, by a grid's share at most.
+constexpr int32_t kMaxTokens = 0x7fffffff - (1 << 20);
+
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
 gdn_status from_cuda(cudaError_t e) { return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA; }
@@ -15,8 +18,9 @@ gdn_status check_cache(const gdn_cache_dims& d, int32_t num_blocks, bool attn) {
   if (d.head_dim != 64 && d.head_dim != 128 && d.head_dim != 256) return GDN_ERR_UNSUPPORTED;
   if (d.block_size != 16 && d.block_size != 32 && d.block_size != 64 && d.block_size != 128) return GDN_ERR_UNSUPPORTED;
   if (d.num_kv_heads > 1024 || (attn && d.num_q_heads > 1024)) return GDN_ERR_UNSUPPORTED;
-  // rows of the cache are addressed by 32-bit TMA coordinates, tokens by 32-bit slots
-  if (static_cast<int64_t>(num_blocks) * d.num_kv_heads * d.block_size > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
+  // rows of the cache are addressed by 32-bit TMA coordinates (a box of up to 128 starts past the last one where there is no
+  // page), tokens by 32-bit slots
+  if (static_cast<int64_t>(num_blocks) * d.num_kv_heads * d.block_size > 0x7fffffffLL - 128) return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }
 
@@ -75,7 +79,7 @@ gdn_status gdn_cache_tables(const int32_t* lens_old, const int32_t* lens_new, in
                             void* stream) {
   if (batch < 0 || max_blocks <= 0 || num_blocks <= 0 || total_tokens < 0) return GDN_ERR_INVALID_ARG;
   if (block_size != 16 && block_size != 32 && block_size != 64 && block_size != 128) return GDN_ERR_UNSUPPORTED;
-  if (batch > gdn::kMaxTableBatch) return GDN_ERR_UNSUPPORTED;
+  if (batch > gdn::kMaxTableBatch || total_tokens > kMaxTokens) return GDN_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(num_blocks) * block_size > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(max_blocks) * block_size > 0x7fffffffLL - 2048) return GDN_ERR_UNSUPPORTED;
   if (batch == 0) return GDN_OK;
@@ -101,6 +105,7 @@ gdn_status gdn_cache_append(const void* k, int64_t k_stride, const void* v, int6
   const gdn_status st = check_cache(dims, num_blocks, false);
   if (st != GDN_OK) return st;
   if (total_tokens < 0) return GDN_ERR_INVALID_ARG;
+  if (total_tokens > kMaxTokens) return GDN_ERR_UNSUPPORTED;
   if (total_tokens == 0) return GDN_OK;
   if (!k || !v || !slot_map || !k_cache || !v_cache || !k_scale || !v_scale) return GDN_ERR_INVALID_ARG;
   const int64_t row = static_cast<int64_t>(dims.num_kv_heads) * dims.head_dim;

@@ -423,7 +423,7 @@ typedef struct {
  *              filled with -1 (a padded step), and a step with more sets GDN_DEVERR_SEQLENS
  *   cu_tokens  [batch + 1] int32;  slot_map, positions [total_tokens] int32 (NULL if 0)
  *   lens       [batch] int32: each row's length after the call; may be lens_old or lens_new
- * Supported: batch <= 8192. batch == 0 is a no-op.
+ * Supported: batch <= 8192, total_tokens < 2^31 - 2^20. batch == 0 is a no-op.
  */
 gdn_status gdn_cache_tables(const int32_t* lens_old, const int32_t* lens_new, int32_t batch,
                             int32_t* block_table, int32_t max_blocks, int32_t* free_ring,
@@ -450,7 +450,7 @@ gdn_status gdn_cache_tables(const int32_t* lens_old, const int32_t* lens_new, in
  *   slot_map   [total_tokens] int32; negative: the token is skipped; past the cache:
  *              GDN_DEVERR_BLOCK_RANGE, skipped
  *   k_cache, v_cache (16-byte aligned), k_scale, v_scale: in place. dims.num_q_heads is not used.
- * total_tokens == 0 is a no-op.
+ * Supported: total_tokens < 2^31 - 2^20. total_tokens == 0 is a no-op.
  */
 gdn_status gdn_cache_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                             const int32_t* slot_map, int32_t total_tokens, void* k_cache,

@@ -36,3 +36,25 @@ def test_decode_tiles_of_a_launch(L):
     assert size(254, 1 << 16, 128, 128, 64, 128) < size(255, 1 << 16, 128, 128, 64, 128)
     # ordinary sizes take as many requests a launch as before
     assert size(319, 1 << 10, 32, 8, 128, 64) < size(320, 1 << 10, 32, 8, 128, 64) == size(321, 1 << 10, 32, 8, 128, 64)
+
+
+def tables(L, T, W=4, bs=16):
+    return L.gdn_cache_tables(FAKE, FAKE, 3, FAKE, W, FAKE, 20, FAKE, FAKE, bs, T, FAKE, FAKE, P(0x10001), FAKE, None, None)
+
+
+def append(L, T, N=10, kv=1):
+    return L.gdn_cache_append(FAKE, 64 * kv, P(0x10002), 64 * kv, FAKE, T, FAKE, FAKE, FAKE, FAKE, N, gdn.gdn_cache_dims(kv, kv, 64, 16), None, None)
+
+
+def test_tokens_of_a_call(L):
+    """The kernels step over tokens in 32 bits, a grid's share (2^17) past the last. (An address that is not aligned ends the
+    calls that the sizes let through.)"""
+    assert tables(L, 2 ** 31 - 1) == tables(L, 2 ** 31 - 2 ** 18) == UNS
+    assert tables(L, 2 ** 31 - 2 ** 21) == INV
+    assert append(L, 2 ** 31 - 1) == append(L, 2 ** 31 - 200) == UNS
+    assert append(L, 2 ** 31 - 2 ** 21) == INV
+
+
+def test_rows_of_a_cache(L):
+    """A page that is none is read past the cache's last row, a box of up to 128 rows in 32 bits."""
+    assert append(L, 4, N=(1 << 27) - 1) == UNS and append(L, 4, N=(1 << 27) - 9) == INV

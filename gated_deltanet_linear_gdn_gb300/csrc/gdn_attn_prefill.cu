@@ -40,6 +40,7 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kBatchPerLaunch = 2048;
 constexpr int kBuckets = 256;
+constexpr int kManyUnits = 1 << 30;
 // key splits: a request with fewer than few_units(d) row tiles x heads gets up to three times as many (head_dim 256:
 // half, as its partial sums are twice as large)
 constexpr int kUnitRows = 128;  // (token, head) rows of a unit
@@ -136,14 +137,16 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
       s_warp[1][warp] = w;
     }
     __syncthreads();
+    // Ranges of cu_tokens that lie over one another may add up to more than 32 bits hold: the sum stops at kManyUnits, which no
+    // list has room for (a warp's requests have at most 32 * (2^24 + 2^10) units)
     int bv = carry, bw = carry_slot;
 #pragma unroll 4
     for (int i = 0; i < kPlanThreads / 32; ++i) {
       if (i < warp) {
-        bv += s_warp[0][i];
+        bv = min(bv + s_warp[0][i], kManyUnits);
         bw += s_warp[1][i];
       }
-      carry += s_warp[0][i];
+      carry = min(carry + s_warp[0][i], kManyUnits);
       carry_slot += s_warp[1][i];
     }
     if (b < p.nb) {

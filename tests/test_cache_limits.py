@@ -1,6 +1,8 @@
 """Sizes at the top of what 32-bit indices hold, through the C ABI, without a GPU: refused before any CUDA call, or split
 into launches that stay below (seen in the workspace's size)."""
 import ctypes
+import os
+import re
 
 import pytest
 
@@ -58,3 +60,21 @@ def test_tokens_of_a_call(L):
 def test_rows_of_a_cache(L):
     """A page that is none is read past the cache's last row, a box of up to 128 rows in 32 bits."""
     assert append(L, 4, N=(1 << 27) - 1) == UNS and append(L, 4, N=(1 << 27) - 9) == INV
+
+
+def test_units_of_a_plan_are_summed_within_32_bits():
+    """The prompt kernels' plan adds up the units of ranges that the caller's table may let lie over one another, each of up to
+    2^31 / 128 rows and 1,024 heads more: its sums, block by block of 32 warps as in csrc/gdn_attn_prefill.cu, stay in
+    32 bits and never come out below what the list holds."""
+    src = open(os.path.join(build.CSRC, "gdn_attn_prefill.cu")).read()
+    assert "carry = min(carry + s_warp[0][i], kManyUnits);" in src and "bv = min(bv + s_warp[0][i], kManyUnits);" in src
+    many = 1 << int(re.search(r"kManyUnits = 1 << (\d+);", src).group(1))
+    most_of_request = (2 ** 31 - 65536) // 128 + 1024
+    largest_list = most_of_request + 1024 * 2048 + 2048 * 3 * 152
+    for each in (1, 1000, 2 ** 16, 2 ** 21, most_of_request):
+        carry = 0
+        for _ in range(2):                        # 2,048 requests, 1,024 at a time
+            for _ in range(32):
+                assert carry + 32 * each < 2 ** 31
+                carry = min(carry + 32 * each, many)
+        assert (carry > largest_list) == (2048 * each > largest_list)

@@ -257,3 +257,20 @@ def test_nan_in_a_value_stays_with_the_rows_that_see_it(Hq, H, d, old, T):
         got = run(c, q, "prefill")
         assert torch.equal(got[:-3].isnan(), want[:-3].isnan()) and torch.equal(got[:-3].nan_to_num(), want[:-3].nan_to_num())
         assert bool(got[-3:].isnan().all())
+
+
+@pytest.mark.parametrize("Hq,H,d", [(4, 2, 64), (8, 2, 128), (16, 2, 256)])
+@pytest.mark.parametrize("scale", [float("inf"), float("nan"), -1.0, 0.0, 3e38, 1e-45])
+def test_scales_of_pages_that_a_row_does_not_see(Hq, H, d, scale):
+    """Whatever stands for the scales of later tokens' pages: the rows before them do not change."""
+    old, T = 100, 60
+    n, r = old + T, rand(d)
+    c = Pages(r(n, H, d), r(n, H, d), 16)
+    q = r(T, Hq, d).bfloat16()
+    want = run(c, q, "prefill")[:28].clone()
+    for which in (c.vs, c.ks):
+        page = c.table[0, 8:].long()          # tokens 128 on: row 28 is the first to see one
+        was = which[page].clone()
+        which[page] = scale
+        assert torch.equal(run(c, q, "prefill")[:28], want)
+        which[page] = was

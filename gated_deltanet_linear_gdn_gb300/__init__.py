@@ -338,7 +338,7 @@ def _tokens(t, shape, name):
     step, of_head, of_d = t.stride()
     if not t.is_cuda or (of_d != 1 and d > 1) or (of_head != d and heads > 1):
         raise ValueError(f"{name} must be a device tensor with dense heads")
-    return t.data_ptr(), (step if n > 1 else max(step, heads * d))
+    return t.data_ptr(), (step if n > 1 else heads * d)  # (one token: its stride means nothing)
 
 
 @functools.lru_cache(maxsize=None)

@@ -274,3 +274,27 @@ def test_scales_of_pages_that_a_row_does_not_see(Hq, H, d, scale):
         which[page] = scale
         assert torch.equal(run(c, q, "prefill")[:28], want)
         which[page] = was
+
+
+@pytest.mark.parametrize("which", ["decode", "prefill"])
+def test_one_token_of_any_stride(which):
+    """The stride of a single token is not used: torch gives any."""
+    n, H, Hq, d, r = 40, 2, 4, 64, rand(1)
+    c = Pages(r(n, H, d), r(n, H, d), 16)
+    q = r(1, Hq, d).bfloat16()
+    for step in (0, 1, Hq * d + 4, 10 ** 6 + 1):
+        want = run(c, q, which)  # (the writes below change a page's scale)
+        odd = q.as_strided(q.shape, (step, d, 1))
+        out = torch.empty(1, Hq, d, dtype=torch.bfloat16, device="cuda")
+        ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+        if which == "decode":
+            gdn.gdn_attn_decode(odd, *c.pools(), c.table, i32([n]), out, ws)
+        else:
+            gdn.gdn_attn_prefill(odd, i32([0, 1]), *c.pools(), c.table, i32([n]), out, ws)
+        assert torch.equal(out, want)
+        k = r(1, H, d).bfloat16()
+        odd = k.as_strided(k.shape, (step, d, 1))
+        gdn.gdn_cache_append(odd, odd, i32([int(c.table[0, 2]) * 16 + 9]), *c.pools())
+        kept = run(c, q, which)
+        gdn.gdn_cache_append(k, k, i32([int(c.table[0, 2]) * 16 + 9]), *c.pools())
+        assert torch.equal(run(c, q, which), kept)

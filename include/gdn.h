@@ -404,7 +404,9 @@ typedef struct {
  *   - a row with n(new) > n(old) takes blocks from the head of the free ring, in row order, into
  *     block_table[b, n(old) ..]; rows are served until the blocks that were free when the call
  *     began run out: a row that needs more than is left is refused (GDN_DEVERR_BLOCKS), keeps its
- *     length, and its new tokens get slot -1;
+ *     length, and its new tokens get slot -1. They are in cu_tokens all the same, and the attention
+ *     calls of the step compute rows for them that mean nothing (see there): a caller looks at the
+ *     error word, or compares lens with lens_new, before it uses them;
  *   - a row with n(new) < n(old) puts block_table[b, n(new) .. n(old)) back at the ring's tail, in
  *     row order. Its table entries stay as they are and mean nothing; the blocks can be
  *     taken from the next call on;
@@ -463,11 +465,12 @@ gdn_status gdn_cache_append(const void* k, int64_t k_stride, const void* v, int6
  *
  * Per request b and query head h (kv head h / (Hq / Hkv)), over its lens[b] cached tokens:
  *   out[b, h] = sum_j softmax_j(scale * q[b, h] . k_j) v_j
- * A request of length 0 (or with no readable block) gives zeros. A length outside [0, max_blocks *
- * block_size] sets GDN_DEVERR_SEQLENS and is clamped. What lies in a block past the request's
- * length is never used, NaN bytes included. Softmax statistics and sums are fp32. Queries are
- * exact to 2^-18 of a head's largest element; for the product with V the probabilities keep 16
- * significant bits, and no less than 2^-26 of the row's largest probability x v_scale.
+ * A request of length 0 (or with no readable block) gives zeros; one that gdn_cache_tables refused
+ * attends without its new token. A length outside [0, max_blocks * block_size] sets
+ * GDN_DEVERR_SEQLENS and is clamped. What lies in a block past the request's length is never used,
+ * NaN bytes included. Softmax statistics and sums are fp32. Queries are exact to 2^-18 of a head's
+ * largest element; for the product with V the probabilities keep 16 significant bits, and no less
+ * than 2^-26 of the row's largest probability x v_scale.
  *
  *   q          [batch] rows of Hq * head_dim bf16, q_stride elements apart (16-byte aligned, a
  *              multiple of 8)
@@ -490,11 +493,12 @@ gdn_status gdn_attn_decode(const void* q, int64_t q_stride, const void* k_cache,
  * gdn_attn_prefill -- attention of prompt tokens over the cache, causal. Request b's new tokens
  * are rows cu_tokens[b] .. cu_tokens[b + 1] of q; their keys and values are in the cache already
  * (append first) as the last of its lens[b] tokens. With n new tokens, token i attends to
- * positions 0 .. lens[b] - n + i; a token that sees nothing (lens[b] < n: its row was refused)
- * gives zeros. Otherwise as gdn_attn_decode, but for the probabilities: for the product with V
- * they keep 11 significant bits, and for head_dim 64 and 128 (f16) 2^-32, for 256 (three e5m2
- * parts) 2^-28 of the row's largest probability x v_scale; scales of keys that a row does not see
- * change nothing, and NaN among their keys or values does not either.
+ * positions 0 .. lens[b] - n + i; a token that sees nothing (lens[b] < n) gives zeros. A row that
+ * gdn_cache_tables refused has its tokens in cu_tokens and not in lens: what comes out for them is
+ * attention of the wrong positions, or zeros. Otherwise as gdn_attn_decode, but for the
+ * probabilities: for the product with V they keep 11 significant bits, and 2^-32 (head_dim 64 and
+ * 128, f16) or 2^-28 (256, three e5m2 parts) of the row's largest probability x v_scale. Keys that
+ * a row does not see change nothing, whatever their bytes and scales, NaN included.
  *
  *   q          [total_tokens] rows of Hq * head_dim bf16, q_stride elements apart
  *   cu_tokens  [num_seqs + 1] int32, non-decreasing, at most total_tokens; rows of q outside it
@@ -502,7 +506,8 @@ gdn_status gdn_attn_decode(const void* q, int64_t q_stride, const void* k_cache,
  *              range is not within total_tokens sets GDN_DEVERR_SEQLENS and counts as empty
  *   out        [total_tokens, Hq, head_dim] bf16, 16-byte aligned
  *   workspace  device scratch of >= gdn_attn_prefill_workspace_size bytes, 256-byte aligned
- * Supported: num_seqs <= 65535, total_tokens * Hq < 2^31 - 65536. num_seqs == 0 or total_tokens == 0 is a no-op.
+ * Supported: num_seqs <= 65535, total_tokens * Hq < 2^31 - 65536. num_seqs == 0 or total_tokens == 0
+ * is a no-op.
  */
 size_t gdn_attn_prefill_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_t max_blocks,
                                        gdn_cache_dims dims);

@@ -146,6 +146,9 @@ __device__ __forceinline__ float exponent_scale(float ks, float factor) { return
 // log2 of the scales of V below which a key's part of the row's sum is computed by itself: from p * vs, as elsewhere, it
 // would be lost where the row's largest p * vs is 2^126 times as large.
 constexpr int kFarScale = -30;
+// log2 of the least scale of V. Smaller ones, zero among them, count as it: a row's sum is of (p vs) / vs, and 2^15 / 2^-90 for
+// each of 2^20 keys is within what fp32 holds. (The writer's least is 2^-64.)
+constexpr int kLeastScale = -90;
 
 // 8-bit MMAs (kind::f8f6f4, e4m3 x e4m3, fp32 accumulators, 32 elements of K per instruction).
 __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t acc) {

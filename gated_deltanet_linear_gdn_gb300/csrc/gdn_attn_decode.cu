@@ -638,8 +638,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
           tmem_load(tmem + C::kNQ * (i & 1) + lanes, s);
           const float2* sc = s_scale + (i % C::kInfoRing) * kGroups;
           own = sc[tid / kGroup];
-          // (e from -64, the writer's least scale, so that zero is one of the scales)
-          e = static_cast<float>(max((__float_as_int(own.y) >> 23) & 255, 63) - 127);
+          e = static_cast<float>(max(((__float_as_int(own.y) >> 23) & 255) - 127, kLeastScale));
           __syncwarp();  // the batch's last tile: its lookups have been read
           if (i % C::kBatch == C::kBatch - 1 && lane == 0) mbar_arrive(b_infoe + 8 * ((i / C::kBatch) % C::kBatches));
           const bool hidden = t * kTile + tid >= keys || own.x < 0.0f;

@@ -252,10 +252,9 @@ __device__ __forceinline__ void look_up(const PrefillParams& p, const PrefillUni
         sc.x = a.k_scale[at];
         sc.y = a.v_scale[at];
         row = (static_cast<int>(at) << shift) + (pos & (a.bs - 1));
-        // The writer's least scale stands for smaller ones, zero among them: 1 / vs has to leave room for sums. Finite in any
-        // case: a hidden score is -infinity and has to stay that.
+        // (finite in any case: a hidden score is -infinity and has to stay that)
         asm("lg2.approx.f32 %0, %0;" : "+f"(sc.y));
-        sc.y = fminf(fmaxf(sc.y, -64.0f), 127.0f);
+        sc.y = fminf(fmaxf(sc.y, kLeastScale), 127.0f);
         sc.z = sc.y < kFarScale ? 0.0f : ex2(-sc.y);
       } else if (a.err) {
         atomicOr(a.err, GDN_DEVERR_BLOCK_RANGE);

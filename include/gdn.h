@@ -383,8 +383,8 @@ void gdn_graph_destroy(gdn_graph* graph);
  *
  * Cache: k_cache and v_cache [num_blocks, Hkv, block_size, head_dim] in e4m3 (one byte, 1-4-3,
  * largest value 448), k_scale and v_scale [num_blocks, Hkv] f32: an element stands for byte *
- * scale of its block and head. Scales are positive and normal (zero is fine for a v_scale; to the
- * prompt call those below 2^-64, the writer's least, are 2^-64). A request's token at position p
+ * scale of its block and head. Scales are positive and normal (the writer's are 2^-64 and above; to
+ * the attention calls a v_scale below 2^-90, zero included, may count as 2^-90). A request's token at position p
  * lies in block block_table[b, p / block_size] at offset p % block_size; its slot is
  * block * block_size + offset.
  */

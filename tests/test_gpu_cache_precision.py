@@ -104,7 +104,7 @@ def exact(c, q, which):
         e = 2 * ((2.0 ** -18 + d * 2.0 ** -24) * size + 2.0 ** -21 * (1 + torch.where(hidden, 0.0, s).abs().amax(dim=1, keepdim=True)))
         mag = p @ vh.abs()
         least = (p * vs[:, h]).amax(dim=1, keepdim=True) * floor * ((~hidden).double() @ (vh.abs() / vs[:, h, None]).nan_to_num())
-        tol[:, m] = (2.0 ** -bits + e + c.n * 2.0 ** -24) * mag + least + 2.0 ** -8 * o.abs() + 1e-30
+        tol[:, m] = (2.0 ** -bits + e + c.n * 2.0 ** -24) * mag + least + 2.0 ** -8 * o.abs() + 1e-38
     return out, tol
 
 
@@ -298,3 +298,14 @@ def test_one_token_of_any_stride(which):
         kept = run(c, q, which)
         gdn.gdn_cache_append(k, k, i32([int(c.table[0, 2]) * 16 + 9]), *c.pools())
         assert torch.equal(run(c, q, which), kept)
+
+
+@pytest.mark.parametrize("which,T", [("decode", 2), ("prefill", 3), ("prefill", 200)])
+@pytest.mark.parametrize("Hq,H,d", HEADS)
+@pytest.mark.parametrize("power", [-78, -50, 60, 100])
+def test_values_of_any_size(which, T, Hq, H, d, power):
+    """All values of a request as small as scales of 2^-90, and as large as bf16 has room for."""
+    n, r = 1000, rand(power + 200)
+    c = Pages(r(n, H, d), 1.0 + r(n, H, d), 16)
+    c.vs *= 2.0 ** power
+    check(c, r(T, Hq, d).bfloat16(), which)

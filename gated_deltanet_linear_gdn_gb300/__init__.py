@@ -29,6 +29,7 @@ GDN_GATE_FUSED, GDN_GATE_DIRECT = 0, 1
 GDN_DEVERR_SLOT_RANGE, GDN_DEVERR_SEQLENS, GDN_DEVERR_TIMEOUT = 1, 2, 4
 GDN_DEVERR_BLOCKS, GDN_DEVERR_BLOCK_RANGE = 8, 16
 GDN_TEST_FAULT_NONE, GDN_TEST_FAULT_DECODE_CONSUMER, GDN_TEST_FAULT_PREFILL_PASS = 0, 1, 2
+GDN_TEST_FAULT_ATTENTION = 4
 GDN_ACT_SILU, GDN_ACT_SIGMOID = 0, 1
 
 

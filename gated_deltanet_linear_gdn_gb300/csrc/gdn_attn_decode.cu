@@ -86,6 +86,11 @@ cudaError_t encode_cache_map(CUtensorMap* map, const uint8_t* cache, int64_t tot
 
 }  // namespace
 
+std::atomic<int>& attention_test_fault() {
+  static std::atomic<int> mode{0};
+  return mode;
+}
+
 cudaError_t encode_cache_maps(CacheMaps* maps, const AttnArgs& a) {
   const int64_t rows = static_cast<int64_t>(a.num_blocks) * a.H * a.bs;
   cudaError_t e = encode_cache_map(&maps->k_group, a.k_cache, rows, a.d, kGroup);
@@ -128,6 +133,7 @@ struct DecodeParams {
   int heads;      // query heads of one unit: min(G, 16)
   int chunks;     // units' head chunks per kv head: ceil(G / 16)
   int b0, nb;     // the launch's requests
+  int fault;      // test hook: CTA 0 looks up one batch of tiles and no more
   int each;       // the most units of a request's (kv head, chunk): unit u of it has slot (b * HC + hc) * each + u
   float2* ml;     // workspace: [slots][heads] (maximum, sum) of a unit that is one of several
   float* part;    // [slots][heads][D]
@@ -390,6 +396,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
     int t = 0;  // the next tile of the walk's unit
     bool ok = true;
     for (int batch = 0; ok; ++batch) {
+      if (p.fault && blockIdx.x == 0 && batch == 1) break;
       int keys = 0, pos = 0, b = 0, h = 0;  // this lane's tile
 #pragma unroll 1
       for (int j = 0; j < C::kBatch && w.more(); ++j) {
@@ -955,6 +962,7 @@ cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s) {
   const int G = a.Hq / a.H;
   DecodeParams p;
   p.a = a;
+  p.fault = attention_test_fault().load(std::memory_order_relaxed);
   p.heads = G < 16 ? G : 16;
   p.chunks = (G + 15) / 16;
   p.each = static_cast<int>(most_units(static_cast<int64_t>(a.max_blocks) * a.bs));

@@ -56,6 +56,7 @@ struct PrefillParams {
   AttnArgs a;
   int b0, nb;
   int max_units, max_slots;
+  int fault;                // test hook: CTA 0 looks up one batch of tiles and no more
   int32_t* counts;          // [0] units, [1] split tiles, [2] units taken after the grid's first
   PrefillUnit* units;       // [max_units]
   PrefillUnit* joins;       // [max_units]: the first split of each split row tile
@@ -242,6 +243,7 @@ __device__ __forceinline__ void look_up(const PrefillParams& p, const PrefillUni
   bool ok = true;
 #pragma unroll 1
   for (int j0 = 0; j0 < tiles && ok; j0 += C::kBatch) {
+    if (p.fault && blockIdx.x == 0 && j0 > 0) break;
     const int j = j0 + lane / kGroups, pos = (u.tile0 + j) * kTile + (lane % kGroups) * kGroup;
     int row = a.num_blocks * a.H * a.bs;                      // past the cache: zeros
     float4 sc = make_float4(0.0f, -INFINITY, 0.0f, 0.0f);     // no key, or a page that is none: not seen
@@ -1335,6 +1337,7 @@ cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t s) {
   for (int b0 = 0; b0 < a.B; b0 += kBatchPerLaunch) {
     PrefillParams p;
     p.a = a;
+    p.fault = attention_test_fault().load(std::memory_order_relaxed);
     p.b0 = b0;
     p.nb = a.B - b0 < kBatchPerLaunch ? a.B - b0 : kBatchPerLaunch;
     const PrefillLayout L = prefill_layout(a.T, p.nb, a.max_blocks, a.Hq, a.H, a.d, a.bs);

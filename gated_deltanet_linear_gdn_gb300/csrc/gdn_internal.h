@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "gdn.h"
 
 namespace gdn {
@@ -114,6 +116,8 @@ cudaError_t launch_prefill_tc(const LayerArgs& a, const PrefillExtra& p, cudaStr
 // prefill translation units
 cudaError_t set_decode_test_fault(int mode);
 cudaError_t set_prefill_test_fault(int mode);
+// and what the attention calls hand to their kernels
+std::atomic<int>& attention_test_fault();
 
 // prefill helpers implemented in gdn_conv.cu: the conv output y of every token of an active
 // sequence (over the chunk table of launch_prefill_prep), then each active sequence's final

@@ -32,10 +32,16 @@ extern "C" {
  * together, drain their bulk copies and MMA groups and free tensor memory; that CTA's
  * sequence and value head get no final state, every other one is computed as usual. */
 #define GDN_TEST_FAULT_PREFILL_PASS 2
+/* gdn_attn_decode and gdn_attn_prefill: in CTA 0 the warp that looks up pages and scales leaves after
+ * its first four tiles (a CTA of fewer is not affected). The waits of its other roles run out (about a
+ * second), copies and products in flight are drained, tensor memory is freed. What CTA 0 was to
+ * compute is not to be trusted; the rest of the call is as usual. */
+#define GDN_TEST_FAULT_ATTENTION 4
 
 /*
  * gdn_testing_set_fault -- sets the fault mode of every kernel launched from now on, on the
- * current device (a synchronous copy to a device flag); GDN_TEST_FAULT_NONE restores normal
+ * current device (a synchronous copy to a device flag; of the attention calls, an argument of their
+ * kernels); GDN_TEST_FAULT_NONE restores normal
  * operation. Returns GDN_ERR_INVALID_ARG for an unknown mode, GDN_ERR_CUDA if the copy fails.
  */
 gdn_status gdn_testing_set_fault(int32_t mode);

@@ -22,8 +22,8 @@
 // Scales of V. With x the exponent of a score and e that of vs, m is the running maximum of x + e, and p = exp2(x - m)
 // goes into the sum, p vs into the product. So what a key is rounded to goes by the largest probability x scale of the row, and
 // not by a scale that weighs nothing. m stands for 2^1.8 and moves when an x + e passes it by 2^5, so that almost only a
-// unit's first tile stops for it: p vs < 2^6.8 * 2 < 256, so that what a part leaves is at most 8, and 256 times 1 / 32 of it. (With
-// 2^8 above 2^-0.2 and factors of 1/16, keys below 2^-22 of the largest were lost.)
+// unit's first tile stops for it. So p vs < 2^6.8 * 2 < 256, what a part leaves of it is at most 8, and 32 times that 256
+// again. (With 2^8 above 2^-0.2 and factors of 1/16, at the same speed, keys below 2^-22 of the largest were lost.)
 //
 // Split. A (request, kv head) is cut into units of 256, 512 or 1,024 keys by its OWN length
 // (unit_shift), never by the batch: a row's result depends on its own inputs alone, bit for bit, as
@@ -103,8 +103,9 @@ cudaError_t encode_cache_maps(CacheMaps* maps, const AttnArgs& a) {
 namespace {
 
 constexpr int kMaxUnitKeys = 1024;
-// Requests of one launch. Their lengths stay in shared memory, next to what two CTAs an SM leave of it (static_assert below):
-// with 384, batches of 330 to 384 ran one CTA an SM (384 requests of 2,000 tokens, 16 / 2 heads of 256: 205 us, and 167 in two launches).
+// Requests of one launch. Their lengths stay in shared memory, next to what two CTAs an SM leave of it (static_assert
+// below): with 384, batches of 330 to 384 ran one CTA an SM (384 requests of 2,000 tokens, 16 / 2 heads of 256: 205 us,
+// and 167 in two launches).
 constexpr int kBatchPerLaunch = 320;
 constexpr int kCoarse = 16;            // requests between two kept tile sums
 constexpr int kThreads = 32 * 8;

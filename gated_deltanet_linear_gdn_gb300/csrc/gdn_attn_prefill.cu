@@ -66,10 +66,10 @@ struct PrefillParams {
 
 // How many pieces the key tiles of a request are cut into: the fewest rounds of an assumed 152
 // CTAs, counted in tiles with a constant cost per piece (a prologue and an epilogue take about 8 tiles). 300 tokens at
-// 60,000 (80 units of 470 tiles): 368 us in 5 pieces, 686 whole; 8 ragged prompts, none of them alone on the GPU: 346
-// and 321, the price of results that do not depend on the batch. Pieces of unequal length that fill 152 CTAs evenly
-// (cuts at multiples of one length over all row tiles, end to end) took 481: row tiles no longer read the same keys at the
-// same time.
+// 60,000 (80 units of 470 tiles): 371 us in 5 pieces, 677 whole; 8 ragged prompts, none of them alone on the GPU: 322
+// and 321. (152 is the SMs of the GPU that the library is built for, as a constant: results stay the same on any.)
+// Pieces of unequal length that fill 152 CTAs evenly (cuts at multiples of one length over all row tiles, end to end)
+// took 481: row tiles no longer read the same keys at the same time.
 __host__ __device__ __forceinline__ int kv_splits(int units, int tiles, int d) {
   if (units >= few_units(d) || tiles < 2 * kMinSplitTiles) return 1;
   int best = 1, cost = 0x7fffffff;
@@ -501,14 +501,17 @@ __device__ __forceinline__ void store_rows(const PrefillParams& p, const Prefill
 
 // ------------------------------------------------------------------------------- head_dim 256
 //
-// Both products on 8-bit operands, no conversion of V: p, rounded to f16, is the sum of three e5m2 values (split_e5m2),
-// each of the part that the ones before leave: 11 significant bits. e5m2 has f16's exponents, so all three have the factor 1 and
-// one accumulator, down to 2^-17: m moves when a score passes it by 2^4 and stands for 2^11, so a key is rounded to 2^-28 of
-// the row's largest whatever stands between. (Two e4m3 parts, a fifth fewer products and 123 us where this takes 138, end at 2^-14 of it:
-// 5,000 keys 10 nats below one of no value came out 14 to 26% small.) Sixteen softmax warps, four threads a row with 32 columns each (they exchange their maxima), two
-// score buffers (2 x 128 columns of tensor memory, 256 of output), a warp that issues MMAs: the 2,610 cycles of products a
-// tile hide most of the softmax. 4,096 tokens (16 / 2 heads): 138 us, 53% of the bf16 rate with the masked half
-// of the diagonal counted out. With f16 probabilities, as below, V alone would take 128 KB of shared memory.
+// Both products on 8-bit operands, no conversion of V: p, rounded to f16, is the sum of three e5m2 values
+// (split_e5m2), each of what the ones before leave: 11 significant bits. e5m2 has f16's exponents, so all three have the
+// factor 1 and one accumulator, down to 2^-17: m stands for 2^11 and moves when a y passes it by 2^4, so a key is
+// rounded to 2^-28 of the row's largest whatever stands between. (Two e4m3 parts, a fifth fewer products and 123 us where
+// this took 138, end at 2^-14 of it: 5,000 keys 10 nats below one of no value came out 14 to 26% small.)
+//
+// Sixteen softmax warps, four threads a row with 32 columns each (they exchange their maxima), two score buffers (2 x
+// 128 columns of tensor memory, 256 of output), a warp that issues MMAs: 2,610 cycles of products a tile. 4,096 tokens
+// (16 / 2 heads): 142 us, 51% of the bf16 rate with the masked half of the diagonal counted out; without the third part's
+// product 129, without the arithmetic of the split 130. With f16 probabilities, as below, V alone would take 128 KB of
+// shared memory.
 struct WideCfg {
   static constexpr int D = 256;
   static constexpr int kSplitC = 4;                      // softmax warpgroups that share the rows, by columns
@@ -845,19 +848,19 @@ __global__ void __launch_bounds__(WideCfg::kThreads, 1)
 // ------------------------------------------------------------------------- head_dim 64 and 128
 //
 // Here a key costs half the MMA time and the same softmax, so the softmax and shared memory decide. Probabilities
-// are f16 (11 significant bits; m stands for 2^7, so a key is rounded to 2^-32 of the row's largest; one conversion for two of them instead of six operations for
-// two e4m3 parts), and a warpgroup converts each tile of V to f16; e4m3 values are exact in f16. m moves when a score
-// passes it by 2^8: p <= 2^15.
+// are f16 (one conversion for two of them), and a warpgroup converts each tile of V to f16; e4m3 values are exact in f16.
+// m stands for 2^7 and moves when a y passes it by 2^8: p <= 2^15, 11 significant bits, and a key is rounded to 2^-32 of
+// the row's largest.
 //
 // Scores of three tiles are in tensor memory (3 x 128 columns, and D of output): Q K of the next tiles runs under
 // the softmax. Two warpgroups take the tiles in turn, thread = row, and hand m on; Q K and P V are issued by a thread
 // each, so that the waits of one pass under the products of the other. A CTA takes units as they come (the list holds up
 // to three times the units that a call has, and a CTA that only finds the list at its end costs as long as any start:
-// 8 ragged prompts 312 us, and 337 with a CTA per place of the list; for head_dim 256 the loop around a unit cost
+// 8 ragged prompts 312 us then, and 337 with a CTA per place of the list; for head_dim 256 the loop around a unit cost
 // more registers than there are). Per tile and 128 rows, the products take
 // about 1,110 cycles of the tensor pipe, and nearly as many of shared memory: Q, K and V in f16 as operands, V read
 // and written by the conversion, the copies; together 1,400. Measured about 1,950: 300 tokens at 60,000 (32 / 8
-// heads of 128) 366 us, against 198 for the same program without the arithmetic of softmax and conversion, and 301
+// heads of 128) 370 us (366 then), against 198 for the same program without the arithmetic of softmax and conversion, and 301
 // with one MMA a product and no conversion (then 371). Not kept: 256 rows (two row tiles, one score buffer each: 402
 // us, each tile's chain of softmax and products exposed); sixteen softmax warps (385: a vote between the two threads of a row); p computed before its tile's
 // maximum is known and again where that passes (420: twice the registers and code).

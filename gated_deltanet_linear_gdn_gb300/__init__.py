@@ -31,6 +31,8 @@ GDN_DEVERR_BLOCKS, GDN_DEVERR_BLOCK_RANGE = 8, 16
 GDN_TEST_FAULT_NONE, GDN_TEST_FAULT_DECODE_CONSUMER, GDN_TEST_FAULT_PREFILL_PASS = 0, 1, 2
 GDN_TEST_FAULT_ATTENTION = 4
 GDN_ACT_SILU, GDN_ACT_SIGMOID = 0, 1
+GDN_ROPE_HALVES, GDN_ROPE_INTERLEAVED = 0, 1
+GDN_ROPE_PLAIN, GDN_ROPE_LINEAR, GDN_ROPE_NTK, GDN_ROPE_YARN = 0, 1, 2, 3
 
 
 class GDNError(RuntimeError):
@@ -154,6 +156,25 @@ def lib():
         L.gdn_attn_prefill.restype = I32
         L.gdn_attn_prefill.argtypes = [P, I64, P, P, P, P, P, I32, P, I32, P, I32, I32,
                                        gdn_cache_dims, F, P, P, SZ, P, P]
+        L.gdn_rope.restype = I32
+        L.gdn_rope.argtypes = [P, I64, P, I64, P, I32, I32, I32, I32, I32, I32, P, F, P, I64, P, I64, P]
+        L.gdn_rope_frequencies.restype = I32
+        L.gdn_rope_frequencies.argtypes = [I32, ctypes.c_double, I32, ctypes.c_double, I32, P, P]
+        L.gdn_rope_turns.restype = I32
+        L.gdn_rope_turns.argtypes = [P, I32, P]
+        L.gdn_cache4_append.restype = I32
+        L.gdn_cache4_append.argtypes = [P, I64, P, I64, P, I32, P, P, P, P, I32, gdn_cache_dims, P, P]
+        L.gdn_cache4_read.restype = I32
+        L.gdn_cache4_read.argtypes = [P, P, P, P, I32, P, I32, gdn_cache_dims, P, I64, P, I64, P, P]
+        L.gdn_attn4_decode_workspace_size.restype = SZ
+        L.gdn_attn4_decode_workspace_size.argtypes = [I32, I32, gdn_cache_dims]
+        L.gdn_attn4_decode.restype = I32
+        L.gdn_attn4_decode.argtypes = L.gdn_attn_decode.argtypes
+        L.gdn_attn4_prefill_workspace_size.restype = SZ
+        L.gdn_attn4_prefill_workspace_size.argtypes = [I32, I32, I32, I32, gdn_cache_dims]
+        L.gdn_attn4_prefill.restype = I32
+        L.gdn_attn4_prefill.argtypes = [P, I64, P, P, P, P, P, I32, P, I32, P, I32, I32, I32,
+                                        gdn_cache_dims, F, P, P, SZ, P, P]
         L.gdn_validate_slots.restype = I32
         L.gdn_validate_slots.argtypes = [P, I32, I32]
         L.gdn_status_string.restype = ctypes.c_char_p
@@ -425,6 +446,119 @@ def gdn_attn_prefill(q, cu_tokens, k_cache, v_cache, k_scale, v_scale, block_tab
         d ** -0.5 if scale is None else scale, _dense(out, _BF16, (T, Hq, d), "out"),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err),
         _stream(stream)))
+
+
+# ---------------------------------------------- rotary positions, the cache in 4 bits
+
+_I64, _U8 = torch.int64, torch.uint8
+_E8M0 = (torch.uint8, torch.float8_e8m0fnu)
+
+
+class RopeTable:
+    """The frequencies of a model's rotary positions, as gdn_rope reads them (include/gdn.h, gdn_rope_frequencies): scaling
+    "none", "linear", "ntk" or "yarn" by `factor`, trained_len the positions that the model was trained on ("yarn" alone); or
+    `freqs`, rot_dim / 2 frequencies of its own with the `factor` of the rotated values. Kept on `device`."""
+
+    def __init__(self, rot_dim, *, base=10000.0, scaling="none", factor=1.0, trained_len=0, freqs=None, device="cuda"):
+        if rot_dim <= 0 or rot_dim % 2:
+            raise ValueError("rot_dim must be even and positive")
+        half = rot_dim // 2
+        w, f = (ctypes.c_double * half)(), ctypes.c_float(float(factor))
+        if freqs is None:
+            kind = {"none": GDN_ROPE_PLAIN, "linear": GDN_ROPE_LINEAR, "ntk": GDN_ROPE_NTK, "yarn": GDN_ROPE_YARN}[scaling]
+            _check(lib().gdn_rope_frequencies(rot_dim, float(base), kind, float(factor), int(trained_len), w, ctypes.byref(f)))
+        else:
+            if len(freqs) != half:
+                raise ValueError(f"freqs must have rot_dim / 2 = {half} frequencies")
+            w[:] = [float(x) for x in freqs]
+        turns = (ctypes.c_uint64 * half)()
+        _check(lib().gdn_rope_turns(w, half, turns))
+        self.rot_dim, self.factor, self.freqs = rot_dim, f.value, list(w)
+        self.turns = torch.frombuffer(bytearray(turns), dtype=_I64).to(device)
+
+
+def gdn_rope(q, k, positions, q_out, k_out, rope: RopeTable, *, interleaved=False, stream=None):
+    """Rotary positions of q [T, Hq, d] and k [T, Hkv, d] (bf16, any token stride) into q_out and k_out (which may be q and k
+    themselves). positions [T] int32; k and k_out may be None."""
+    T, Hq, d = q.shape
+    H = 0 if k is None else k.shape[1]
+    at = *_tokens(q, (T, Hq, d), "q"), *((None, 0) if k is None else _tokens(k, (T, H, d), "k"))
+    to = *_tokens(q_out, (T, Hq, d), "q_out"), *((None, 0) if k is None else _tokens(k_out, (T, H, d), "k_out"))
+    _check(lib().gdn_rope(*at, _dense(positions, _I32, (T,), "positions"), T, Hq, H, d, rope.rot_dim, int(bool(interleaved)),
+                          _dense(rope.turns, _I64, (rope.rot_dim // 2,), "rope.turns"), rope.factor, *to, _stream(stream)))
+
+
+def _cache4(k_cache, v_cache, k_scale, v_scale):
+    """The 4-bit cache's addresses and num_blocks, Hkv, block_size, head_dim."""
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [num_blocks, Hkv, block_size, head_dim / 2]")
+    NB, H, bs, half = k_cache.shape
+    d = 2 * half
+    if k_scale.dtype not in _E8M0 or v_scale.dtype is not k_scale.dtype:
+        raise ValueError("the scales must be float8_e8m0fnu (or its bytes)")
+    scales = (NB, H, bs, d // 32)
+    return (_dense(k_cache, _U8, (NB, H, bs, half), "k_cache"), _dense(v_cache, _U8, (NB, H, bs // 2, d), "v_cache"),
+            _dense(k_scale, k_scale.dtype, scales, "k_scale"), _dense(v_scale, k_scale.dtype, scales, "v_scale")), (NB, H, bs, d)
+
+
+def gdn_cache4_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, *, err=None, stream=None):
+    """Writes k, v [T, Hkv, d] (bf16, any token stride) into the 4-bit cache at slot_map [T] (include/gdn.h). k_cache
+    [num_blocks, Hkv, block_size, d / 2] and v_cache [num_blocks, Hkv, block_size / 2, d] uint8; the scales [num_blocks, Hkv,
+    block_size, d / 32] float8_e8m0fnu or its bytes."""
+    addresses, (NB, H, bs, d) = _cache4(k_cache, v_cache, k_scale, v_scale)
+    (T,) = slot_map.shape
+    _check(lib().gdn_cache4_append(*_tokens(k, (T, H, d), "k"), *_tokens(v, (T, H, d), "v"),
+                                   _dense(slot_map, _I32, (T,), "slot_map"), T, *addresses, NB,
+                                   _cache_dims(H, H, d, bs), _ptr(err), _stream(stream)))
+
+
+def gdn_cache4_read(k_cache, v_cache, k_scale, v_scale, slot_map, k, v, *, err=None, stream=None):
+    """The values of the 4-bit cache's tokens at slot_map [T], into k and v [T, Hkv, d] (bf16, any token stride)."""
+    addresses, (NB, H, bs, d) = _cache4(k_cache, v_cache, k_scale, v_scale)
+    (T,) = slot_map.shape
+    _check(lib().gdn_cache4_read(*addresses, NB, _dense(slot_map, _I32, (T,), "slot_map"), T, _cache_dims(H, H, d, bs),
+                                 *_tokens(k, (T, H, d), "k"), *_tokens(v, (T, H, d), "v"), _ptr(err), _stream(stream)))
+
+
+def gdn_attn4_decode_workspace_size(batch, max_blocks, num_q_heads, num_kv_heads, head_dim, block_size) -> int:
+    return int(lib().gdn_attn4_decode_workspace_size(
+        int(batch), int(max_blocks), gdn_cache_dims(num_q_heads, num_kv_heads, head_dim, block_size)))
+
+
+def gdn_attn4_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, out, workspace, *, scale=None, err=None,
+                     stream=None):
+    """Attention of one token per request over the 4-bit cache. q, out: [B, Hq, d] bf16 (q with any token stride); scale:
+    head_dim ** -0.5 if None."""
+    addresses, (NB, H, bs, d) = _cache4(k_cache, v_cache, k_scale, v_scale)
+    B, Hq, W = q.shape[0], q.shape[1], block_table.shape[-1]
+    _check(lib().gdn_attn4_decode(
+        *_tokens(q, (B, Hq, d), "q"), *addresses, NB, _dense(block_table, _I32, (B, W), "block_table"), W,
+        _dense(lens, _I32, (B,), "lens"), B, _cache_dims(Hq, H, d, bs), d ** -0.5 if scale is None else scale,
+        _dense(out, _BF16, (B, Hq, d), "out"), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err),
+        _stream(stream)))
+
+
+def gdn_attn4_prefill_workspace_size(total_tokens, num_seqs, max_blocks, num_q_heads, num_kv_heads, head_dim, block_size, *,
+                                     held_blocks=None) -> int:
+    """held_blocks: a bound on the blocks that the call's requests hold together; num_seqs * max_blocks if None."""
+    return int(lib().gdn_attn4_prefill_workspace_size(
+        int(total_tokens), int(num_seqs), int(max_blocks),
+        min(num_seqs * max_blocks, 0x7fffffff) if held_blocks is None else int(held_blocks),
+        gdn_cache_dims(num_q_heads, num_kv_heads, head_dim, block_size)))
+
+
+def gdn_attn4_prefill(q, cu_tokens, k_cache, v_cache, k_scale, v_scale, block_table, lens, out, workspace, *,
+                      held_blocks=None, scale=None, err=None, stream=None):
+    """Causal attention of packed prompt tokens over the 4-bit cache, which holds them already. q, out: [T, Hq, d] bf16 (q
+    with any token stride); cu_tokens [B + 1], lens [B] int32; held_blocks as for the workspace's size."""
+    addresses, (NB, H, bs, d) = _cache4(k_cache, v_cache, k_scale, v_scale)
+    T, Hq, B, W = q.shape[0], q.shape[1], lens.shape[0], block_table.shape[-1]
+    _check(lib().gdn_attn4_prefill(
+        *_tokens(q, (T, Hq, d), "q"), _dense(cu_tokens, _I32, (B + 1,), "cu_tokens"), *addresses, NB,
+        _dense(block_table, _I32, (B, W), "block_table"), W, _dense(lens, _I32, (B,), "lens"), B, T,
+        min(B * W, 0x7fffffff) if held_blocks is None else held_blocks, _cache_dims(Hq, H, d, bs),
+        d ** -0.5 if scale is None else scale, _dense(out, _BF16, (T, Hq, d), "out"), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream)))
 
 
 class DecodeGraph:

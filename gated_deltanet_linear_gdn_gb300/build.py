@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libgdn.so")
 SOURCES = ["gdn_api.cu", "gdn_conv.cu", "gdn_decode.cu", "gdn_prefill.cu", "gdn_prefill_tc.cu",
            "gdn_graph.cu", "gdn_noalloc.cu", "gdn_gate.cu", "gdn_mixed.cu",
            "gdn_cache_api.cu", "gdn_cache.cu", "gdn_attn_decode.cu",
-           "gdn_attn_prefill.cu"]
+           "gdn_attn_prefill.cu", "gdn_rope.cu", "gdn_cache4.cu", "gdn_attn4_decode.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE]
 

@@ -1,6 +1,7 @@
-// gdn_cache_api.cu -- the C ABI of the paged cache and its attention (include/gdn.h): argument
+// gdn_cache_api.cu -- the C ABI of the paged caches and their attention (include/gdn.h): argument
 // checks and error mapping. No allocation, no synchronisation.
 #include "gdn_cache.cuh"
+#include "gdn_cache4.cuh"
 
 namespace {
 
@@ -65,6 +66,39 @@ gdn_status check_attn(const void* q, int64_t q_stride, const void* k_cache, cons
   a.workspace = workspace;
   a.err = err;
   return GDN_OK;
+}
+
+// The arrays of a 4-bit cache.
+gdn_status check_cache4(const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale) {
+  if (!k_cache || !v_cache || !k_scale || !v_scale) return GDN_ERR_INVALID_ARG;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 16) || !aligned(v_scale, 16))
+    return GDN_ERR_INVALID_ARG;
+  return GDN_OK;
+}
+
+// Workspace of a prompt call over the 4-bit cache: its requests' pages in 8 bits, their table and lengths, then the 8-bit
+// call's own.
+struct Prefill4Layout {
+  size_t lens, k, v, k_scale, v_scale, rest, total;
+  int32_t held;  // pages there is room for; 0: too many for 32-bit rows
+};
+Prefill4Layout prefill4_layout(int32_t T, int32_t B, int32_t max_blocks, int32_t held, const gdn_cache_dims& d) {
+  Prefill4Layout L = {};
+  const int64_t most = static_cast<int64_t>(B) * max_blocks;
+  const int64_t pages = held < most ? held : most;
+  if (pages * d.num_kv_heads * d.block_size > 0x7fffffffLL - 128) return L;
+  L.held = static_cast<int32_t>(pages);
+  auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  const size_t bytes = static_cast<size_t>(pages) * d.num_kv_heads * d.block_size * d.head_dim;
+  const size_t scales = static_cast<size_t>(pages) * d.num_kv_heads * sizeof(float);
+  L.lens = up(static_cast<size_t>(most) * sizeof(int32_t));
+  L.k = up(L.lens + static_cast<size_t>(B) * sizeof(int32_t));
+  L.v = up(L.k + bytes);
+  L.k_scale = up(L.v + bytes);
+  L.v_scale = up(L.k_scale + scales);
+  L.rest = up(L.v_scale + scales);
+  L.total = L.rest + gdn::attn_prefill_workspace(T, B, max_blocks, d.num_q_heads, d.num_kv_heads, d.head_dim, d.block_size);
+  return L;
 }
 
 }  // namespace
@@ -168,6 +202,132 @@ gdn_status gdn_attn_prefill(const void* q, int64_t q_stride, const int32_t* cu_t
     return GDN_ERR_INVALID_ARG;
   a.cu_tokens = cu_tokens;
   a.T = total_tokens;
+  return from_cuda(gdn::launch_attn_prefill(a, static_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_cache4_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                             const int32_t* slot_map, int32_t total_tokens, void* k_cache,
+                             void* v_cache, uint8_t* k_scale, uint8_t* v_scale, int32_t num_blocks,
+                             gdn_cache_dims dims, int32_t* err, void* stream) {
+  gdn_status st = check_cache(dims, num_blocks, false);
+  if (st != GDN_OK) return st;
+  if (total_tokens < 0) return GDN_ERR_INVALID_ARG;
+  if (total_tokens > kMaxTokens) return GDN_ERR_UNSUPPORTED;
+  if (total_tokens == 0) return GDN_OK;
+  if (!k || !v || !slot_map) return GDN_ERR_INVALID_ARG;
+  st = check_cache4(k_cache, v_cache, k_scale, v_scale);
+  if (st != GDN_OK) return st;
+  const int64_t row = static_cast<int64_t>(dims.num_kv_heads) * dims.head_dim;
+  if (k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0) return GDN_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 4)) return GDN_ERR_INVALID_ARG;
+  gdn::Append4Args a{static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), k_stride, v_stride, slot_map, total_tokens,
+                     {static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), k_scale, v_scale, num_blocks,
+                      dims.num_kv_heads, dims.head_dim, dims.block_size},
+                     err};
+  return from_cuda(gdn::launch_cache4_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_cache4_read(const void* k_cache, const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
+                           int32_t num_blocks, const int32_t* slot_map, int32_t total_tokens, gdn_cache_dims dims,
+                           void* k, int64_t k_stride, void* v, int64_t v_stride, int32_t* err, void* stream) {
+  gdn_status st = check_cache(dims, num_blocks, false);
+  if (st != GDN_OK) return st;
+  if (total_tokens < 0) return GDN_ERR_INVALID_ARG;
+  if (total_tokens > kMaxTokens) return GDN_ERR_UNSUPPORTED;
+  if (total_tokens == 0) return GDN_OK;
+  if (!k || !v || !slot_map) return GDN_ERR_INVALID_ARG;
+  st = check_cache4(k_cache, v_cache, k_scale, v_scale);
+  if (st != GDN_OK) return st;
+  const int64_t row = static_cast<int64_t>(dims.num_kv_heads) * dims.head_dim;
+  if (k_stride < row || v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0) return GDN_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 4)) return GDN_ERR_INVALID_ARG;
+  gdn::Read4Args a{{static_cast<uint8_t*>(const_cast<void*>(k_cache)), static_cast<uint8_t*>(const_cast<void*>(v_cache)),
+                    const_cast<uint8_t*>(k_scale), const_cast<uint8_t*>(v_scale), num_blocks, dims.num_kv_heads, dims.head_dim,
+                    dims.block_size},
+                   slot_map, total_tokens, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v), k_stride, v_stride, err};
+  return from_cuda(gdn::launch_cache4_read(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t gdn_attn4_decode_workspace_size(int32_t batch, int32_t max_blocks, gdn_cache_dims dims) {
+  if (batch <= 0 || max_blocks <= 0 || check_cache(dims, 1, true) != GDN_OK) return 0;
+  if (gdn::attn_decode_batch(max_blocks, dims.num_q_heads, dims.num_kv_heads, dims.block_size) == 0) return 0;
+  return gdn::attn4_decode_workspace(batch, max_blocks, dims.num_q_heads, dims.num_kv_heads, dims.head_dim,
+                                     dims.block_size);
+}
+
+gdn_status gdn_attn4_decode(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                            const uint8_t* k_scale, const uint8_t* v_scale, int32_t num_blocks,
+                            const int32_t* block_table, int32_t max_blocks, const int32_t* lens,
+                            int32_t batch, gdn_cache_dims dims, float scale, void* out,
+                            void* workspace, size_t workspace_bytes, int32_t* err, void* stream) {
+  if (batch == 0) return GDN_OK;
+  gdn::AttnArgs a;
+  gdn_status st = check_attn(q, q_stride, k_cache, v_cache, reinterpret_cast<const float*>(k_scale),
+                             reinterpret_cast<const float*>(v_scale), num_blocks, block_table, max_blocks, lens, batch, dims,
+                             scale, out, workspace, err, a);
+  if (st == GDN_OK) st = check_cache4(k_cache, v_cache, k_scale, v_scale);
+  if (st != GDN_OK) return st;
+  if (gdn::attn_decode_batch(max_blocks, dims.num_q_heads, dims.num_kv_heads, dims.block_size) == 0) return GDN_ERR_UNSUPPORTED;
+  if (workspace_bytes < gdn_attn4_decode_workspace_size(batch, max_blocks, dims)) return GDN_ERR_INVALID_ARG;
+  return from_cuda(gdn::launch_attn4_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t gdn_attn4_prefill_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_t max_blocks, int32_t held_blocks,
+                                        gdn_cache_dims dims) {
+  if (total_tokens < 0 || num_seqs <= 0 || max_blocks <= 0 || held_blocks <= 0 || check_cache(dims, 1, true) != GDN_OK) return 0;
+  return prefill4_layout(total_tokens, num_seqs, max_blocks, held_blocks, dims).total;
+}
+
+gdn_status gdn_attn4_prefill(const void* q, int64_t q_stride, const int32_t* cu_tokens,
+                             const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                             const uint8_t* v_scale, int32_t num_blocks, const int32_t* block_table,
+                             int32_t max_blocks, const int32_t* lens, int32_t num_seqs,
+                             int32_t total_tokens, int32_t held_blocks, gdn_cache_dims dims, float scale, void* out,
+                             void* workspace, size_t workspace_bytes, int32_t* err, void* stream) {
+  if (total_tokens < 0 || num_seqs < 0 || held_blocks < 0) return GDN_ERR_INVALID_ARG;
+  if (num_seqs == 0 || total_tokens == 0) return GDN_OK;
+  if (held_blocks == 0) return GDN_ERR_INVALID_ARG;
+  gdn::AttnArgs a;
+  gdn_status st = check_attn(q, q_stride, k_cache, v_cache, reinterpret_cast<const float*>(k_scale),
+                             reinterpret_cast<const float*>(v_scale), num_blocks, block_table, max_blocks, lens, num_seqs, dims,
+                             scale, out, workspace, err, a);
+  if (st == GDN_OK) st = check_cache4(k_cache, v_cache, k_scale, v_scale);
+  if (st != GDN_OK) return st;
+  if (!cu_tokens || !aligned(cu_tokens, 4)) return GDN_ERR_INVALID_ARG;
+  if (num_seqs > gdn::kExpandBatch) return GDN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(total_tokens) * dims.num_q_heads > 0x7fffffffLL - 65536) return GDN_ERR_UNSUPPORTED;
+  const Prefill4Layout L = prefill4_layout(total_tokens, num_seqs, max_blocks, held_blocks, dims);
+  if (L.held == 0) return GDN_ERR_UNSUPPORTED;
+  if (workspace_bytes < L.total) return GDN_ERR_INVALID_ARG;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  gdn::Expand4Args x{};
+  x.c = {static_cast<uint8_t*>(const_cast<void*>(k_cache)), static_cast<uint8_t*>(const_cast<void*>(v_cache)),
+         const_cast<uint8_t*>(k_scale), const_cast<uint8_t*>(v_scale), num_blocks, dims.num_kv_heads, dims.head_dim, dims.block_size};
+  x.block_table = block_table;
+  x.max_blocks = max_blocks;
+  x.lens = lens;
+  x.cu_tokens = cu_tokens;
+  x.B = num_seqs;
+  x.held = L.held;
+  x.table = reinterpret_cast<int32_t*>(ws);
+  x.new_lens = reinterpret_cast<int32_t*>(ws + L.lens);
+  x.k = ws + L.k;
+  x.v = ws + L.v;
+  x.k_scale = reinterpret_cast<float*>(ws + L.k_scale);
+  x.v_scale = reinterpret_cast<float*>(ws + L.v_scale);
+  x.err = err;
+  const cudaError_t e = gdn::launch_cache4_expand(x, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return GDN_ERR_CUDA;
+  a.cu_tokens = cu_tokens;
+  a.T = total_tokens;
+  a.k_cache = x.k;
+  a.v_cache = x.v;
+  a.k_scale = x.k_scale;
+  a.v_scale = x.v_scale;
+  a.block_table = x.table;
+  a.lens = x.new_lens;
+  a.num_blocks = L.held;
+  a.workspace = ws + L.rest;
   return from_cuda(gdn::launch_attn_prefill(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -1,0 +1,32 @@
+// gdn_rope.cuh -- argument block and launch declaration of the rotary positions.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gdn.h"
+
+namespace gdn {
+
+constexpr int kRopeMaxDim = 1024;  // of a head: sines and cosines of kRopeTokens tokens fit in 32 KB
+constexpr int kRopeTokens = 4;     // tokens of a CTA, where there are more than kRopeFew
+constexpr int kRopeFew = 1024;
+
+struct RopeArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  uint16_t* q_out;
+  uint16_t* k_out;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;  // elements from one token to the next
+  const int32_t* positions;
+  const uint64_t* turns;  // [rot / 2]: frequencies in turns a position, times 2^64
+  int T, Hq, H, d, rot, interleaved;
+  float factor;
+  // set by the launch: tokens of a CTA, items of a (token, head) row, and 2^32 / items and / rows, rounded up
+  int tokens, items;
+  uint32_t by_items, by_rows;
+};
+
+cudaError_t launch_rope(RopeArgs a, cudaStream_t s);
+
+}  // namespace gdn

@@ -128,7 +128,8 @@ typedef struct {
 
 #define GDN_DEVERR_BLOCKS 8       /* gdn_cache_tables: the pool of free blocks ran short (or its head or
                                      count is out of range): the rows that it could not serve keep
-                                     their old length and get no slots */
+                                     their old length and get no slots. gdn_attn4_prefill: held_blocks
+                                     is less than the requests hold */
 #define GDN_DEVERR_BLOCK_RANGE 16 /* a block or slot id that is not in the cache: its tokens are not
                                      written, or not seen */
 
@@ -517,6 +518,112 @@ gdn_status gdn_attn_prefill(const void* q, int64_t q_stride, const int32_t* cu_t
                             int32_t max_blocks, const int32_t* lens, int32_t num_seqs,
                             int32_t total_tokens, gdn_cache_dims dims, float scale, void* out,
                             void* workspace, size_t workspace_bytes, int32_t* err, void* stream);
+
+/*
+ * Rotary positions -- what the attention layer's q and k need between their projection and the cache. gdn_cache_tables gives
+ * the positions.
+ *
+ * Per token with position p, head, and pair i of the head's first rot_dim elements (HALVES: elements i and i + rot_dim / 2;
+ * INTERLEAVED: 2 i and 2 i + 1), with a = p * w_i:
+ *   (x1, x2) -> factor * (x1 cos a - x2 sin a, x2 cos a + x1 sin a)
+ * The elements past rot_dim are copied, as bits. Angles are exact to 2^-31 of a turn at any position, sines and products are
+ * fp32, and the result is rounded once.
+ *
+ *   q, k       [total_tokens] rows of heads * head_dim bf16, q_stride and k_stride elements apart (slices of one projection are
+ *              fine); either may have 0 heads, its pointers are not used then
+ *   positions  [total_tokens] int32; a token with a negative one (a padded step's) is left out: nothing is written
+ *   turns      [rot_dim / 2] uint64: w_i / (2 pi) modulo 1, times 2^64 (gdn_rope_turns)
+ *   q_out, k_out  rows as q and k with strides of their own; may be q and k themselves (in place, where only the first
+ *              rot_dim elements are touched), and may not overlap them otherwise
+ * Any alignment and stride is right; rows on 16-byte boundaries with rot_dim a multiple of 16 go in vectors.
+ * Supported: head_dim <= 1024, rot_dim even, up to 1,024 heads each, total_tokens < 2^31 - 4. total_tokens == 0 is a no-op.
+ */
+typedef enum { GDN_ROPE_HALVES = 0, GDN_ROPE_INTERLEAVED = 1 } gdn_rope_layout;
+gdn_status gdn_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                    const int32_t* positions, int32_t total_tokens, int32_t num_q_heads,
+                    int32_t num_kv_heads, int32_t head_dim, int32_t rot_dim, gdn_rope_layout layout,
+                    const uint64_t* turns, float factor, void* q_out, int64_t q_out_stride,
+                    void* k_out, int64_t k_out_stride, void* stream);
+
+/*
+ * Host-side tables for gdn_rope (HOST pointers, no CUDA call). gdn_rope_frequencies writes rot_dim / 2 frequencies and the
+ * factor that goes with them; gdn_rope_turns turns frequencies (these, or a model's own) into what gdn_rope reads.
+ *   PLAIN   w_i = base^(-2 i / rot_dim)
+ *   LINEAR  w_i / factor
+ *   NTK     base * factor^(rot_dim / (rot_dim - 2)) for base: the last pair slows down by factor, the first keeps its w
+ *   YARN    pairs that turn 32 times or more over trained_len positions keep w_i, those that turn once or less have
+ *           w_i / factor, the ones between mix the two along their index (its bounds rounded outward); the values'
+ *           factor is 0.1 ln(factor) + 1
+ * factor (not below 1) is not used by PLAIN, trained_len by YARN alone.
+ */
+typedef enum { GDN_ROPE_PLAIN = 0, GDN_ROPE_LINEAR = 1, GDN_ROPE_NTK = 2, GDN_ROPE_YARN = 3 } gdn_rope_scaling;
+gdn_status gdn_rope_frequencies(int32_t rot_dim, double base, gdn_rope_scaling scaling, double factor,
+                                int32_t trained_len, double* host_freqs, float* host_factor);
+gdn_status gdn_rope_turns(const double* host_freqs, int32_t count, uint64_t* host_turns);
+
+/*
+ * The cache in 4 bits -- half the bytes of the cache above, with the same block tables, slots and calls. A value is one of
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign (e2m1), times the power of two of its group: 32 neighbouring elements of a token's
+ * head share one byte e (e8m0), which stands for 2^(e - 127); 255 stands for NaN. That is the OCP microscaling format MXFP4.
+ *   k_cache  [num_blocks, Hkv, block_size, head_dim / 2] bytes: elements 2 i (low four bits) and 2 i + 1 of a token
+ *   v_cache  [num_blocks, Hkv, block_size / 2, head_dim] bytes: an element of tokens 2 j (low four bits) and 2 j + 1
+ *   k_scale, v_scale  [num_blocks, Hkv, block_size, head_dim / 32] bytes
+ * all 16-byte aligned. Bytes of positions that no request holds may be anything.
+ *
+ * gdn_cache4_append -- writes the step's keys and values. Per token, head and group, with a = max |x| over its finite values:
+ *   e = the least with a <= 7 * 2^(e - 127), at least 63;   code = e2m1(x * 2^(127 - e)), to nearest, ties to even, +-6 beyond
+ * (7 because up to there the rounding to 6 is no worse than half the step from 4 to 6.) A group with a NaN has e = 255. Tokens
+ * do not touch one another, so nothing is rounded twice, and a token may be written again (speculation taken back). The two
+ * tokens 2 j and 2 j + 1 of a block share V's bytes: where a call has both they follow each other (gdn_cache_tables gives that
+ * order); no slot comes twice in a call.
+ *   arguments as gdn_cache_append
+ *
+ * gdn_cache4_read -- the values of the tokens at slot_map, in bf16, which holds them exactly. A negative slot: the token's
+ * rows are left as they are; one past the cache: that, and GDN_DEVERR_BLOCK_RANGE. A slot may come more than once.
+ *   k, v     [total_tokens] rows of Hkv * head_dim bf16, k_stride and v_stride elements apart, 16-byte aligned, multiples of 8
+ */
+gdn_status gdn_cache4_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                             const int32_t* slot_map, int32_t total_tokens, void* k_cache,
+                             void* v_cache, uint8_t* k_scale, uint8_t* v_scale, int32_t num_blocks,
+                             gdn_cache_dims dims, int32_t* err, void* stream);
+gdn_status gdn_cache4_read(const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                           const uint8_t* v_scale, int32_t num_blocks, const int32_t* slot_map,
+                           int32_t total_tokens, gdn_cache_dims dims, void* k, int64_t k_stride,
+                           void* v, int64_t v_stride, int32_t* err, void* stream);
+
+/*
+ * gdn_attn4_decode -- gdn_attn_decode over the 4-bit cache: same arguments but for the scales, same lengths, tables, errors
+ * and limits. Queries are exact to 2^-31 of a head's largest element; for the product with V the probabilities keep 11
+ * significant bits, and no less than 2^-34 of the row's largest probability x scale of V. A group's scale of V counts down to
+ * 2^-24 of the largest of its token and head; scales of K below 2^-126 count as 0.
+ */
+size_t gdn_attn4_decode_workspace_size(int32_t batch, int32_t max_blocks, gdn_cache_dims dims);
+gdn_status gdn_attn4_decode(const void* q, int64_t q_stride, const void* k_cache,
+                            const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
+                            int32_t num_blocks, const int32_t* block_table, int32_t max_blocks,
+                            const int32_t* lens, int32_t batch, gdn_cache_dims dims, float scale,
+                            void* out, void* workspace, size_t workspace_bytes, int32_t* err,
+                            void* stream);
+
+/*
+ * gdn_attn4_prefill -- gdn_attn_prefill over the 4-bit cache. The call first writes the pages that its requests with new
+ * tokens hold into its workspace, in 8 bits (values down to 2^-14 of a block's and head's largest scale as they are, below
+ * that rounded to 2^-18 of its largest value); the rest is that call, with its arithmetic.
+ *   held_blocks  what there is room for: a bound on the blocks that those requests hold together (a block that two of them
+ *                hold counts twice). Requests past it, in row order, set GDN_DEVERR_BLOCKS and count as empty: zeros come out
+ *   workspace    device scratch of >= gdn_attn4_prefill_workspace_size bytes (about 2 * held_blocks * Hkv * block_size *
+ *                head_dim and what gdn_attn_prefill takes), 256-byte aligned
+ * Supported: num_seqs <= 4096, held_blocks * Hkv * block_size < 2^31 - 128, otherwise as gdn_attn_prefill.
+ */
+size_t gdn_attn4_prefill_workspace_size(int32_t total_tokens, int32_t num_seqs, int32_t max_blocks,
+                                        int32_t held_blocks, gdn_cache_dims dims);
+gdn_status gdn_attn4_prefill(const void* q, int64_t q_stride, const int32_t* cu_tokens,
+                             const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                             const uint8_t* v_scale, int32_t num_blocks, const int32_t* block_table,
+                             int32_t max_blocks, const int32_t* lens, int32_t num_seqs,
+                             int32_t total_tokens, int32_t held_blocks, gdn_cache_dims dims,
+                             float scale, void* out, void* workspace, size_t workspace_bytes,
+                             int32_t* err, void* stream);
 
 /*
  * gdn_validate_slots -- host-side check of a HOST slot table ([P1] Notes,

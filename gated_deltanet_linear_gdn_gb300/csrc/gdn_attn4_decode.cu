@@ -40,13 +40,14 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStep = 16;              // keys of a step
+constexpr int kStep = 16;              // keys of a warp's step
+constexpr int kTileKeys = kStep * kWarps;
 constexpr float kRise = 5.0f;          // log2 of what a score may pass the running maximum by
 constexpr float kTop = 9.0f;           // log2 of what the running maximum stands for
 
 using Units = UnitRule<8, 10, 24>;
 using Walk = WalkOf<Units>;
-static_assert((1 << 10) / kStep / kWarps <= 32, "a lane for each of a warp's steps of a unit");
+static_assert(kWarps == 4 && (1 << 10) / kTileKeys <= 32, "a lane for each tile of a unit");
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -57,19 +58,19 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_gr
 
 __device__ __forceinline__ uint32_t lds32(uint32_t at) {
   uint32_t r;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(at));
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(at) : "memory");
   return r;
 }
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-  uint4 r;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at));
-  return r;
-}
-// c += a b, 16 x 16 by 16 x 8, f16 in, fp32 sums
+// c += a b, 16 x 16 by 16 x 8, f16 in, fp32 sums; and the first of a chain, a b
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
@@ -86,39 +87,123 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// whether one of four bytes is 255
+__device__ __forceinline__ bool has_255(uint32_t w) { return ((~w - 0x01010101u) & w & 0x80808080u) != 0; }
+
+// A key's scales, from N of its bytes of K and of V (in the words' low bytes) and the largest of V's, `top`.
+template <int N>
+struct KeyScales {
+  uint32_t k[N];              // fp32 2^(e - 127)
+  uint32_t v[(N + 1) / 2];    // f16 pairs 2^(e - top)
+  __device__ __forceinline__ static int largest(uint32_t w) {  // of the bytes of V, 255 apart
+    if (has_255(w)) {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (((w >> 8 * j) & 255u) == 255u) w &= ~(255u << 8 * j);
+    }
+    uint32_t m = N > 1 ? max_u16x2(__byte_perm(w, 0, 0x4140), N > 2 ? __byte_perm(w, 0, 0x4342) : 0u) : w;
+    return static_cast<int>(N > 1 ? max(m & 0xFFFFu, m >> 16) : m);
+  }
+  __device__ __forceinline__ void make(uint32_t kw, uint32_t vw, int top) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) k[j] = (j == 0 ? kw << 23 : j == 1 ? kw << 15 : j == 2 ? kw << 7 : kw >> 1) & 0x7F800000u;
+    if (has_255(kw)) {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (k[j] == 0x7F800000u) k[j] = 0x7FC00000u;
+    }
+    // 25 + e - top is the exponent field of 2^(e - top + 10), times 2^-10 (rounded to an f16 subnormal where that is one)
+    const uint32_t add = static_cast<uint32_t>(256 + 25 - top) * 0x10001u;
+#pragma unroll
+    for (int j = 0; j < (N + 1) / 2; ++j) {
+      const uint32_t t = max_u16x2(__byte_perm(vw, 0, j ? 0x4342 : 0x4140) + add, 0x01000100u);
+      v[j] = mul_f16x2((t & 0x001F001Fu) << 10, 0x14001400u);
+    }
+    if (has_255(vw)) {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (((vw >> 8 * j) & 255u) == 255u) v[j / 2] = (v[j / 2] & (j % 2 ? 0xFFFFu : 0xFFFF0000u)) | (j % 2 ? 0x7E000000u : 0x7E00u);
+    }
+  }
+};
+
+template <class T, int N>
+__device__ __forceinline__ void load_words(const unsigned char* p, T (&v)[N]) {
+  static_assert((N == 2 || N == 4) && sizeof(T) == 4, "8 or 16 bytes");
+  if constexpr (N == 4) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    v[0] = reinterpret_cast<const T&>(u.x);
+    v[1] = reinterpret_cast<const T&>(u.y);
+    v[2] = reinterpret_cast<const T&>(u.z);
+    v[3] = reinterpret_cast<const T&>(u.w);
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    v[0] = reinterpret_cast<const T&>(u.x);
+    v[1] = reinterpret_cast<const T&>(u.y);
+  }
+}
 
 // NT: query heads of a unit by eights, 1 or 2.
 template <int D, int NT>
 struct Cfg {
-  static constexpr int kG = D / kGroup4;                  // groups of a head
-  static constexpr int kRowK = D / 2 + 16, kRowV = D + 32;  // bytes of a key's, of a key pair's row in a stage
-  static constexpr int kAtV = kStep * kRowK, kAtScale = kAtV + kStep / 2 * kRowV;
-  static constexpr int kStage = kAtScale + 2 * kStep * kG;
-  static constexpr int kStages = 3;
-  static constexpr int kScaleK = kStep * kG * 4, kScaleV = kStep * kG * 2;  // the step's scales as the products want them
-  static constexpr int kWarp = kStages * kStage + kScaleK + kScaleV;        // of each warp
-  static constexpr int kQ = NT * kG * 512;
-  static constexpr int kRowO = D + 4;                     // floats of a head's row in the join
-  static constexpr int kAtFactor = kWarps * kWarp + kQ, kAtMl = kAtFactor + 64, kAtLens = kAtMl + kWarps * 16 * 8;
-  static constexpr int smem_of(int nb) { return kAtLens + 4 * (nb + nb / kCoarse + 2); }
-  static_assert(kStage % 16 == 0 && kWarp % 16 == 0 && kWarp >= 8 * kRowO * 4, "alignment; the join's rows are in the rings");
+  static constexpr int kG = D / kGroup4;                    // groups of a head
+  static constexpr int kM = D / 16 / kWarps;                // 16-row tiles of O^T a warp has
+  static constexpr int kRowK = D / 2, kRowV = D;            // bytes of a key, of a key pair's values
+  static constexpr int kKeys = kStep * kRowK + 2 * kStep * kG;  // a warp's keys of a tile, and the scales of its keys and values
+  static constexpr int kValues = kTileKeys / 2 * kRowV;     // a tile's values
+  static constexpr int kScaleK = kStep * kG * 4, kScaleV = kStep * kG * 2;  // of a warp's keys, as the products want them
+  static constexpr int kAtV = kWarps * 2 * kKeys, kAtSk = kAtV + 2 * kValues, kAtSv = kAtSk + kWarps * kScaleK, kAtP = kAtSv + kWarps * kScaleV,
+                       kAtQ = kAtP + kWarps * NT * 256, kAtFactor = kAtQ + NT * kG * 512, kAtMax = kAtFactor + 64, kAtSum = kAtMax + kWarps * 64,
+                       kAtLens = kAtSum + kWarps * 64;
+  // CTAs of an SM: what shared memory holds for a head of 256, and registers without spills below that
+  static constexpr int kCtas = D == 256 ? (NT == 2 ? 4 : 5) : D == 128 ? (NT == 2 ? 5 : 6) : (NT == 2 ? 6 : 8);
+  static constexpr int smem_of(int nb) { return 128 + kAtLens + 4 * (nb + nb / kCoarse + 2); }
+  static_assert(kKeys % (D == 64 ? 64 : 128) == 0 && kAtP % 16 == 0, "alignment: a place in a row is changed by bits of the address");
+  // Where 16 bytes lie in a row, as bits of the address to change: no bank twice for eight rows' (four pairs') operand words
+  // of one group.
+  static __device__ __forceinline__ uint32_t swap_k(int row) { return (D == 256 ? row & 7 : D == 128 ? row >> 1 & 3 : row >> 2 & 1) << 4; }
+  static __device__ __forceinline__ uint32_t swap_v(int row) { return (D == 64 ? row & 2 : 2 * (row & 3)) << 4; }
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 2 && D == 256 ? 2 : 3) attn4_decode_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kernel(const __grid_constant__ DecodeParams p) {
   using C = Cfg<D, NT>;
-  extern __shared__ __align__(128) unsigned char smem[];
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + (-smem_addr(smem_raw) & 127u);
   __shared__ int32_t s_scan[kWarps];
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   const int g = lane >> 2, c = lane & 3;
-  const uint32_t base = smem_addr(smem), ring = base + warp * C::kWarp, s_k = ring + C::kStages * C::kStage, s_v = s_k + C::kScaleK;
-  const uint32_t s_q = base + kWarps * C::kWarp;
+  unsigned char* my_keys = smem + warp * 2 * C::kKeys;       // the warp's two stages of keys
+  unsigned char* values = smem + C::kAtV;                    // the CTA's two stages of values
+  unsigned char* my_k = smem + C::kAtSk + warp * C::kScaleK; // scales of the warp's keys: [key][group] fp32
+  unsigned char* all_v = smem + C::kAtSv;                    // scales of the tile's values: [warp][pair][group], f16 pairs
+  unsigned char* all_p = smem + C::kAtP;                     // the tile's probabilities as operands: [warp][n][lane]
+  unsigned char* all_q = smem + C::kAtQ;                     // queries as operands: [n][group][lane]
   float* s_factor = reinterpret_cast<float*>(smem + C::kAtFactor);
-  float2* s_ml = reinterpret_cast<float2*>(smem + C::kAtMl);  // [warp][16]
+  float* s_max = reinterpret_cast<float*>(smem + C::kAtMax);  // [head][warp]
+  float* s_sum = reinterpret_cast<float*>(smem + C::kAtSum);  // [head][warp]
   int32_t* lens = reinterpret_cast<int32_t*>(smem + C::kAtLens);
   int32_t* tsum = lens + p.nb;
+  constexpr int kPart = C::kG < 4 ? C::kG : 4;               // groups whose scales of K a load takes
   const int cap = a.max_blocks * a.bs, shift = 31 - __clz(a.bs), G = a.Hq / a.H;
+
+  // where the lane's 16 bytes of a copy of 512 go: the swap of a row is that of the copy's first row and that of the row in it
+  const uint32_t to_keys = smem_addr(my_keys) + lane * 16 / C::kRowK * C::kRowK + (lane * 16 % C::kRowK ^ C::swap_k(lane * 16 / C::kRowK));
+  const uint32_t to_values = smem_addr(values) + warp * (kStep / 2 * C::kRowV) + lane * 16 / C::kRowV * C::kRowV + (lane * 16 % C::kRowV ^ C::swap_v(lane * 16 / C::kRowV));
+  const uint32_t my_scales = smem_addr(my_keys) + kStep * C::kRowK + lane * 16;
+  // the lane's words: of group 0 of key g and of key pair c, at the group of the warp's first d
+  const uint32_t word_k = g * C::kRowK + (c * 4 ^ C::swap_k(g)), word_v = c * C::kRowV + ((warp * C::kM / 2 * 32) ^ C::swap_v(c)) + g * 4;
 
   // lengths, and tiles before every kCoarse-th request
   {
@@ -160,41 +245,51 @@ __global__ void __launch_bounds__(kThreads, NT == 2 && D == 256 ? 2 : 3) attn4_d
   w.H = a.H;
   w.chunks = p.chunks;
   w.start(blockIdx.x, gridDim.x);
+  int held = -1;  // the head of q that shared memory holds
+#pragma unroll 1
   for (; w.more(); w.next()) {
     const int head0 = w.h * G + w.chunk * 16, heads = min(p.heads, G - w.chunk * 16), keys = w.keys();
-    const int steps = (keys + kStep - 1) / kStep, mine = steps > warp ? (steps - warp + kWarps - 1) / kWarps : 0;
-    // the row of the cache that each of the warp's steps starts at, one to a lane
+    const int tiles = (keys + kTileKeys - 1) / kTileKeys;
+    // the row of the cache that the warp's 16 keys of each tile start at, a lane for each tile; -1: no such page, or no key
     int row = -1;
-    if (lane < mine) {
-      const int pos = w.first() + (warp + kWarps * lane) * kStep;
-      const int page = a.block_table[static_cast<int64_t>(p.b0 + w.b) * a.max_blocks + (pos >> shift)];
-      if (page >= 0 && page < a.num_blocks) row = ((page * a.H + w.h) << shift) + (pos & (a.bs - 1));
-      else if (a.err) atomicOr(a.err, GDN_DEVERR_BLOCK_RANGE);
+    {
+      const int at = lane * kTileKeys + warp * kStep, pos = w.first() + at;
+      if (at < keys) {
+        const int page = a.block_table[static_cast<int64_t>(p.b0 + w.b) * a.max_blocks + (pos >> shift)];
+        if (page >= 0 && page < a.num_blocks) row = ((page * a.H + w.h) << shift) + (pos & (a.bs - 1));
+        else if (a.err) atomicOr(a.err, GDN_DEVERR_BLOCK_RANGE);
+      }
     }
-    auto fetch = [&](int i) {  // the warp's i-th step into its ring
-      const int from = __shfl_sync(0xFFFFFFFFu, row, i & 31);
-      if (i < mine && from >= 0) {
-        const uint32_t to = ring + (i % C::kStages) * C::kStage;
-        const uint8_t* k = a.k_cache + static_cast<int64_t>(from) * (D / 2);
-        const uint8_t* v = a.v_cache + static_cast<int64_t>(from) * (D / 2);
+    auto fetch_keys = [&](int t) {  // of the warp, into its stage t & 1
+      const int from = __shfl_sync(0xFFFFFFFFu, row, t & 31);
+      if (t < tiles && from >= 0) {
+        const uint32_t to = to_keys + (t & 1) * C::kKeys;
+        const uint8_t* k = a.k_cache + static_cast<int64_t>(from) * C::kRowK + lane * 16;
 #pragma unroll
-        for (int x = 0; x < D / 64; ++x) {
-          const int at = (lane + 32 * x) * 16;
-          cp_async16(to + at / (D / 2) * C::kRowK + at % (D / 2), k + at);
-          cp_async16(to + C::kAtV + at / D * C::kRowV + at % D, v + at);
-        }
-        if (lane < 2 * C::kG) {  // 16 bytes each: K's scales, V's
-          const uint8_t* sc = reinterpret_cast<const uint8_t*>(lane < C::kG ? a.k_scale : a.v_scale);
-          cp_async16(to + C::kAtScale + lane * 16, sc + static_cast<int64_t>(from) * C::kG + (lane % C::kG) * 16);
-        }
+        for (int x = 0; x < D / 64; ++x) cp_async16((to ^ C::swap_k(x * (512 / C::kRowK))) + x * 512, k + x * 512);
+        if (lane < 2 * C::kG)  // 16 bytes each: K's scales, V's
+          cp_async16(my_scales + (t & 1) * C::kKeys, (lane < C::kG ? reinterpret_cast<const uint8_t*>(a.k_scale) : reinterpret_cast<const uint8_t*>(a.v_scale)) + static_cast<int64_t>(from) * C::kG + (lane % C::kG) * 16);
       }
       cp_async_commit();
     };
+    auto fetch_values = [&](int t) {  // the warp's part of stage t & 1
+      const int from = __shfl_sync(0xFFFFFFFFu, row, t & 31);
+      if (t < tiles && from >= 0) {
+        const uint32_t to = to_values + (t & 1) * C::kValues;
+        const uint8_t* v = a.v_cache + static_cast<int64_t>(from) * (D / 2) + lane * 16;
 #pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) fetch(i);
+        for (int x = 0; x < D / 64; ++x) cp_async16((to ^ C::swap_v(x * (512 / C::kRowV))) + x * 512, v + x * 512);
+      }
+      cp_async_commit();
+    };
+    fetch_keys(0);
+    fetch_values(0);
+    fetch_keys(1);
 
     // queries as the second operand of K's product: for each eight heads and group, a lane's four registers
-    {
+    const int wanted = w.b * a.Hq + head0;
+    if (wanted != held) {
+      held = wanted;
       constexpr int kLanes = D / 8, kAtOnce = kThreads / kLanes;
       for (int h0 = 0; h0 < 8 * NT; h0 += kAtOnce) {
         const int h = h0 + tid / kLanes, e = tid % kLanes;  // 8 elements of a head
@@ -214,16 +309,15 @@ __global__ void __launch_bounds__(kThreads, NT == 2 && D == 256 ? 2 : 3) attn4_d
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = pack_f16(__uint_as_float(x[i] << 16) * put, __uint_as_float(x[i] & 0xFFFF0000u) * put);
         if (h >= 8 * NT) continue;  // (a head of 64 takes 8 lanes, and all of them 16 heads)
-        const uint32_t to = s_q + ((h / 8) * C::kG + e / 4) * 512 + ((h % 8) * 4 + e % 4) * 16;
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
+        *reinterpret_cast<uint4*>(all_q + ((h / 8) * C::kG + e / 4) * 512 + ((h % 8) * 4 + e % 4) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
         // a query that is not finite makes its head NaN through its factor
         if (e == 0)
           s_factor[h] = top < 0x7F80u ? fabsf(a.scale) * kLog2e * __uint_as_float(static_cast<uint32_t>(field - 14) << 23) : __int_as_float(0x7FC00000);
       }
+      __syncthreads();
     }
-    __syncthreads();
 
-    float o[D / 16][NT][4], m[NT][2], l[NT][2], fac[NT][2];
+    float o[C::kM][NT][4], m[NT][2], l[NT][2], fac[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -233,198 +327,347 @@ __global__ void __launch_bounds__(kThreads, NT == 2 && D == 256 ? 2 : 3) attn4_d
         fac[n][j] = s_factor[n * 8 + 2 * c + j];
       }
 #pragma unroll
-    for (int t = 0; t < D / 16; ++t)
+    for (int t = 0; t < C::kM; ++t)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[t][n][j] = 0.0f;
 
 #pragma unroll 1
-    for (int i = 0; i < mine; ++i) {
-      __syncwarp();  // the stage that is filled next, and the scales, have been read
-      fetch(i + C::kStages - 1);
-      cp_async_wait<C::kStages - 1>();
+    for (int t = 0; t < tiles; ++t) {
+      if (t == 0) cp_async_wait<2>();  // (behind the first keys: their values, the next keys; later ones came before values)
       __syncwarp();
-      const uint32_t st = ring + (i % C::kStages) * C::kStage;
-      const bool there = __shfl_sync(0xFFFFFFFFu, row, i) >= 0;
-      const int live = there ? keys - (warp + kWarps * i) * kStep : 0;  // keys of the step that are seen
-      // the step's scales: lane = (key, half of its groups)
+      const unsigned char* st = my_keys + (t & 1) * C::kKeys;
+      const bool there = __shfl_sync(0xFFFFFFFFu, row, t) >= 0;
+      const int live = there ? keys - t * kTileKeys - warp * kStep : 0;  // how many of the warp's keys are seen
+      // their scales: lane = (key, half of its groups)
       int e_own;
       {
         constexpr int kN = C::kG / 2;
-        const int key = lane >> 1, g0 = (lane & 1) * kN;
-        uint32_t kb[kN], vb[kN];
-        const uint32_t at = st + C::kAtScale + key * C::kG + g0;
-#pragma unroll
-        for (int j = 0; j < kN; ++j) {
-          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(kb[j]) : "r"(at + j));
-          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(vb[j]) : "r"(at + kStep * C::kG + j));
+        const int key = lane >> 1;
+        const unsigned char* raw = st + kStep * C::kRowK;
+        uint32_t kw, vw;
+        if constexpr (kN == 4) {
+          kw = reinterpret_cast<const uint32_t*>(raw)[lane];
+          vw = reinterpret_cast<const uint32_t*>(raw + kStep * C::kG)[lane];
+        } else if constexpr (kN == 2) {
+          kw = reinterpret_cast<const uint16_t*>(raw)[lane];
+          vw = reinterpret_cast<const uint16_t*>(raw + kStep * C::kG)[lane];
+        } else {
+          kw = raw[lane];
+          vw = (raw + kStep * C::kG)[lane];
         }
-        int top = kBias4 + kLeastScale;
-#pragma unroll
-        for (int j = 0; j < kN; ++j) top = max(top, vb[j] == kNaN4 ? 0 : static_cast<int>(vb[j]));
-        top = min(max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1)), 253);
+        KeyScales<kN> sc;
+        int top = sc.largest(vw);
+        top = min(max(max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1)), kBias4 + kLeastScale), 253);
         e_own = top - kBias4;
+        sc.make(kw, vw, top);
+        // K: [key][group]. V: keys 2 j and 2 j + 1 side by side, [j][group]; of a pair the even key's lane writes the first
+        // half of its groups, the odd one the second
 #pragma unroll
-        for (int j = 0; j < kN; ++j) {
-          const uint32_t f = kb[j] == kNaN4 ? 0x7FC00000u : kb[j] << 23;
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(s_k + (key * C::kG + g0 + j) * 4), "r"(f) : "memory");
-          // 2^(e_group - e) in f16, subnormals too
-          const int d = 15 + static_cast<int>(vb[j]) - top;
-          uint32_t v = d > 0 ? static_cast<uint32_t>(d) << 10 : 0x200u >> min(-d, 31);
-          if (vb[j] == kNaN4) v = 0x7E00u;
-          if (key >= live) v = 0;
-          // [lane's c][group][pair c or c + 4][key of the pair]
-          asm volatile("st.shared.b16 [%0], %1;" ::"r"(s_v + (((key & 7) >> 1) * C::kG + g0 + j) * 8 + (key >> 3) * 4 + (key & 1) * 2),
-                       "h"(static_cast<uint16_t>(v))
-                       : "memory");
+        for (int j = 0; j < (kN + 1) / 2; ++j)
+          if (key >= live) sc.v[j] = 0;
+        if constexpr (kN == 4) *reinterpret_cast<uint4*>(my_k + lane * 16) = make_uint4(sc.k[0], sc.k[1], sc.k[2], sc.k[3]);
+        else if constexpr (kN == 2) *reinterpret_cast<uint2*>(my_k + lane * 8) = make_uint2(sc.k[0], sc.k[1]);
+        else *reinterpret_cast<uint32_t*>(my_k + lane * 4) = sc.k[0];
+        __syncwarp();
+        // scores of keys g and g + 8, heads 2 c and 2 c + 1
+        float s[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[n][j] = 0.0f;
+        const uint32_t keys_at = smem_addr(st) + word_k;  // (rows g and g + 8 have the same swap)
+#pragma unroll
+        for (int gr = 0; gr < C::kG; gr += kPart) {
+          float k0[kPart], k1[kPart];
+          load_words(my_k + (g * C::kG + gr) * 4, k0);
+          load_words(my_k + ((g + 8) * C::kG + gr) * 4, k1);
+#pragma unroll
+          for (int z = 0; z < kPart; ++z) {
+            const uint32_t at = keys_at ^ (gr + z) * 16;
+            uint32_t x[4], y[4];
+            e2m1x8(lds32(at), x);
+            e2m1x8(lds32(at + 8 * C::kRowK), y);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const uint4 q = *reinterpret_cast<const uint4*>(all_q + (n * C::kG + gr + z) * 512 + lane * 16);
+              float r[4];
+              mma0(r, x[0], y[0], x[1], y[1], q.x, q.y);
+              mma(r, x[2], y[2], x[3], y[3], q.z, q.w);
+              s[n][0] = fmaf(r[0], k0[z], s[n][0]);
+              s[n][1] = fmaf(r[1], k0[z], s[n][1]);
+              s[n][2] = fmaf(r[2], k1[z], s[n][2]);
+              s[n][3] = fmaf(r[3], k1[z], s[n][3]);
+            }
+          }
         }
-      }
-      __syncwarp();
-      // scores of keys g and g + 8, heads 2 c and 2 c + 1
-      float2 s[NT][2];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int gr = 0; gr < C::kG; ++gr) {
-        uint32_t x[4], y[4];
-        e2m1x8(lds32(st + g * C::kRowK + gr * 16 + c * 4), x);
-        e2m1x8(lds32(st + (g + 8) * C::kRowK + gr * 16 + c * 4), y);
-        const float k0 = __uint_as_float(lds32(s_k + (g * C::kG + gr) * 4)), k1 = __uint_as_float(lds32(s_k + ((g + 8) * C::kG + gr) * 4));
+        __syncwarp();  // the keys have been read
+        fetch_keys(t + 2);
+        const int i0 = __shfl_sync(0xFFFFFFFFu, e_own, 2 * g), i1 = __shfl_sync(0xFFFFFFFFu, e_own, 2 * g + 16);
+        const float e0 = __int_as_float(0x4B400000 + i0) - 12582912.0f, e1 = __int_as_float(0x4B400000 + i1) - 12582912.0f;  // (as floats)
+        const bool hidden0 = g >= live, hidden1 = g + 8 >= live;
+        bool above = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const uint4 q = lds128(s_q + (n * C::kG + gr) * 512 + lane * 16);
-          float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          mma(t, x[0], y[0], x[1], y[1], q.x, q.y);
-          mma(t, x[2], y[2], x[3], y[3], q.z, q.w);
-          s[n][0] = fma2(make_float2(t[0], t[1]), make_float2(k0, k0), s[n][0]);
-          s[n][1] = fma2(make_float2(t[2], t[3]), make_float2(k1, k1), s[n][1]);
-        }
-      }
-      const float e0 = static_cast<float>(__shfl_sync(0xFFFFFFFFu, e_own, 2 * g)), e1 = static_cast<float>(__shfl_sync(0xFFFFFFFFu, e_own, 2 * g + 16));
-      const bool hidden0 = g >= live, hidden1 = g + 8 >= live;
-      bool above = false;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        s[n][0].x = hidden0 ? -INFINITY : s[n][0].x * fac[n][0] + e0;
-        s[n][0].y = hidden0 ? -INFINITY : s[n][0].y * fac[n][1] + e0;
-        s[n][1].x = hidden1 ? -INFINITY : s[n][1].x * fac[n][0] + e1;
-        s[n][1].y = hidden1 ? -INFINITY : s[n][1].y * fac[n][1] + e1;
-        above |= fmaxf(s[n][0].x, s[n][1].x) > m[n][0] + kRise || fmaxf(s[n][0].y, s[n][1].y) > m[n][1] + kRise;
-      }
-      if (__any_sync(0xFFFFFFFFu, above)) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float corr[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float top = j ? fmaxf(s[n][0].y, s[n][1].y) : fmaxf(s[n][0].x, s[n][1].x);
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-            const float to = top > m[n][j] + kRise ? top : m[n][j];  // by the head alone, whatever the others do
-            const float root = to == -INFINITY ? 1.0f : ex2_root(m[n][j] - to);
-            m[n][j] = to;
-            l[n][j] = l[n][j] * root * root;
-            corr[j] = root * root;
-          }
-#pragma unroll
-          for (int t = 0; t < D / 16; ++t) {
-            o[t][n][0] *= corr[0];
-            o[t][n][1] *= corr[1];
-            o[t][n][2] *= corr[0];
-            o[t][n][3] *= corr[1];
+            s[n][j] = hidden0 ? -INFINITY : fmaf(s[n][j], fac[n][j], e0);
+            s[n][2 + j] = hidden1 ? -INFINITY : fmaf(s[n][2 + j], fac[n][j], e1);
+            above |= fmaxf(s[n][j], s[n][2 + j]) > m[n][j] + kRise;
           }
         }
-      }
-      // p 2^e, and p into the sum; both keys' rows turned into columns
-      const float d0 = __int_as_float((kBias4 - static_cast<int>(e0)) << 23), d1 = __int_as_float((kBias4 - static_cast<int>(e1)) << 23);
-      uint32_t pb[NT][2];
+        // from here on every warp is done with the tile before: its values, their scales and the probabilities are free
+        if (__syncthreads_or(above)) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float mx = m[n][0] == -INFINITY ? 0.0f : m[n][0] - kTop, my = m[n][1] == -INFINITY ? 0.0f : m[n][1] - kTop;
-        const float px0 = ex2(s[n][0].x - mx), py0 = ex2(s[n][0].y - my), px1 = ex2(s[n][1].x - mx), py1 = ex2(s[n][1].y - my);
-        l[n][0] += px0 * d0 + px1 * d1;
-        l[n][1] += py0 * d0 + py1 * d1;
-        pb[n][0] = transpose8(pack_f16(px0, py0));
-        pb[n][1] = transpose8(pack_f16(px1, py1));
-      }
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int gr = 0; gr < C::kG; ++gr) {
-        uint32_t x[4], y[4];
-        e2m1x8(lds32(st + C::kAtV + c * C::kRowV + gr * 32 + g * 4), x);
-        e2m1x8(lds32(st + C::kAtV + (c + 4) * C::kRowV + gr * 32 + g * 4), y);
-        const uint32_t v0 = lds32(s_v + (c * C::kG + gr) * 8), v1 = lds32(s_v + (c * C::kG + gr) * 8 + 4);
+            for (int j = 0; j < 2; ++j) {
+              float top = fmaxf(s[n][j], s[n][2 + j]);
+#pragma unroll
+              for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+              if (g == 0) s_max[(n * 8 + 2 * c + j) * kWarps + warp] = top;
+            }
+          __syncthreads();
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float corr[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float4 v = *reinterpret_cast<const float4*>(s_max + (n * 8 + 2 * c + j) * kWarps);
+              const float top = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+              const float to = top > m[n][j] + kRise ? top : m[n][j];  // by the head alone, whatever the others do
+              const float root = to == -INFINITY ? 1.0f : ex2_root(m[n][j] - to);
+              m[n][j] = to;
+              l[n][j] = l[n][j] * root * root;
+              corr[j] = root * root;
+            }
+#pragma unroll
+            for (int x = 0; x < C::kM; ++x) {
+              o[x][n][0] *= corr[0];
+              o[x][n][1] *= corr[1];
+              o[x][n][2] *= corr[0];
+              o[x][n][3] *= corr[1];
+            }
+          }
+        }
+        fetch_values(t + 1);
+        // p 2^e, and p into the sum; both keys' rows turned into columns
+        const float d0 = __int_as_float((kBias4 - i0) << 23), d1 = __int_as_float((kBias4 - i1) << 23);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const uint32_t b0 = mul_f16x2(pb[n][0], v0), b1 = mul_f16x2(pb[n][1], v1);
-          mma(o[2 * gr][n], x[0], x[1], y[0], y[1], b0, b1);
-          mma(o[2 * gr + 1][n], x[2], x[3], y[2], y[3], b0, b1);
+          float x[4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float from = m[n][j] == -INFINITY ? 0.0f : m[n][j] - kTop;
+            x[j] = ex2(s[n][j] - from);
+            x[2 + j] = ex2(s[n][2 + j] - from);
+            l[n][j] = fmaf(x[j], d0, fmaf(x[2 + j], d1, l[n][j]));
+          }
+          *reinterpret_cast<uint2*>(all_p + ((warp * NT + n) * 32 + lane) * 8) =
+              make_uint2(transpose8(pack_f16(x[0], x[1])), transpose8(pack_f16(x[2], x[3])));
+        }
+        const bool odd = key & 1;
+        uint32_t* put = reinterpret_cast<uint32_t*>(all_v + warp * C::kScaleV) + (key >> 1) * C::kG + (lane & 1) * kN;
+        if constexpr (kN == 4) {
+          const uint32_t mine_v = odd ? sc.v[1] : sc.v[0], got = __shfl_xor_sync(0xFFFFFFFFu, odd ? sc.v[0] : sc.v[1], 2);
+          const uint32_t lo = odd ? got : mine_v, hi = odd ? mine_v : got;
+          *reinterpret_cast<uint2*>(put + (odd ? 2 : 0)) = make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+        } else {
+          const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, sc.v[0], 2);
+          const uint32_t lo = odd ? got : sc.v[0], hi = odd ? sc.v[0] : got;
+          if constexpr (kN == 2) put[odd] = __byte_perm(lo, hi, odd ? 0x7632 : 0x5410);
+          else if (!odd) put[0] = __byte_perm(lo, hi, 0x5410);
+        }
+      }
+      cp_async_wait<2>();  // (behind these values: the keys of the tile after the next, the next values)
+      __syncthreads();
+      // O^T: the warp's d, all keys of the tile
+      {
+        const uint32_t values_at = smem_addr(values) + (t & 1) * C::kValues + word_v;  // (pairs c and c + 4 have the same swap)
+#pragma unroll
+        for (int sub = 0; sub < kWarps; ++sub) {
+          uint2 pr[NT];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) pr[n] = *reinterpret_cast<const uint2*>(all_p + ((sub * NT + n) * 32 + lane) * 8);
+          const unsigned char* sv = all_v + sub * C::kScaleV + (c * C::kG + warp * C::kM / 2) * 4;
+          uint32_t v0[2], v1[2];
+          if constexpr (C::kM == 4) {
+            load_words(sv, v0);
+            load_words(sv + 4 * C::kG * 4, v1);
+          } else {
+            v0[0] = *reinterpret_cast<const uint32_t*>(sv);
+            v1[0] = *reinterpret_cast<const uint32_t*>(sv + 4 * C::kG * 4);
+          }
+#pragma unroll
+          for (int z = 0; z < (C::kM + 1) / 2; ++z) {
+            const uint32_t at = (values_at ^ z * 32) + sub * (kStep / 2 * C::kRowV);
+            uint32_t lo = lds32(at), hi = lds32(at + 4 * C::kRowV);
+            if constexpr (C::kM == 1) {  // half of a group
+              lo >>= (warp & 1) * 16;
+              hi >>= (warp & 1) * 16;
+            }
+            uint32_t x[4], y[4];
+            e2m1x8(lo, x);
+            e2m1x8(hi, y);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const uint32_t b0 = mul_f16x2(pr[n].x, v0[z]), b1 = mul_f16x2(pr[n].y, v1[z]);
+              mma(o[2 * z][n], x[0], x[1], y[0], y[1], b0, b1);
+              if constexpr (C::kM > 1) mma(o[2 * z + 1][n], x[2], x[3], y[2], y[3], b0, b1);
+            }
+          }
         }
       }
     }
     cp_async_wait<0>();
-    // the unit's sums: over the warp's lanes, then over the warps
+    // the unit's sums, over the lanes and the warps
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[n][j] += __shfl_xor_sync(0xFFFFFFFFu, l[n][j], x);
-        if (g == 0) s_ml[warp * 16 + n * 8 + 2 * c + j] = make_float2(m[n][j], l[n][j]);
+        if (g == 0) s_sum[(n * 8 + 2 * c + j) * kWarps + warp] = l[n][j];
       }
     __syncthreads();
-    // a warp's weight (its root: a sum is multiplied with it twice)
-    auto weight = [&](float2 e, float top) { return e.x == -INFINITY ? (e.y == 0.0f ? 0.0f : 1.0f) : ex2_root(e.x - top); };
-    auto largest = [&](int h) { return fmaxf(fmaxf(s_ml[h].x, s_ml[16 + h].x), fmaxf(s_ml[32 + h].x, s_ml[48 + h].x)); };
     const int64_t f = ((static_cast<int64_t>(w.b) * a.H + w.h) * p.chunks + w.chunk) * p.each + w.index;
     const bool alone = w.count == 1;
-    float* rows = reinterpret_cast<float*>(smem);  // [warp]'s part of the rings: [8][kRowO]
+    uint16_t* out = a.out + (static_cast<int64_t>(p.b0 + w.b) * a.Hq + head0) * D;
+    float* part = p.part + f * p.heads * D;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float corr[2];
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float root = weight(make_float2(m[n][j], l[n][j]), largest(n * 8 + 2 * c + j));
-        corr[j] = root * root;
-      }
-      // a lane has d 32 gr + 4 g .. + 3 of heads 2 c and 2 c + 1 (a warp without a key: zeros, not 0 * what is there)
+        const int h = n * 8 + 2 * c + j;
+        const float4 l4 = *reinterpret_cast<const float4*>(s_sum + h * kWarps);
+        const float sum = (l4.x + l4.y) + (l4.z + l4.w), inv = sum > 0.0f || sum != sum ? __fdividef(1.0f, sum) : 0.0f;
+        if (h < heads) {
+          if (!alone && warp == 0 && g == 0) p.ml[f * p.heads + h] = make_float2(m[n][j], sum);
+          if constexpr (C::kM == 1) {  // d of the warp's half of a group: 4 g + 0 and 1, or 2 and 3
+            const int d = (warp >> 1) * 32 + g * 4 + (warp & 1) * 2;
+            if (alone) *reinterpret_cast<uint32_t*>(out + h * D + d) = pack_bf16(o[0][n][j] * inv, o[0][n][2 + j] * inv);
+            else *reinterpret_cast<float2*>(part + h * D + d) = make_float2(o[0][n][j], o[0][n][2 + j]);
+          } else {
 #pragma unroll
-      for (int gr = 0; gr < C::kG; ++gr)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float4 v = make_float4(o[2 * gr][n][j] * corr[j], o[2 * gr][n][2 + j] * corr[j], o[2 * gr + 1][n][j] * corr[j], o[2 * gr + 1][n][2 + j] * corr[j]);
-          *reinterpret_cast<float4*>(rows + warp * (C::kWarp / 4) + (2 * c + j) * C::kRowO + gr * 32 + g * 4) = v;
-        }
-      __syncthreads();
-      for (int i = tid; i < 8 * (D / 4); i += kThreads) {
-        const int h = n * 8 + i / (D / 4), d = i % (D / 4) * 4;
-        if (h >= heads) break;
-        const float top = largest(h);
-        float sum = 0.0f;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int x = 0; x < kWarps; ++x) {
-          const float root = weight(s_ml[x * 16 + h], top);
-          sum += s_ml[x * 16 + h].y * root * root;
-          const float4 y = *reinterpret_cast<const float4*>(rows + x * (C::kWarp / 4) + (h - n * 8) * C::kRowO + d);
-          v.x += y.x;
-          v.y += y.y;
-          v.z += y.z;
-          v.w += y.w;
-        }
-        if (alone) {
-          const float inv = sum > 0.0f || sum != sum ? __fdividef(1.0f, sum) : 0.0f;
-          uint2 st;
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(st.x) : "f"(v.y * inv), "f"(v.x * inv));
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(st.y) : "f"(v.w * inv), "f"(v.z * inv));
-          *reinterpret_cast<uint2*>(a.out + (static_cast<int64_t>(p.b0 + w.b) * a.Hq + head0 + h) * D + d) = st;
-        } else {
-          if (d == 0) p.ml[f * p.heads + h] = make_float2(top, sum);
-          *reinterpret_cast<float4*>(p.part + (f * p.heads + h) * D + d) = v;
+            for (int z = 0; z < C::kM / 2; ++z) {
+              const int d = (warp * C::kM / 2 + z) * 32 + g * 4;
+              const float4 v = make_float4(o[2 * z][n][j], o[2 * z][n][2 + j], o[2 * z + 1][n][j], o[2 * z + 1][n][2 + j]);
+              if (alone) *reinterpret_cast<uint2*>(out + h * D + d) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+              else *reinterpret_cast<float4*>(part + h * D + d) = v;
+            }
+          }
         }
       }
-      __syncthreads();  // the rings are filled anew
+    __syncthreads();  // sums, scales, probabilities and the last values have been read
+  }
+}
+
+// Joins the units of one request, kv head and head chunk in unit order; an empty request gets zeros. The units' weights are
+// made once for a head, in shared memory; a thread then has four d of a head. Up to kJoinFew units it takes in order; more are
+// taken by kJoinRows4 threads, unit u by u mod kJoinRows4, whose sums are taken in order then.
+constexpr int kJoinFew = 32, kJoinRows4 = 16;
+constexpr int kJoinUnits = 1024;  // weights that are kept at a time
+
+template <int D>
+__global__ void __launch_bounds__(256) attn4_join_kernel(const __grid_constant__ DecodeParams p) {
+  constexpr int kLanes = D / 4;  // threads of a head
+  __shared__ float s_w[kJoinUnits];
+  __shared__ float s_red[16];
+  __shared__ float4 s_o[kJoinRows4][16];
+  const AttnArgs& a = p.a;
+  const int HC = a.H * p.chunks, G = a.Hq / a.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x / HC, hc = blockIdx.x - b * HC, h = hc / p.chunks, chunk = hc - h * p.chunks;
+  const int heads = min(p.heads, G - chunk * 16);
+  const int n = Units::count(min(max(a.lens[p.b0 + b], 0), a.max_blocks * a.bs));
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // (by every CTA: this kernel's end stands for the call's)
+  if (n == 1) return;
+  const int64_t f = static_cast<int64_t>(blockIdx.x) * p.each * p.heads;
+  const float2* ml = p.ml + f;
+  const float4* part = reinterpret_cast<const float4*>(p.part + f * D);
+  uint16_t* out = a.out + (static_cast<int64_t>(p.b0 + b) * a.Hq + h * G + chunk * 16) * D;
+  const int step = p.heads * kLanes;  // vectors of a unit
+  // A unit's weight by its root: a sum is multiplied with it twice. (Without keys m = -inf, l = 0; with only NaN scores
+  // m = -inf, l = NaN.)
+  auto root_of = [](float2 e, float top) { return e.x == -INFINITY ? (e.y == 0.0f ? 0.0f : 1.0f) : ex2_root(e.x - top); };
+  auto inverse = [](float l) { return l > 0.0f || l != l ? __fdividef(1.0f, l) : 0.0f; };
+  auto fma4 = [](float4& o, const float4& v, float w) {
+    o.x = fmaf(v.x, w, o.x);
+    o.y = fmaf(v.y, w, o.y);
+    o.z = fmaf(v.z, w, o.z);
+    o.w = fmaf(v.w, w, o.w);
+  };
+  auto store = [&](int i, const float4& o, float inv) {
+    *reinterpret_cast<uint2*>(out + i * 4) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  };
+  if (n <= kJoinFew) {
+    const int i = blockIdx.y * 256 + tid, first = blockIdx.y * (256 / kLanes);  // the block's heads
+    if (first >= heads) return;
+#pragma unroll
+    for (int in = warp; in < 256 / kLanes; in += 8) {  // a head, a lane for each unit
+      float2 e = make_float2(-INFINITY, 0.0f);
+      if (first + in < heads && lane < n) e = ml[lane * p.heads + first + in];
+      float top = e.x;
+#pragma unroll
+      for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+      const float root = root_of(e, top);
+      float l = e.y * root * root;
+#pragma unroll
+      for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
+      s_w[in * 32 + lane] = root * root;
+      if (lane == 0) s_red[in] = inverse(l);
     }
+    __syncthreads();
+    if (i >= heads * kLanes) return;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int u = 0; u < n; ++u) fma4(o, part[static_cast<int64_t>(u) * step + i], s_w[tid / kLanes * 32 + u]);
+    store(i, o, s_red[tid / kLanes]);
+    return;
+  }
+  const int row = tid / 16, in = tid % 16;
+#pragma unroll 1
+  for (int i0 = blockIdx.y * 16; i0 < heads * kLanes; i0 += gridDim.y * 16) {  // 16 lanes of one head
+    const float2* e = ml + i0 / kLanes;
+    float top = -INFINITY, l = 0.0f;
+#pragma unroll 1
+    for (int u = tid; u < n; u += 256) top = fmaxf(top, e[static_cast<int64_t>(u) * p.heads].x);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+    if (lane == 0) s_red[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < 8; ++x) top = fmaxf(top, s_red[x]);
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+    for (int u0 = 0; u0 < n; u0 += kJoinUnits) {
+      const int here = min(kJoinUnits, n - u0);
+#pragma unroll 1
+      for (int u = tid; u < here; u += 256) {
+        const float2 x = e[static_cast<int64_t>(u0 + u) * p.heads];
+        const float root = root_of(x, top);
+        l += x.y * root * root;
+        s_w[u] = root * root;
+      }
+      __syncthreads();
+#pragma unroll 8
+      for (int u = row; u < here; u += kJoinRows4) fma4(o, part[static_cast<int64_t>(u0 + u) * step + i0 + in], s_w[u]);
+      __syncthreads();
+    }
+    s_o[row][in] = o;
+#pragma unroll
+    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
+    if (lane == 0) s_red[8 + warp] = l;
+    __syncthreads();
+    if (row == 0) {
+#pragma unroll
+      for (int x = 1; x < kJoinRows4; ++x) fma4(o, s_o[x][in], 1.0f);
+      l = 0.0f;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) l += s_red[8 + x];
+      store(i0 + in, o, inverse(l));
+    }
+    __syncthreads();
   }
 }
 
@@ -447,7 +690,22 @@ cudaError_t launch_d(DecodeParams& p, cudaStream_t s) {
   const int grid = static_cast<int>(most < static_cast<int64_t>(per_sm) * sm_count() ? most : per_sm * sm_count());
   kern<<<grid, kThreads, smem, s>>>(p);
   e = cudaGetLastError();
-  return e != cudaSuccess ? e : launch_join<D, Units>(p, s);
+  if (e != cudaSuccess) return e;
+  // The join, a programmatic dependent: four d of a head to a thread, or to kJoinRows4 of them where requests may have many
+  // units; of those CTAs no more than fill the GPU (512 x 32, most of them for requests of few units, took 27 us, and 512 x 2 ??).
+  cudaLaunchConfig_t cfg = {};
+  const int pairs = p.nb * p.a.H * p.chunks, few = (p.heads * D + 1023) / 1024;
+  int wide = p.heads * D / 64;
+  if (wide > 16 * sm_count() / pairs) wide = 16 * sm_count() / pairs;
+  cfg.gridDim = dim3(pairs, p.each > kJoinFew && wide > few ? wide : few, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn4_join_kernel<D>, p);
 }
 
 template <int D>

@@ -105,23 +105,19 @@ template <int N>
 struct KeyScales {
   uint32_t k[N];              // fp32 2^(e - 127)
   uint32_t v[(N + 1) / 2];    // f16 pairs 2^(e - top)
-  __device__ __forceinline__ static int largest(uint32_t w) {  // of the bytes of V, 255 apart
-    if (has_255(w)) {
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (((w >> 8 * j) & 255u) == 255u) w &= ~(255u << 8 * j);
-    }
-    uint32_t m = N > 1 ? max_u16x2(__byte_perm(w, 0, 0x4140), N > 2 ? __byte_perm(w, 0, 0x4342) : 0u) : w;
+  __device__ __forceinline__ static int largest(uint32_t w) {  // of N bytes
+    const uint32_t m = N > 1 ? max_u16x2(__byte_perm(w, 0, 0x4140), N > 2 ? __byte_perm(w, 0, 0x4342) : 0u) : w;
     return static_cast<int>(N > 1 ? max(m & 0xFFFFu, m >> 16) : m);
+  }
+  __device__ __forceinline__ static uint32_t without_255(uint32_t w) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (((w >> 8 * j) & 255u) == 255u) w &= ~(255u << 8 * j);
+    return w;
   }
   __device__ __forceinline__ void make(uint32_t kw, uint32_t vw, int top) {
 #pragma unroll
     for (int j = 0; j < N; ++j) k[j] = (j == 0 ? kw << 23 : j == 1 ? kw << 15 : j == 2 ? kw << 7 : kw >> 1) & 0x7F800000u;
-    if (has_255(kw)) {
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (k[j] == 0x7F800000u) k[j] = 0x7FC00000u;
-    }
     // 25 + e - top is the exponent field of 2^(e - top + 10), times 2^-10 (rounded to an f16 subnormal where that is one)
     const uint32_t add = static_cast<uint32_t>(256 + 25 - top) * 0x10001u;
 #pragma unroll
@@ -129,10 +125,12 @@ struct KeyScales {
       const uint32_t t = max_u16x2(__byte_perm(vw, 0, j ? 0x4342 : 0x4140) + add, 0x01000100u);
       v[j] = mul_f16x2((t & 0x001F001Fu) << 10, 0x14001400u);
     }
-    if (has_255(vw)) {
+  }
+  __device__ __forceinline__ void mark(uint32_t kw, uint32_t vw) {  // NaN for 255
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (((vw >> 8 * j) & 255u) == 255u) v[j / 2] = (v[j / 2] & (j % 2 ? 0xFFFFu : 0xFFFF0000u)) | (j % 2 ? 0x7E000000u : 0x7E00u);
+    for (int j = 0; j < N; ++j) {
+      if (((kw >> 8 * j) & 255u) == 255u) k[j] = 0x7FC00000u;
+      if (((vw >> 8 * j) & 255u) == 255u) v[j / 2] = (v[j / 2] & (j % 2 ? 0xFFFFu : 0xFFFF0000u)) | (j % 2 ? 0x7E000000u : 0x7E00u);
     }
   }
 };
@@ -165,8 +163,9 @@ struct Cfg {
   static constexpr int kAtV = kWarps * 2 * kKeys, kAtSk = kAtV + 2 * kValues, kAtSv = kAtSk + kWarps * kScaleK, kAtP = kAtSv + kWarps * kScaleV,
                        kAtQ = kAtP + kWarps * NT * 256, kAtFactor = kAtQ + NT * kG * 512, kAtMax = kAtFactor + 64, kAtSum = kAtMax + kWarps * 64,
                        kAtLens = kAtSum + kWarps * 64;
-  // CTAs of an SM: what shared memory holds for a head of 256, and registers without spills below that
-  static constexpr int kCtas = D == 256 ? (NT == 2 ? 4 : 5) : D == 128 ? (NT == 2 ? 5 : 6) : (NT == 2 ? 6 : 8);
+  // CTAs of an SM. One more each costs registers, and with them instructions that are computed again: 256 requests of about
+  // 8,000 tokens (D = 256, 8 heads) 213 us with 4 and 217 with 5.
+  static constexpr int kCtas = D == 256 ? (NT == 2 ? 3 : 4) : D == 128 ? (NT == 2 ? 4 : 5) : (NT == 2 ? 6 : 8);
   static constexpr int smem_of(int nb) { return 128 + kAtLens + 4 * (nb + nb / kCoarse + 2); }
   static_assert(kKeys % (D == 64 ? 64 : 128) == 0 && kAtP % 16 == 0, "alignment: a place in a row is changed by bits of the address");
   // Where 16 bytes lie in a row, as bits of the address to change: no bank twice for eight rows' (four pairs') operand words
@@ -358,15 +357,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kern
           vw = (raw + kStep * C::kG)[lane];
         }
         KeyScales<kN> sc;
-        int top = sc.largest(vw);
+        const bool nan = has_255(kw) | has_255(vw);
+        int top = sc.largest(nan ? sc.without_255(vw) : vw);
         top = min(max(max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1)), kBias4 + kLeastScale), 253);
         e_own = top - kBias4;
         sc.make(kw, vw, top);
+        if (nan) sc.mark(kw, vw);
+        if (key >= live) {
+#pragma unroll
+          for (int j = 0; j < (kN + 1) / 2; ++j) sc.v[j] = 0;
+        }
         // K: [key][group]. V: keys 2 j and 2 j + 1 side by side, [j][group]; of a pair the even key's lane writes the first
         // half of its groups, the odd one the second
-#pragma unroll
-        for (int j = 0; j < (kN + 1) / 2; ++j)
-          if (key >= live) sc.v[j] = 0;
         if constexpr (kN == 4) *reinterpret_cast<uint4*>(my_k + lane * 16) = make_uint4(sc.k[0], sc.k[1], sc.k[2], sc.k[3]);
         else if constexpr (kN == 2) *reinterpret_cast<uint2*>(my_k + lane * 8) = make_uint2(sc.k[0], sc.k[1]);
         else *reinterpret_cast<uint32_t*>(my_k + lane * 4) = sc.k[0];
@@ -406,19 +408,29 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kern
         fetch_keys(t + 2);
         const int i0 = __shfl_sync(0xFFFFFFFFu, e_own, 2 * g), i1 = __shfl_sync(0xFFFFFFFFu, e_own, 2 * g + 16);
         const float e0 = __int_as_float(0x4B400000 + i0) - 12582912.0f, e1 = __int_as_float(0x4B400000 + i1) - 12582912.0f;  // (as floats)
-        const bool hidden0 = g >= live, hidden1 = g + 8 >= live;
-        bool above = false;
+        float above = -INFINITY;  // what the scores pass the running maxima by, at most
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            s[n][j] = hidden0 ? -INFINITY : fmaf(s[n][j], fac[n][j], e0);
-            s[n][2 + j] = hidden1 ? -INFINITY : fmaf(s[n][2 + j], fac[n][j], e1);
-            above |= fmaxf(s[n][j], s[n][2 + j]) > m[n][j] + kRise;
+            s[n][j] = fmaf(s[n][j], fac[n][j], e0);
+            s[n][2 + j] = fmaf(s[n][2 + j], fac[n][j], e1);
           }
+        if (live < kStep) {  // the request's last keys, or a page that is none
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if (g >= live) s[n][j] = -INFINITY;
+              if (g + 8 >= live) s[n][2 + j] = -INFINITY;
+            }
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) above = fmaxf(above, fmaxf(s[n][j], s[n][2 + j]) - m[n][j]);  // (-inf - -inf is left out)
         // from here on every warp is done with the tile before: its values, their scales and the probabilities are free
-        if (__syncthreads_or(above)) {
+        if (__syncthreads_or(above > kRise)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -679,12 +691,8 @@ cudaError_t launch_d(DecodeParams& p, cudaStream_t s) {
   // the same for every call: the limit is the kernel's, whichever thread sets it last
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem_of(kBatchPerLaunch));
   if (e != cudaSuccess) return e;
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, kern);
-  if (e != cudaSuccess) return e;
-  int per_sm = kSmemPerSm / (smem + static_cast<int>(fa.sharedSizeBytes) + 1024);
-  const int by_regs = 65536 / (((fa.numRegs + 7) & ~7) * kThreads);
-  if (per_sm > by_regs) per_sm = by_regs;
+  int per_sm = kSmemPerSm / (smem + 256 + 1024);  // (256: what the kernel declares itself)
+  if (per_sm > C::kCtas) per_sm = C::kCtas;       // (registers for as many by its launch bounds)
   if (per_sm < 1) per_sm = 1;
   const int64_t most = static_cast<int64_t>(p.nb) * p.a.H * p.chunks * p.each;
   const int grid = static_cast<int>(most < static_cast<int64_t>(per_sm) * sm_count() ? most : per_sm * sm_count());

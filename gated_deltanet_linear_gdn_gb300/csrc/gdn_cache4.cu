@@ -26,115 +26,162 @@ constexpr int kThreads = 256;
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
 
-// The byte of a group's scale, from the eight bf16 values that each of the group's four lanes has.
-__device__ __forceinline__ uint32_t group_byte(const uint4& u) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  uint32_t top = 0, nan = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;  // |x| orders like its bits, from 0x7F80 on not finite
-    top = max(top, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
-    nan |= (lo > 0x7F80u) | (hi > 0x7F80u);
+// 16 elements of a token's head, as a thread has them: two lanes make a group.
+struct Sixteen {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    a = *reinterpret_cast<const uint4*>(p);
+    b = *reinterpret_cast<const uint4*>(p + 8);
   }
-  uint32_t m = top | (nan << 16);
+  __device__ __forceinline__ void word(int i, uint32_t& w) const { w = i == 0 ? a.x : i == 1 ? a.y : i == 2 ? a.z : i == 3 ? a.w : i == 4 ? b.x : i == 5 ? b.y : i == 6 ? b.z : b.w; }
+  // The byte of the group's scale. |x| orders like its bits, two at a time; from 0x7F80 on it is not finite.
+  __device__ __forceinline__ uint32_t group_byte() const {
+    uint32_t m = 0, w;
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    const uint32_t n = __shfl_xor_sync(0xFFFFFFFFu, m, o);
-    m = max(m & 0xFFFFu, n & 0xFFFFu) | ((m | n) & 0x10000u);
+    for (int i = 0; i < 8; ++i) {
+      word(i, w);
+      asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(w & 0x7FFF7FFFu));
+    }
+    m = max(m & 0xFFFFu, m >> 16);
+    uint32_t all = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    if (__any_sync(0xFFFFFFFFu, all >= 0x7F80u)) {  // an infinity or NaN: once more over the finite values
+      if (m >= 0x7F80u) {
+        const bool nan = m > 0x7F80u;
+        m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          word(i, w);
+          const uint32_t lo = w & 0x7FFFu, hi = (w >> 16) & 0x7FFFu;
+          m = max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+        }
+        if (nan) m = 0xFFFFu;
+      }
+      all = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      if (all == 0xFFFFu) return kNaN4;
+    }
+    // the largest = 2^(E - 127) * (1 + M / 128) <= 1.75 * 2^2 * 2^(e - 127)
+    const int e = static_cast<int>(all >> 7) - 2 + ((all & 127u) > 96u);
+    return max(e, kLeastByte4);
   }
-  if (m >> 16) return kNaN4;
-  // top = 2^(E - 127) * (1 + M / 128) <= 1.75 * 2^2 * 2^(e - 127)
-  const int e = static_cast<int>(m >> 7) - 2 + ((m & 127u) > 96u);
-  return max(e, kLeastByte4);
-}
+  // values 8 i .. 8 i + 7 times r
+  __device__ __forceinline__ void scaled(int i, float r, float (&f)[8]) const {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      uint32_t w;
+      word(4 * i + x, w);
+      f[2 * x] = bf_lo(w) * r;
+      f[2 * x + 1] = bf_hi(w) * r;
+    }
+  }
+};
 // 2^(127 - byte), which a value is multiplied with (of a group with NaN, anything: its codes mean nothing)
 __device__ __forceinline__ float down_by(uint32_t byte) { return __uint_as_float((254u - min(byte, 253u)) << 23); }
 
-__device__ __forceinline__ void scaled(const uint4& u, float r, float (&f)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf_lo(w[i]) * r;
-    f[2 * i + 1] = bf_hi(w[i]) * r;
+// The place of a token's 16 elements: j counts the sixteens of all its heads.
+struct Place {
+  int64_t row;  // (block, head, offset) as a row of the cache
+  int e;        // which 16 of the head
+  __device__ __forceinline__ Place(const Cache4& c, int slot, int j, int sixteens, int block) {
+    const int h = j >> sixteens, blk = slot >> block, off = slot & (c.bs - 1);
+    e = j - (h << sixteens);
+    row = (static_cast<int64_t>(blk) * c.H + h) * c.bs + off;
   }
-}
+};
 
-// Four bits each of two words side by side: byte i = (element i of a, element i of b).
-__device__ __forceinline__ uint2 interleave(uint32_t a, uint32_t b) {
-  auto spread = [](uint32_t x) {  // 16 bits: four bits to each byte
-    x = (x | (x << 8)) & 0x00FF00FFu;
-    return (x | (x << 4)) & 0x0F0F0F0Fu;
-  };
-  return make_uint2(spread(a & 0xFFFFu) | (spread(b & 0xFFFFu) << 4), spread(a >> 16) | (spread(b >> 16) << 4));
-}
-
-// grid: (tokens, keys or values). A CTA has `at_once` tokens at a time, `rounds` times; a thread has 8 elements of a head.
+// grid: (tokens, keys or values). A CTA has `at_once` tokens at a time, `rounds` times, two of them in flight; a thread has 16
+// elements of a head.
 __global__ void __launch_bounds__(kThreads) cache4_append_kernel(const __grid_constant__ Append4Args a, int per, int at_once, int rounds) {
   const Cache4& c = a.c;
   const bool is_v = blockIdx.y != 0;
   const int lt = threadIdx.x / per, j0 = threadIdx.x - lt * per;
-  const int chunks = 31 - __clz(c.d >> 3), all = c.H << chunks, groups = c.d / kGroup4;  // chunks: log2 of a head's
+  const int sixteens = 27 - __clz(c.d), all = c.H << sixteens, groups = c.d / kGroup4;  // (log2 of a head's sixteens)
   const int cap = c.num_blocks * c.bs, block = 31 - __clz(c.bs);
   const uint16_t* x = is_v ? a.v : a.k;
   const int64_t stride = is_v ? a.v_stride : a.k_stride, first = static_cast<int64_t>(blockIdx.x) * at_once * rounds + lt;
   uint8_t* scales = is_v ? c.v_scale : c.k_scale;
+  constexpr int kFlight = 2;
 #pragma unroll 1
   for (int j = j0; j - j0 < all; j += per) {  // (the same number of turns for all threads: per divides all, or is the CTA)
-#pragma unroll 2
-    for (int r = 0; r < rounds; ++r) {
-      const int64_t t = first + static_cast<int64_t>(r) * at_once;
-      int slot = -1, next = -1;
-      bool mine = lt < at_once && t < a.T && j < all;
-      if (mine) {
-        slot = a.slot_map[t];
-        if (slot >= cap && j == 0 && a.err && !is_v) atomicOr(a.err, GDN_DEVERR_BLOCK_RANGE);
-        mine = slot >= 0 && slot < cap;
-        if (mine && is_v) {
-          if (slot & 1) {
-            mine = !(t > 0 && a.slot_map[t - 1] == slot - 1);  // the token before writes for both
-          } else if (t + 1 < a.T && a.slot_map[t + 1] == slot + 1) {
-            next = slot + 1;
+#pragma unroll 1
+    for (int r0 = 0; r0 < rounds; r0 += kFlight) {
+      int slot[kFlight];
+      bool pair[kFlight], mine[kFlight];
+      Sixteen u[kFlight], w[kFlight];
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+        const int64_t t = first + static_cast<int64_t>(r0 + i) * at_once;
+        slot[i] = -1;
+        pair[i] = false;
+        mine[i] = r0 + i < rounds && lt < at_once && t < a.T && j < all;
+        if (mine[i]) {
+          slot[i] = a.slot_map[t];
+          if (is_v) {
+            const int before = t > 0 ? a.slot_map[t - 1] : -1, after = t + 1 < a.T ? a.slot_map[t + 1] : -1;
+            mine[i] = !((slot[i] & 1) && before == slot[i] - 1);  // (the token before writes for both)
+            pair[i] = !(slot[i] & 1) && after == slot[i] + 1;
           }
+          if (slot[i] >= cap && j == 0 && a.err && !is_v) atomicOr(a.err, GDN_DEVERR_BLOCK_RANGE);
+          if (slot[i] < 0 || slot[i] >= cap) mine[i] = pair[i] = false;
         }
+        u[i].a = u[i].b = w[i].a = w[i].b = make_uint4(0, 0, 0, 0);
+        const uint16_t* src = x + t * stride + j * 16;
+        if (mine[i]) u[i].load(src);
+        if (mine[i] && pair[i]) w[i].load(src + stride);
       }
-      const uint16_t* src = x + t * stride + j * 8;
-      uint4 u = make_uint4(0, 0, 0, 0), w = u;
-      if (mine) u = *reinterpret_cast<const uint4*>(src);
-      if (mine && next >= 0) w = *reinterpret_cast<const uint4*>(src + stride);
-      const uint32_t byte = group_byte(u);
-      float f[8];
-      scaled(u, down_by(byte), f);
-      const uint32_t codes = to_e2m1x8(f);
-      const int h = j >> chunks, e = j - (h << chunks);  // the head, and which 8 of its elements
-      const int blk = slot >> block, off = slot & (c.bs - 1);
-      const int64_t of_head = static_cast<int64_t>(blk) * c.H + h;
-      uint8_t* sc = scales + (of_head * c.bs + off) * groups + e / 4;
-      if (!is_v) {
-        if (mine) *reinterpret_cast<uint32_t*>(c.k + (of_head * c.bs + off) * (c.d / 2) + e * 4) = codes;
-      } else {
-        const uint32_t byte2 = group_byte(w);
-        uint2* put = reinterpret_cast<uint2*>(c.v + (of_head * c.bs + off) / 2 * c.d + e * 8);
-        if (mine && next >= 0) {
-          scaled(w, down_by(byte2), f);
-          *put = interleave(codes, to_e2m1x8(f));
-          if (e % 4 == 0) sc[groups] = static_cast<uint8_t>(byte2);
-        } else if (mine) {
-          const uint2 was = *put, got = (slot & 1) ? interleave(0, codes) : interleave(codes, 0);
-          const uint32_t keep = (slot & 1) ? 0x0F0F0F0Fu : 0xF0F0F0F0u;
-          *put = make_uint2((was.x & keep) | got.x, (was.y & keep) | got.y);
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+        const Place at(c, slot[i], j, sixteens, block);
+        uint8_t* sc = scales + at.row * groups + at.e / 2;
+        const uint32_t byte = u[i].group_byte();
+        const float down = down_by(byte);
+        float f[8], y[8];
+        if (!is_v) {
+          uint2 codes;
+          u[i].scaled(0, down, f);
+          codes.x = to_e2m1x8(f);
+          u[i].scaled(1, down, f);
+          codes.y = to_e2m1x8(f);
+          if (mine[i]) *reinterpret_cast<uint2*>(c.k + at.row * (c.d / 2) + at.e * 8) = codes;
+        } else {
+          // the pair's bytes; a token alone keeps its neighbour's half of them
+          const uint32_t byte2 = w[i].group_byte();
+          const float down2 = down_by(byte2);
+          uint32_t put[4];
+          const bool odd = slot[i] & 1;
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            u[i].scaled(z / 2, down, f);
+            w[i].scaled(z / 2, down2, y);
+            float v[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float own = f[z % 2 * 4 + q], other = y[z % 2 * 4 + q];
+              v[2 * q] = odd ? other : own;
+              v[2 * q + 1] = odd ? own : other;
+            }
+            put[z] = to_e2m1x8(v);
+          }
+          uint4* to = reinterpret_cast<uint4*>(c.v + at.row / 2 * c.d + at.e * 16);
+          if (mine[i] && !pair[i]) {
+            const uint4 was = *to;
+            const uint32_t own = odd ? 0xF0F0F0F0u : 0x0F0F0F0Fu;
+            put[0] = (was.x & ~own) | (put[0] & own);
+            put[1] = (was.y & ~own) | (put[1] & own);
+            put[2] = (was.z & ~own) | (put[2] & own);
+            put[3] = (was.w & ~own) | (put[3] & own);
+          }
+          if (mine[i]) *to = make_uint4(put[0], put[1], put[2], put[3]);
+          if (pair[i] && at.e % 2 == 0) sc[groups] = static_cast<uint8_t>(byte2);
         }
+        if (mine[i] && at.e % 2 == 0) *sc = static_cast<uint8_t>(byte);
       }
-      if (mine && e % 4 == 0) *sc = static_cast<uint8_t>(byte);
     }
   }
 }
 
-// Eight codes of a group as bf16. Every value is exact: a code has two significant bits.
-__device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t byte) {
-  // 2^(byte - 127), the least of them a subnormal
-  const float s = byte == kNaN4 ? __uint_as_float(0x7FC00000u) : byte == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
-  uint32_t h[4], o[4];
-  e2m1x8(codes, h);
+// Eight values (f16 pairs) times 2^(byte - 127) as bf16. Exact: a code has two significant bits.
+__device__ __forceinline__ uint4 scaled_bf16(const uint32_t (&h)[4], float s) {
+  uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float lo, hi;
@@ -143,44 +190,72 @@ __device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t byte) {
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
+// 2^(byte - 127), the least of them a subnormal
+__device__ __forceinline__ float group_scale(uint32_t byte) {
+  return __uint_as_float(byte == kNaN4 ? 0x7FC00000u : byte == 0 ? 0x00400000u : byte << 23);
+}
 
 __global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_constant__ Read4Args a, int per, int at_once, int rounds) {
   const Cache4& c = a.c;
   const bool is_v = blockIdx.y != 0;
   const int lt = threadIdx.x / per, j0 = threadIdx.x - lt * per;
-  const int chunks = 31 - __clz(c.d >> 3), all = c.H << chunks, groups = c.d / kGroup4;
+  const int sixteens = 27 - __clz(c.d), all = c.H << sixteens, groups = c.d / kGroup4;
   const int cap = c.num_blocks * c.bs, block = 31 - __clz(c.bs);
   uint16_t* x = is_v ? a.v : a.k;
   const int64_t stride = is_v ? a.v_stride : a.k_stride, first = static_cast<int64_t>(blockIdx.x) * at_once * rounds + lt;
   const uint8_t* scales = is_v ? c.v_scale : c.k_scale;
   if (lt >= at_once) return;
+  constexpr int kFlight = 4;
 #pragma unroll 1
   for (int j = j0; j < all; j += per) {
-    const int h = j >> chunks, e = j - (h << chunks);
-#pragma unroll 4
-    for (int r = 0; r < rounds; ++r) {
-      const int64_t t = first + static_cast<int64_t>(r) * at_once;
-      if (t >= a.T) continue;
-      const int slot = a.slot_map[t];
-      if (slot >= cap && j == 0 && a.err && !is_v) atomicOr(a.err, GDN_DEVERR_BLOCK_RANGE);
-      if (slot < 0 || slot >= cap) continue;
-      const int blk = slot >> block, off = slot & (c.bs - 1);
-      const int64_t at = (static_cast<int64_t>(blk) * c.H + h) * c.bs + off;
-      const uint32_t byte = scales[at * groups + e / 4];
-      uint32_t codes;
-      if (!is_v) {
-        codes = *reinterpret_cast<const uint32_t*>(c.k + at * (c.d / 2) + e * 4);
-      } else {
-        const uint2 two = *reinterpret_cast<const uint2*>(c.v + at / 2 * c.d + e * 8);
-        auto gather = [](uint32_t y) {  // the low four bits of each byte, side by side
-          y &= 0x0F0F0F0Fu;
-          y = (y | (y >> 4)) & 0x00FF00FFu;
-          return (y | (y >> 8)) & 0xFFFFu;
-        };
-        const int up = (slot & 1) * 4;
-        codes = gather(two.x >> up) | (gather(two.y >> up) << 16);
+#pragma unroll 1
+    for (int r0 = 0; r0 < rounds; r0 += kFlight) {
+      int slot[kFlight];
+      uint32_t byte[kFlight];
+      uint4 raw[kFlight];
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+        const int64_t t = first + static_cast<int64_t>(r0 + i) * at_once;
+        slot[i] = r0 + i < rounds && t < a.T ? a.slot_map[t] : -1;
+        if (slot[i] >= cap) {
+          if (j == 0 && a.err && !is_v) atomicOr(a.err, GDN_DEVERR_BLOCK_RANGE);
+          slot[i] = -1;
+        }
       }
-      *reinterpret_cast<uint4*>(x + t * stride + j * 8) = values8(codes, byte);
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+        if (slot[i] < 0) continue;
+        const Place at(c, slot[i], j, sixteens, block);
+        byte[i] = scales[at.row * groups + at.e / 2];
+        if (is_v) {
+          raw[i] = *reinterpret_cast<const uint4*>(c.v + at.row / 2 * c.d + at.e * 16);
+        } else {
+          const uint2 two = *reinterpret_cast<const uint2*>(c.k + at.row * (c.d / 2) + at.e * 8);
+          raw[i] = make_uint4(two.x, two.y, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+        if (slot[i] < 0) continue;
+        uint32_t h[2][4];
+        if (is_v) {  // of each byte the half of the slot's token
+          const uint32_t pick = (slot[i] & 1) ? 0x7632u : 0x5410u, w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            uint32_t y[4];
+            e2m1x8(w[z], y);
+            h[z / 2][z % 2 * 2] = __byte_perm(y[0], y[1], pick);
+            h[z / 2][z % 2 * 2 + 1] = __byte_perm(y[2], y[3], pick);
+          }
+        } else {
+          e2m1x8(raw[i].x, h[0]);
+          e2m1x8(raw[i].y, h[1]);
+        }
+        const float s = group_scale(byte[i]);
+        uint4* to = reinterpret_cast<uint4*>(x + (first + static_cast<int64_t>(r0 + i) * at_once) * stride + j * 16);
+        to[0] = scaled_bf16(h[0], s);
+        to[1] = scaled_bf16(h[1], s);
+      }
     }
   }
 }
@@ -191,7 +266,7 @@ struct Shape {
   dim3 grid;
 };
 Shape shape_of(int T, int H, int d) {
-  const int all = H * d / 8;
+  const int all = H * d / 16;
   Shape s;
   s.per = all < kThreads ? all : kThreads;
   s.at_once = kThreads / s.per;

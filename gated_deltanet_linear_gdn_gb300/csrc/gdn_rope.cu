@@ -37,8 +37,56 @@ template <bool WIDE, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   extern __shared__ float2 s_cs[];  // [tokens of the CTA][rot / 2]
   __shared__ int32_t s_pos[kRopeTokens];
-  const int tid = threadIdx.x, half = a.rot / 2;
-  const int t0 = blockIdx.x * a.tokens, here = min(a.tokens, a.T - t0);
+  constexpr int kFlight = WIDE ? 2 : 4;  // items that a thread loads at a time
+  const int tid = threadIdx.x, half = a.rot / 2, rows = a.Hq + a.H;
+  const int t0 = blockIdx.x * a.tokens, here = min(a.tokens, a.T - t0), total = here * rows * a.items;
+  struct Item {
+    const uint16_t* src;
+    uint16_t* dst;
+    int t, at, to, item;  // token of the CTA; the two vectors (or elements) of the row
+    bool turns, two;
+  };
+  auto find = [&](int i) {
+    // (i x the divisor is below 2^32, so the product with its reciprocal is exact; 2^32 / 1 is not a 32-bit number)
+    Item x;
+    const int row_all = a.items == 1 ? i : __umulhi(i, a.by_items);
+    x.item = i - row_all * a.items;
+    x.t = rows == 1 ? row_all : __umulhi(row_all, a.by_rows);
+    const int row = row_all - x.t * rows;
+    const bool is_k = row >= a.Hq;
+    const int h = is_k ? row - a.Hq : row;
+    const int64_t tok = t0 + x.t;
+    x.src = (is_k ? a.k + tok * a.k_stride : a.q + tok * a.q_stride) + h * a.d;
+    x.dst = (is_k ? a.k_out + tok * a.k_out_stride : a.q_out + tok * a.q_out_stride) + h * a.d;
+    if constexpr (WIDE) {
+      x.turns = x.item < a.rot / 16;
+      x.at = INTER || !x.turns ? x.item * 16 : x.item * 8;
+      x.to = INTER || !x.turns ? x.at + 8 : x.at + half;
+    } else {
+      x.turns = x.item < half;
+      x.at = INTER || !x.turns ? x.item * 2 : x.item;
+      x.to = INTER || !x.turns ? x.at + 1 : x.at + half;
+    }
+    x.two = x.to < a.d;
+    return x;
+  };
+  uint4 u[kFlight], v[kFlight];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int y = 0; y < kFlight; ++y) {
+      const int i = i0 + y * kRopeThreads;
+      if (i >= total) break;
+      const Item x = find(i);
+      if constexpr (WIDE) {
+        u[y] = *reinterpret_cast<const uint4*>(x.src + x.at);
+        if (x.two) v[y] = *reinterpret_cast<const uint4*>(x.src + x.to);
+      } else {
+        u[y].x = x.src[x.at];
+        v[y].x = x.two ? x.src[x.to] : 0u;
+      }
+    }
+  };
+  load(tid);  // (on its way under the sines)
   if (tid < here) s_pos[tid] = a.positions[t0 + tid];
   __syncthreads();
   for (int i = tid; i < here * half; i += kRopeThreads) {
@@ -49,58 +97,49 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     s_cs[i] = make_float2(c * a.factor, s * a.factor);
   }
   __syncthreads();
-  const int rows = a.Hq + a.H;
-#pragma unroll 2
-  for (int i = tid; i < here * rows * a.items; i += kRopeThreads) {
-    // (i x the divisor is below 2^32, so the product with its reciprocal is exact; 2^32 / 1 is not a 32-bit number)
-    const int row_all = a.items == 1 ? i : __umulhi(i, a.by_items), item = i - row_all * a.items;
-    const int t = rows == 1 ? row_all : __umulhi(row_all, a.by_rows), row = row_all - t * rows;
-    if (s_pos[t] < 0) continue;  // a padded step's row
-    const bool is_k = row >= a.Hq;
-    const int h = is_k ? row - a.Hq : row;
-    const int64_t tok = t0 + t;
-    const uint16_t* src = (is_k ? a.k + tok * a.k_stride : a.q + tok * a.q_stride) + h * a.d;
-    uint16_t* dst = (is_k ? a.k_out + tok * a.k_out_stride : a.q_out + tok * a.q_out_stride) + h * a.d;
-    const float2* cs = s_cs + t * half;
-    if constexpr (WIDE) {
-      const bool turns = item < a.rot / 16;
-      // the item's two vectors, in elements
-      const int at = INTER || !turns ? item * 16 : item * 8;
-      const int to = INTER || !turns ? at + 8 : at + half;
-      const bool two = to < a.d;
-      const uint4 u = *reinterpret_cast<const uint4*>(src + at);
-      const uint4 v = two ? *reinterpret_cast<const uint4*>(src + to) : make_uint4(0, 0, 0, 0);
-      uint32_t x[4] = {u.x, u.y, u.z, u.w}, y[4] = {v.x, v.y, v.z, v.w};
-      if (turns) {
+#pragma unroll 1
+  for (int i0 = tid; i0 < total; i0 += kFlight * kRopeThreads) {
+    if (i0 != tid) load(i0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (INTER) {
-            const float2 c0 = cs[item * 8 + j], c1 = cs[item * 8 + 4 + j];
-            const float xa = bf_lo(x[j]), xb = bf_hi(x[j]), ya = bf_lo(y[j]), yb = bf_hi(y[j]);
-            x[j] = pack(first(xa, xb, c0), second(xa, xb, c0));
-            y[j] = pack(first(ya, yb, c1), second(ya, yb, c1));
-          } else {
-            const float2 c0 = cs[item * 8 + 2 * j], c1 = cs[item * 8 + 2 * j + 1];
-            const float xa = bf_lo(x[j]), xb = bf_hi(x[j]), ya = bf_lo(y[j]), yb = bf_hi(y[j]);
-            x[j] = pack(first(xa, ya, c0), first(xb, yb, c1));
-            y[j] = pack(second(xa, ya, c0), second(xb, yb, c1));
+    for (int y = 0; y < kFlight; ++y) {
+      const int i = i0 + y * kRopeThreads;
+      if (i >= total) break;
+      const Item x = find(i);
+      if (s_pos[x.t] < 0) continue;  // a padded step's row
+      const float2* cs = s_cs + x.t * half;
+      if constexpr (WIDE) {
+        uint32_t p[4] = {u[y].x, u[y].y, u[y].z, u[y].w}, q[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+        if (x.turns) {
+          // eight angles, two at a time
+          const float4* at = reinterpret_cast<const float4*>(cs + x.item * 8);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 two = at[j];
+            const float2 c0 = make_float2(two.x, two.y), c1 = make_float2(two.z, two.w);
+            if constexpr (INTER) {
+              uint32_t& w0 = j < 2 ? p[2 * j] : q[2 * j - 4];
+              uint32_t& w1 = j < 2 ? p[2 * j + 1] : q[2 * j - 3];
+              const float xa = bf_lo(w0), xb = bf_hi(w0), ya = bf_lo(w1), yb = bf_hi(w1);
+              w0 = pack(first(xa, xb, c0), second(xa, xb, c0));
+              w1 = pack(first(ya, yb, c1), second(ya, yb, c1));
+            } else {
+              const float xa = bf_lo(p[j]), xb = bf_hi(p[j]), ya = bf_lo(q[j]), yb = bf_hi(q[j]);
+              p[j] = pack(first(xa, ya, c0), first(xb, yb, c1));
+              q[j] = pack(second(xa, ya, c0), second(xb, yb, c1));
+            }
           }
         }
+        *reinterpret_cast<uint4*>(x.dst + x.at) = make_uint4(p[0], p[1], p[2], p[3]);
+        if (x.two) *reinterpret_cast<uint4*>(x.dst + x.to) = make_uint4(q[0], q[1], q[2], q[3]);
+      } else {
+        uint32_t w = u[y].x | (v[y].x << 16);
+        if (x.turns) {
+          const float p = bf_lo(u[y].x), q = bf_lo(v[y].x);
+          w = pack(first(p, q, cs[x.item]), second(p, q, cs[x.item]));
+        }
+        x.dst[x.at] = static_cast<uint16_t>(w);
+        if (x.two) x.dst[x.to] = static_cast<uint16_t>(w >> 16);
       }
-      *reinterpret_cast<uint4*>(dst + at) = make_uint4(x[0], x[1], x[2], x[3]);
-      if (two) *reinterpret_cast<uint4*>(dst + to) = make_uint4(y[0], y[1], y[2], y[3]);
-    } else {
-      const bool turns = item < half;
-      const int at = INTER || !turns ? item * 2 : item, to = INTER || !turns ? at + 1 : at + half;
-      const bool two = to < a.d;
-      const uint32_t u = src[at], v = two ? src[to] : 0u;
-      uint32_t w = u | (v << 16);
-      if (turns) {
-        const float x = bf_lo(u), y = bf_lo(v);
-        w = pack(first(x, y, cs[item]), second(x, y, cs[item]));
-      }
-      dst[at] = static_cast<uint16_t>(w);
-      if (two) dst[to] = static_cast<uint16_t>(w >> 16);
     }
   }
 }

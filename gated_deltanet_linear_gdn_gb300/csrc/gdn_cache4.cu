@@ -145,32 +145,29 @@ __global__ void __launch_bounds__(kThreads) cache4_append_kernel(const __grid_co
         } else {
           // the pair's bytes; a token alone keeps its neighbour's half of them
           const uint32_t byte2 = w[i].group_byte();
-          const float down2 = down_by(byte2);
-          uint32_t put[4];
-          const bool odd = slot[i] & 1;
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            u[i].scaled(z / 2, down, f);
-            w[i].scaled(z / 2, down2, y);
-            float v[8];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float own = f[z % 2 * 4 + q], other = y[z % 2 * 4 + q];
-              v[2 * q] = odd ? other : own;
-              v[2 * q + 1] = odd ? own : other;
-            }
-            put[z] = to_e2m1x8(v);
-          }
           uint4* to = reinterpret_cast<uint4*>(c.v + at.row / 2 * c.d + at.e * 16);
-          if (mine[i] && !pair[i]) {
+          uint32_t put[4];
+          if (pair[i]) {
+            const float down2 = down_by(byte2);
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              u[i].scaled(z, down, f);
+              w[i].scaled(z, down2, y);
+              put[2 * z] = to_e2m1x8({f[0], y[0], f[1], y[1], f[2], y[2], f[3], y[3]});
+              put[2 * z + 1] = to_e2m1x8({f[4], y[4], f[5], y[5], f[6], y[6], f[7], y[7]});
+            }
+            *to = make_uint4(put[0], put[1], put[2], put[3]);
+          } else if (mine[i]) {
+            const uint32_t own = (slot[i] & 1) ? 0xF0F0F0F0u : 0x0F0F0F0Fu;
             const uint4 was = *to;
-            const uint32_t own = odd ? 0xF0F0F0F0u : 0x0F0F0F0Fu;
-            put[0] = (was.x & ~own) | (put[0] & own);
-            put[1] = (was.y & ~own) | (put[1] & own);
-            put[2] = (was.z & ~own) | (put[2] & own);
-            put[3] = (was.w & ~own) | (put[3] & own);
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              u[i].scaled(z, down, f);
+              put[2 * z] = to_e2m1x8({f[0], f[0], f[1], f[1], f[2], f[2], f[3], f[3]});
+              put[2 * z + 1] = to_e2m1x8({f[4], f[4], f[5], f[5], f[6], f[6], f[7], f[7]});
+            }
+            *to = make_uint4((was.x & ~own) | (put[0] & own), (was.y & ~own) | (put[1] & own), (was.z & ~own) | (put[2] & own), (was.w & ~own) | (put[3] & own));
           }
-          if (mine[i]) *to = make_uint4(put[0], put[1], put[2], put[3]);
           if (pair[i] && at.e % 2 == 0) sc[groups] = static_cast<uint8_t>(byte2);
         }
         if (mine[i] && at.e % 2 == 0) *sc = static_cast<uint8_t>(byte);
@@ -205,56 +202,68 @@ __global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_cons
   const int64_t stride = is_v ? a.v_stride : a.k_stride, first = static_cast<int64_t>(blockIdx.x) * at_once * rounds + lt;
   const uint8_t* scales = is_v ? c.v_scale : c.k_scale;
   if (lt >= at_once) return;
+  // a thread has two eights of a head, half a head apart: what a warp stores at a time is in one piece
   constexpr int kFlight = 4;
 #pragma unroll 1
   for (int j = j0; j < all; j += per) {
-#pragma unroll 1
-    for (int r0 = 0; r0 < rounds; r0 += kFlight) {
-      int slot[kFlight];
-      uint32_t byte[kFlight];
-      uint4 raw[kFlight];
+    int slot[kFlight], next[kFlight];
+    auto look = [&](int r0) {
 #pragma unroll
       for (int i = 0; i < kFlight; ++i) {
         const int64_t t = first + static_cast<int64_t>(r0 + i) * at_once;
-        slot[i] = r0 + i < rounds && t < a.T ? a.slot_map[t] : -1;
+        next[i] = r0 + i < rounds && t < a.T ? a.slot_map[t] : -1;
+      }
+    };
+    look(0);
+#pragma unroll 1
+    for (int r0 = 0; r0 < rounds; r0 += kFlight) {
+      uint32_t byte[kFlight][2];
+      uint2 raw[kFlight][2];
+#pragma unroll
+      for (int i = 0; i < kFlight; ++i) {
+        slot[i] = next[i];
         if (slot[i] >= cap) {
           if (j == 0 && a.err && !is_v) atomicOr(a.err, GDN_DEVERR_BLOCK_RANGE);
           slot[i] = -1;
         }
-      }
-#pragma unroll
-      for (int i = 0; i < kFlight; ++i) {
         if (slot[i] < 0) continue;
         const Place at(c, slot[i], j, sixteens, block);
-        byte[i] = scales[at.row * groups + at.e / 2];
+        const uint8_t* sc = scales + at.row * groups + at.e / 4;
+        byte[i][0] = sc[0];
+        byte[i][1] = sc[groups / 2];
         if (is_v) {
-          raw[i] = *reinterpret_cast<const uint4*>(c.v + at.row / 2 * c.d + at.e * 16);
+          const uint8_t* v = c.v + at.row / 2 * c.d + at.e * 8;
+          raw[i][0] = *reinterpret_cast<const uint2*>(v);
+          raw[i][1] = *reinterpret_cast<const uint2*>(v + c.d / 2);
         } else {
-          const uint2 two = *reinterpret_cast<const uint2*>(c.k + at.row * (c.d / 2) + at.e * 8);
-          raw[i] = make_uint4(two.x, two.y, 0, 0);
+          const uint8_t* k = c.k + at.row * (c.d / 2) + at.e * 4;
+          raw[i][0].x = *reinterpret_cast<const uint32_t*>(k);
+          raw[i][1].x = *reinterpret_cast<const uint32_t*>(k + c.d / 4);
         }
       }
+      look(r0 + kFlight);  // (on its way under what follows)
 #pragma unroll
       for (int i = 0; i < kFlight; ++i) {
         if (slot[i] < 0) continue;
-        uint32_t h[2][4];
-        if (is_v) {  // of each byte the half of the slot's token
-          const uint32_t pick = (slot[i] & 1) ? 0x7632u : 0x5410u, w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        const int h = j >> sixteens, e = j - (h << sixteens);
+        uint16_t* to = x + (first + static_cast<int64_t>(r0 + i) * at_once) * stride + h * c.d + e * 8;
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
+        for (int z = 0; z < 2; ++z) {
+          uint32_t f[4];
+          if (is_v) {  // of each byte the half of the slot's token
+            const uint32_t pick = (slot[i] & 1) ? 0x7632u : 0x5410u;
             uint32_t y[4];
-            e2m1x8(w[z], y);
-            h[z / 2][z % 2 * 2] = __byte_perm(y[0], y[1], pick);
-            h[z / 2][z % 2 * 2 + 1] = __byte_perm(y[2], y[3], pick);
+            e2m1x8(raw[i][z].x, y);
+            f[0] = __byte_perm(y[0], y[1], pick);
+            f[1] = __byte_perm(y[2], y[3], pick);
+            e2m1x8(raw[i][z].y, y);
+            f[2] = __byte_perm(y[0], y[1], pick);
+            f[3] = __byte_perm(y[2], y[3], pick);
+          } else {
+            e2m1x8(raw[i][z].x, f);
           }
-        } else {
-          e2m1x8(raw[i].x, h[0]);
-          e2m1x8(raw[i].y, h[1]);
+          *reinterpret_cast<uint4*>(to + z * (c.d / 2)) = scaled_bf16(f, group_scale(byte[i][z]));
         }
-        const float s = group_scale(byte[i]);
-        uint4* to = reinterpret_cast<uint4*>(x + (first + static_cast<int64_t>(r0 + i) * at_once) * stride + j * 16);
-        to[0] = scaled_bf16(h[0], s);
-        to[1] = scaled_bf16(h[1], s);
       }
     }
   }
@@ -271,7 +280,7 @@ Shape shape_of(int T, int H, int d) {
   s.per = all < kThreads ? all : kThreads;
   s.at_once = kThreads / s.per;
   const int64_t ctas = (static_cast<int64_t>(T) + s.at_once - 1) / s.at_once;
-  s.rounds = ctas >= 16 * sm_count() ? 4 : 1;
+  s.rounds = ctas >= 32 * sm_count() ? 8 : 1;
   s.grid = dim3(static_cast<unsigned>((ctas + s.rounds - 1) / s.rounds), 2);
   return s;
 }

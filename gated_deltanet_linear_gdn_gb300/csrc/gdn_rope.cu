@@ -8,8 +8,8 @@
 // modulo 2^64, is one integer product without rounding, its upper half the angle to 2^-32 of a turn. The table is off by
 // 2^-55 of a turn (it is made from doubles), at position 2^31 2^-24.
 //
-// Bound by memory: an element is read and written once. A CTA takes a few tokens: it makes their sines and cosines once, in
-// shared memory, for all heads of q and k.
+// Bound by memory: an element is read and written once. Sines and cosines are made once for a token, in shared memory, for all
+// heads of q and k.
 #include <math.h>
 
 #include "gdn_internal.h"
@@ -20,6 +20,7 @@ namespace gdn {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeWide = 256;
 
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
@@ -31,116 +32,122 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
 __device__ __forceinline__ float first(float a, float b, float2 cs) { return a * cs.x - b * cs.y; }
 __device__ __forceinline__ float second(float a, float b, float2 cs) { return b * cs.x + a * cs.y; }
 
-// WIDE: rot_dim is a multiple of 16 and rows are vectors of 16 bytes: an item is two vectors (8 pairs in the half layout,
-// twice 4 neighbours in the interleaved one, or two vectors of what is only copied). Otherwise an item is one pair.
-template <bool WIDE, bool INTER>
+// Rows as vectors of 16 bytes, rot_dim a multiple of 16: a CTA has one token, a thread one item of its rows: two vectors with
+// eight pairs (the half layout's two halves of them, or twice four neighbours), or two that are only copied. The item's sines
+// and cosines stay in registers for all of its rows (read from shared memory for each row they kept that at 91%, 123 us for
+// 31,779 tokens of 40 heads of 128).
+template <bool INTER>
+__global__ void __launch_bounds__(kRopeWide) rope_wide_kernel(const __grid_constant__ RopeArgs a) {
+  extern __shared__ float s_angle[];  // cosines, sines: [2][rot / 2]
+  constexpr int kFlight = 3;          // rows that a thread loads at a time
+  const int tid = threadIdx.x, half = a.rot / 2, eights = a.rot / 16;  // (rotated items)
+  const int64_t t = blockIdx.x;
+  const int at_once = blockDim.x / a.items, row0 = tid / a.items, item = tid - row0 * a.items;
+  const bool turns = item < eights;
+  // the item's vectors, in elements
+  const int at = !turns ? item * 16 : item * 8, to = !turns ? at + 8 : at + half;
+  const bool two = to < a.d;
+  const int rows = row0 < at_once ? a.Hq + a.H : 0;
+  const uint16_t* q = a.q + t * a.q_stride;
+  const uint16_t* k = a.k + t * a.k_stride - static_cast<int64_t>(a.Hq) * a.d;
+  uint4 u[kFlight], v[kFlight];
+  auto load = [&](int r0) {
+#pragma unroll
+    for (int y = 0; y < kFlight; ++y) {
+      const int r = r0 + y * at_once;
+      if (r >= rows) break;
+      const uint16_t* src = (r < a.Hq ? q : k) + r * a.d;
+      u[y] = *reinterpret_cast<const uint4*>(src + at);
+      if (two) v[y] = *reinterpret_cast<const uint4*>(src + to);
+    }
+  };
+  const int pos = a.positions[t];
+  load(row0);  // (on its way under the sines)
+  if (pos < 0) return;  // a padded step's row
+  for (int i = tid; i < half; i += blockDim.x) {
+    const uint64_t turn = a.turns[i] * static_cast<uint32_t>(pos) + 0x80000000ull;
+    float s, c;
+    sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31 half turns
+    s_angle[i] = c * a.factor;
+    s_angle[half + i] = s * a.factor;
+  }
+  __syncthreads();
+  float2 cs[8];
+  if (turns) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = INTER ? (j < 4 ? item * 4 + j : (item + eights) * 4 + j - 4) : item * 8 + j;
+      cs[j] = make_float2(s_angle[i], s_angle[half + i]);
+    }
+  }
+  uint16_t* q_out = a.q_out + t * a.q_out_stride;
+  uint16_t* k_out = a.k_out + t * a.k_out_stride - static_cast<int64_t>(a.Hq) * a.d;
+#pragma unroll 1
+  for (int r0 = row0; r0 < rows; r0 += kFlight * at_once) {
+    if (r0 != row0) load(r0);
+#pragma unroll
+    for (int y = 0; y < kFlight; ++y) {
+      const int r = r0 + y * at_once;
+      if (r >= rows) break;
+      uint32_t p[4] = {u[y].x, u[y].y, u[y].z, u[y].w}, w[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
+      if (turns) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float pa = bf_lo(p[j]), pb = bf_hi(p[j]), wa = bf_lo(w[j]), wb = bf_hi(w[j]);
+          if constexpr (INTER) {
+            p[j] = pack(first(pa, pb, cs[j]), second(pa, pb, cs[j]));
+            w[j] = pack(first(wa, wb, cs[4 + j]), second(wa, wb, cs[4 + j]));
+          } else {
+            p[j] = pack(first(pa, wa, cs[2 * j]), first(pb, wb, cs[2 * j + 1]));
+            w[j] = pack(second(pa, wa, cs[2 * j]), second(pb, wb, cs[2 * j + 1]));
+          }
+        }
+      }
+      uint16_t* dst = (r < a.Hq ? q_out : k_out) + r * a.d;
+      *reinterpret_cast<uint4*>(dst + at) = make_uint4(p[0], p[1], p[2], p[3]);
+      if (two) *reinterpret_cast<uint4*>(dst + to) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+// Any sizes, strides and alignment: an item is one pair, or two elements that are only copied. A CTA has a few tokens.
+template <bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   extern __shared__ float2 s_cs[];  // [tokens of the CTA][rot / 2]
   __shared__ int32_t s_pos[kRopeTokens];
-  constexpr int kFlight = WIDE ? 2 : 4;  // items that a thread loads at a time
   const int tid = threadIdx.x, half = a.rot / 2, rows = a.Hq + a.H;
-  const int t0 = blockIdx.x * a.tokens, here = min(a.tokens, a.T - t0), total = here * rows * a.items;
-  struct Item {
-    const uint16_t* src;
-    uint16_t* dst;
-    int t, at, to, item;  // token of the CTA; the two vectors (or elements) of the row
-    bool turns, two;
-  };
-  auto find = [&](int i) {
-    // (i x the divisor is below 2^32, so the product with its reciprocal is exact; 2^32 / 1 is not a 32-bit number)
-    Item x;
-    const int row_all = a.items == 1 ? i : __umulhi(i, a.by_items);
-    x.item = i - row_all * a.items;
-    x.t = rows == 1 ? row_all : __umulhi(row_all, a.by_rows);
-    const int row = row_all - x.t * rows;
-    const bool is_k = row >= a.Hq;
-    const int h = is_k ? row - a.Hq : row;
-    const int64_t tok = t0 + x.t;
-    x.src = (is_k ? a.k + tok * a.k_stride : a.q + tok * a.q_stride) + h * a.d;
-    x.dst = (is_k ? a.k_out + tok * a.k_out_stride : a.q_out + tok * a.q_out_stride) + h * a.d;
-    if constexpr (WIDE) {
-      x.turns = x.item < a.rot / 16;
-      x.at = INTER || !x.turns ? x.item * 16 : x.item * 8;
-      x.to = INTER || !x.turns ? x.at + 8 : x.at + half;
-    } else {
-      x.turns = x.item < half;
-      x.at = INTER || !x.turns ? x.item * 2 : x.item;
-      x.to = INTER || !x.turns ? x.at + 1 : x.at + half;
-    }
-    x.two = x.to < a.d;
-    return x;
-  };
-  uint4 u[kFlight], v[kFlight];
-  auto load = [&](int i0) {
-#pragma unroll
-    for (int y = 0; y < kFlight; ++y) {
-      const int i = i0 + y * kRopeThreads;
-      if (i >= total) break;
-      const Item x = find(i);
-      if constexpr (WIDE) {
-        u[y] = *reinterpret_cast<const uint4*>(x.src + x.at);
-        if (x.two) v[y] = *reinterpret_cast<const uint4*>(x.src + x.to);
-      } else {
-        u[y].x = x.src[x.at];
-        v[y].x = x.two ? x.src[x.to] : 0u;
-      }
-    }
-  };
-  load(tid);  // (on its way under the sines)
+  const int t0 = blockIdx.x * kRopeTokens, here = min(kRopeTokens, a.T - t0), total = here * rows * a.items;
   if (tid < here) s_pos[tid] = a.positions[t0 + tid];
   __syncthreads();
   for (int i = tid; i < here * half; i += kRopeThreads) {
     const int t = i / half;
     const uint64_t turn = a.turns[i - t * half] * static_cast<uint32_t>(s_pos[t]) + 0x80000000ull;
     float s, c;
-    sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31 half turns
+    sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f, &s, &c);
     s_cs[i] = make_float2(c * a.factor, s * a.factor);
   }
   __syncthreads();
-#pragma unroll 1
-  for (int i0 = tid; i0 < total; i0 += kFlight * kRopeThreads) {
-    if (i0 != tid) load(i0);
-#pragma unroll
-    for (int y = 0; y < kFlight; ++y) {
-      const int i = i0 + y * kRopeThreads;
-      if (i >= total) break;
-      const Item x = find(i);
-      if (s_pos[x.t] < 0) continue;  // a padded step's row
-      const float2* cs = s_cs + x.t * half;
-      if constexpr (WIDE) {
-        uint32_t p[4] = {u[y].x, u[y].y, u[y].z, u[y].w}, q[4] = {v[y].x, v[y].y, v[y].z, v[y].w};
-        if (x.turns) {
-          // eight angles, two at a time
-          const float4* at = reinterpret_cast<const float4*>(cs + x.item * 8);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 two = at[j];
-            const float2 c0 = make_float2(two.x, two.y), c1 = make_float2(two.z, two.w);
-            if constexpr (INTER) {
-              uint32_t& w0 = j < 2 ? p[2 * j] : q[2 * j - 4];
-              uint32_t& w1 = j < 2 ? p[2 * j + 1] : q[2 * j - 3];
-              const float xa = bf_lo(w0), xb = bf_hi(w0), ya = bf_lo(w1), yb = bf_hi(w1);
-              w0 = pack(first(xa, xb, c0), second(xa, xb, c0));
-              w1 = pack(first(ya, yb, c1), second(ya, yb, c1));
-            } else {
-              const float xa = bf_lo(p[j]), xb = bf_hi(p[j]), ya = bf_lo(q[j]), yb = bf_hi(q[j]);
-              p[j] = pack(first(xa, ya, c0), first(xb, yb, c1));
-              q[j] = pack(second(xa, ya, c0), second(xb, yb, c1));
-            }
-          }
-        }
-        *reinterpret_cast<uint4*>(x.dst + x.at) = make_uint4(p[0], p[1], p[2], p[3]);
-        if (x.two) *reinterpret_cast<uint4*>(x.dst + x.to) = make_uint4(q[0], q[1], q[2], q[3]);
-      } else {
-        uint32_t w = u[y].x | (v[y].x << 16);
-        if (x.turns) {
-          const float p = bf_lo(u[y].x), q = bf_lo(v[y].x);
-          w = pack(first(p, q, cs[x.item]), second(p, q, cs[x.item]));
-        }
-        x.dst[x.at] = static_cast<uint16_t>(w);
-        if (x.two) x.dst[x.to] = static_cast<uint16_t>(w >> 16);
-      }
+#pragma unroll 4
+  for (int i = tid; i < total; i += kRopeThreads) {
+    // (i x the divisor is below 2^32, so the product with its reciprocal is exact; 2^32 / 1 is not a 32-bit number)
+    const int row_all = a.items == 1 ? i : __umulhi(i, a.by_items), item = i - row_all * a.items;
+    const int t = rows == 1 ? row_all : __umulhi(row_all, a.by_rows), row = row_all - t * rows;
+    if (s_pos[t] < 0) continue;  // a padded step's row
+    const bool is_k = row >= a.Hq, turns = item < half;
+    const int h = is_k ? row - a.Hq : row;
+    const int64_t tok = t0 + t;
+    const uint16_t* src = (is_k ? a.k + tok * a.k_stride : a.q + tok * a.q_stride) + h * a.d;
+    uint16_t* dst = (is_k ? a.k_out + tok * a.k_out_stride : a.q_out + tok * a.q_out_stride) + h * a.d;
+    const int at = INTER || !turns ? item * 2 : item, to = INTER || !turns ? at + 1 : at + half;
+    const bool two = to < a.d;
+    const uint32_t u = src[at], v = two ? src[to] : 0u;
+    uint32_t w = u | (v << 16);
+    if (turns) {
+      const float2 cs = s_cs[t * half + item];
+      w = pack(first(bf_lo(u), bf_lo(v), cs), second(bf_lo(u), bf_lo(v), cs));
     }
+    dst[at] = static_cast<uint16_t>(w);
+    if (two) dst[to] = static_cast<uint16_t>(w >> 16);
   }
 }
 
@@ -158,16 +165,17 @@ cudaError_t launch_rope(RopeArgs a, cudaStream_t s) {
   a.items = in_place ? a.rot / per : a.rot / per + (a.d - a.rot + per - 1) / per;
   a.by_items = reciprocal(a.items);
   a.by_rows = reciprocal(a.Hq + a.H);
-  // tokens of a CTA: one while they are few
-  a.tokens = a.T <= kRopeFew ? 1 : kRopeTokens;
-  const int smem = a.tokens * (a.rot / 2) * static_cast<int>(sizeof(float2));
-  const int grid = (a.T + a.tokens - 1) / a.tokens;
-  auto go = [&](auto kern) {
-    kern<<<grid, kRopeThreads, smem, s>>>(a);
-    return cudaGetLastError();
-  };
-  if (wide) return a.interleaved ? go(rope_kernel<true, true>) : go(rope_kernel<true, false>);
-  return a.interleaved ? go(rope_kernel<false, true>) : go(rope_kernel<false, false>);
+  const int half = a.rot / 2;
+  if (wide) {
+    // threads of a token: as many as its items while tokens are few, and a quarter of them, with rows in turn, for many
+    const int threads = a.T <= kRopeFew ? kRopeWide : 64;
+    auto kern = a.interleaved ? rope_wide_kernel<true> : rope_wide_kernel<false>;
+    kern<<<a.T, threads, 2 * half * sizeof(float), s>>>(a);
+  } else {
+    auto kern = a.interleaved ? rope_kernel<true> : rope_kernel<false>;
+    kern<<<(a.T + kRopeTokens - 1) / kRopeTokens, kRopeThreads, kRopeTokens * half * sizeof(float2), s>>>(a);
+  }
+  return cudaGetLastError();
 }
 
 }  // namespace gdn

@@ -8,9 +8,9 @@
 
 namespace gdn {
 
-constexpr int kRopeMaxDim = 1024;  // of a head: sines and cosines of kRopeTokens tokens fit in 32 KB
-constexpr int kRopeTokens = 4;     // tokens of a CTA, where there are more than kRopeFew
-constexpr int kRopeFew = 1024;
+constexpr int kRopeMaxDim = 1024;  // of a head: its items fit in 64 threads, sines and cosines of kRopeTokens tokens in 16 KB
+constexpr int kRopeTokens = 4;     // tokens of a CTA of narrow items
+constexpr int kRopeFew = 1024;     // tokens up to which each has more threads
 
 struct RopeArgs {
   const uint16_t* q;
@@ -22,8 +22,8 @@ struct RopeArgs {
   const uint64_t* turns;  // [rot / 2]: frequencies in turns a position, times 2^64
   int T, Hq, H, d, rot, interleaved;
   float factor;
-  // set by the launch: tokens of a CTA, items of a (token, head) row, and 2^32 / items and / rows, rounded up
-  int tokens, items;
+  // set by the launch: items of a (token, head) row, and 2^32 / items and / rows, rounded up
+  int items;
   uint32_t by_items, by_rows;
 };
 

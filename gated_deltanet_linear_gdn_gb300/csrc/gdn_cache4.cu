@@ -308,12 +308,15 @@ __device__ __forceinline__ uint32_t f16_scale(int byte, int top) {
   return e > 0 ? static_cast<uint32_t>(e) << 10 : 0u;
 }
 
+// An item is a page's keys or values of one head; a team of TS warps has it.
+template <int TS>
 __global__ void __launch_bounds__(kThreads) cache4_expand_kernel(const __grid_constant__ Expand4Args a) {
   extern __shared__ int32_t s_first[];  // [B + 1]: pages before each request
   __shared__ int32_t s_warp[kThreads / 32];
   __shared__ int32_t s_top[kThreads / 32];
+  constexpr int kTeams = kThreads / 32 / TS, kLanes = 32 * TS;
   const Cache4& c = a.c;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, team = warp / TS, in = tid - team * kLanes;
   const int cap = a.max_blocks * c.bs, block = 31 - __clz(c.bs);
   // pages of the requests that have new tokens; one that there is no room for counts as empty
   {
@@ -359,7 +362,7 @@ __global__ void __launch_bounds__(kThreads) cache4_expand_kernel(const __grid_co
   const int groups = c.d / kGroup4, H2 = 2 * c.H;
   const int64_t items = static_cast<int64_t>(s_first[a.B]) * H2;
 #pragma unroll 1
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kTeams + team; item < items; item += static_cast<int64_t>(gridDim.x) * kTeams) {
     const int page = static_cast<int>(item / H2), hk = static_cast<int>(item - static_cast<int64_t>(page) * H2);
     const bool is_v = hk >= c.H;
     const int h = is_v ? hk - c.H : hk;
@@ -373,72 +376,72 @@ __global__ void __launch_bounds__(kThreads) cache4_expand_kernel(const __grid_co
     const int keys = min(c.bs, min(max(a.lens[b], 0), cap) - (j << block));
     const int from = a.block_table[static_cast<int64_t>(b) * a.max_blocks + j];
     const bool good = from >= 0 && from < c.num_blocks && keys > 0;
-    if (hk == 0 && tid == 0) a.table[static_cast<int64_t>(b) * a.max_blocks + j] = good ? page : -1;
+    if (hk == 0 && in == 0) a.table[static_cast<int64_t>(b) * a.max_blocks + j] = good ? page : -1;
     if (!good) continue;
     const int64_t of_head = static_cast<int64_t>(from) * c.H + h;
     const uint8_t* sc = (is_v ? c.v_scale : c.k_scale) + of_head * c.bs * groups;
     // the page's largest scale
     int top = 0;
-    for (int i = tid; i < keys * groups; i += kThreads) {
+#pragma unroll 4
+    for (int i = in; i < keys * groups; i += kLanes) {
       const int e = sc[i];
-      if (e != kNaN4) top = max(top, e);
+      top = max(top, e == kNaN4 ? 0 : e);
     }
     top = __reduce_max_sync(0xFFFFFFFFu, top);
-    if (lane == 0) s_top[warp] = top;
-    __syncthreads();
+    if constexpr (TS > 1) {
+      if (lane == 0) s_top[warp] = top;
+      asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + team), "n"(kLanes) : "memory");
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) top = max(top, s_top[w]);
+      for (int w = 0; w < TS; ++w) top = max(top, s_top[team * TS + w]);
+    }
     top = max(top, 16);  // (the page's scale stays a normal number)
     const int64_t to_head = static_cast<int64_t>(page) * c.H + h;
-    if (tid == 0) (is_v ? a.v_scale : a.k_scale)[to_head] = __uint_as_float(static_cast<uint32_t>(top - 6) << 23);
+    if (in == 0) (is_v ? a.v_scale : a.k_scale)[to_head] = __uint_as_float(static_cast<uint32_t>(top - 6) << 23);
     uint8_t* dst = (is_v ? a.v : a.k) + to_head * c.bs * c.d;
     if (!is_v) {
-      const uint4* src = reinterpret_cast<const uint4*>(c.k + of_head * c.bs * (c.d / 2));
-      for (int i = tid; i < c.bs * groups; i += kThreads) {  // a group
-        uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (i < keys * groups) {
-          const uint4 u = src[i];
-          const uint32_t s = f16_scale(sc[i], top) * 0x10001u, w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t y[4];
-            e2m1x8(w[x], y);
-            o[2 * x] = mul_e4m3(y[0], s) | (mul_e4m3(y[1], s) << 16);
-            o[2 * x + 1] = mul_e4m3(y[2], s) | (mul_e4m3(y[3], s) << 16);
-          }
-        }
-        uint4* put = reinterpret_cast<uint4*>(dst + i * kGroup4);
-        put[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        put[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      const uint2* src = reinterpret_cast<const uint2*>(c.k + of_head * c.bs * (c.d / 2));
+      const int live = keys * groups * 2;
+#pragma unroll 4
+      for (int i = in; i < c.bs * groups * 2; i += kLanes) {  // half a group
+        const uint2 u = i < live ? src[i] : make_uint2(0, 0);
+        const uint32_t s = i < live ? f16_scale(sc[i / 2], top) * 0x10001u : 0u;
+        uint32_t y[4], o[4];
+        e2m1x8(u.x, y);
+        o[0] = mul_e4m3(y[0], s) | (mul_e4m3(y[1], s) << 16);
+        o[1] = mul_e4m3(y[2], s) | (mul_e4m3(y[3], s) << 16);
+        e2m1x8(u.y, y);
+        o[2] = mul_e4m3(y[0], s) | (mul_e4m3(y[1], s) << 16);
+        o[3] = mul_e4m3(y[2], s) | (mul_e4m3(y[3], s) << 16);
+        *reinterpret_cast<uint4*>(dst + i * 16) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     } else {
       const uint4* src = reinterpret_cast<const uint4*>(c.v + of_head * c.bs / 2 * c.d);
       const int vectors = 27 - __clz(c.d);  // log2 of the 16-byte vectors of a pair of tokens, d bytes
-      for (int i = tid; i < (c.bs / 2) << vectors; i += kThreads) {  // 16 elements of two tokens
+#pragma unroll 4
+      for (int i = in; i < (c.bs / 2) << vectors; i += kLanes) {  // 16 elements of two tokens
         const int pair = i >> vectors, x0 = (i - (pair << vectors)) * 16, t = 2 * pair;
-        uint32_t even[4] = {0, 0, 0, 0}, odd[4] = {0, 0, 0, 0};
+        uint4 u = make_uint4(0, 0, 0, 0);
+        uint32_t s = 0;
         if (t < keys) {
-          const uint4 u = src[i];
-          const uint32_t s = f16_scale(sc[t * groups + x0 / kGroup4], top) |
-                             (t + 1 < keys ? f16_scale(sc[(t + 1) * groups + x0 / kGroup4], top) << 16 : 0u);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          u = src[i];
+          s = f16_scale(sc[t * groups + x0 / kGroup4], top) |
+              (t + 1 < keys ? f16_scale(sc[(t + 1) * groups + x0 / kGroup4], top) << 16 : 0u);
+        }
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint32_t even[4], odd[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t y[4];
-            e2m1x8(w[x], y);  // (even token, odd token) of four elements
-            uint32_t z[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) z[q] = mul_e4m3(y[q], s);
-            const uint32_t p = z[0] | (z[1] << 16), q = z[2] | (z[3] << 16);
-            even[x] = __byte_perm(p, q, 0x6420);
-            odd[x] = __byte_perm(p, q, 0x7531);
-          }
+        for (int x = 0; x < 4; ++x) {
+          uint32_t y[4];
+          e2m1x8(w[x], y);  // (even token, odd token) of four elements
+          const uint32_t p = mul_e4m3(y[0], s) | (mul_e4m3(y[1], s) << 16), q = mul_e4m3(y[2], s) | (mul_e4m3(y[3], s) << 16);
+          even[x] = __byte_perm(p, q, 0x6420);
+          odd[x] = __byte_perm(p, q, 0x7531);
         }
         *reinterpret_cast<uint4*>(dst + t * c.d + x0) = make_uint4(even[0], even[1], even[2], even[3]);
         *reinterpret_cast<uint4*>(dst + (t + 1) * c.d + x0) = make_uint4(odd[0], odd[1], odd[2], odd[3]);
       }
     }
-    __syncthreads();  // s_top is written anew
+    if constexpr (TS > 1) asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + team), "n"(kLanes) : "memory");  // s_top is written anew
   }
 }
 
@@ -457,9 +460,12 @@ cudaError_t launch_cache4_read(const Read4Args& a, cudaStream_t s) {
 }
 
 cudaError_t launch_cache4_expand(const Expand4Args& a, cudaStream_t s) {
-  const int64_t items = static_cast<int64_t>(a.held) * a.c.H * 2, most = 8 * static_cast<int64_t>(sm_count());
+  // warps of an item: one for each 4,096 values
+  const int size = a.c.bs * a.c.d, ts = size >= 32768 ? 8 : size >= 16384 ? 4 : size >= 8192 ? 2 : 1, teams = kThreads / 32 / ts;
+  const int64_t items = (static_cast<int64_t>(a.held) * a.c.H * 2 + teams - 1) / teams, most = 8 * static_cast<int64_t>(sm_count());
   const int grid = static_cast<int>(items < most ? items : most);
-  cache4_expand_kernel<<<grid, kThreads, (a.B + 1) * sizeof(int32_t), s>>>(a);
+  auto kern = ts == 8 ? cache4_expand_kernel<8> : ts == 4 ? cache4_expand_kernel<4> : ts == 2 ? cache4_expand_kernel<2> : cache4_expand_kernel<1>;
+  kern<<<grid, kThreads, (a.B + 1) * sizeof(int32_t), s>>>(a);
   return cudaGetLastError();
 }
 

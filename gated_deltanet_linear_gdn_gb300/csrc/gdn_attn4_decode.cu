@@ -408,14 +408,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kern
         fetch_keys(t + 2);
         const int i0 = __shfl_sync(0xFFFFFFFFu, e_own, 2 * g), i1 = __shfl_sync(0xFFFFFFFFu, e_own, 2 * g + 16);
         const float e0 = __int_as_float(0x4B400000 + i0) - 12582912.0f, e1 = __int_as_float(0x4B400000 + i1) - 12582912.0f;  // (as floats)
-        float above = -INFINITY;  // what the scores pass the running maxima by, at most
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            s[n][j] = fmaf(s[n][j], fac[n][j], e0);
-            s[n][2 + j] = fmaf(s[n][2 + j], fac[n][j], e1);
-          }
         if (live < kStep) {  // the request's last keys, or a page that is none
 #pragma unroll
           for (int n = 0; n < NT; ++n)
@@ -425,17 +417,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kern
               if (g + 8 >= live) s[n][2 + j] = -INFINITY;
             }
         }
+        // the exponents x; their largest x + e of each head, and what that passes the running maxima by, at most
+        float above = -INFINITY, most[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) above = fmaxf(above, fmaxf(s[n][j], s[n][2 + j]) - m[n][j]);  // (-inf - -inf is left out)
+          for (int j = 0; j < 2; ++j) {
+            if (live >= kStep || g < live) s[n][j] *= fac[n][j];
+            if (live >= kStep || g + 8 < live) s[n][2 + j] *= fac[n][j];
+            most[n][j] = fmaxf(s[n][j] + e0, s[n][2 + j] + e1);
+            above = fmaxf(above, most[n][j] - m[n][j]);  // (-inf - -inf is left out)
+          }
         // from here on every warp is done with the tile before: its values, their scales and the probabilities are free
         if (__syncthreads_or(above > kRise)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              float top = fmaxf(s[n][j], s[n][2 + j]);
+              float top = most[n][j];
 #pragma unroll
               for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
               if (g == 0) s_max[(n * 8 + 2 * c + j) * kWarps + warp] = top;
@@ -464,17 +463,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kern
           }
         }
         fetch_values(t + 1);
-        // p 2^e, and p into the sum; both keys' rows turned into columns
-        const float d0 = __int_as_float((kBias4 - i0) << 23), d1 = __int_as_float((kBias4 - i1) << 23);
+        // p 2^e, both keys' rows turned into columns, and p into the sum: from its own exponent, as p 2^e is 0 next to a scale
+        // 2^126 times as large
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float x[4];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const float from = m[n][j] == -INFINITY ? 0.0f : m[n][j] - kTop;
-            x[j] = ex2(s[n][j] - from);
-            x[2 + j] = ex2(s[n][2 + j] - from);
-            l[n][j] = fmaf(x[j], d0, fmaf(x[2 + j], d1, l[n][j]));
+            x[j] = ex2(s[n][j] + (e0 - from));
+            x[2 + j] = ex2(s[n][2 + j] + (e1 - from));
+            l[n][j] += ex2(s[n][j] - from) + ex2(s[n][2 + j] - from);
           }
           *reinterpret_cast<uint2*>(all_p + ((warp * NT + n) * 32 + lane) * 8) =
               make_uint2(transpose8(pack_f16(x[0], x[1])), transpose8(pack_f16(x[2], x[3])));

@@ -2,16 +2,16 @@
 //
 // Format. e2m1 codes (a sign and 0, 0.5, 1, 1.5, 2, 3, 4, 6) in groups of 32 along the head; a group has one byte e and its
 // values are code * 2^(e - 127). A power of two for a scale makes both directions exact but for the one rounding to a code:
-// value * 2^(127 - e) is exact in fp32, and code * 2^(e - 127) is a bf16 value.
+// value * 2^(127 - e) is exact in fp32, and code * 2^(e - 127) is a bf16 value below 2^128.
 //
 // Writer. Per token, head and group, with a the largest |x| of the finite values: e the least with a <= 7 * 2^(e - 127), at
 // least 63. (Up to 7 rounds to 6 by no more than the half step that 4 to 6 have anyway, so a limit of 6 would only make
 // every group between 6 and 7 twice as coarse.) Tokens do not touch one another: nothing that was written is rounded again,
-// a token may be written in any step, and the order of tokens does not matter but for the two that share V's bytes.
+// a token may be written in any step, and the order of a call's tokens does not matter.
 //
 // V's bytes hold the same element of two neighbouring tokens, so that the attention's product over tokens finds its operand
 // pairs as they lie. The token with the even slot writes for both where the next one follows it in the call; a token alone
-// keeps its neighbour's half.
+// changes its half of the bytes by atomics (each bit has one writer, so the result has no order).
 //
 // Bound by memory, 2 bytes read and 17 / 32 written a value (the read-back the other way round).
 #include "gdn_cache4.cuh"
@@ -159,14 +159,19 @@ __global__ void __launch_bounds__(kThreads) cache4_append_kernel(const __grid_co
             *to = make_uint4(put[0], put[1], put[2], put[3]);
           } else if (mine[i]) {
             const uint32_t own = (slot[i] & 1) ? 0xF0F0F0F0u : 0x0F0F0F0Fu;
-            const uint4 was = *to;
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
               u[i].scaled(z, down, f);
               put[2 * z] = to_e2m1x8({f[0], f[0], f[1], f[1], f[2], f[2], f[3], f[3]});
               put[2 * z + 1] = to_e2m1x8({f[4], f[4], f[5], f[5], f[6], f[6], f[7], f[7]});
             }
-            *to = make_uint4((was.x & ~own) | (put[0] & own), (was.y & ~own) | (put[1] & own), (was.z & ~own) | (put[2] & own), (was.w & ~own) | (put[3] & own));
+            // (atomics: the neighbour may be written by another thread of this call, where the two do not follow each other)
+            uint32_t* word = reinterpret_cast<uint32_t*>(to);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              atomicAnd(word + z, ~own);
+              atomicOr(word + z, put[z] & own);
+            }
           }
           if (pair[i] && at.e % 2 == 0) sc[groups] = static_cast<uint8_t>(byte2);
         }

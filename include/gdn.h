@@ -573,13 +573,14 @@ gdn_status gdn_rope_turns(const double* host_freqs, int32_t count, uint64_t* hos
  * gdn_cache4_append -- writes the step's keys and values. Per token, head and group, with a = max |x| over its finite values:
  *   e = the least with a <= 7 * 2^(e - 127), at least 63;   code = e2m1(x * 2^(127 - e)), to nearest, ties to even, +-6 beyond
  * (7 because up to there the rounding to 6 is no worse than half the step from 4 to 6.) A group with a NaN has e = 255. Tokens
- * do not touch one another, so nothing is rounded twice, and a token may be written again (speculation taken back). The two
- * tokens 2 j and 2 j + 1 of a block share V's bytes: where a call has both they follow each other (gdn_cache_tables gives that
- * order); no slot comes twice in a call.
+ * do not touch one another, so nothing is rounded twice, a token may be written again (speculation taken back), and a call's
+ * tokens may come in any order (in the order of gdn_cache_tables two neighbours are written together). No slot comes twice in
+ * a call.
  *   arguments as gdn_cache_append
  *
- * gdn_cache4_read -- the values of the tokens at slot_map, in bf16, which holds them exactly. A negative slot: the token's
- * rows are left as they are; one past the cache: that, and GDN_DEVERR_BLOCK_RANGE. A slot may come more than once.
+ * gdn_cache4_read -- the values of the tokens at slot_map, in bf16, which holds them exactly (but for 2^128 and above, which
+ * the largest bf16 numbers are rounded to: infinite). A negative slot: the token's rows are left as they are; one past the
+ * cache: that, and GDN_DEVERR_BLOCK_RANGE. A slot may come more than once.
  *   k, v     [total_tokens] rows of Hkv * head_dim bf16, k_stride and v_stride elements apart, 16-byte aligned, multiples of 8
  */
 gdn_status gdn_cache4_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride,

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import os
 from dataclasses import dataclass
 
@@ -19,6 +20,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libgdn.so")
+BINDING_PATH = os.path.join(_PKG, "_binding.so")
 
 GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_CUDA = 0, 1, 2, 3
 GDN_ERR_SCRATCH_LIMIT = 4
@@ -450,8 +452,7 @@ def gdn_attn_prefill(q, cu_tokens, k_cache, v_cache, k_scale, v_scale, block_tab
 
 # ---------------------------------------------- rotary positions, the cache in 4 bits
 
-_I64, _U8 = torch.int64, torch.uint8
-_E8M0 = (torch.uint8, torch.float8_e8m0fnu)
+# These calls' arguments are marshalled in C++ (_binding.so, csrc/gdn_binding.cpp): the smallest take 2 us on the GPU.
 
 
 class RopeTable:
@@ -474,50 +475,57 @@ class RopeTable:
         turns = (ctypes.c_uint64 * half)()
         _check(lib().gdn_rope_turns(w, half, turns))
         self.rot_dim, self.factor, self.freqs = rot_dim, f.value, list(w)
-        self.turns = torch.frombuffer(bytearray(turns), dtype=_I64).to(device)
+        self.turns = torch.frombuffer(bytearray(turns), dtype=torch.int64).to(device)
+
+
+_marshal = None
+
+
+def _binding():
+    """The marshalling functions of _binding.so, bound to the library's entry points (raises if it is absent)."""
+    global _marshal
+    if _marshal is None:
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} is missing: it must be built "
+                               "(gated_deltanet_linear_gdn_gb300.build.build_library())")
+        spec = importlib.util.spec_from_file_location(__name__ + "._binding", BINDING_PATH)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        L = lib()
+        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.gdn_rope, L.gdn_cache4_append, L.gdn_cache4_read, L.gdn_attn4_decode, L.gdn_attn4_prefill)))
+        _marshal = m
+    return _marshal
+
+
+def _raw(stream):
+    """A stream as an address; None for the current one."""
+    return stream if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def gdn_rope(q, k, positions, q_out, k_out, rope: RopeTable, *, interleaved=False, stream=None):
     """Rotary positions of q [T, Hq, d] and k [T, Hkv, d] (bf16, any token stride) into q_out and k_out (which may be q and k
     themselves). positions [T] int32; k and k_out may be None."""
-    T, Hq, d = q.shape
-    H = 0 if k is None else k.shape[1]
-    at = *_tokens(q, (T, Hq, d), "q"), *((None, 0) if k is None else _tokens(k, (T, H, d), "k"))
-    to = *_tokens(q_out, (T, Hq, d), "q_out"), *((None, 0) if k is None else _tokens(k_out, (T, H, d), "k_out"))
-    _check(lib().gdn_rope(*at, _dense(positions, _I32, (T,), "positions"), T, Hq, H, d, rope.rot_dim, int(bool(interleaved)),
-                          _dense(rope.turns, _I64, (rope.rot_dim // 2,), "rope.turns"), rope.factor, *to, _stream(stream)))
-
-
-def _cache4(k_cache, v_cache, k_scale, v_scale):
-    """The 4-bit cache's addresses and num_blocks, Hkv, block_size, head_dim."""
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache must be [num_blocks, Hkv, block_size, head_dim / 2]")
-    NB, H, bs, half = k_cache.shape
-    d = 2 * half
-    if k_scale.dtype not in _E8M0 or v_scale.dtype is not k_scale.dtype:
-        raise ValueError("the scales must be float8_e8m0fnu (or its bytes)")
-    scales = (NB, H, bs, d // 32)
-    return (_dense(k_cache, _U8, (NB, H, bs, half), "k_cache"), _dense(v_cache, _U8, (NB, H, bs // 2, d), "v_cache"),
-            _dense(k_scale, k_scale.dtype, scales, "k_scale"), _dense(v_scale, k_scale.dtype, scales, "v_scale")), (NB, H, bs, d)
+    status = (_marshal or _binding()).rope(q, k, positions, q_out, k_out, rope.turns, rope.rot_dim, rope.factor, bool(interleaved),
+                                           _raw(stream))
+    if status:
+        _check(status)
 
 
 def gdn_cache4_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, *, err=None, stream=None):
     """Writes k, v [T, Hkv, d] (bf16, any token stride) into the 4-bit cache at slot_map [T] (include/gdn.h). k_cache
     [num_blocks, Hkv, block_size, d / 2] and v_cache [num_blocks, Hkv, block_size / 2, d] uint8; the scales [num_blocks, Hkv,
     block_size, d / 32] float8_e8m0fnu or its bytes."""
-    addresses, (NB, H, bs, d) = _cache4(k_cache, v_cache, k_scale, v_scale)
-    (T,) = slot_map.shape
-    _check(lib().gdn_cache4_append(*_tokens(k, (T, H, d), "k"), *_tokens(v, (T, H, d), "v"),
-                                   _dense(slot_map, _I32, (T,), "slot_map"), T, *addresses, NB,
-                                   _cache_dims(H, H, d, bs), _ptr(err), _stream(stream)))
+    status = (_marshal or _binding()).cache4_append(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, err, _raw(stream))
+    if status:
+        _check(status)
 
 
 def gdn_cache4_read(k_cache, v_cache, k_scale, v_scale, slot_map, k, v, *, err=None, stream=None):
     """The values of the 4-bit cache's tokens at slot_map [T], into k and v [T, Hkv, d] (bf16, any token stride)."""
-    addresses, (NB, H, bs, d) = _cache4(k_cache, v_cache, k_scale, v_scale)
-    (T,) = slot_map.shape
-    _check(lib().gdn_cache4_read(*addresses, NB, _dense(slot_map, _I32, (T,), "slot_map"), T, _cache_dims(H, H, d, bs),
-                                 *_tokens(k, (T, H, d), "k"), *_tokens(v, (T, H, d), "v"), _ptr(err), _stream(stream)))
+    status = (_marshal or _binding()).cache4_read(k_cache, v_cache, k_scale, v_scale, slot_map, k, v, err, _raw(stream))
+    if status:
+        _check(status)
 
 
 def gdn_attn4_decode_workspace_size(batch, max_blocks, num_q_heads, num_kv_heads, head_dim, block_size) -> int:
@@ -529,13 +537,10 @@ def gdn_attn4_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, o
                      stream=None):
     """Attention of one token per request over the 4-bit cache. q, out: [B, Hq, d] bf16 (q with any token stride); scale:
     head_dim ** -0.5 if None."""
-    addresses, (NB, H, bs, d) = _cache4(k_cache, v_cache, k_scale, v_scale)
-    B, Hq, W = q.shape[0], q.shape[1], block_table.shape[-1]
-    _check(lib().gdn_attn4_decode(
-        *_tokens(q, (B, Hq, d), "q"), *addresses, NB, _dense(block_table, _I32, (B, W), "block_table"), W,
-        _dense(lens, _I32, (B,), "lens"), B, _cache_dims(Hq, H, d, bs), d ** -0.5 if scale is None else scale,
-        _dense(out, _BF16, (B, Hq, d), "out"), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err),
-        _stream(stream)))
+    status = (_marshal or _binding()).attn4_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, out, workspace, scale,
+                                                   err, _raw(stream))
+    if status:
+        _check(status)
 
 
 def gdn_attn4_prefill_workspace_size(total_tokens, num_seqs, max_blocks, num_q_heads, num_kv_heads, head_dim, block_size, *,
@@ -551,14 +556,10 @@ def gdn_attn4_prefill(q, cu_tokens, k_cache, v_cache, k_scale, v_scale, block_ta
                       held_blocks=None, scale=None, err=None, stream=None):
     """Causal attention of packed prompt tokens over the 4-bit cache, which holds them already. q, out: [T, Hq, d] bf16 (q
     with any token stride); cu_tokens [B + 1], lens [B] int32; held_blocks as for the workspace's size."""
-    addresses, (NB, H, bs, d) = _cache4(k_cache, v_cache, k_scale, v_scale)
-    T, Hq, B, W = q.shape[0], q.shape[1], lens.shape[0], block_table.shape[-1]
-    _check(lib().gdn_attn4_prefill(
-        *_tokens(q, (T, Hq, d), "q"), _dense(cu_tokens, _I32, (B + 1,), "cu_tokens"), *addresses, NB,
-        _dense(block_table, _I32, (B, W), "block_table"), W, _dense(lens, _I32, (B,), "lens"), B, T,
-        min(B * W, 0x7fffffff) if held_blocks is None else held_blocks, _cache_dims(Hq, H, d, bs),
-        d ** -0.5 if scale is None else scale, _dense(out, _BF16, (T, Hq, d), "out"), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(err), _stream(stream)))
+    status = (_marshal or _binding()).attn4_prefill(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, out, workspace, scale,
+                                                    err, _raw(stream), cu_tokens, held_blocks)
+    if status:
+        _check(status)
 
 
 class DecodeGraph:

@@ -1,5 +1,7 @@
 """Build step of the C-ABI library: nvcc for sm_103a, one object per .cu in
-parallel, linked into ``libgdn.so`` inside the package directory (in-tree).
+parallel, linked into ``libgdn.so`` inside the package directory (in-tree), and
+of the binding's argument marshalling, ``_binding.so`` beside it (g++, against
+torch's headers).
 
 No fast-math flags: the kernels rely on IEEE division, expf/log1pf and
 explicit round-to-nearest adds and multiplies.
@@ -9,6 +11,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -16,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
+BINDING = os.path.join(PKG, "_binding.so")
 SOURCES = ["gdn_api.cu", "gdn_conv.cu", "gdn_decode.cu", "gdn_prefill.cu", "gdn_prefill_tc.cu",
            "gdn_graph.cu", "gdn_noalloc.cu", "gdn_gate.cu", "gdn_mixed.cu",
            "gdn_cache_api.cu", "gdn_cache.cu", "gdn_attn_decode.cu",
@@ -37,14 +41,28 @@ def _inputs():
 
 
 def stale() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
+def _binding_command(out: str) -> list[str]:
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    lib = os.path.join(home, "lib")
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    include = [INCLUDE, os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", *("-I" + i for i in include),
+            os.path.join(CSRC, "gdn_binding.cpp"), "-o", out, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            "-Wl,-rpath," + lib]
+
+
 def build_library(force: bool = False, verbose: bool = False) -> str:
-    """Compile every CUDA source for sm_103a and link libgdn.so (skipped when up to date)."""
+    """Compile every CUDA source for sm_103a, link libgdn.so and compile the binding (skipped when up to date)."""
     if not force and not stale():
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -58,6 +76,9 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    tmp_binding = BINDING + f".tmp{os.getpid()}"
+    cmd = _binding_command(tmp_binding)
+    procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for cmd, p in procs:
         out, _ = p.communicate()
@@ -65,10 +86,11 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
             failed.append((cmd, out.decode(errors="replace")))
     if failed:
         msg = "\n".join(" ".join(c) + "\n" + o for c, o in failed)
-        raise RuntimeError("nvcc failed:\n" + msg)
+        raise RuntimeError("the build failed:\n" + msg)
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.check_call([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
     os.replace(tmp, LIB)
+    os.replace(tmp_binding, BINDING)
     return LIB
 
 

@@ -40,14 +40,12 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStep = 16;              // keys of a warp's step
-constexpr int kTileKeys = kStep * kWarps;
 constexpr float kRise = 5.0f;          // log2 of what a score may pass the running maximum by
 constexpr float kTop = 9.0f;           // log2 of what the running maximum stands for
 
 using Units = UnitRule<8, 10, 24>;
 using Walk = WalkOf<Units>;
-static_assert(kWarps == 4 && (1 << 10) / kTileKeys <= 32, "a lane for each tile of a unit");
+static_assert(kWarps == 4 && (1 << 10) / 16 / kWarps <= 32, "a lane for each 16 of a warp's keys of a unit");
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -100,35 +98,32 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // whether one of four bytes is 255
 __device__ __forceinline__ bool has_255(uint32_t w) { return ((~w - 0x01010101u) & w & 0x80808080u) != 0; }
 
-// A key's scales, from N of its bytes of K and of V (in the words' low bytes) and the largest of V's, `top`.
-template <int N>
-struct KeyScales {
-  uint32_t k[N];              // fp32 2^(e - 127)
-  uint32_t v[(N + 1) / 2];    // f16 pairs 2^(e - top)
-  __device__ __forceinline__ static int largest(uint32_t w) {  // of N bytes
-    const uint32_t m = N > 1 ? max_u16x2(__byte_perm(w, 0, 0x4140), N > 2 ? __byte_perm(w, 0, 0x4342) : 0u) : w;
-    return static_cast<int>(N > 1 ? max(m & 0xFFFFu, m >> 16) : m);
-  }
+// Scales from four bytes each of K and of V; the largest scale of V of the first two's and of the last two's key (one key or two).
+struct FourScales {
+  uint32_t k[4];  // fp32 2^(e - 127)
+  uint32_t v[2];  // f16 pairs 2^(e - top)
   __device__ __forceinline__ static uint32_t without_255(uint32_t w) {
 #pragma unroll
-    for (int j = 0; j < N; ++j)
+    for (int j = 0; j < 4; ++j)
       if (((w >> 8 * j) & 255u) == 255u) w &= ~(255u << 8 * j);
     return w;
   }
-  __device__ __forceinline__ void make(uint32_t kw, uint32_t vw, int top) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) k[j] = (j == 0 ? kw << 23 : j == 1 ? kw << 15 : j == 2 ? kw << 7 : kw >> 1) & 0x7F800000u;
+  __device__ __forceinline__ void make(uint32_t kw, uint32_t vw, int top0, int top1) {
+    k[0] = (kw << 23) & 0x7F800000u;
+    k[1] = (kw << 15) & 0x7F800000u;
+    k[2] = (kw << 7) & 0x7F800000u;
+    k[3] = (kw >> 1) & 0x7F800000u;
     // 25 + e - top is the exponent field of 2^(e - top + 10), times 2^-10 (rounded to an f16 subnormal where that is one)
-    const uint32_t add = static_cast<uint32_t>(256 + 25 - top) * 0x10001u;
 #pragma unroll
-    for (int j = 0; j < (N + 1) / 2; ++j) {
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t add = static_cast<uint32_t>(256 + 25 - (j ? top1 : top0)) * 0x10001u;
       const uint32_t t = max_u16x2(__byte_perm(vw, 0, j ? 0x4342 : 0x4140) + add, 0x01000100u);
       v[j] = mul_f16x2((t & 0x001F001Fu) << 10, 0x14001400u);
     }
   }
   __device__ __forceinline__ void mark(uint32_t kw, uint32_t vw) {  // NaN for 255
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
+    for (int j = 0; j < 4; ++j) {
       if (((kw >> 8 * j) & 255u) == 255u) k[j] = 0x7FC00000u;
       if (((vw >> 8 * j) & 255u) == 255u) v[j / 2] = (v[j / 2] & (j % 2 ? 0xFFFFu : 0xFFFF0000u)) | (j % 2 ? 0x7E000000u : 0x7E00u);
     }
@@ -151,23 +146,26 @@ __device__ __forceinline__ void load_words(const unsigned char* p, T (&v)[N]) {
   }
 }
 
-// NT: query heads of a unit by eights, 1 or 2.
+// NT: query heads of a unit by eights, 1 or 2. A warp's step has 16 keys of a head of 256, 32 of 128, 64 of 64: the same bytes,
+// and what a step costs besides is the same.
 template <int D, int NT>
 struct Cfg {
+  static constexpr int kT = 256 / D, kStep = 16 * kT;       // 16-row tiles of a step, its keys
+  static constexpr int kTileKeys = kStep * kWarps;
   static constexpr int kG = D / kGroup4;                    // groups of a head
   static constexpr int kM = D / 16 / kWarps;                // 16-row tiles of O^T a warp has
   static constexpr int kRowK = D / 2, kRowV = D;            // bytes of a key, of a key pair's values
   static constexpr int kKeys = kStep * kRowK + 2 * kStep * kG;  // a warp's keys of a tile, and the scales of its keys and values
   static constexpr int kValues = kTileKeys / 2 * kRowV;     // a tile's values
-  static constexpr int kScaleK = kStep * kG * 4, kScaleV = kStep * kG * 2;  // of a warp's keys, as the products want them
-  static constexpr int kAtV = kWarps * 2 * kKeys, kAtSk = kAtV + 2 * kValues, kAtSv = kAtSk + kWarps * kScaleK, kAtP = kAtSv + kWarps * kScaleV,
-                       kAtQ = kAtP + kWarps * NT * 256, kAtFactor = kAtQ + NT * kG * 512, kAtMax = kAtFactor + 64, kAtSum = kAtMax + kWarps * 64,
+  static constexpr int kScaleK = kStep * kG * 4, kScaleV = 16 * kG * 2;  // of a warp's keys, of 16 keys' values, as the products want them
+  static constexpr int kAtV = kWarps * 2 * kKeys, kAtSk = kAtV + 2 * kValues, kAtSv = kAtSk + kWarps * kScaleK, kAtP = kAtSv + kWarps * kT * kScaleV,
+                       kAtQ = kAtP + kWarps * kT * NT * 256, kAtFactor = kAtQ + NT * kG * 512, kAtMax = kAtFactor + 64, kAtSum = kAtMax + kWarps * 64,
                        kAtLens = kAtSum + kWarps * 64;
   // CTAs of an SM. One more each costs registers, and with them instructions that are computed again: 256 requests of about
   // 8,000 tokens (D = 256, 8 heads) 213 us with 4 and 217 with 5.
-  static constexpr int kCtas = D == 256 ? (NT == 2 ? 3 : 4) : D == 128 ? (NT == 2 ? 4 : 5) : (NT == 2 ? 6 : 8);
+  static constexpr int kCtas = NT == 2 ? 3 : 4;
   static constexpr int smem_of(int nb) { return 128 + kAtLens + 4 * (nb + nb / kCoarse + 2); }
-  static_assert(kKeys % (D == 64 ? 64 : 128) == 0 && kAtP % 16 == 0, "alignment: a place in a row is changed by bits of the address");
+  static_assert(kKeys % 128 == 0 && kAtP % 16 == 0 && kStep * kG == 128, "alignment: a place in a row is changed by bits of the address; 4 scales a lane");
   // Where 16 bytes lie in a row, as bits of the address to change: no bank twice for eight rows' (four pairs') operand words
   // of one group.
   static __device__ __forceinline__ uint32_t swap_k(int row) { return (D == 256 ? row & 7 : D == 128 ? row >> 1 & 3 : row >> 2 & 1) << 4; }
@@ -186,8 +184,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kern
   unsigned char* my_keys = smem + warp * 2 * C::kKeys;       // the warp's two stages of keys
   unsigned char* values = smem + C::kAtV;                    // the CTA's two stages of values
   unsigned char* my_k = smem + C::kAtSk + warp * C::kScaleK; // scales of the warp's keys: [key][group] fp32
-  unsigned char* all_v = smem + C::kAtSv;                    // scales of the tile's values: [warp][pair][group], f16 pairs
-  unsigned char* all_p = smem + C::kAtP;                     // the tile's probabilities as operands: [warp][n][lane]
+  unsigned char* all_v = smem + C::kAtSv;                    // scales of the tile's values: [16 keys][pair][group], f16 pairs
+  unsigned char* all_p = smem + C::kAtP;                     // the tile's probabilities as operands: [16 keys][n][lane]
   unsigned char* all_q = smem + C::kAtQ;                     // queries as operands: [n][group][lane]
   float* s_factor = reinterpret_cast<float*>(smem + C::kAtFactor);
   float* s_max = reinterpret_cast<float*>(smem + C::kAtMax);  // [head][warp]
@@ -199,8 +197,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kern
 
   // where the lane's 16 bytes of a copy of 512 go: the swap of a row is that of the copy's first row and that of the row in it
   const uint32_t to_keys = smem_addr(my_keys) + lane * 16 / C::kRowK * C::kRowK + (lane * 16 % C::kRowK ^ C::swap_k(lane * 16 / C::kRowK));
-  const uint32_t to_values = smem_addr(values) + warp * (kStep / 2 * C::kRowV) + lane * 16 / C::kRowV * C::kRowV + (lane * 16 % C::kRowV ^ C::swap_v(lane * 16 / C::kRowV));
-  const uint32_t my_scales = smem_addr(my_keys) + kStep * C::kRowK + lane * 16;
+  const uint32_t to_values = smem_addr(values) + warp * (C::kStep / 2 * C::kRowV) + lane * 16 / C::kRowV * C::kRowV + (lane * 16 % C::kRowV ^ C::swap_v(lane * 16 / C::kRowV));
+  const uint32_t my_scales = smem_addr(my_keys) + C::kStep * C::kRowK + lane * 16;
   // the lane's words: of group 0 of key g and of key pair c, at the group of the warp's first d
   const uint32_t word_k = g * C::kRowK + (c * 4 ^ C::swap_k(g)), word_v = c * C::kRowV + ((warp * C::kM / 2 * 32) ^ C::swap_v(c)) + g * 4;
 
@@ -248,36 +246,44 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kern
 #pragma unroll 1
   for (; w.more(); w.next()) {
     const int head0 = w.h * G + w.chunk * 16, heads = min(p.heads, G - w.chunk * 16), keys = w.keys();
-    const int tiles = (keys + kTileKeys - 1) / kTileKeys;
-    // the row of the cache that the warp's 16 keys of each tile start at, a lane for each tile; -1: no such page, or no key
+    const int tiles = (keys + C::kTileKeys - 1) / C::kTileKeys;
+    // the row of the cache that each 16 of the warp's keys start at, one to a lane; -1: no such page, or no key
     int row = -1;
     {
-      const int at = lane * kTileKeys + warp * kStep, pos = w.first() + at;
+      const int at = lane / C::kT * C::kTileKeys + warp * C::kStep + lane % C::kT * 16, pos = w.first() + at;
       if (at < keys) {
         const int page = a.block_table[static_cast<int64_t>(p.b0 + w.b) * a.max_blocks + (pos >> shift)];
         if (page >= 0 && page < a.num_blocks) row = ((page * a.H + w.h) << shift) + (pos & (a.bs - 1));
         else if (a.err) atomicOr(a.err, GDN_DEVERR_BLOCK_RANGE);
       }
     }
+    auto row_of = [&](int t, int i) { return __shfl_sync(0xFFFFFFFFu, row, (t * C::kT + i) & 31); };  // of the tile's i-th 16
     auto fetch_keys = [&](int t) {  // of the warp, into its stage t & 1
-      const int from = __shfl_sync(0xFFFFFFFFu, row, t & 31);
-      if (t < tiles && from >= 0) {
-        const uint32_t to = to_keys + (t & 1) * C::kKeys;
-        const uint8_t* k = a.k_cache + static_cast<int64_t>(from) * C::kRowK + lane * 16;
+      const uint32_t to = to_keys + (t & 1) * C::kKeys;
 #pragma unroll
-        for (int x = 0; x < D / 64; ++x) cp_async16((to ^ C::swap_k(x * (512 / C::kRowK))) + x * 512, k + x * 512);
-        if (lane < 2 * C::kG)  // 16 bytes each: K's scales, V's
-          cp_async16(my_scales + (t & 1) * C::kKeys, (lane < C::kG ? reinterpret_cast<const uint8_t*>(a.k_scale) : reinterpret_cast<const uint8_t*>(a.v_scale)) + static_cast<int64_t>(from) * C::kG + (lane % C::kG) * 16);
+      for (int i = 0; i < C::kT; ++i) {
+        const int from = row_of(t, i);
+        if (t < tiles && from >= 0) {
+          const uint8_t* k = a.k_cache + static_cast<int64_t>(from) * C::kRowK + lane * 16;
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x) cp_async16((to ^ C::swap_k(x * (512 / C::kRowK))) + (i * (D / 64) + x) * 512, k + x * 512);
+        }
       }
+      const int from = row_of(t, lane % 8 / C::kG);
+      if (lane < 16 && t < tiles && from >= 0)  // 16 bytes each: K's scales, V's
+        cp_async16(my_scales + (t & 1) * C::kKeys, (lane < 8 ? reinterpret_cast<const uint8_t*>(a.k_scale) : reinterpret_cast<const uint8_t*>(a.v_scale)) + static_cast<int64_t>(from) * C::kG + lane % C::kG * 16);
       cp_async_commit();
     };
     auto fetch_values = [&](int t) {  // the warp's part of stage t & 1
-      const int from = __shfl_sync(0xFFFFFFFFu, row, t & 31);
-      if (t < tiles && from >= 0) {
-        const uint32_t to = to_values + (t & 1) * C::kValues;
-        const uint8_t* v = a.v_cache + static_cast<int64_t>(from) * (D / 2) + lane * 16;
+      const uint32_t to = to_values + (t & 1) * C::kValues;
 #pragma unroll
-        for (int x = 0; x < D / 64; ++x) cp_async16((to ^ C::swap_v(x * (512 / C::kRowV))) + x * 512, v + x * 512);
+      for (int i = 0; i < C::kT; ++i) {
+        const int from = row_of(t, i);
+        if (t < tiles && from >= 0) {
+          const uint8_t* v = a.v_cache + static_cast<int64_t>(from) * (D / 2) + lane * 16;
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x) cp_async16((to ^ C::swap_v(x * (512 / C::kRowV))) + (i * (D / 64) + x) * 512, v + x * 512);
+        }
       }
       cp_async_commit();
     };
@@ -337,97 +343,124 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kern
       if (t == 0) cp_async_wait<2>();  // (behind the first keys: their values, the next keys; later ones came before values)
       __syncwarp();
       const unsigned char* st = my_keys + (t & 1) * C::kKeys;
-      const bool there = __shfl_sync(0xFFFFFFFFu, row, t) >= 0;
-      const int live = there ? keys - t * kTileKeys - warp * kStep : 0;  // how many of the warp's keys are seen
-      // their scales: lane = (key, half of its groups)
+      const int live = keys - t * C::kTileKeys - warp * C::kStep;  // how many of the warp's keys the request has
+      // their scales, four a lane: half of a key's groups (D = 256), a key's, or two keys'
       int e_own;
       {
-        constexpr int kN = C::kG / 2;
-        const int key = lane >> 1;
-        const unsigned char* raw = st + kStep * C::kRowK;
-        uint32_t kw, vw;
-        if constexpr (kN == 4) {
-          kw = reinterpret_cast<const uint32_t*>(raw)[lane];
-          vw = reinterpret_cast<const uint32_t*>(raw + kStep * C::kG)[lane];
-        } else if constexpr (kN == 2) {
-          kw = reinterpret_cast<const uint16_t*>(raw)[lane];
-          vw = reinterpret_cast<const uint16_t*>(raw + kStep * C::kG)[lane];
-        } else {
-          kw = raw[lane];
-          vw = (raw + kStep * C::kG)[lane];
-        }
-        KeyScales<kN> sc;
+        const int key = D == 256 ? lane >> 1 : D == 128 ? lane : 2 * lane;
+        const unsigned char* raw = st + C::kStep * C::kRowK;
+        const uint32_t kw = reinterpret_cast<const uint32_t*>(raw)[lane], vw = reinterpret_cast<const uint32_t*>(raw + 128)[lane];
+        const int key_live = row_of(t, key / 16) >= 0 ? live : 0;  // (a page that is none: no key)
         const bool nan = has_255(kw) | has_255(vw);
-        int top = sc.largest(nan ? sc.without_255(vw) : vw);
-        top = min(max(max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1)), kBias4 + kLeastScale), 253);
-        e_own = top - kBias4;
-        sc.make(kw, vw, top);
-        if (nan) sc.mark(kw, vw);
-        if (key >= live) {
-#pragma unroll
-          for (int j = 0; j < (kN + 1) / 2; ++j) sc.v[j] = 0;
+        FourScales sc;
+        int top0, top1;
+        {
+          const uint32_t w = nan ? sc.without_255(vw) : vw;
+          const uint32_t lo = __byte_perm(w, 0, 0x4140), hi = __byte_perm(w, 0, 0x4342);
+          if constexpr (D == 64) {
+            top0 = max(lo & 0xFFFFu, lo >> 16);
+            top1 = max(hi & 0xFFFFu, hi >> 16);
+            top1 = min(max(top1, kBias4 + kLeastScale), 253);
+          } else {
+            const uint32_t m = max_u16x2(lo, hi);
+            top0 = max(m & 0xFFFFu, m >> 16);
+            if constexpr (D == 256) top0 = max(top0, __shfl_xor_sync(0xFFFFFFFFu, top0, 1));
+          }
+          top0 = min(max(top0, kBias4 + kLeastScale), 253);
+          if constexpr (D != 64) top1 = top0;
         }
-        // K: [key][group]. V: keys 2 j and 2 j + 1 side by side, [j][group]; of a pair the even key's lane writes the first
-        // half of its groups, the odd one the second
-        if constexpr (kN == 4) *reinterpret_cast<uint4*>(my_k + lane * 16) = make_uint4(sc.k[0], sc.k[1], sc.k[2], sc.k[3]);
-        else if constexpr (kN == 2) *reinterpret_cast<uint2*>(my_k + lane * 8) = make_uint2(sc.k[0], sc.k[1]);
-        else *reinterpret_cast<uint32_t*>(my_k + lane * 4) = sc.k[0];
+        e_own = D == 64 ? ((top0 - kBias4) & 0xFFFF) | (top1 - kBias4) << 16 : top0 - kBias4;
+        sc.make(kw, vw, top0, top1);
+        if (nan) sc.mark(kw, vw);
+        if (key + (D == 64) >= key_live) {
+          sc.v[1] = 0;
+          if (D != 64 || key >= key_live) sc.v[0] = 0;
+        }
+        *reinterpret_cast<uint4*>(my_k + lane * 16) = make_uint4(sc.k[0], sc.k[1], sc.k[2], sc.k[3]);  // [key][group]
         __syncwarp();
-        // scores of keys g and g + 8, heads 2 c and 2 c + 1
-        float s[NT][4];
+        // scores of keys 16 i + g and 16 i + g + 8, heads 2 c and 2 c + 1
+        float s[C::kT][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int i = 0; i < C::kT; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[n][j] = 0.0f;
-        const uint32_t keys_at = smem_addr(st) + word_k;  // (rows g and g + 8 have the same swap)
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][n][j] = 0.0f;
+        const uint32_t keys_at = smem_addr(st) + word_k;  // (rows that are 8 apart have the same swap)
 #pragma unroll
         for (int gr = 0; gr < C::kG; gr += kPart) {
-          float k0[kPart], k1[kPart];
-          load_words(my_k + (g * C::kG + gr) * 4, k0);
-          load_words(my_k + ((g + 8) * C::kG + gr) * 4, k1);
+          float k0[C::kT][kPart], k1[C::kT][kPart];
+#pragma unroll
+          for (int i = 0; i < C::kT; ++i) {
+            load_words(my_k + ((16 * i + g) * C::kG + gr) * 4, k0[i]);
+            load_words(my_k + ((16 * i + g + 8) * C::kG + gr) * 4, k1[i]);
+          }
 #pragma unroll
           for (int z = 0; z < kPart; ++z) {
             const uint32_t at = keys_at ^ (gr + z) * 16;
-            uint32_t x[4], y[4];
-            e2m1x8(lds32(at), x);
-            e2m1x8(lds32(at + 8 * C::kRowK), y);
+            uint4 q[NT];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const uint4 q = *reinterpret_cast<const uint4*>(all_q + (n * C::kG + gr + z) * 512 + lane * 16);
-              float r[4];
-              mma0(r, x[0], y[0], x[1], y[1], q.x, q.y);
-              mma(r, x[2], y[2], x[3], y[3], q.z, q.w);
-              s[n][0] = fmaf(r[0], k0[z], s[n][0]);
-              s[n][1] = fmaf(r[1], k0[z], s[n][1]);
-              s[n][2] = fmaf(r[2], k1[z], s[n][2]);
-              s[n][3] = fmaf(r[3], k1[z], s[n][3]);
+            for (int n = 0; n < NT; ++n) q[n] = *reinterpret_cast<const uint4*>(all_q + (n * C::kG + gr + z) * 512 + lane * 16);
+#pragma unroll
+            for (int i = 0; i < C::kT; ++i) {
+              uint32_t x[4], y[4];
+              e2m1x8(lds32(at + i * 16 * C::kRowK), x);
+              e2m1x8(lds32(at + (i * 16 + 8) * C::kRowK), y);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                float r[4];
+                mma0(r, x[0], y[0], x[1], y[1], q[n].x, q[n].y);
+                mma(r, x[2], y[2], x[3], y[3], q[n].z, q[n].w);
+                s[i][n][0] = fmaf(r[0], k0[i][z], s[i][n][0]);
+                s[i][n][1] = fmaf(r[1], k0[i][z], s[i][n][1]);
+                s[i][n][2] = fmaf(r[2], k1[i][z], s[i][n][2]);
+                s[i][n][3] = fmaf(r[3], k1[i][z], s[i][n][3]);
+              }
             }
           }
         }
         __syncwarp();  // the keys have been read
         fetch_keys(t + 2);
-        const int i0 = __shfl_sync(0xFFFFFFFFu, e_own, 2 * g), i1 = __shfl_sync(0xFFFFFFFFu, e_own, 2 * g + 16);
-        const float e0 = __int_as_float(0x4B400000 + i0) - 12582912.0f, e1 = __int_as_float(0x4B400000 + i1) - 12582912.0f;  // (as floats)
-        if (live < kStep) {  // the request's last keys, or a page that is none
+        // the largest scale of V of each of the lane's keys, as floats
+        float e[C::kT][2];
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+        for (int i = 0; i < C::kT; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              if (g >= live) s[n][j] = -INFINITY;
-              if (g + 8 >= live) s[n][2 + j] = -INFINITY;
-            }
-        }
+          for (int j = 0; j < 2; ++j) {
+            const int k = 16 * i + g + 8 * j;
+            int x = __shfl_sync(0xFFFFFFFFu, e_own, D == 256 ? 2 * k : D == 128 ? k : k >> 1);
+            if (D == 64) x = g & 1 ? x >> 16 : static_cast<int16_t>(x);
+            e[i][j] = __int_as_float(0x4B400000 + x) - 12582912.0f;
+          }
         // the exponents x; their largest x + e of each head, and what that passes the running maxima by, at most
         float above = -INFINITY, most[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (live >= kStep || g < live) s[n][j] *= fac[n][j];
-            if (live >= kStep || g + 8 < live) s[n][2 + j] *= fac[n][j];
-            most[n][j] = fmaxf(s[n][j] + e0, s[n][2 + j] + e1);
-            above = fmaxf(above, most[n][j] - m[n][j]);  // (-inf - -inf is left out)
+          for (int j = 0; j < 2; ++j) most[n][j] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < C::kT; ++i) {
+          const int seen = row_of(t, i) >= 0 ? live - 16 * i : 0;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][n][j] *= fac[n][j & 1];
+          if (seen < 16) {  // the request's last keys, or a page that is none
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (g + (j & 2) * 4 >= seen) s[i][n][j] = -INFINITY;
           }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) most[n][j] = fmaxf(most[n][j], fmaxf(s[i][n][j] + e[i][0], s[i][n][2 + j] + e[i][1]));
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) above = fmaxf(above, most[n][j] - m[n][j]);  // (-inf - -inf is left out)
         // from here on every warp is done with the tile before: its values, their scales and the probabilities are free
         if (__syncthreads_or(above > kRise)) {
 #pragma unroll
@@ -463,32 +496,36 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kern
           }
         }
         fetch_values(t + 1);
-        // p 2^e, both keys' rows turned into columns, and p into the sum: from its own exponent, as p 2^e is 0 next to a scale
-        // 2^126 times as large
+        // p 2^e, keys' rows turned into columns, and p into the sum: from its own exponent, as p 2^e is 0 next to a scale 2^126
+        // times as large
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          float x[4];
+          float from[2];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float from = m[n][j] == -INFINITY ? 0.0f : m[n][j] - kTop;
-            x[j] = ex2(s[n][j] + (e0 - from));
-            x[2 + j] = ex2(s[n][2 + j] + (e1 - from));
-            l[n][j] += ex2(s[n][j] - from) + ex2(s[n][2 + j] - from);
+          for (int j = 0; j < 2; ++j) from[j] = m[n][j] == -INFINITY ? 0.0f : m[n][j] - kTop;
+#pragma unroll
+          for (int i = 0; i < C::kT; ++i) {
+            float x[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              x[j] = ex2(s[i][n][j] + (e[i][0] - from[j]));
+              x[2 + j] = ex2(s[i][n][2 + j] + (e[i][1] - from[j]));
+              l[n][j] += ex2(s[i][n][j] - from[j]) + ex2(s[i][n][2 + j] - from[j]);
+            }
+            *reinterpret_cast<uint2*>(all_p + (((warp * C::kT + i) * NT + n) * 32 + lane) * 8) =
+                make_uint2(transpose8(pack_f16(x[0], x[1])), transpose8(pack_f16(x[2], x[3])));
           }
-          *reinterpret_cast<uint2*>(all_p + ((warp * NT + n) * 32 + lane) * 8) =
-              make_uint2(transpose8(pack_f16(x[0], x[1])), transpose8(pack_f16(x[2], x[3])));
         }
-        const bool odd = key & 1;
-        uint32_t* put = reinterpret_cast<uint32_t*>(all_v + warp * C::kScaleV) + (key >> 1) * C::kG + (lane & 1) * kN;
-        if constexpr (kN == 4) {
-          const uint32_t mine_v = odd ? sc.v[1] : sc.v[0], got = __shfl_xor_sync(0xFFFFFFFFu, odd ? sc.v[0] : sc.v[1], 2);
-          const uint32_t lo = odd ? got : mine_v, hi = odd ? mine_v : got;
-          *reinterpret_cast<uint2*>(put + (odd ? 2 : 0)) = make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+        // V's scales: keys 2 j and 2 j + 1 side by side, [j][group]. Where they are two lanes', the even key's lane writes the
+        // first half of its groups, the odd one the second.
+        uint32_t* put = reinterpret_cast<uint32_t*>(all_v + warp * (C::kT * C::kScaleV)) + (key >> 1) * C::kG;
+        if constexpr (D == 64) {
+          *reinterpret_cast<uint2*>(put) = make_uint2(__byte_perm(sc.v[0], sc.v[1], 0x5410), __byte_perm(sc.v[0], sc.v[1], 0x7632));
         } else {
-          const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, sc.v[0], 2);
-          const uint32_t lo = odd ? got : sc.v[0], hi = odd ? sc.v[0] : got;
-          if constexpr (kN == 2) put[odd] = __byte_perm(lo, hi, odd ? 0x7632 : 0x5410);
-          else if (!odd) put[0] = __byte_perm(lo, hi, 0x5410);
+          const bool odd = key & 1;
+          const uint32_t mine_v = odd ? sc.v[1] : sc.v[0], got = __shfl_xor_sync(0xFFFFFFFFu, odd ? sc.v[0] : sc.v[1], D == 256 ? 2 : 1);
+          const uint32_t lo = odd ? got : mine_v, hi = odd ? mine_v : got;
+          *reinterpret_cast<uint2*>(put + (D == 256 ? (lane & 1) * 4 : 0) + (odd ? 2 : 0)) = make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
         }
       }
       cp_async_wait<2>();  // (behind these values: the keys of the tile after the next, the next values)
@@ -497,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kern
       {
         const uint32_t values_at = smem_addr(values) + (t & 1) * C::kValues + word_v;  // (pairs c and c + 4 have the same swap)
 #pragma unroll
-        for (int sub = 0; sub < kWarps; ++sub) {
+        for (int sub = 0; sub < kWarps * C::kT; ++sub) {  // 16 keys
           uint2 pr[NT];
 #pragma unroll
           for (int n = 0; n < NT; ++n) pr[n] = *reinterpret_cast<const uint2*>(all_p + ((sub * NT + n) * 32 + lane) * 8);
@@ -512,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kern
           }
 #pragma unroll
           for (int z = 0; z < (C::kM + 1) / 2; ++z) {
-            const uint32_t at = (values_at ^ z * 32) + sub * (kStep / 2 * C::kRowV);
+            const uint32_t at = (values_at ^ z * 32) + sub * (8 * C::kRowV);
             uint32_t lo = lds32(at), hi = lds32(at + 4 * C::kRowV);
             if constexpr (C::kM == 1) {  // half of a group
               lo >>= (warp & 1) * 16;

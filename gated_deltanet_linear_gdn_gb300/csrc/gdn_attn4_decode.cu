@@ -43,9 +43,13 @@ constexpr int kThreads = 32 * kWarps;
 constexpr float kRise = 5.0f;          // log2 of what a score may pass the running maximum by
 constexpr float kTop = 9.0f;           // log2 of what the running maximum stands for
 
-using Units = UnitRule<8, 10, 24>;
-using Walk = WalkOf<Units>;
-static_assert(kWarps == 4 && (1 << 10) / 16 / kWarps <= 32, "a lane for each 16 of a warp's keys of a unit");
+// Small units shorten the chain that a small batch waits for, and cost a large one partial sums and the start of a pipeline;
+// a unit of 256 keys of 256, 512 of 128 or 1,024 of 64 is the same 70 KB. 256 requests of about 8,000 tokens (16 / 2 heads of
+// 256) 216 us in up to 24 of the smaller ones and 206 in up to 12, one of 4,097 11.9 and 12.5; 128 of 4,096 (32 / 8 of 64) 99 us
+// from 512 keys on and 89 from 1,024.
+template <int D>
+using Units = UnitRule<D == 256 ? 8 : D == 128 ? 9 : 10, D == 256 ? 10 : 11, 12>;
+static_assert(kWarps == 4 && (1 << 11) / 16 / kWarps <= 32, "a lane for each 16 of a warp's keys of a unit");
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -175,6 +179,7 @@ struct Cfg {
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kernel(const __grid_constant__ DecodeParams p) {
   using C = Cfg<D, NT>;
+  using Walk = WalkOf<Units<D>>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + (-smem_addr(smem_raw) & 127u);
   __shared__ int32_t s_scan[kWarps];
@@ -627,7 +632,7 @@ __global__ void __launch_bounds__(256) attn4_join_kernel(const __grid_constant__
   const int HC = a.H * p.chunks, G = a.Hq / a.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / HC, hc = blockIdx.x - b * HC, h = hc / p.chunks, chunk = hc - h * p.chunks;
   const int heads = min(p.heads, G - chunk * 16);
-  const int n = Units::count(min(max(a.lens[p.b0 + b], 0), a.max_blocks * a.bs));
+  const int n = Units<D>::count(min(max(a.lens[p.b0 + b], 0), a.max_blocks * a.bs));
   asm volatile("griddepcontrol.wait;" ::: "memory");  // (by every CTA: this kernel's end stands for the call's)
   if (n == 1) return;
   const int64_t f = static_cast<int64_t>(blockIdx.x) * p.each * p.heads;
@@ -736,7 +741,7 @@ cudaError_t launch_d(DecodeParams& p, cudaStream_t s) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // The join, a programmatic dependent: four d of a head to a thread, or to kJoinRows4 of them where requests may have many
-  // units; of those CTAs no more than fill the GPU (512 x 32, most of them for requests of few units, took 27 us, and 512 x 2 ??).
+  // units; of those CTAs no more than fill the GPU (512 x 32, most of them for requests of few units, took 27 us, and 512 x 2 eight).
   cudaLaunchConfig_t cfg = {};
   const int pairs = p.nb * p.a.H * p.chunks, few = (p.heads * D + 1023) / 1024;
   int wide = p.heads * D / 64;
@@ -753,38 +758,40 @@ cudaError_t launch_d(DecodeParams& p, cudaStream_t s) {
 }
 
 template <int D>
-cudaError_t launch_h(DecodeParams& p, cudaStream_t s) {
-  return p.heads <= 8 ? launch_d<D, 1>(p, s) : launch_d<D, 2>(p, s);
-}
-
-}  // namespace
-
-size_t attn4_decode_workspace(int B, int max_blocks, int Hq, int H, int d, int bs) {
-  const int most = attn_decode_batch(max_blocks, Hq, H, bs);
-  return decode_layout<Units>(B < most ? B : most, max_blocks, Hq, H, d, bs).total;
-}
-
-cudaError_t launch_attn4_decode(const AttnArgs& a, cudaStream_t s) {
+cudaError_t launch_all(const AttnArgs& a, cudaStream_t s) {
   const int G = a.Hq / a.H;
   DecodeParams p;
   p.a = a;
   p.fault = 0;
   p.heads = G < 16 ? G : 16;
   p.chunks = (G + 15) / 16;
-  p.each = static_cast<int>(Units::most(static_cast<int64_t>(a.max_blocks) * a.bs));
+  p.each = static_cast<int>(Units<D>::most(static_cast<int64_t>(a.max_blocks) * a.bs));
   const int most = attn_decode_batch(a.max_blocks, a.Hq, a.H, a.bs);  // (not 0: the caller has checked)
   const int launches = (a.B + most - 1) / most, per = (a.B + launches - 1) / launches;
   for (int b0 = 0; b0 < a.B; b0 += per) {
     p.b0 = b0;
     p.nb = a.B - b0 < per ? a.B - b0 : per;
-    const DecodeLayout L = decode_layout<Units>(p.nb, a.max_blocks, a.Hq, a.H, a.d, a.bs);
+    const DecodeLayout L = decode_layout<Units<D>>(p.nb, a.max_blocks, a.Hq, a.H, D, a.bs);
     char* ws = static_cast<char*>(a.workspace);
     p.ml = reinterpret_cast<float2*>(ws);
     p.part = reinterpret_cast<float*>(ws + L.part);
-    const cudaError_t e = a.d == 64 ? launch_h<64>(p, s) : a.d == 128 ? launch_h<128>(p, s) : launch_h<256>(p, s);
+    const cudaError_t e = p.heads <= 8 ? launch_d<D, 1>(p, s) : launch_d<D, 2>(p, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
+}
+
+}  // namespace
+
+size_t attn4_decode_workspace(int B, int max_blocks, int Hq, int H, int d, int bs) {
+  const int most = attn_decode_batch(max_blocks, Hq, H, bs), nb = B < most ? B : most;
+  return d == 64    ? decode_layout<Units<64>>(nb, max_blocks, Hq, H, d, bs).total
+         : d == 128 ? decode_layout<Units<128>>(nb, max_blocks, Hq, H, d, bs).total
+                    : decode_layout<Units<256>>(nb, max_blocks, Hq, H, d, bs).total;
+}
+
+cudaError_t launch_attn4_decode(const AttnArgs& a, cudaStream_t s) {
+  return a.d == 64 ? launch_all<64>(a, s) : a.d == 128 ? launch_all<128>(a, s) : launch_all<256>(a, s);
 }
 
 }  // namespace gdn

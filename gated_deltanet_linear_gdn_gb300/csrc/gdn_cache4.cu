@@ -14,6 +14,7 @@
 // changes its half of the bytes by atomics (each bit has one writer, so the result has no order).
 //
 // Bound by memory, 2 bytes read and 17 / 32 written a value (the read-back the other way round).
+#include "gdn_attn.cuh"
 #include "gdn_cache4.cuh"
 #include "gdn_internal.h"
 
@@ -69,113 +70,153 @@ struct Sixteen {
     for (int x = 0; x < 4; ++x) {
       uint32_t w;
       word(4 * i + x, w);
-      f[2 * x] = bf_lo(w) * r;
-      f[2 * x + 1] = bf_hi(w) * r;
+      const float2 v = mul2(make_float2(bf_lo(w), bf_hi(w)), make_float2(r, r));
+      f[2 * x] = v.x;
+      f[2 * x + 1] = v.y;
     }
   }
 };
 // 2^(127 - byte), which a value is multiplied with (of a group with NaN, anything: its codes mean nothing)
 __device__ __forceinline__ float down_by(uint32_t byte) { return __uint_as_float((254u - min(byte, 253u)) << 23); }
 
-// The place of a token's 16 elements: j counts the sixteens of all its heads.
-struct Place {
-  int64_t row;  // (block, head, offset) as a row of the cache
-  int e;        // which 16 of the head
-  __device__ __forceinline__ Place(const Cache4& c, int slot, int j, int sixteens, int block) {
-    const int h = j >> sixteens, blk = slot >> block, off = slot & (c.bs - 1);
-    e = j - (h << sixteens);
-    row = (static_cast<int64_t>(blk) * c.H + h) * c.bs + off;
+// Rows of the cache, (block, head, offset), are fewer than 2^31: everything but the address itself is in 32 bits.
+struct Rows {
+  uint32_t of_block, of_head;  // rows of a block; the head's first one in it
+  int shift, mask;
+  __device__ __forceinline__ Rows(const Cache4& c, int h) {
+    of_block = c.H * c.bs;
+    of_head = h * c.bs;
+    shift = 31 - __clz(c.bs);
+    mask = c.bs - 1;
   }
+  __device__ __forceinline__ uint32_t of(int slot) const { return static_cast<uint32_t>(slot >> shift) * of_block + static_cast<uint32_t>(slot & mask) + of_head; }
 };
+__device__ __forceinline__ uint64_t wide(uint32_t a, uint32_t b) { return static_cast<uint64_t>(a) * b; }
 
-// grid: (tokens, keys or values). A CTA has `at_once` tokens at a time, `rounds` times, two of them in flight; a thread has 16
-// elements of a head.
+// grid: (tokens, keys or values). A CTA has `at_once` tokens at a time, `rounds` times (of values
+// twice as many half as often, where it has several). A thread has 16 elements of a head, of keys for two tokens at a time.
 __global__ void __launch_bounds__(kThreads) cache4_append_kernel(const __grid_constant__ Append4Args a, int per, int at_once, int rounds) {
   const Cache4& c = a.c;
-  const bool is_v = blockIdx.y != 0;
   const int lt = threadIdx.x / per, j0 = threadIdx.x - lt * per;
   const int sixteens = 27 - __clz(c.d), all = c.H << sixteens, groups = c.d / kGroup4;  // (log2 of a head's sixteens)
-  const int cap = c.num_blocks * c.bs, block = 31 - __clz(c.bs);
-  const uint16_t* x = is_v ? a.v : a.k;
-  const int64_t stride = is_v ? a.v_stride : a.k_stride, first = static_cast<int64_t>(blockIdx.x) * at_once * rounds + lt;
-  uint8_t* scales = is_v ? c.v_scale : c.k_scale;
+  const int cap = c.num_blocks * c.bs;
   constexpr int kFlight = 2;
+  // (below: the same number of turns of every loop for all threads, as lanes exchange their groups' maxima)
+  if (blockIdx.y == 0) {
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * at_once * rounds + lt;
 #pragma unroll 1
-  for (int j = j0; j - j0 < all; j += per) {  // (the same number of turns for all threads: per divides all, or is the CTA)
+    for (int j = j0; j - j0 < all; j += per) {
+      const int h = j >> sixteens, e = j - (h << sixteens);  // the head, and which 16 of it
+      const Rows rows(c, h);
 #pragma unroll 1
-    for (int r0 = 0; r0 < rounds; r0 += kFlight) {
-      int slot[kFlight];
-      bool pair[kFlight], mine[kFlight];
-      Sixteen u[kFlight], w[kFlight];
+      for (int r0 = 0; r0 < rounds; r0 += kFlight) {
+        int slot[kFlight];
+        Sixteen u[kFlight];
 #pragma unroll
-      for (int i = 0; i < kFlight; ++i) {
-        const int64_t t = first + static_cast<int64_t>(r0 + i) * at_once;
-        slot[i] = -1;
-        pair[i] = false;
-        mine[i] = r0 + i < rounds && lt < at_once && t < a.T && j < all;
-        if (mine[i]) {
-          slot[i] = a.slot_map[t];
-          if (is_v) {
-            const int before = t > 0 ? a.slot_map[t - 1] : -1, after = t + 1 < a.T ? a.slot_map[t + 1] : -1;
-            mine[i] = !((slot[i] & 1) && before == slot[i] - 1);  // (the token before writes for both)
-            pair[i] = !(slot[i] & 1) && after == slot[i] + 1;
+        for (int i = 0; i < kFlight; ++i) {
+          const int64_t t = first + static_cast<int64_t>(r0 + i) * at_once;
+          slot[i] = r0 + i < rounds && lt < at_once && t < a.T && j < all ? a.slot_map[t] : -1;
+          if (slot[i] >= cap) {
+            if (j == 0 && a.err) atomicOr(a.err, GDN_DEVERR_BLOCK_RANGE);
+            slot[i] = -1;
           }
-          if (slot[i] >= cap && j == 0 && a.err && !is_v) atomicOr(a.err, GDN_DEVERR_BLOCK_RANGE);
-          if (slot[i] < 0 || slot[i] >= cap) mine[i] = pair[i] = false;
+          u[i].a = u[i].b = make_uint4(0, 0, 0, 0);
+          if (slot[i] >= 0) u[i].load(a.k + t * a.k_stride + j * 16);
         }
-        u[i].a = u[i].b = w[i].a = w[i].b = make_uint4(0, 0, 0, 0);
-        const uint16_t* src = x + t * stride + j * 16;
-        if (mine[i]) u[i].load(src);
-        if (mine[i] && pair[i]) w[i].load(src + stride);
-      }
 #pragma unroll
-      for (int i = 0; i < kFlight; ++i) {
-        const Place at(c, slot[i], j, sixteens, block);
-        uint8_t* sc = scales + at.row * groups + at.e / 2;
-        const uint32_t byte = u[i].group_byte();
-        const float down = down_by(byte);
-        float f[8], y[8];
-        if (!is_v) {
+        for (int i = 0; i < kFlight; ++i) {
+          const uint32_t byte = u[i].group_byte(), row = rows.of(slot[i]);
+          const float down = down_by(byte);
+          float f[8];
           uint2 codes;
           u[i].scaled(0, down, f);
           codes.x = to_e2m1x8(f);
           u[i].scaled(1, down, f);
           codes.y = to_e2m1x8(f);
-          if (mine[i]) *reinterpret_cast<uint2*>(c.k + at.row * (c.d / 2) + at.e * 8) = codes;
-        } else {
-          // the pair's bytes; a token alone keeps its neighbour's half of them
-          const uint32_t byte2 = w[i].group_byte();
-          uint4* to = reinterpret_cast<uint4*>(c.v + at.row / 2 * c.d + at.e * 16);
-          uint32_t put[4];
-          if (pair[i]) {
-            const float down2 = down_by(byte2);
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              u[i].scaled(z, down, f);
-              w[i].scaled(z, down2, y);
-              put[2 * z] = to_e2m1x8({f[0], y[0], f[1], y[1], f[2], y[2], f[3], y[3]});
-              put[2 * z + 1] = to_e2m1x8({f[4], y[4], f[5], y[5], f[6], y[6], f[7], y[7]});
-            }
-            *to = make_uint4(put[0], put[1], put[2], put[3]);
-          } else if (mine[i]) {
-            const uint32_t own = (slot[i] & 1) ? 0xF0F0F0F0u : 0x0F0F0F0Fu;
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              u[i].scaled(z, down, f);
-              put[2 * z] = to_e2m1x8({f[0], f[0], f[1], f[1], f[2], f[2], f[3], f[3]});
-              put[2 * z + 1] = to_e2m1x8({f[4], f[4], f[5], f[5], f[6], f[6], f[7], f[7]});
-            }
-            // (atomics: the neighbour may be written by another thread of this call, where the two do not follow each other)
-            uint32_t* word = reinterpret_cast<uint32_t*>(to);
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              atomicAnd(word + z, ~own);
-              atomicOr(word + z, put[z] & own);
-            }
+          if (slot[i] >= 0) {
+            *reinterpret_cast<uint2*>(c.k + wide(row, c.d / 2) + e * 8) = codes;
+            if (e % 2 == 0) c.k_scale[wide(row, groups) + e / 2] = static_cast<uint8_t>(byte);
           }
-          if (pair[i] && at.e % 2 == 0) sc[groups] = static_cast<uint8_t>(byte2);
         }
-        if (mine[i] && at.e % 2 == 0) *sc = static_cast<uint8_t>(byte);
+      }
+    }
+    return;
+  }
+  // a thread has two tokens of a long call, as one of two in a run writes for both, and one of a short call
+  const int turns = rounds > 1 ? rounds / 2 : 1, step = rounds > 1 ? 2 : 1;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * at_once * turns + lt;
+  auto slot_at = [&](int64_t t) {
+    const int s = t >= 0 && t < a.T ? a.slot_map[t] : -1;
+    return s < cap ? s : -1;
+  };
+#pragma unroll 1
+  for (int j = j0; j - j0 < all; j += per) {
+    const int h = j >> sixteens, e = j - (h << sixteens);
+    const Rows rows(c, h);
+    // Writes token t, at `slot` (negative: nothing), and the next one with it where that is the pair's other half.
+    auto put = [&](int slot, bool pair, const Sixteen& u, const Sixteen& w) {
+      const uint32_t row = rows.of(slot), byte = u.group_byte(), byte2 = w.group_byte();
+      const float down = down_by(byte);
+      uint8_t* sc = c.v_scale + wide(row, groups) + e / 2;
+      uint4* to = reinterpret_cast<uint4*>(c.v + wide(row / 2, c.d) + e * 16);
+      float f[8], y[8];
+      uint32_t codes[4];
+      if (pair) {
+        const float down2 = down_by(byte2);
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          u.scaled(z, down, f);
+          w.scaled(z, down2, y);
+          codes[2 * z] = to_e2m1x8({f[0], y[0], f[1], y[1], f[2], y[2], f[3], y[3]});
+          codes[2 * z + 1] = to_e2m1x8({f[4], y[4], f[5], y[5], f[6], y[6], f[7], y[7]});
+        }
+        *to = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+        if (e % 2 == 0) sc[groups] = static_cast<uint8_t>(byte2);
+      } else if (slot >= 0) {
+        const uint32_t own = (slot & 1) ? 0xF0F0F0F0u : 0x0F0F0F0Fu;
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          u.scaled(z, down, f);
+          codes[2 * z] = to_e2m1x8({f[0], f[0], f[1], f[1], f[2], f[2], f[3], f[3]});
+          codes[2 * z + 1] = to_e2m1x8({f[4], f[4], f[5], f[5], f[6], f[6], f[7], f[7]});
+        }
+        // (atomics: the neighbour may be written by another thread of this call, where the two do not follow each other)
+        uint32_t* word = reinterpret_cast<uint32_t*>(to);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          atomicAnd(word + z, ~own);
+          atomicOr(word + z, codes[z] & own);
+        }
+      }
+      if (slot >= 0 && e % 2 == 0) *sc = static_cast<uint8_t>(byte);
+    };
+#pragma unroll 1
+    for (int r = 0; r < turns; ++r) {
+      // of two tokens that follow each other in a run one writes: the one at an even slot, for the next one, too; the other is
+      // written by it or by the thread before
+      const int64_t t = step * (first + static_cast<int64_t>(r) * at_once);
+      int slot0 = -1, slot1 = -1;
+      bool pair0 = false, pair1 = false;
+      if (lt < at_once && t < a.T && j < all) {
+        const int before = slot_at(t - 1), s0 = slot_at(t), s1 = slot_at(t + 1), after = step == 2 ? slot_at(t + 2) : -1;
+        slot0 = (s0 & 1) && before == s0 - 1 ? -1 : s0;
+        slot1 = step == 1 || ((s1 & 1) && s0 == s1 - 1) ? -1 : s1;
+        pair0 = slot0 >= 0 && !(s0 & 1) && s1 == s0 + 1;
+        pair1 = slot1 >= 0 && !(s1 & 1) && after == s1 + 1;
+      }
+      const uint16_t* src = a.v + t * a.v_stride + j * 16;
+      Sixteen u, w;
+      auto load = [&](const uint16_t* p, bool one, bool two) {
+        u.a = u.b = w.a = w.b = make_uint4(0, 0, 0, 0);
+        if (one) u.load(p);
+        if (two) w.load(p + a.v_stride);
+      };
+      const bool first0 = slot0 >= 0, both = first0 && slot1 >= 0;  // (both: tokens of no run, or of two)
+      load(first0 ? src : src + a.v_stride, first0 || slot1 >= 0, first0 ? pair0 : pair1);
+      put(first0 ? slot0 : slot1, first0 ? pair0 : pair1, u, w);
+      if (__any_sync(0xFFFFFFFFu, both)) {
+        load(src + a.v_stride, both, both && pair1);
+        put(both ? slot1 : -1, both && pair1, u, w);
       }
     }
   }
@@ -188,7 +229,8 @@ __device__ __forceinline__ uint4 scaled_bf16(const uint32_t (&h)[4], float s) {
   for (int i = 0; i < 4; ++i) {
     float lo, hi;
     asm("{.reg .b16 x, y; mov.b32 {x, y}, %2; cvt.f32.f16 %0, x; cvt.f32.f16 %1, y;}" : "=f"(lo), "=f"(hi) : "r"(h[i]));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(hi * s), "f"(lo * s));
+    const float2 v = mul2(make_float2(lo, hi), make_float2(s, s));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(v.y), "f"(v.x));
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
@@ -202,7 +244,7 @@ __global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_cons
   const bool is_v = blockIdx.y != 0;
   const int lt = threadIdx.x / per, j0 = threadIdx.x - lt * per;
   const int sixteens = 27 - __clz(c.d), all = c.H << sixteens, groups = c.d / kGroup4;
-  const int cap = c.num_blocks * c.bs, block = 31 - __clz(c.bs);
+  const int cap = c.num_blocks * c.bs;
   uint16_t* x = is_v ? a.v : a.k;
   const int64_t stride = is_v ? a.v_stride : a.k_stride, first = static_cast<int64_t>(blockIdx.x) * at_once * rounds + lt;
   const uint8_t* scales = is_v ? c.v_scale : c.k_scale;
@@ -211,6 +253,10 @@ __global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_cons
   constexpr int kFlight = 4;
 #pragma unroll 1
   for (int j = j0; j < all; j += per) {
+    const int h = j >> sixteens, e = j - (h << sixteens);  // the head, and which eight of its first half
+    const Rows rows(c, h);
+    const uint8_t* codes = is_v ? c.v + e * 8 : c.k + e * 4;
+    uint16_t* out = x + first * stride + h * c.d + e * 8;
     int slot[kFlight], next[kFlight];
     auto look = [&](int r0) {
 #pragma unroll
@@ -232,16 +278,16 @@ __global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_cons
           slot[i] = -1;
         }
         if (slot[i] < 0) continue;
-        const Place at(c, slot[i], j, sixteens, block);
-        const uint8_t* sc = scales + at.row * groups + at.e / 4;
+        const uint32_t row = rows.of(slot[i]);
+        const uint8_t* sc = scales + wide(row, groups) + e / 4;
         byte[i][0] = sc[0];
         byte[i][1] = sc[groups / 2];
         if (is_v) {
-          const uint8_t* v = c.v + at.row / 2 * c.d + at.e * 8;
+          const uint8_t* v = codes + wide(row / 2, c.d);
           raw[i][0] = *reinterpret_cast<const uint2*>(v);
           raw[i][1] = *reinterpret_cast<const uint2*>(v + c.d / 2);
         } else {
-          const uint8_t* k = c.k + at.row * (c.d / 2) + at.e * 4;
+          const uint8_t* k = codes + wide(row, c.d / 2);
           raw[i][0].x = *reinterpret_cast<const uint32_t*>(k);
           raw[i][1].x = *reinterpret_cast<const uint32_t*>(k + c.d / 4);
         }
@@ -250,8 +296,7 @@ __global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_cons
 #pragma unroll
       for (int i = 0; i < kFlight; ++i) {
         if (slot[i] < 0) continue;
-        const int h = j >> sixteens, e = j - (h << sixteens);
-        uint16_t* to = x + (first + static_cast<int64_t>(r0 + i) * at_once) * stride + h * c.d + e * 8;
+        uint16_t* to = out + static_cast<int64_t>((r0 + i) * at_once) * stride;
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           uint32_t f[4];
@@ -279,13 +324,13 @@ struct Shape {
   int per, at_once, rounds;
   dim3 grid;
 };
-Shape shape_of(int T, int H, int d) {
+Shape shape_of(int T, int H, int d, int many) {
   const int all = H * d / 16;
   Shape s;
   s.per = all < kThreads ? all : kThreads;
   s.at_once = kThreads / s.per;
   const int64_t ctas = (static_cast<int64_t>(T) + s.at_once - 1) / s.at_once;
-  s.rounds = ctas >= 32 * sm_count() ? 8 : 1;
+  s.rounds = ctas >= 4 * many * sm_count() ? many : 1;
   s.grid = dim3(static_cast<unsigned>((ctas + s.rounds - 1) / s.rounds), 2);
   return s;
 }
@@ -453,13 +498,13 @@ __global__ void __launch_bounds__(kThreads) cache4_expand_kernel(const __grid_co
 }  // namespace
 
 cudaError_t launch_cache4_append(const Append4Args& a, cudaStream_t s) {
-  const Shape sh = shape_of(a.T, a.c.H, a.c.d);
+  const Shape sh = shape_of(a.T, a.c.H, a.c.d, 2);
   cache4_append_kernel<<<sh.grid, kThreads, 0, s>>>(a, sh.per, sh.at_once, sh.rounds);
   return cudaGetLastError();
 }
 
 cudaError_t launch_cache4_read(const Read4Args& a, cudaStream_t s) {
-  const Shape sh = shape_of(a.T, a.c.H, a.c.d);
+  const Shape sh = shape_of(a.T, a.c.H, a.c.d, 8);
   cache4_read_kernel<<<sh.grid, kThreads, 0, s>>>(a, sh.per, sh.at_once, sh.rounds);
   return cudaGetLastError();
 }

@@ -236,3 +236,62 @@ def test_captured_and_on_a_stream():
         call()
     side.synchronize()
     assert torch.equal(out, first) and bool((out[0] != 0).any())
+
+
+@pytest.mark.parametrize("H,d,bs", [(16, 256, 64), (40, 128, 16)])
+def test_long_calls_are_short_ones(H, d, bs):
+    """Calls long enough that a thread has several tokens: runs that start at odd and even slots, single tokens, padding and
+    any order give the bytes that calls of 50 tokens at a time give, and read back the same."""
+    rng = np.random.default_rng(d)
+    NB, T = 6000 // bs + 40, 6000
+    slots, blocks = [], list(rng.permutation(NB))
+    while len(slots) < T:
+        blk, kind = int(blocks.pop()), rng.random()
+        first = int(rng.integers(0, bs))
+        run = list(range(blk * bs + first, blk * bs + bs)) if kind < 0.8 else [blk * bs + int(x) for x in rng.permutation(bs)]
+        slots += run + ([-1] if rng.random() < 0.3 else [])
+        if len(blocks) == 1:
+            break
+    slots = slots[:T]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    kv = torch.randn(len(slots), 2, H, d, device="cuda", generator=g).bfloat16()
+    ids = i32(slots)
+    start = [torch.from_numpy(x).cuda() for x in cache(rng, NB, H, bs, d)]
+    one, many = [x.clone() for x in start], [x.clone() for x in start]
+    gdn.gdn_cache4_append(kv[:, 0], kv[:, 1], ids, *one)
+    for t in range(0, len(slots), 50):
+        gdn.gdn_cache4_append(kv[t:t + 50, 0], kv[t:t + 50, 1], ids[t:t + 50], *many)
+    for a, b in zip(one, many):
+        assert torch.equal(a, b)
+    assert not torch.equal(one[0], start[0])
+    out, parts = torch.full((2, 2, len(slots), H, d), 3.0, dtype=torch.bfloat16, device="cuda")
+    gdn.gdn_cache4_read(*one, ids, out[0], out[1])
+    for t in range(0, len(slots), 50):
+        gdn.gdn_cache4_read(*one, ids[t:t + 50], parts[0, t:t + 50], parts[1, t:t + 50])
+    assert torch.equal(out, parts)
+    k, v = co.unpack(*(x[:64] for x in one))
+    at = torch.nonzero((ids >= 0) & (ids < 64 * bs))[:, 0]
+    assert same_values(out[0, at], k[ids[at].long() // bs, :, ids[at].long() % bs])
+    assert same_values(out[1, at], v[ids[at].long() // bs, :, ids[at].long() % bs])
+
+
+def test_refused_before_the_call():
+    rng = np.random.default_rng(1)
+    t = [torch.from_numpy(x).cuda() for x in cache(rng, 4, 2, 16, 64)]
+    k = values(rng, 3, 2, 64).cuda()
+    slots, err = i32([1, 2, 3]), torch.zeros(1, dtype=torch.int32, device="cuda")
+    gdn.gdn_cache4_append(k, k, slots, *t, err=err)
+    before = [x.clone() for x in t]
+    bad_calls = [lambda: gdn.gdn_cache4_append(k, k, slots.long(), *t), lambda: gdn.gdn_cache4_append(k.float(), k, slots, *t),
+                 lambda: gdn.gdn_cache4_append(k, k[:, :1], slots, *t), lambda: gdn.gdn_cache4_append(k, k, slots, *t, err=err.float()),
+                 lambda: gdn.gdn_cache4_append(k, k, slots.cpu(), *t), lambda: gdn.gdn_cache4_append(k.transpose(1, 2).contiguous().transpose(1, 2), k, slots, *t),
+                 lambda: gdn.gdn_cache4_append(k, k, slots, t[0][:, :, ::2], *t[1:]), lambda: gdn.gdn_cache4_append(k, k, slots, t[0][:2], *t[1:]),
+                 lambda: gdn.gdn_cache4_append(k, k, slots, t[0], t[1], t[2], t[3].float()), lambda: gdn.gdn_cache4_append(k, k, None, *t),
+                 lambda: gdn.gdn_cache4_read(*t, slots, k, k[:2]), lambda: gdn.gdn_cache4_read(*t, slots, k.view(torch.float16), k)]
+    for call in bad_calls:
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(gdn.GDNError):                       # a row that does not start on 16 bytes
+        flat = torch.zeros(3 * 128 + 8, dtype=torch.bfloat16, device="cuda")
+        gdn.gdn_cache4_append(flat[4:4 + 384].view(3, 2, 64), k, slots, *t)
+    assert all(torch.equal(x, y) for x, y in zip(t, before))

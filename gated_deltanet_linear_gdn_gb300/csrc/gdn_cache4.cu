@@ -428,38 +428,51 @@ __global__ void __launch_bounds__(kThreads) cache4_expand_kernel(const __grid_co
     const bool good = from >= 0 && from < c.num_blocks && keys > 0;
     if (hk == 0 && in == 0) a.table[static_cast<int64_t>(b) * a.max_blocks + j] = good ? page : -1;
     if (!good) continue;
-    const int64_t of_head = static_cast<int64_t>(from) * c.H + h;
+    const int64_t of_head = static_cast<int64_t>(from) * c.H + h, to_head = static_cast<int64_t>(page) * c.H + h;
     const uint8_t* sc = (is_v ? c.v_scale : c.k_scale) + of_head * c.bs * groups;
-    // the page's largest scale
-    int top = 0;
-#pragma unroll 4
-    for (int i = in; i < keys * groups; i += kLanes) {
-      const int e = sc[i];
-      top = max(top, e == kNaN4 ? 0 : e);
-    }
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    if constexpr (TS > 1) {
-      if (lane == 0) s_top[warp] = top;
-      asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + team), "n"(kLanes) : "memory");
-#pragma unroll
-      for (int w = 0; w < TS; ++w) top = max(top, s_top[team * TS + w]);
-    }
-    top = max(top, 16);  // (the page's scale stays a normal number)
-    const int64_t to_head = static_cast<int64_t>(page) * c.H + h;
-    if (in == 0) (is_v ? a.v_scale : a.k_scale)[to_head] = __uint_as_float(static_cast<uint32_t>(top - 6) << 23);
     uint8_t* dst = (is_v ? a.v : a.k) + to_head * c.bs * c.d;
+    // the team's part in registers, 128 values a lane, between the largest scale and the conversion
+    auto page_top = [&](int top) {
+      top = __reduce_max_sync(0xFFFFFFFFu, top);
+      if constexpr (TS > 1) {
+        if (lane == 0) s_top[warp] = top;
+        asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + team), "n"(kLanes) : "memory");
+#pragma unroll
+        for (int w = 0; w < TS; ++w) top = max(top, s_top[team * TS + w]);
+      }
+      top = max(top, 16);  // (the page's scale stays a normal number)
+      if (in == 0) (is_v ? a.v_scale : a.k_scale)[to_head] = __uint_as_float(static_cast<uint32_t>(top - 6) << 23);
+      return top;
+    };
+    auto finite = [](int e) { return e == kNaN4 ? 0 : e; };
     if (!is_v) {
       const uint2* src = reinterpret_cast<const uint2*>(c.k + of_head * c.bs * (c.d / 2));
-      const int live = keys * groups * 2;
-#pragma unroll 4
-      for (int i = in; i < c.bs * groups * 2; i += kLanes) {  // half a group
-        const uint2 u = i < live ? src[i] : make_uint2(0, 0);
-        const uint32_t s = i < live ? f16_scale(sc[i / 2], top) * 0x10001u : 0u;
+      const int live = keys * groups * 2;  // half groups
+      uint2 u[8];
+      int byte[8], top = 0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int i = in + q * kLanes;
+        u[q] = make_uint2(0, 0);
+        byte[q] = 0;
+        if (i < live) {
+          u[q] = src[i];
+          byte[q] = sc[i / 2];
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) top = max(top, finite(byte[q]));
+      top = page_top(top);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int i = in + q * kLanes;
+        if (i >= c.bs * groups * 2) break;
+        const uint32_t s = f16_scale(byte[q], top) * 0x10001u;
         uint32_t y[4], o[4];
-        e2m1x8(u.x, y);
+        e2m1x8(u[q].x, y);
         o[0] = mul_e4m3(y[0], s) | (mul_e4m3(y[1], s) << 16);
         o[1] = mul_e4m3(y[2], s) | (mul_e4m3(y[3], s) << 16);
-        e2m1x8(u.y, y);
+        e2m1x8(u[q].y, y);
         o[2] = mul_e4m3(y[0], s) | (mul_e4m3(y[1], s) << 16);
         o[3] = mul_e4m3(y[2], s) | (mul_e4m3(y[3], s) << 16);
         *reinterpret_cast<uint4*>(dst + i * 16) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -467,25 +480,37 @@ __global__ void __launch_bounds__(kThreads) cache4_expand_kernel(const __grid_co
     } else {
       const uint4* src = reinterpret_cast<const uint4*>(c.v + of_head * c.bs / 2 * c.d);
       const int vectors = 27 - __clz(c.d);  // log2 of the 16-byte vectors of a pair of tokens, d bytes
-#pragma unroll 4
-      for (int i = in; i < (c.bs / 2) << vectors; i += kLanes) {  // 16 elements of two tokens
-        const int pair = i >> vectors, x0 = (i - (pair << vectors)) * 16, t = 2 * pair;
-        uint4 u = make_uint4(0, 0, 0, 0);
-        uint32_t s = 0;
+      uint4 u[4];
+      int even_byte[4], odd_byte[4], top = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = in + q * kLanes, pair = i >> vectors, group = (i - (pair << vectors)) / 2, t = 2 * pair;
+        u[q] = make_uint4(0, 0, 0, 0);
+        even_byte[q] = odd_byte[q] = 0;
         if (t < keys) {
-          u = src[i];
-          s = f16_scale(sc[t * groups + x0 / kGroup4], top) |
-              (t + 1 < keys ? f16_scale(sc[(t + 1) * groups + x0 / kGroup4], top) << 16 : 0u);
+          u[q] = src[i];
+          even_byte[q] = sc[t * groups + group];
+          if (t + 1 < keys) odd_byte[q] = sc[(t + 1) * groups + group];
         }
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) top = max(top, max(finite(even_byte[q]), finite(odd_byte[q])));
+      top = page_top(top);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = in + q * kLanes, pair = i >> vectors, x0 = (i - (pair << vectors)) * 16, t = 2 * pair;
+        if (t >= c.bs) break;
+        // (a token past the last: a scale of 0)
+        const uint32_t s = (t < keys ? f16_scale(even_byte[q], top) : 0u) | (t + 1 < keys ? f16_scale(odd_byte[q], top) << 16 : 0u);
+        const uint32_t w[4] = {u[q].x, u[q].y, u[q].z, u[q].w};
         uint32_t even[4], odd[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           uint32_t y[4];
           e2m1x8(w[x], y);  // (even token, odd token) of four elements
-          const uint32_t p = mul_e4m3(y[0], s) | (mul_e4m3(y[1], s) << 16), q = mul_e4m3(y[2], s) | (mul_e4m3(y[3], s) << 16);
-          even[x] = __byte_perm(p, q, 0x6420);
-          odd[x] = __byte_perm(p, q, 0x7531);
+          const uint32_t p = mul_e4m3(y[0], s) | (mul_e4m3(y[1], s) << 16), q2 = mul_e4m3(y[2], s) | (mul_e4m3(y[3], s) << 16);
+          even[x] = __byte_perm(p, q2, 0x6420);
+          odd[x] = __byte_perm(p, q2, 0x7531);
         }
         *reinterpret_cast<uint4*>(dst + t * c.d + x0) = make_uint4(even[0], even[1], even[2], even[3]);
         *reinterpret_cast<uint4*>(dst + (t + 1) * c.d + x0) = make_uint4(odd[0], odd[1], odd[2], odd[3]);

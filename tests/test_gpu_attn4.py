@@ -428,3 +428,20 @@ def test_a_step_of_a_model():
                 assert bool(((got - x).abs() <= x.abs().amax(dim=-1, keepdim=True) * 2 / 7).all())
         want, tol = co.attention(q[:n], None if which == "decode" else cu.tolist(), kk, vv, table, lens, d ** -0.5, **ROUNDING[which](d))
         assert bool(((out[:n].double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("which", ["decode", "prefill"])
+def test_a_large_cache(which):
+    """Pages behind 2^32 bytes of a cache."""
+    NB, H, bs, d = 70000, 4, 128, 256
+    c = Case(18, [1, 1] if which == "decode" else [3, 30], [300, 200], 8, H, d, bs)
+    n = c.cache[0].shape[0]
+    big = [torch.zeros(NB, *x.shape[1:], dtype=torch.uint8, device="cuda") for x in c.cache]
+    assert big[0].numel() > 1 << 32
+    for x, y in zip(big, c.cache):
+        x[NB - n:] = y
+    want = getattr(c, which)()
+    c.check(want, which)
+    c.cache = big
+    c.table = torch.where(c.table >= 0, c.table + NB - n, -1).int()
+    assert torch.equal(getattr(c, which)(), want) and int(c.err) == 0

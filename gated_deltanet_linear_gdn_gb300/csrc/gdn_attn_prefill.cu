@@ -31,6 +31,7 @@
 #include <type_traits>
 
 #include "gdn_attn.cuh"
+#include "gdn_cache4.cuh"
 #include "gdn_internal.h"
 
 namespace gdn {
@@ -57,6 +58,7 @@ struct PrefillParams {
   int b0, nb;
   int max_units, max_slots;
   int fault;                // test hook: CTA 0 looks up one batch of tiles and no more
+  int beside;               // the plan's dependent may start at once
   int32_t* counts;          // [0] units, [1] split tiles, [2] units taken after the grid's first
   PrefillUnit* units;       // [max_units]
   PrefillUnit* joins;       // [max_units]: the first split of each split row tile
@@ -107,6 +109,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
   __shared__ int32_t s_joins;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const AttnArgs& a = p.a;
+  if (p.beside) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int G = a.Hq / a.H;
   int flags = 0, carry = 0, carry_slot = 0;
   if (tid < kBuckets) s_count[tid] = 0;
@@ -1307,7 +1310,7 @@ cudaError_t launch_after(void (*kern)(KArgs...), dim3 grid, int threads, int sme
 }
 
 template <int D>
-cudaError_t launch_prefill_d(const PrefillParams& p, const PrefillLayout& L, const CacheMaps& maps, cudaStream_t s) {
+cudaError_t launch_prefill_d(const PrefillParams& p, const PrefillLayout& L, const CacheMaps& maps, const Expand4Args* expand, cudaStream_t s) {
   using C = std::conditional_t<D == 256, WideCfg, NarrowCfg<D == 256 ? 128 : D>>;
   auto kern = [] {
     if constexpr (D == 256) return attn_prefill_wide_kernel;
@@ -1317,6 +1320,7 @@ cudaError_t launch_prefill_d(const PrefillParams& p, const PrefillLayout& L, con
   if (e != cudaSuccess) return e;
   attn_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
   e = cudaGetLastError();
+  if (e == cudaSuccess && p.beside) e = launch_cache4_expand(*expand, s);
   if (e != cudaSuccess) return e;
   // head_dim 256: a CTA for each place of the list; otherwise one an SM, which takes units as they come
   const int grid = D == 256 || L.max_units < sm_count() ? L.max_units : sm_count();
@@ -1333,7 +1337,7 @@ size_t attn_prefill_workspace(int T, int B, int max_blocks, int Hq, int H, int d
   return prefill_layout(T, B < kBatchPerLaunch ? B : kBatchPerLaunch, max_blocks, Hq, H, d, bs).total;
 }
 
-cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t s) {
+cudaError_t launch_attn_prefill(const AttnArgs& a, const Expand4Args* expand, cudaStream_t s) {
   CacheMaps maps;
   cudaError_t e = encode_cache_maps(&maps, a);
   if (e != cudaSuccess) return e;
@@ -1343,6 +1347,7 @@ cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t s) {
     p.fault = attention_test_fault().load(std::memory_order_relaxed);
     p.b0 = b0;
     p.nb = a.B - b0 < kBatchPerLaunch ? a.B - b0 : kBatchPerLaunch;
+    p.beside = expand != nullptr && b0 == 0;  // (the pages of all launches)
     const PrefillLayout L = prefill_layout(a.T, p.nb, a.max_blocks, a.Hq, a.H, a.d, a.bs);
     p.max_units = L.max_units;
     p.max_slots = L.max_slots;
@@ -1352,9 +1357,9 @@ cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t s) {
     p.joins = reinterpret_cast<PrefillUnit*>(ws + L.joins);
     p.ml = reinterpret_cast<float2*>(ws + L.ml);
     p.part = reinterpret_cast<float*>(ws + L.part);
-    e = a.d == 64    ? launch_prefill_d<64>(p, L, maps, s)
-        : a.d == 128 ? launch_prefill_d<128>(p, L, maps, s)
-                     : launch_prefill_d<256>(p, L, maps, s);
+    e = a.d == 64    ? launch_prefill_d<64>(p, L, maps, expand, s)
+        : a.d == 128 ? launch_prefill_d<128>(p, L, maps, expand, s)
+                     : launch_prefill_d<256>(p, L, maps, expand, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

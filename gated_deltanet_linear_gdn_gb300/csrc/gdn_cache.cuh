@@ -79,7 +79,9 @@ int attn_decode_batch(int max_blocks, int Hq, int H, int bs);
 size_t attn_decode_workspace(int B, int max_blocks, int Hq, int H, int d, int bs);
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s);
 size_t attn_prefill_workspace(int T, int B, int max_blocks, int Hq, int H, int d, int bs);
-cudaError_t launch_attn_prefill(const AttnArgs& a, cudaStream_t s);
+struct Expand4Args;
+// expand: a kernel that fills the cache of `a` in, between the plan and the attention (null: it holds its pages already).
+cudaError_t launch_attn_prefill(const AttnArgs& a, const Expand4Args* expand, cudaStream_t s);
 
 // Tensor maps of the two pools as rows of d bytes, read in boxes of 16 rows (the smallest block) or of a
 // block's rows by min(d, 128) bytes that land swizzled (128-byte pattern; 64-byte for d = 64) in

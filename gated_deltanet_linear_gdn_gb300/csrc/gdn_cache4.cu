@@ -368,19 +368,16 @@ __global__ void __launch_bounds__(kThreads) cache4_expand_kernel(const __grid_co
   const Cache4& c = a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, team = warp / TS, in = tid - team * kLanes;
   const int cap = a.max_blocks * c.bs, block = 31 - __clz(c.bs);
-  // pages of the requests that have new tokens; one that there is no room for counts as empty
+  // pages of the requests that have new tokens. One that there is no room for gets a table of no pages, as those behind it
+  auto pages_of = [&](int b) {
+    const int len = min(max(a.lens[b], 0), cap);
+    return a.cu_tokens[b + 1] > a.cu_tokens[b] ? (len + c.bs - 1) >> block : 0;
+  };
   {
-    int carry = 0, flags = 0;
+    int carry = 0;
+    bool refused = false;
     for (int at = 0; at < a.B; at += kThreads) {
-      const int b = at + tid;
-      int len = 0;
-      if (b < a.B) {
-        len = a.lens[b];
-        if (len < 0 || len > cap) flags |= GDN_DEVERR_SEQLENS;
-        len = min(max(len, 0), cap);
-        if (a.cu_tokens[b + 1] <= a.cu_tokens[b]) len = 0;
-      }
-      const int pages = (len + c.bs - 1) >> block;
+      const int b = at + tid, pages = b < a.B ? pages_of(b) : 0;
       long long v = pages;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -396,18 +393,23 @@ __global__ void __launch_bounds__(kThreads) cache4_expand_kernel(const __grid_co
         total += s_warp[w];
       }
       const long long end = before + v;
-      const bool fits = end <= a.held;
       if (b < a.B) {
-        if (!fits && pages > 0) flags |= GDN_DEVERR_BLOCKS;
+        refused |= pages > 0 && end > a.held;
         s_first[b + 1] = static_cast<int32_t>(min(end, static_cast<long long>(a.held)));
-        if (blockIdx.x == 0) a.new_lens[b] = fits ? len : 0;
       }
       carry = static_cast<int32_t>(min(total, 0x3FFFFFFFll));
       __syncthreads();
     }
     if (tid == 0) s_first[0] = 0;
     __syncthreads();
-    if (flags && a.err && blockIdx.x == 0) atomicOr(a.err, flags);
+    if (refused && a.err && blockIdx.x == 0) atomicOr(a.err, GDN_DEVERR_BLOCKS);
+  }
+  auto fits = [&](int b, int pages) { return s_first[b + 1] - s_first[b] == pages; };
+#pragma unroll 1
+  for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+    const int pages = pages_of(b);
+    if (fits(b, pages)) continue;
+    for (int j = tid; j < pages; j += kThreads) a.table[static_cast<int64_t>(b) * a.max_blocks + j] = -1;
   }
   const int groups = c.d / kGroup4, H2 = 2 * c.H;
   const int64_t items = static_cast<int64_t>(s_first[a.B]) * H2;
@@ -423,6 +425,7 @@ __global__ void __launch_bounds__(kThreads) cache4_expand_kernel(const __grid_co
       if (s_first[mid] <= page) lo = mid; else hi = mid - 1;
     }
     const int b = lo, j = page - s_first[b];
+    if (!fits(b, pages_of(b))) continue;
     const int keys = min(c.bs, min(max(a.lens[b], 0), cap) - (j << block));
     const int from = a.block_table[static_cast<int64_t>(b) * a.max_blocks + j];
     const bool good = from >= 0 && from < c.num_blocks && keys > 0;
@@ -518,6 +521,10 @@ __global__ void __launch_bounds__(kThreads) cache4_expand_kernel(const __grid_co
     }
     if constexpr (TS > 1) asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + team), "n"(kLanes) : "memory");  // s_top is written anew
   }
+  // The kernel runs beside the call's plan (it needs nothing of it), and the attention's prologue beside this one's end; that
+  // this one is done stands for the plan, too.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace
@@ -540,8 +547,17 @@ cudaError_t launch_cache4_expand(const Expand4Args& a, cudaStream_t s) {
   const int64_t items = (static_cast<int64_t>(a.held) * a.c.H * 2 + teams - 1) / teams, most = 8 * static_cast<int64_t>(sm_count());
   const int grid = static_cast<int>(items < most ? items : most);
   auto kern = ts == 8 ? cache4_expand_kernel<8> : ts == 4 ? cache4_expand_kernel<4> : ts == 2 ? cache4_expand_kernel<2> : cache4_expand_kernel<1>;
-  kern<<<grid, kThreads, (a.B + 1) * sizeof(int32_t), s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = (a.B + 1) * sizeof(int32_t);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 }  // namespace gdn

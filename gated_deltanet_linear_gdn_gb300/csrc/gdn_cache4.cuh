@@ -54,7 +54,6 @@ struct Expand4Args {
   int B;
   int held;               // pages that there is room for
   int32_t* table;         // [B, max_blocks]
-  int32_t* new_lens;      // [B]
   uint8_t* k;             // [held, H, bs, d] e4m3
   uint8_t* v;
   float* k_scale;         // [held, H]
@@ -65,6 +64,7 @@ constexpr int kExpandBatch = 4096;  // requests of one call: their pages are cou
 
 cudaError_t launch_cache4_append(const Append4Args& a, cudaStream_t s);
 cudaError_t launch_cache4_read(const Read4Args& a, cudaStream_t s);
+// (a programmatic dependent of the prompts' plan: launch_attn_prefill launches it)
 cudaError_t launch_cache4_expand(const Expand4Args& a, cudaStream_t s);
 
 // AttnArgs over the 4-bit cache: k_cache, v_cache as bytes, k_scale and v_scale the scales' bytes.

@@ -76,10 +76,10 @@ gdn_status check_cache4(const void* k_cache, const void* v_cache, const void* k_
   return GDN_OK;
 }
 
-// Workspace of a prompt call over the 4-bit cache: its requests' pages in 8 bits, their table and lengths, then the 8-bit
+// Workspace of a prompt call over the 4-bit cache: the table of its requests' pages in 8 bits, those pages, then the 8-bit
 // call's own.
 struct Prefill4Layout {
-  size_t lens, k, v, k_scale, v_scale, rest, total;
+  size_t k, v, k_scale, v_scale, rest, total;
   int32_t held;  // pages there is room for; 0: too many for 32-bit rows
 };
 Prefill4Layout prefill4_layout(int32_t T, int32_t B, int32_t max_blocks, int32_t held, const gdn_cache_dims& d) {
@@ -91,8 +91,7 @@ Prefill4Layout prefill4_layout(int32_t T, int32_t B, int32_t max_blocks, int32_t
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   const size_t bytes = static_cast<size_t>(pages) * d.num_kv_heads * d.block_size * d.head_dim;
   const size_t scales = static_cast<size_t>(pages) * d.num_kv_heads * sizeof(float);
-  L.lens = up(static_cast<size_t>(most) * sizeof(int32_t));
-  L.k = up(L.lens + static_cast<size_t>(B) * sizeof(int32_t));
+  L.k = up(static_cast<size_t>(most) * sizeof(int32_t));
   L.v = up(L.k + bytes);
   L.k_scale = up(L.v + bytes);
   L.v_scale = up(L.k_scale + scales);
@@ -202,7 +201,7 @@ gdn_status gdn_attn_prefill(const void* q, int64_t q_stride, const int32_t* cu_t
     return GDN_ERR_INVALID_ARG;
   a.cu_tokens = cu_tokens;
   a.T = total_tokens;
-  return from_cuda(gdn::launch_attn_prefill(a, static_cast<cudaStream_t>(stream)));
+  return from_cuda(gdn::launch_attn_prefill(a, nullptr, static_cast<cudaStream_t>(stream)));
 }
 
 gdn_status gdn_cache4_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
@@ -310,14 +309,11 @@ gdn_status gdn_attn4_prefill(const void* q, int64_t q_stride, const int32_t* cu_
   x.B = num_seqs;
   x.held = L.held;
   x.table = reinterpret_cast<int32_t*>(ws);
-  x.new_lens = reinterpret_cast<int32_t*>(ws + L.lens);
   x.k = ws + L.k;
   x.v = ws + L.v;
   x.k_scale = reinterpret_cast<float*>(ws + L.k_scale);
   x.v_scale = reinterpret_cast<float*>(ws + L.v_scale);
   x.err = err;
-  const cudaError_t e = gdn::launch_cache4_expand(x, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return GDN_ERR_CUDA;
   a.cu_tokens = cu_tokens;
   a.T = total_tokens;
   a.k_cache = x.k;
@@ -325,10 +321,9 @@ gdn_status gdn_attn4_prefill(const void* q, int64_t q_stride, const int32_t* cu_
   a.k_scale = x.k_scale;
   a.v_scale = x.v_scale;
   a.block_table = x.table;
-  a.lens = x.new_lens;
   a.num_blocks = L.held;
   a.workspace = ws + L.rest;
-  return from_cuda(gdn::launch_attn_prefill(a, static_cast<cudaStream_t>(stream)));
+  return from_cuda(gdn::launch_attn_prefill(a, &x, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -611,7 +611,8 @@ gdn_status gdn_attn4_decode(const void* q, int64_t q_stride, const void* k_cache
  * tokens hold into its workspace, in 8 bits (values down to 2^-14 of a block's and head's largest scale as they are, below
  * that rounded to 2^-18 of its largest value); the rest is that call, with its arithmetic.
  *   held_blocks  what there is room for: a bound on the blocks that those requests hold together (a block that two of them
- *                hold counts twice). Requests past it, in row order, set GDN_DEVERR_BLOCKS and count as empty: zeros come out
+ *                hold counts twice). Requests past it, in row order, set GDN_DEVERR_BLOCKS and have no block (which sets
+ *                GDN_DEVERR_BLOCK_RANGE, too): zeros come out
  *   workspace    device scratch of >= gdn_attn4_prefill_workspace_size bytes (about 2 * held_blocks * Hkv * block_size *
  *                head_dim and what gdn_attn_prefill takes), 256-byte aligned
  * Supported: num_seqs <= 4096, held_blocks * Hkv * block_size < 2^31 - 128, otherwise as gdn_attn_prefill.

@@ -303,12 +303,31 @@ def test_prefill_blocks_that_there_is_no_room_for():
     full = c.prefill()
     rows = c.cu.tolist()
     got = c.prefill(held=10)
-    assert int(c.err) == gdn.GDN_DEVERR_BLOCKS
+    assert int(c.err) == gdn.GDN_DEVERR_BLOCKS | gdn.GDN_DEVERR_BLOCK_RANGE
     assert torch.equal(got[:rows[2]], full[:rows[2]]) and bool((got[rows[2]:] == 0).all())
     c.err.zero_()
     got = c.prefill(held=9)       # the second has no room, and no request behind one that has none
-    assert int(c.err) == gdn.GDN_DEVERR_BLOCKS
+    assert int(c.err) == gdn.GDN_DEVERR_BLOCKS | gdn.GDN_DEVERR_BLOCK_RANGE
     assert torch.equal(got[:rows[1]], full[:rows[1]]) and bool((got[rows[1]:] == 0).all())
+
+
+def test_prefill_lengths_that_are_none():
+    c = Case(19, [4, 5, 6], [40, 40, 40], 4, 2, 64, 16)
+    good = c.prefill()
+    assert int(c.err) == 0
+    rows = c.cu.tolist()
+    c.lens[1], c.lens[2] = -3, c.W * 16 + 1
+    got = c.prefill()
+    assert int(c.err) & gdn.GDN_DEVERR_SEQLENS
+    assert torch.equal(got[:rows[1]], good[:rows[1]]) and bool((got[rows[1]:rows[2]] == 0).all())
+
+
+def test_prefill_more_requests_than_a_launch():
+    """2,500 requests: two plans, one cache of pages."""
+    new = [(i * 7) % 3 for i in range(2500)]
+    c = Case(20, new, [(i * 13) % 40 for i in range(2500)], 2, 1, 64, 16)
+    c.check(c.prefill(held=c.blocks), "prefill")
+    assert int(c.err) == 0
 
 
 def test_prefill_many_requests():

@@ -177,7 +177,7 @@ struct Cfg {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kernel(const __grid_constant__ DecodeParams p, int sms) {
   using C = Cfg<D, NT>;
   using Walk = WalkOf<Units<D>>;
   extern __shared__ unsigned char smem_raw[];
@@ -246,7 +246,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kern
   w.nb = p.nb;
   w.H = a.H;
   w.chunks = p.chunks;
-  w.start(blockIdx.x, gridDim.x);
+  // A full grid's CTAs are dealt to the SMs in turn: an SM's get neighbouring shares, so that what shares are rounded to (whole
+  // units) adds up to one unit an SM and not one a CTA.
+  const int per_sm = gridDim.x / sms;
+  w.start(per_sm * sms == static_cast<int>(gridDim.x) ? blockIdx.x % sms * per_sm + blockIdx.x / sms : blockIdx.x, gridDim.x);
   int held = -1;  // the head of q that shared memory holds
 #pragma unroll 1
   for (; w.more(); w.next()) {
@@ -737,7 +740,7 @@ cudaError_t launch_d(DecodeParams& p, cudaStream_t s) {
   if (per_sm < 1) per_sm = 1;
   const int64_t most = static_cast<int64_t>(p.nb) * p.a.H * p.chunks * p.each;
   const int grid = static_cast<int>(most < static_cast<int64_t>(per_sm) * sm_count() ? most : per_sm * sm_count());
-  kern<<<grid, kThreads, smem, s>>>(p);
+  kern<<<grid, kThreads, smem, s>>>(p, sm_count());
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // The join, a programmatic dependent: four d of a head to a thread, or to kJoinRows4 of them where requests may have many

@@ -2,20 +2,28 @@
 //
 //   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j - m),  k_j, v_j = code * 2^(e - 127) by groups of 32 of the head
 //
-// Bound by memory on paper (17 / 32 bytes a value, read once), and next to that by instructions: the tensor cores take no
-// 4-bit operand whose scale goes by groups of V's rows, so every code passes through registers once. Per 16 keys of a head
-// of 256 (8,192 values, 4.35 KB) a warp has about 30 cycles of its scheduler's issue slots a KB, so the design counts
-// instructions:
+// Bound by memory on paper (17 / 32 bytes a value, read once), and next to that by instructions: no tensor-core operand is 4
+// bits with a scale by groups of V's rows, so every code passes through registers once. 16 keys of a head of 256 (8,192
+// values, 4.35 KB) are 187 clocks of an SM's share of the memory's rate, so the design counts instructions:
 //   - codes become f16 pairs by one conversion of a byte (exact), straight into the operand registers of the warp-level
 //     product, m16n8k16: keys (or d) on the 16-row side, query heads on the 8-column side, so that groups of up to 8 heads
 //     waste nothing. A byte of K has two elements of a key, a byte of V one element of two keys: the pairs that the two
 //     products' operands want.
 //   - a scale is never multiplied with a value. K's enters after a group's 32 elements, on the 16 x 8 scores; V's is
-//     multiplied with the probabilities, once for a group's 32 d.
+//     multiplied with the probabilities, once for a group's 32 d. Both are made once for a step, four a lane, and shared.
 //   - the tensor cores behind tcgen05 would want the same conversion and then a second trip through shared memory, which at
-//     this rate is full: 3 bytes a value and 40 values a clock are 120 of its 128 bytes a clock.
-// Measured on the GPU: the conversion 1.35 a clock and SM and more, the warp-level product 0.5 a clock and SM; a tile of 128
-// keys needs 1,024 and 256 of them, and 1,480 clocks of memory.
+//     this rate is full: 3 bytes a value and 40 values a clock are 120 of its 128 bytes a clock. The warp-level product's
+//     rate suffices: 0.5 a clock and SM, and these 16 keys are 32 of them.
+// The ALU does 2 conversions a clock and SM, 128 of them for 16 keys of 256; about 540 instructions in all (K 170, V 130,
+// scales 70, copies 60, softmax and the rest), 2.2 issued a clock: 240 clocks where the copies alone would take 190.
+//
+// A CTA of four warps takes a unit's tiles in turn, one step of each warp to a tile: 16 keys of a head of 256, 32 of 128, 64 of
+// 64 (the same bytes; what a step costs besides is the same). A warp has the scores of its own keys, and then the quarter of d
+// of all the tile's keys: the probabilities, as operands, and the scales of V go through shared memory. So an output is in
+// registers once (a first version in which each warp had all d of its own keys needed 64 registers for it and joined four
+// outputs at a unit's end: 274 us for the largest case). Two barriers a tile; the first carries the vote whether a running
+// maximum moves. Copies (cp.async, a warp's own keys two tiles ahead, values one) run beside that; 16-byte pieces of a row
+// change places so that no operand load has a bank twice.
 //
 // Queries are f16, scaled by a power of two per head so that the largest element lies in [2^14, 2^15): exact for bf16
 // values down to 2^-31 of it. Probabilities x V's largest scale of the key are f16: 11 significant bits, and 2^-34 of the
@@ -25,10 +33,11 @@
 // and stands for 2^9; it moves when an x + e passes it by 2^5. p 2^e goes into the product, next to 2^(e_group - e), and p
 // itself into the sum.
 //
-// Split: units of a request's own length (gdn_attn_units.cuh). A CTA's warps take a unit's steps of 16 keys in turn, each
-// with a running maximum, a sum and an output of its own, without a barrier between; at the unit's end the four are joined in
-// order, in shared memory. Copies run ahead in a ring of each warp's own (cp.async: a step of a page is contiguous; rows are
-// padded so that the operand loads have no bank twice).
+// Split: units of a request's own length (gdn_attn_units.cuh), joined by a second, programmatically dependent kernel in unit
+// order.
+//
+// Measured: 256 requests of 7,000 to 8,192 tokens (16 / 2 heads of 256) 204 us, 5.2 TB/s (copies alone 158 without partial sums
+// and join); 64 of 1 to 8,192 (28 / 4 of 128) 46 us; 2 of 131,071 38 us; one of 4,097 12.6 us.
 #include "gdn_attn.cuh"
 #include "gdn_attn_units.cuh"
 #include "gdn_cache4.cuh"
@@ -165,8 +174,8 @@ struct Cfg {
   static constexpr int kAtV = kWarps * 2 * kKeys, kAtSk = kAtV + 2 * kValues, kAtSv = kAtSk + kWarps * kScaleK, kAtP = kAtSv + kWarps * kT * kScaleV,
                        kAtQ = kAtP + kWarps * kT * NT * 256, kAtFactor = kAtQ + NT * kG * 512, kAtMax = kAtFactor + 64, kAtSum = kAtMax + kWarps * 64,
                        kAtLens = kAtSum + kWarps * 64;
-  // CTAs of an SM. One more each costs registers, and with them instructions that are computed again: 256 requests of about
-  // 8,000 tokens (D = 256, 8 heads) 213 us with 4 and 217 with 5.
+  // CTAs of an SM. One more costs registers, and with them instructions that are computed again: 256 requests of about 8,000
+  // tokens (D = 256, 8 heads) 213 us with 4 and 217 with 5.
   static constexpr int kCtas = NT == 2 ? 3 : 4;
   static constexpr int smem_of(int nb) { return 128 + kAtLens + 4 * (nb + nb / kCoarse + 2); }
   static_assert(kKeys % 128 == 0 && kAtP % 16 == 0 && kStep * kG == 128, "alignment: a place in a row is changed by bits of the address; 4 scales a lane");

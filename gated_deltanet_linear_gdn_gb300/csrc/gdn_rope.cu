@@ -9,7 +9,7 @@
 // 2^-55 of a turn (it is made from doubles), at position 2^31 2^-24.
 //
 // Bound by memory: an element is read and written once. Sines and cosines are made once for a token, in shared memory, for all
-// heads of q and k.
+// heads of q and k. 31,779 tokens (40 heads of 128, all of them turned) 95.5 us, 6.8 TB/s: the rate of a copy; 64 tokens 2.2 us.
 #include <math.h>
 
 #include "gdn_internal.h"

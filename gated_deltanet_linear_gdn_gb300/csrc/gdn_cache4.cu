@@ -242,7 +242,7 @@ __device__ __forceinline__ float group_scale(uint32_t byte) {
   return __uint_as_float(byte == kNaN4 ? 0x7FC00000u : byte == 0 ? 0x00400000u : byte << 23);
 }
 
-__global__ void __launch_bounds__(kThreads) cache4_read_kernel(const __grid_constant__ Read4Args a, int per, int at_once, int rounds) {
+__global__ void __launch_bounds__(kThreads, 4) cache4_read_kernel(const __grid_constant__ Read4Args a, int per, int at_once, int rounds) {
   const Cache4& c = a.c;
   const bool is_v = blockIdx.y != 0;
   const int lt = threadIdx.x / per, j0 = threadIdx.x - lt * per;
@@ -363,7 +363,7 @@ __device__ __forceinline__ uint32_t f16_scale(int byte, int top) {
 
 // An item is a page's keys or values of one head; a team of TS warps has it.
 template <int TS>
-__global__ void __launch_bounds__(kThreads) cache4_expand_kernel(const __grid_constant__ Expand4Args a) {
+__global__ void __launch_bounds__(kThreads, 4) cache4_expand_kernel(const __grid_constant__ Expand4Args a) {
   extern __shared__ int32_t s_first[];  // [B + 1]: pages before each request
   __shared__ int32_t s_warp[kThreads / 32];
   __shared__ int32_t s_top[kThreads / 32];

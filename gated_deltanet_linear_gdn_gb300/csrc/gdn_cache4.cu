@@ -15,8 +15,8 @@
 //
 // Bound by memory, 2 bytes read and 17 / 32 written a value (the read-back the other way round), and next to that by
 // instructions: about 120 to a thread's 16 values, 2.2 to 2.6 issued a clock. 131,071 tokens (2 heads of 256) read back in 59 us,
-// 5.8 TB/s (61 with three CTAs an SM, of 67 registers); 24,200 tokens of prompts (8 heads of 128) written in 32 us, 3.9 TB/s, and read back in 27; 256 single tokens 2.4 us
-// each way.
+// 5.8 TB/s (61 with three CTAs an SM, of 67 registers); 24,200 tokens of prompts (8 heads of 128) written in 32 us, 3.9 TB/s,
+// and read back in 27; 256 single tokens 2.4 us each way.
 #include "gdn_attn.cuh"
 #include "gdn_cache4.cuh"
 #include "gdn_internal.h"

@@ -111,6 +111,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // whether one of four bytes is 255
 __device__ __forceinline__ bool has_255(uint32_t w) { return ((~w - 0x01010101u) & w & 0x80808080u) != 0; }
 
+// whether one of four bytes is 192 or more
+__device__ __forceinline__ bool has_192(uint32_t w) { return (w & (w << 1) & 0x80808080u) != 0; }
+
+// A score is summed up times its query's power of two, up to 2^26 (elements below 2^15, codes up to 6, 256 of them). With a scale
+// of K of 2^65 or more among a warp's keys, their scales are lowered by as much until that power is out again: up to 2^127 no
+// score is infinite that is not so itself. (The raising stands in the branch of a request's last keys: in a branch of its own,
+// or as another factor, 207 and 209 us for the largest case; here 204.5, and 205.3 before.)
+constexpr float kLower = 0x1p-26f;
+
 // Scales from four bytes each of K and of V; the largest scale of V of the first two's and of the last two's key (one key or two).
 struct FourScales {
   uint32_t k[4];  // fp32 2^(e - 127)
@@ -133,6 +142,10 @@ struct FourScales {
       const uint32_t t = max_u16x2(__byte_perm(vw, 0, j ? 0x4342 : 0x4140) + add, 0x01000100u);
       v[j] = mul_f16x2((t & 0x001F001Fu) << 10, 0x14001400u);
     }
+  }
+  __device__ __forceinline__ void lower() {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k[j] = __float_as_uint(__uint_as_float(k[j]) * kLower);
   }
   __device__ __forceinline__ void mark(uint32_t kw, uint32_t vw) {  // NaN for 255
 #pragma unroll
@@ -369,6 +382,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kern
         const uint32_t kw = reinterpret_cast<const uint32_t*>(raw)[lane], vw = reinterpret_cast<const uint32_t*>(raw + 128)[lane];
         const int key_live = row_of(t, key / 16) >= 0 ? live : 0;  // (a page that is none: no key)
         const bool nan = has_255(kw) | has_255(vw);
+        // (of the keys that the request has: what lies behind them changes no bit)
+        const bool high = __any_sync(0xFFFFFFFFu, has_192(key < key_live ? D == 64 && key + 1 >= key_live ? kw & 0xFFFFu : kw : 0u));
         FourScales sc;
         int top0, top1;
         {
@@ -388,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kern
         }
         e_own = D == 64 ? ((top0 - kBias4) & 0xFFFF) | (top1 - kBias4) << 16 : top0 - kBias4;
         sc.make(kw, vw, top0, top1);
+        if (high) sc.lower();
         if (nan) sc.mark(kw, vw);
         if (key + (D == 64) >= key_live) {
           sc.v[1] = 0;
@@ -462,7 +478,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kern
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int j = 0; j < 4; ++j) s[i][n][j] *= fac[n][j & 1];
-          if (seen < 16) {  // the request's last keys, or a page that is none
+          if (seen < 16 || high) {  // the request's last keys, a page that is none; scales that were lowered
+            if (high) {
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[i][n][j] *= 1.0f / kLower;
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll

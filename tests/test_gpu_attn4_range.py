@@ -1,0 +1,44 @@
+"""Attention over the 4-bit cache near the ends of what its scales can say, against the 64-bit restatement of
+tests/_cache4_oracle.py: scales of K next to 2^127."""
+import pytest
+import torch
+
+from test_gpu_attn4 import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from gated_deltanet_linear_gdn_gb300 import build
+    build.build_library()
+    assert torch.cuda.is_available()
+
+
+@pytest.mark.parametrize("which", ["decode", "prefill"])
+@pytest.mark.parametrize("up", [64, 68, 100, 112])
+@pytest.mark.parametrize("d,Hq,H", [(64, 4, 2), (128, 9, 1), (256, 16, 2)])
+def test_large_keys(which, up, d, Hq, H):
+    """Keys 2^up times as large (bytes up to 127 + up) and queries as much smaller: the scores are the usual ones. Then every
+    third key as it was: its scores are 0 to 2^-60, next to the others' in the same tiles."""
+    new = [1, 1] if which == "decode" else [9, 40]
+    c = Case(101 + up, new, [300, 33], Hq, H, d, 32, q_size=3.0)
+    # (elements of 2^-120 and less have 8 bits in bf16, those below 2^-126 fewer: the reference takes what is there)
+    q = (c.q.double() * 2.0 ** -up).bfloat16()
+    c.cache[2] += up
+    got = getattr(c, which)(q=q)
+    assert bool(torch.isfinite(got).all())
+    c.check(got, which, q=q)
+    c.cache[2][:, :, ::3] -= up
+    c.check(getattr(c, which)(q=q), which, q=q)
+    assert int(c.err) == 0
+
+
+def test_a_large_key_that_no_one_sees():
+    """Scales of 2^127 behind the last token of a request and in other heads change no bit of its rows."""
+    c = Case(7, [1], [40], 4, 2, 64, 16)
+    clean = c.decode()
+    c.cache[2][c.table[0, 2].long(), :, 9:] = 254        # (41 tokens: the third page has nine)
+    assert torch.equal(c.decode(), clean)
+    c.cache[2][c.table[0, 2].long(), 1] = 254
+    assert torch.equal(c.decode()[:, :2], clean[:, :2])

@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const __grid_cons
 #pragma unroll
           for (int o = 1; o < kPer; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
           const int e = min(max(static_cast<int>(top >> 7), 1), 254);  // 127 + exponent of the largest
-          const int down = min(max(127 + 7 - (e - 127), 1), 254);      // * 2^(7 - exponent)
+          const int down = min(max(127 + 7 - (e - 127), 1), 253);      // * 2^(7 - exponent), whose inverse is a normal number
           const float sc = __int_as_float(down << 23);
           const float put = a.scale < 0.0f ? -sc : sc;                 // the factor is kept positive
           uint32_t hi[4], lo[4];

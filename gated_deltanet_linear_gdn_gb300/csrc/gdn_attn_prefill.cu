@@ -396,7 +396,7 @@ __device__ __forceinline__ void split_queries(const AttnArgs& a, const PrefillUn
         for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
       }
       const int e = min(max(static_cast<int>(top >> 7), 1), 254);       // 127 + exponent of the largest
-      const int down = min(max(127 + 7 - (e - 127), 1), 254);           // * 2^(7 - exponent)
+      const int down = min(max(127 + 7 - (e - 127), 1), 253);           // * 2^(7 - exponent), whose inverse is a normal number
       const float sc = __int_as_float(down << 23), put = sc * sign;
       uint32_t hi[2], lo[2];
 #pragma unroll

@@ -1,8 +1,9 @@
 """Attention over the 4-bit cache near the ends of what its scales can say, against the 64-bit restatement of
-tests/_cache4_oracle.py: scales of K next to 2^127."""
+tests/_cache4_oracle.py: scales of K next to 2^127, queries next to 2^-120."""
 import pytest
 import torch
 
+import test_gpu_cache_precision as eight
 from test_gpu_attn4 import Case
 
 pytestmark = pytest.mark.gpu
@@ -42,3 +43,24 @@ def test_a_large_key_that_no_one_sees():
     assert torch.equal(c.decode(), clean)
     c.cache[2][c.table[0, 2].long(), 1] = 254
     assert torch.equal(c.decode()[:, :2], clean[:, :2])
+
+
+@pytest.mark.parametrize("which", ["decode", "prefill"])
+@pytest.mark.parametrize("up", [116, 119, 122])
+@pytest.mark.parametrize("d,Hq,H", [(64, 4, 2), (128, 9, 1), (256, 16, 2)])
+def test_small_queries(which, up, d, Hq, H):
+    """Queries whose largest element is around 2^-120, with keys as much larger."""
+    c = Case(131 + up, [1, 1] if which == "decode" else [9, 40], [300, 33], Hq, H, d, 32, q_size=3.0)
+    q = (c.q.double() * 2.0 ** -up).bfloat16()
+    c.cache[2] += up
+    c.check(getattr(c, which)(q=q), which, q=q)
+
+
+@pytest.mark.parametrize("which,T", [("decode", 5), ("prefill", 300)])
+@pytest.mark.parametrize("up", [112, 118, 121])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_small_queries_over_the_8_bit_cache(which, T, up, d):
+    r = eight.rand(up + d)
+    k, v = r(700, 2, d) * 2.0 ** up, 1.0 + 0.3 * r(700, 2, d)
+    q = (r(T, 8, d).double() * 2.0 ** -up).bfloat16()
+    eight.check(eight.Pages(k, v, 16), q, which)

@@ -446,7 +446,9 @@ __global__ void __launch_bounds__(kThreads, 4) cache4_expand_kernel(const __grid
 #pragma unroll
         for (int w = 0; w < TS; ++w) top = max(top, s_top[team * TS + w]);
       }
-      top = max(top, 16);  // (the page's scale stays a normal number)
+      // K's scale of the page stays a normal number, V's what the attention takes as it is: of smaller values, 2^-99 and its
+      // multiples remain
+      top = max(top, is_v ? kBias4 + 6 + kLeastScale : 16);
       if (in == 0) (is_v ? a.v_scale : a.k_scale)[to_head] = __uint_as_float(static_cast<uint32_t>(top - 6) << 23);
       return top;
     };

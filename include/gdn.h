@@ -596,7 +596,7 @@ gdn_status gdn_cache4_read(const void* k_cache, const void* v_cache, const uint8
  * gdn_attn4_decode -- gdn_attn_decode over the 4-bit cache: same arguments but for the scales, same lengths, tables, errors
  * and limits. Queries are exact to 2^-31 of a head's largest element; for the product with V the probabilities keep 11
  * significant bits, and no less than 2^-34 of the row's largest probability x scale of V. A group's scale of V counts down to
- * 2^-24 of the largest of its token and head; scales of K below 2^-126 count as 0.
+ * 2^-24 of the largest of its token and head (or of 2^-90); scales of K below 2^-126 count as 0.
  */
 size_t gdn_attn4_decode_workspace_size(int32_t batch, int32_t max_blocks, gdn_cache_dims dims);
 gdn_status gdn_attn4_decode(const void* q, int64_t q_stride, const void* k_cache,
@@ -609,7 +609,8 @@ gdn_status gdn_attn4_decode(const void* q, int64_t q_stride, const void* k_cache
 /*
  * gdn_attn4_prefill -- gdn_attn_prefill over the 4-bit cache. The call first writes the pages that its requests with new
  * tokens hold into its workspace, in 8 bits (values down to 2^-14 of a block's and head's largest scale as they are, below
- * that rounded to 2^-18 of its largest value); the rest is that call, with its arithmetic.
+ * that rounded to 2^-18 of its largest value; V's largest scale counts as 2^-84 at least, so that of smaller values multiples of
+ * 2^-99 remain); the rest is that call, with its arithmetic.
  *   held_blocks  what there is room for: a bound on the blocks that those requests hold together (a block that two of them
  *                hold counts twice). Requests past it, in row order, set GDN_DEVERR_BLOCKS and have no block (which sets
  *                GDN_DEVERR_BLOCK_RANGE, too): zeros come out

@@ -1,10 +1,12 @@
 """Attention over the 4-bit cache near the ends of what its scales can say, against the 64-bit restatement of
-tests/_cache4_oracle.py: scales of K next to 2^127, queries next to 2^-120."""
+tests/_cache4_oracle.py: scales of K next to 2^127, queries next to 2^-120,
+values below 2^-90."""
 import pytest
 import torch
 
+import _cache4_oracle as co
 import test_gpu_cache_precision as eight
-from test_gpu_attn4 import Case
+from test_gpu_attn4 import ROUNDING, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +66,19 @@ def test_small_queries_over_the_8_bit_cache(which, T, up, d):
     k, v = r(700, 2, d) * 2.0 ** up, 1.0 + 0.3 * r(700, 2, d)
     q = (r(T, 8, d).double() * 2.0 ** -up).bfloat16()
     eight.check(eight.Pages(k, v, 16), q, which)
+
+
+@pytest.mark.parametrize("down", [60, 80, 86, 92, 100, 115])
+@pytest.mark.parametrize("d,Hq,H", [(64, 4, 2), (128, 9, 1), (256, 16, 2)])
+def test_small_values_of_prompts(down, d, Hq, H):
+    """Values of 2^-60 to 2^-115: exact in a block's 8 bits as long as its largest scale is 2^-84 or more, in steps of 2^-99 below
+    that (half a step for each value, and so for their mean)."""
+    c = Case(151 + down, [9, 40], [300, 33], Hq, H, d, 32)
+    c.cache[3] -= down
+    got = c.prefill()
+    k, v = co.unpack(*c.cache)
+    want, tol = co.attention(c.q, c.cu.tolist(), k, v, c.table, c.lens, d ** -0.5, v_exp=down + 3, **ROUNDING["prefill"](d))
+    # (the restatement's bound ends in 1e-30, which is larger than some of these values)
+    tol = tol - 0.999 * 1e-30 + (1.01 * 2.0 ** -100 if down > 80 else 0)
+    off = (got.double() - want).abs()
+    assert bool((off <= tol).all()), float((off / tol).max())

@@ -31,7 +31,8 @@
 //
 // Scales of V: with x the exponent of a score and e that of the key's largest scale of V, m is the running maximum of x + e
 // and stands for 2^9; it moves when an x + e passes it by 2^5. p 2^e goes into the product, next to 2^(e_group - e), and p
-// itself into the sum.
+// itself into the sum: 2^(kTop - e) for the row's largest, so that next to a scale of V of 2^101 or more what counts may be a
+// subnormal number, which the exponential does not give. It is added by itself where such a scale has set a running maximum.
 //
 // Split: units of a request's own length (gdn_attn_units.cuh), joined by a second, programmatically dependent kernel in unit
 // order.
@@ -51,6 +52,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kRise = 5.0f;          // log2 of what a score may pass the running maximum by
 constexpr float kTop = 9.0f;           // log2 of what the running maximum stands for
+constexpr float kFarAbove = 90.0f;     // log2 of the scales of V next to which p in the sum may be below 2^-126, and of the largest not below 2^-34
 
 // Small units shorten the chain that a small batch waits for, and cost a large one partial sums and the start of a pipeline;
 // a unit of 256 keys of 256, 512 of 128 or 1,024 of 64 is the same 70 KB. 256 requests of about 8,000 tokens (16 / 2 heads of
@@ -368,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kern
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[t][n][j] = 0.0f;
 
+    bool far = false;  // a running maximum was set next to a scale of V above 2^kFarAbove
 #pragma unroll 1
     for (int t = 0; t < tiles; ++t) {
       if (t == 0) cp_async_wait<2>();  // (behind the first keys: their values, the next keys; later ones came before values)
@@ -511,7 +514,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kern
               for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
               if (g == 0) s_max[(n * 8 + 2 * c + j) * kWarps + warp] = top;
             }
-          __syncthreads();
+          float largest = e[0][0];
+#pragma unroll
+          for (int i = 0; i < C::kT; ++i) largest = max3(largest, e[i][0], e[i][1]);
+          far |= __syncthreads_or(largest > kFarAbove) != 0;
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             float corr[2];
@@ -554,6 +560,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kern
             *reinterpret_cast<uint2*>(all_p + (((warp * C::kT + i) * NT + n) * 32 + lane) * 8) =
                 make_uint2(transpose8(pack_f16(x[0], x[1])), transpose8(pack_f16(x[2], x[3])));
           }
+        }
+        if (far) {  // what the sum has lost below 2^-126
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float from = m[n][j] == -INFINITY ? 0.0f : m[n][j] - kTop;
+#pragma unroll
+              for (int i = 0; i < C::kT; ++i)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const float x = s[i][n][2 * z + j] - from;
+                  if (x < -126.0f) l[n][j] += ex2(x + 64.0f) * 0x1p-64f;
+                }
+            }
         }
         // V's scales: keys 2 j and 2 j + 1 side by side, [j][group]. Where they are two lanes', the even key's lane writes the
         // first half of its groups, the odd one the second.

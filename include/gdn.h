@@ -471,7 +471,8 @@ gdn_status gdn_cache_append(const void* k, int64_t k_stride, const void* v, int6
  * GDN_DEVERR_SEQLENS and is clamped. What lies in a block past the request's length is never used,
  * NaN bytes included. Softmax statistics and sums are fp32. Queries are exact to 2^-18 of a head's
  * largest element; for the product with V the probabilities keep 16 significant bits, and no less
- * than 2^-26 of the row's largest probability x v_scale.
+ * than 2^-26 of the row's largest probability x v_scale. The sum of a row has them from 2^-26 of its
+ * largest on while no v_scale is above 2^100.
  *
  *   q          [batch] rows of Hq * head_dim bf16, q_stride elements apart (16-byte aligned, a
  *              multiple of 8)
@@ -498,8 +499,9 @@ gdn_status gdn_attn_decode(const void* q, int64_t q_stride, const void* k_cache,
  * gdn_cache_tables refused has its tokens in cu_tokens and not in lens: what comes out for them is
  * attention of the wrong positions, or zeros. Otherwise as gdn_attn_decode, but for the
  * probabilities: for the product with V they keep 11 significant bits, and 2^-32 (head_dim 64 and
- * 128, f16) or 2^-28 (256, three e5m2 parts) of the row's largest probability x v_scale. Keys that
- * a row does not see change nothing, whatever their bytes and scales, NaN included.
+ * 128, f16) or 2^-28 (256, three e5m2 parts) of the row's largest probability x v_scale (the row's
+ * sum: of its largest, while no v_scale is above 2^64). Keys that a row does not see change nothing,
+ * whatever their bytes and scales, NaN included.
  *
  *   q          [total_tokens] rows of Hq * head_dim bf16, q_stride elements apart
  *   cu_tokens  [num_seqs + 1] int32, non-decreasing, at most total_tokens; rows of q outside it

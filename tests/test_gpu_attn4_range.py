@@ -1,6 +1,7 @@
 """Attention over the 4-bit cache near the ends of what its scales can say, against the 64-bit restatement of
 tests/_cache4_oracle.py: scales of K next to 2^127, queries next to 2^-120,
-values below 2^-90."""
+values below 2^-90 and
+next to 2^127."""
 import pytest
 import torch
 
@@ -82,3 +83,27 @@ def test_small_values_of_prompts(down, d, Hq, H):
     tol = tol - 0.999 * 1e-30 + (1.01 * 2.0 ** -100 if down > 80 else 0)
     off = (got.double() - want).abs()
     assert bool((off <= tol).all()), float((off / tol).max())
+
+
+@pytest.mark.parametrize("up", [60, 100, 112, 119, 125])
+@pytest.mark.parametrize("d,Hq", [(64, 2), (128, 16), (256, 3)])
+def test_a_large_value_among_many_small_ones(up, d, Hq):
+    """One key with nearly all of a row's largest probability and a value of 2^up, 70,000 with 2^-17 of it each: together they
+    are a third of the sum."""
+    n, bs = 70001, 64
+    c = Case(171 + up, [1], [n - 1], Hq, 1, d, bs)
+    c.q = torch.where(c.q > 0, 0.5, -0.5).bfloat16()
+    c.cache[0].zero_()
+    c.cache[2][:] = 127
+    at = 30000                                            # the key: k with the queries' signs (the heads have the same)
+    c.q[:] = c.q[:, :1]
+    score = 0.5 * d * d ** -0.5                           # ... of a key of ones
+    k = {64: 3.0, 128: 2.0, 256: 1.5}[d]                  # exact codes; 12, 11.3 and 12 nats
+    code = {3.0: 5, 2.0: 4, 1.5: 3}[k]
+    assert 11 < score * k < 12.5
+    sign = torch.signbit(c.q[0, 0]).to(torch.uint8) * 8 + code
+    c.cache[0][c.table[0, at // bs].long(), 0, at % bs] = sign[0::2] | sign[1::2] << 4
+    c.cache[3][c.table[0, at // bs].long(), 0, at % bs] = 127 + up
+    c.cache[1][c.table[0, at // bs].long(), 0, at % bs // 2] = 0x21       # 0.5 (the even token, 30,000) and 1
+    got = c.decode()
+    c.check(got, "decode", v_exp=up)

@@ -107,3 +107,24 @@ def test_a_large_value_among_many_small_ones(up, d, Hq):
     c.cache[1][c.table[0, at // bs].long(), 0, at % bs // 2] = 0x21       # 0.5 (the even token, 30,000) and 1
     got = c.decode()
     c.check(got, "decode", v_exp=up)
+
+
+@pytest.mark.parametrize("up", [100, 123, 125, 126])
+@pytest.mark.parametrize("d,Hq,k", [(64, 2, 2.0), (128, 16, 1.5), (256, 3, 1.0)])
+def test_a_large_value_in_a_unit(up, d, Hq, k):
+    """The same within one unit (256, 512 or 1,024 keys): one key of 2^up next to keys with 2^-11.5 or 2^-12.2 of its probability,
+    where a sum that ends at 2^-126 is off by a tenth to a third from 2^124 or 2^123 on."""
+    n, bs, at = {64: 1024, 128: 512, 256: 256}[d], 32, 100
+    c = Case(191 + up, [1], [n - 1], Hq, 1, d, bs)
+    c.q[:] = torch.where(c.q[:, :1] > 0, 0.5, -0.5)
+    c.cache[0].zero_()
+    c.cache[2][:] = 127
+    page = c.table[0, at // bs].long()
+    sign = torch.signbit(c.q[0, 0]).to(torch.uint8) * 8 + {2.0: 4, 1.5: 3, 1.0: 2}[k]
+    c.cache[0][page, 0, at % bs] = sign[0::2] | sign[1::2] << 4
+    c.cache[3][page, 0, at % bs] = 127 + up
+    c.cache[1][page, 0, at % bs // 2] = 0x21              # the (even) token's values are 0.5 * 2^up
+    got = c.decode()
+    c.check(got, "decode", v_exp=up)
+    share = n * 2.0 ** (-k * 0.5 * d ** 0.5 * 1.4427)
+    assert share > 0.08 and bool((got.double() < 2.0 ** (up - 1) / (1 + 0.9 * share)).all())

@@ -202,6 +202,7 @@ gdn_status gdn_rope_frequencies(int32_t rot_dim, double base, gdn_rope_scaling s
   if (scaling == GDN_ROPE_YARN && trained_len <= 0) return GDN_ERR_INVALID_ARG;
   const int half = rot_dim / 2;
   if (scaling == GDN_ROPE_NTK && rot_dim > 2) base *= pow(factor, rot_dim / (rot_dim - 2.0));
+  if (!isfinite(base)) return GDN_ERR_INVALID_ARG;  // (all but the first pair would stand still)
   *host_factor = scaling == GDN_ROPE_YARN ? static_cast<float>(0.1 * log(factor) + 1.0) : 1.0f;
   // YARN: the (real) index of the pair that turns `turns` times over the trained length
   auto index = [&](double turns) { return rot_dim * log(trained_len / (2.0 * kPi * turns)) / (2.0 * log(base)); };

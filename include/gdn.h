@@ -556,7 +556,7 @@ gdn_status gdn_rope(const void* q, int64_t q_stride, const void* k, int64_t k_st
  *   YARN    pairs that turn 32 times or more over trained_len positions keep w_i, those that turn once or less have
  *           w_i / factor, the ones between mix the two along their index (its bounds rounded outward); the values'
  *           factor is 0.1 ln(factor) + 1
- * factor (not below 1) is not used by PLAIN, trained_len by YARN alone.
+ * factor (not below 1) is not used by PLAIN, trained_len by YARN alone. NTK's base has to be finite.
  */
 typedef enum { GDN_ROPE_PLAIN = 0, GDN_ROPE_LINEAR = 1, GDN_ROPE_NTK = 2, GDN_ROPE_YARN = 3 } gdn_rope_scaling;
 gdn_status gdn_rope_frequencies(int32_t rot_dim, double base, gdn_rope_scaling scaling, double factor,

@@ -139,6 +139,7 @@ gdn_status rope(PyObject* const* a) {
   const Call c{};
   const int64_t n = size_of(a[0], "q", 3, 0), hq = size_of(a[0], "q", 3, 1), d = size_of(a[0], "q", 3, 2);
   const bool keys = a[1] != Py_None;
+  if (!keys && a[4] != Py_None) refuse("k_out without k: nothing would be written to it");
   const int64_t h = keys ? size_of(a[1], "k", 3, 1) : 0;
   const int32_t rot = small(a[6], "rot_dim");
   const auto q = c.tokens(a[0], "q", n, hq, d), q_out = c.tokens(a[3], "q_out", n, hq, d);

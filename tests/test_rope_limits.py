@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 import gated_deltanet_linear_gdn_gb300 as gdn
 from gated_deltanet_linear_gdn_gb300 import build
@@ -24,3 +25,9 @@ def test_a_base_that_is_not_finite():
     assert frequencies(4, 1e4, gdn.GDN_ROPE_NTK, 1e153)[0] == gdn.GDN_ERR_INVALID_ARG
     assert frequencies(64, 1e300, gdn.GDN_ROPE_NTK, 1e10)[0] == gdn.GDN_ERR_INVALID_ARG
     assert frequencies(64, 1e300, gdn.GDN_ROPE_LINEAR, 1e10)[0] == gdn.GDN_OK
+
+
+def test_an_output_without_its_input():
+    q, pos = torch.zeros(3, 2, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="k_out without k"):
+        gdn.gdn_rope(q, None, pos, q, q, gdn.RopeTable(64, device="cpu"))

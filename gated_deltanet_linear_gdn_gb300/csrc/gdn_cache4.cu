@@ -96,58 +96,55 @@ struct Rows {
 };
 __device__ __forceinline__ uint64_t wide(uint32_t a, uint32_t b) { return static_cast<uint64_t>(a) * b; }
 
-// grid: (tokens, keys or values). A CTA has `at_once` tokens at a time, `rounds` times (of values
-// twice as many half as often, where it has several). A thread has 16 elements of a head, of keys for two tokens at a time.
-__global__ void __launch_bounds__(kThreads) cache4_append_kernel(const __grid_constant__ Append4Args a, int per, int at_once, int rounds) {
+// grid: (tokens, keys or values). A CTA has `at_once` tokens, or of a long call (N = 2) twice as many: of keys each thread has two
+// that are at_once apart, of values two neighbours. A thread has 16 elements of a head.
+// (Four CTAs an SM, 64 registers: with the 70 that the compiler takes by itself, 26,734 tokens of 8 heads of 128 written and read
+// back took 62.6 us instead of 58.0.)
+template <int N>
+__global__ void __launch_bounds__(kThreads, 4) cache4_append_kernel(const __grid_constant__ Append4Args a, int per, int at_once) {
   const Cache4& c = a.c;
   const int lt = threadIdx.x / per, j0 = threadIdx.x - lt * per;
   const int sixteens = 27 - __clz(c.d), all = c.H << sixteens, groups = c.d / kGroup4;  // (log2 of a head's sixteens)
   const int cap = c.num_blocks * c.bs;
-  constexpr int kFlight = 2;
   // (below: the same number of turns of every loop for all threads, as lanes exchange their groups' maxima)
   if (blockIdx.y == 0) {
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * at_once * rounds + lt;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * at_once * N + lt;
 #pragma unroll 1
     for (int j = j0; j - j0 < all; j += per) {
       const int h = j >> sixteens, e = j - (h << sixteens);  // the head, and which 16 of it
       const Rows rows(c, h);
-#pragma unroll 1
-      for (int r0 = 0; r0 < rounds; r0 += kFlight) {
-        int slot[kFlight];
-        Sixteen u[kFlight];
+      int slot[N];
+      Sixteen u[N];
 #pragma unroll
-        for (int i = 0; i < kFlight; ++i) {
-          const int64_t t = first + static_cast<int64_t>(r0 + i) * at_once;
-          slot[i] = r0 + i < rounds && lt < at_once && t < a.T && j < all ? a.slot_map[t] : -1;
-          if (slot[i] >= cap) {
-            if (j == 0 && a.err) atomicOr(a.err, GDN_DEVERR_BLOCK_RANGE);
-            slot[i] = -1;
-          }
-          u[i].a = u[i].b = make_uint4(0, 0, 0, 0);
-          if (slot[i] >= 0) u[i].load(a.k + t * a.k_stride + j * 16);
+      for (int i = 0; i < N; ++i) {
+        const int64_t t = first + static_cast<int64_t>(i) * at_once;
+        slot[i] = lt < at_once && t < a.T && j < all ? a.slot_map[t] : -1;
+        if (slot[i] >= cap) {
+          if (j == 0 && a.err) atomicOr(a.err, GDN_DEVERR_BLOCK_RANGE);
+          slot[i] = -1;
         }
+        u[i].a = u[i].b = make_uint4(0, 0, 0, 0);
+        if (slot[i] >= 0) u[i].load(a.k + t * a.k_stride + j * 16);
+      }
 #pragma unroll
-        for (int i = 0; i < kFlight; ++i) {
-          const uint32_t byte = u[i].group_byte(), row = rows.of(slot[i]);
-          const float down = down_by(byte);
-          float f[8];
-          uint2 codes;
-          u[i].scaled(0, down, f);
-          codes.x = to_e2m1x8(f);
-          u[i].scaled(1, down, f);
-          codes.y = to_e2m1x8(f);
-          if (slot[i] >= 0) {
-            *reinterpret_cast<uint2*>(c.k + wide(row, c.d / 2) + e * 8) = codes;
-            if (e % 2 == 0) c.k_scale[wide(row, groups) + e / 2] = static_cast<uint8_t>(byte);
-          }
+      for (int i = 0; i < N; ++i) {
+        const uint32_t byte = u[i].group_byte(), row = rows.of(slot[i]);
+        const float down = down_by(byte);
+        float f[8];
+        uint2 codes;
+        u[i].scaled(0, down, f);
+        codes.x = to_e2m1x8(f);
+        u[i].scaled(1, down, f);
+        codes.y = to_e2m1x8(f);
+        if (slot[i] >= 0) {
+          *reinterpret_cast<uint2*>(c.k + wide(row, c.d / 2) + e * 8) = codes;
+          if (e % 2 == 0) c.k_scale[wide(row, groups) + e / 2] = static_cast<uint8_t>(byte);
         }
       }
     }
     return;
   }
-  // a thread has two tokens of a long call, as one of two in a run writes for both, and one of a short call
-  const int turns = rounds > 1 ? rounds / 2 : 1, step = rounds > 1 ? 2 : 1;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * at_once * turns + lt;
+  const int64_t t = N * (static_cast<int64_t>(blockIdx.x) * at_once + lt);
   auto slot_at = [&](int64_t t) {
     const int s = t >= 0 && t < a.T ? a.slot_map[t] : -1;
     return s < cap ? s : -1;
@@ -193,34 +190,30 @@ __global__ void __launch_bounds__(kThreads) cache4_append_kernel(const __grid_co
       }
       if (slot >= 0 && e % 2 == 0) *sc = static_cast<uint8_t>(byte);
     };
-#pragma unroll 1
-    for (int r = 0; r < turns; ++r) {
-      // of two tokens that follow each other in a run one writes: the one at an even slot, for the next one, too; the other is
-      // written by it or by the thread before
-      const int64_t t = step * (first + static_cast<int64_t>(r) * at_once);
-      int slot0 = -1, slot1 = -1;
-      bool pair0 = false, pair1 = false;
-      if (lt < at_once && t < a.T && j < all) {
-        const int before = slot_at(t - 1), s0 = slot_at(t), s1 = slot_at(t + 1), after = step == 2 ? slot_at(t + 2) : -1;
-        slot0 = (s0 & 1) && before == s0 - 1 ? -1 : s0;
-        slot1 = step == 1 || ((s1 & 1) && s0 == s1 - 1) ? -1 : s1;
-        pair0 = slot0 >= 0 && !(s0 & 1) && s1 == s0 + 1;
-        pair1 = slot1 >= 0 && !(s1 & 1) && after == s1 + 1;
-      }
-      const uint16_t* src = a.v + t * a.v_stride + j * 16;
-      Sixteen u, w;
-      auto load = [&](const uint16_t* p, bool one, bool two) {
-        u.a = u.b = w.a = w.b = make_uint4(0, 0, 0, 0);
-        if (one) u.load(p);
-        if (two) w.load(p + a.v_stride);
-      };
-      const bool first0 = slot0 >= 0, both = first0 && slot1 >= 0;  // (both: tokens of no run, or of two)
-      load(first0 ? src : src + a.v_stride, first0 || slot1 >= 0, first0 ? pair0 : pair1);
-      put(first0 ? slot0 : slot1, first0 ? pair0 : pair1, u, w);
-      if (__any_sync(0xFFFFFFFFu, both)) {
-        load(src + a.v_stride, both, both && pair1);
-        put(both ? slot1 : -1, both && pair1, u, w);
-      }
+    // of two tokens that follow each other in a run one writes: the one at an even slot, for the next one, too; the other is
+    // written by it or by the thread before
+    int slot0 = -1, slot1 = -1;
+    bool pair0 = false, pair1 = false;
+    if (lt < at_once && t < a.T && j < all) {
+      const int before = slot_at(t - 1), s0 = slot_at(t), s1 = slot_at(t + 1), after = N == 2 ? slot_at(t + 2) : -1;
+      slot0 = (s0 & 1) && before == s0 - 1 ? -1 : s0;
+      slot1 = N == 1 || ((s1 & 1) && s0 == s1 - 1) ? -1 : s1;
+      pair0 = slot0 >= 0 && !(s0 & 1) && s1 == s0 + 1;
+      pair1 = slot1 >= 0 && !(s1 & 1) && after == s1 + 1;
+    }
+    const uint16_t* src = a.v + t * a.v_stride + j * 16;
+    Sixteen u, w;
+    auto load = [&](const uint16_t* p, bool one, bool two) {
+      u.a = u.b = w.a = w.b = make_uint4(0, 0, 0, 0);
+      if (one) u.load(p);
+      if (two) w.load(p + a.v_stride);
+    };
+    const bool first0 = slot0 >= 0, both = first0 && slot1 >= 0;  // (both: tokens of no run, or of two)
+    load(first0 ? src : src + a.v_stride, first0 || slot1 >= 0, first0 ? pair0 : pair1);
+    put(first0 ? slot0 : slot1, first0 ? pair0 : pair1, u, w);
+    if (__any_sync(0xFFFFFFFFu, both)) {
+      load(src + a.v_stride, both, both && pair1);
+      put(both ? slot1 : -1, both && pair1, u, w);
     }
   }
 }
@@ -536,7 +529,8 @@ __global__ void __launch_bounds__(kThreads, 4) cache4_expand_kernel(const __grid
 
 cudaError_t launch_cache4_append(const Append4Args& a, cudaStream_t s) {
   const Shape sh = shape_of(a.T, a.c.H, a.c.d, 2);
-  cache4_append_kernel<<<sh.grid, kThreads, 0, s>>>(a, sh.per, sh.at_once, sh.rounds);
+  auto kern = sh.rounds == 2 ? cache4_append_kernel<2> : cache4_append_kernel<1>;
+  kern<<<sh.grid, kThreads, 0, s>>>(a, sh.per, sh.at_once);
   return cudaGetLastError();
 }
 

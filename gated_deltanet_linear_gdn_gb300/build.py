@@ -40,10 +40,11 @@ def _inputs():
     return files
 
 
-def stale() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
+def stale(binding: bool = True) -> bool:
+    built = [LIB, BINDING] if binding else [LIB]
+    if not all(os.path.exists(f) for f in built):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = min(os.path.getmtime(f) for f in built)
     return any(os.path.getmtime(f) > t for f in _inputs())
 
 
@@ -61,38 +62,59 @@ def _binding_command(out: str) -> list[str]:
             "-Wl,-rpath," + lib]
 
 
-def build_library(force: bool = False, verbose: bool = False) -> str:
-    """Compile every CUDA source for sm_103a, link libgdn.so and compile the binding (skipped when up to date)."""
-    if not force and not stale():
+def _finish(procs) -> str:
+    """What the commands that failed wrote; empty if none did."""
+    failed = []
+    for cmd, p in procs:
+        out, _ = p.communicate()
+        if p.returncode != 0:
+            failed.append(" ".join(cmd) + "\n" + out.decode(errors="replace"))
+    return "\n".join(failed)
+
+
+def build_library(force: bool = False, verbose: bool = False, binding: bool = True) -> str:
+    """Compile every CUDA source for sm_103a, link libgdn.so and compile the binding (skipped when up to date). The library
+    stands by itself: where the binding does not compile, it is linked all the same before that is raised. binding=False
+    leaves the binding out, for users of the C ABI without torch's and Python's headers."""
+    if not force and not stale(binding):
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
     nvcc = _nvcc()
+
+    def start(cmd):
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        return cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
     procs = []
     objs = []
     for src in SOURCES:
         obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
         objs.append(obj)
-        cmd = [nvcc, *ARCH, *NVCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
-        if verbose:
-            print(" ".join(cmd), file=sys.stderr)
-        procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+        procs.append(start([nvcc, *ARCH, *NVCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]))
     tmp_binding = BINDING + f".tmp{os.getpid()}"
-    cmd = _binding_command(tmp_binding)
-    procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    failed = []
-    for cmd, p in procs:
-        out, _ = p.communicate()
-        if p.returncode != 0:
-            failed.append((cmd, out.decode(errors="replace")))
-    if failed:
-        msg = "\n".join(" ".join(c) + "\n" + o for c, o in failed)
-        raise RuntimeError("the build failed:\n" + msg)
-    tmp = LIB + f".tmp{os.getpid()}"
-    subprocess.check_call([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
-    os.replace(tmp, LIB)
-    os.replace(tmp_binding, BINDING)
+    binding_procs, no_binding = [], ""
+    if binding:
+        try:
+            binding_procs.append(start(_binding_command(tmp_binding)))
+        except (ImportError, OSError) as e:  # no torch, or no g++
+            no_binding = repr(e)
+    msg = _finish(procs)
+    if not msg:
+        tmp = LIB + f".tmp{os.getpid()}"
+        subprocess.check_call([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
+        os.replace(tmp, LIB)
+    no_binding = no_binding or _finish(binding_procs)
+    if msg:
+        if os.path.exists(tmp_binding):
+            os.remove(tmp_binding)
+        raise RuntimeError("nvcc failed:\n" + msg)
+    if no_binding:
+        raise RuntimeError(f"{LIB} is built, its binding for Python failed:\n" + no_binding)
+    if binding:
+        os.replace(tmp_binding, BINDING)
     return LIB
 
 
 if __name__ == "__main__":
-    print(build_library(force="--force" in sys.argv, verbose=True))
+    print(build_library(force="--force" in sys.argv, verbose=True, binding="--library" not in sys.argv))

@@ -14,13 +14,15 @@ import ctypes
 import functools
 import importlib.util
 import os
+import sysconfig
 from dataclasses import dataclass
 
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libgdn.so")
-BINDING_PATH = os.path.join(_PKG, "_binding.so")
+# (build.binding_path; its name says which torch and which Python it links)
+BINDING_PATH = os.path.join(_PKG, f"_binding.{torch.__version__}.{sysconfig.get_config_var('SOABI')}.so")
 
 GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_CUDA = 0, 1, 2, 3
 GDN_ERR_SCRATCH_LIMIT = 4
@@ -452,7 +454,7 @@ def gdn_attn_prefill(q, cu_tokens, k_cache, v_cache, k_scale, v_scale, block_tab
 
 # ---------------------------------------------- rotary positions, the cache in 4 bits
 
-# These calls' arguments are marshalled in C++ (_binding.so, csrc/gdn_binding.cpp): the smallest take 2 us on the GPU.
+# These calls' arguments are marshalled in C++ (csrc/gdn_binding.cpp): the smallest take 2 us on the GPU.
 
 
 class RopeTable:
@@ -482,11 +484,12 @@ _marshal = None
 
 
 def _binding():
-    """The marshalling functions of _binding.so, bound to the library's entry points (raises if it is absent)."""
+    """The marshalling functions of the binding in C++, bound to the library's entry points. Raises if it is absent, or there for
+    another torch or Python alone."""
     global _marshal
     if _marshal is None:
         if not os.path.exists(BINDING_PATH):
-            raise RuntimeError(f"{BINDING_PATH} is missing: it must be built "
+            raise RuntimeError(f"{BINDING_PATH} is missing: it must be built, for this torch and this Python "
                                "(gated_deltanet_linear_gdn_gb300.build.build_library())")
         spec = importlib.util.spec_from_file_location(__name__ + "._binding", BINDING_PATH)
         m = importlib.util.module_from_spec(spec)

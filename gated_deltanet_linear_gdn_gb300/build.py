@@ -1,7 +1,7 @@
 """Build step of the C-ABI library: nvcc for sm_103a, one object per .cu in
 parallel, linked into ``libgdn.so`` inside the package directory (in-tree), and
-of the binding's argument marshalling, ``_binding.so`` beside it (g++, against
-torch's headers).
+of the binding's argument marshalling, ``_binding.<torch>.<python>.so`` beside it
+(g++, against torch's headers).
 
 No fast-math flags: the kernels rely on IEEE division, expf/log1pf and
 explicit round-to-nearest adds and multiplies.
@@ -19,7 +19,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
-BINDING = os.path.join(PKG, "_binding.so")
 SOURCES = ["gdn_api.cu", "gdn_conv.cu", "gdn_decode.cu", "gdn_prefill.cu", "gdn_prefill_tc.cu",
            "gdn_graph.cu", "gdn_noalloc.cu", "gdn_gate.cu", "gdn_mixed.cu",
            "gdn_cache_api.cu", "gdn_cache.cu", "gdn_attn_decode.cu",
@@ -40,8 +39,15 @@ def _inputs():
     return files
 
 
+def binding_path() -> str:
+    """The binding links torch's C++ libraries and Python's: its name says which, so another version finds none of its own."""
+    import torch
+
+    return os.path.join(PKG, f"_binding.{torch.__version__}.{sysconfig.get_config_var('SOABI')}.so")
+
+
 def stale(binding: bool = True) -> bool:
-    built = [LIB, BINDING] if binding else [LIB]
+    built = [LIB, binding_path()] if binding else [LIB]
     if not all(os.path.exists(f) for f in built):
         return True
     t = min(os.path.getmtime(f) for f in built)
@@ -76,8 +82,11 @@ def build_library(force: bool = False, verbose: bool = False, binding: bool = Tr
     """Compile every CUDA source for sm_103a, link libgdn.so and compile the binding (skipped when up to date). The library
     stands by itself: where the binding does not compile, it is linked all the same before that is raised. binding=False
     leaves the binding out, for users of the C ABI without torch's and Python's headers."""
-    if not force and not stale(binding):
-        return LIB
+    try:
+        if not force and not stale(binding):
+            return LIB
+    except ImportError:  # no torch: the library at least
+        pass
     os.makedirs(BUILD_DIR, exist_ok=True)
     nvcc = _nvcc()
 
@@ -92,10 +101,10 @@ def build_library(force: bool = False, verbose: bool = False, binding: bool = Tr
         obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
         objs.append(obj)
         procs.append(start([nvcc, *ARCH, *NVCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]))
-    tmp_binding = BINDING + f".tmp{os.getpid()}"
-    binding_procs, no_binding = [], ""
+    binding_procs, no_binding, tmp_binding = [], "", ""
     if binding:
         try:
+            tmp_binding = binding_path() + f".tmp{os.getpid()}"
             binding_procs.append(start(_binding_command(tmp_binding)))
         except (ImportError, OSError) as e:  # no torch, or no g++
             no_binding = repr(e)
@@ -112,7 +121,7 @@ def build_library(force: bool = False, verbose: bool = False, binding: bool = Tr
     if no_binding:
         raise RuntimeError(f"{LIB} is built, its binding for Python failed:\n" + no_binding)
     if binding:
-        os.replace(tmp_binding, BINDING)
+        os.replace(tmp_binding, binding_path())
     return LIB
 
 

@@ -315,18 +315,24 @@ __global__ void __launch_bounds__(kThreads, 4) cache4_read_kernel(const __grid_c
   }
 }
 
-// Tokens that a CTA has at a time, and how often: one round while they are few.
+// Tokens that a CTA has at a time, and how often, by the CTAs an SM that one round would make: more loads in flight a thread
+// against fewer CTAs. Measured (8 heads of 128, 4 tokens a CTA; read back in 1, 2, 4, 8 rounds): 256 tokens 2.5, 2.7, 3.2, 4.9 us;
+// 1,024 (1.7 CTAs an SM) 3.6, 3.1, 3.3, 4.8; 3,500 (5.8) 7.7, 5.7, 4.7, 6.1; 14,000 (23) 28.3, 19.4, 15.4, 16.5; 26,734 (44) 52.3,
+// 35.2, 27.4, 26.5. Written in 1 and 2: 256 tokens 2.1, 2.3; 1,024 2.8, 2.6; 26,734 42.0, 30.0. 2 heads of 64 and of 256 turn at
+// the same counts of CTAs.
 struct Shape {
   int per, at_once, rounds;
   dim3 grid;
 };
-Shape shape_of(int T, int H, int d, int many) {
+Shape shape_of(int T, int H, int d, int most) {
   const int all = H * d / 16;
   Shape s;
   s.per = all < kThreads ? all : kThreads;
   s.at_once = kThreads / s.per;
   const int64_t ctas = (static_cast<int64_t>(T) + s.at_once - 1) / s.at_once;
-  s.rounds = ctas >= 4 * many * sm_count() ? many : 1;
+  const int64_t sms = sm_count();
+  const int rounds = ctas <= sms ? 1 : ctas <= 3 * sms ? 2 : ctas < 32 * sms ? 4 : 8;
+  s.rounds = rounds < most ? rounds : most;
   s.grid = dim3(static_cast<unsigned>((ctas + s.rounds - 1) / s.rounds), 2);
   return s;
 }

@@ -20,10 +20,11 @@ def _built():
 
 
 def in_rounds(H, d):
-    """Tokens that are more than 32 CTAs an SM of 256 threads with 16 elements each, and no whole number of rounds."""
-    at_once = 256 // (H * d // 16)
+    """Tokens that are more than 32 CTAs an SM of 256 threads with 16 elements each (all of either call's rounds), and no whole number
+    of rounds; tokens of half a CTA an SM (one round)."""
+    at_once, sms = 256 // (H * d // 16), torch.cuda.get_device_properties(0).multi_processor_count
     assert at_once > 1
-    return 33 * torch.cuda.get_device_properties(0).multi_processor_count * at_once + 5 * at_once // 2
+    return 33 * sms * at_once + 5 * at_once // 2, sms * at_once // 2
 
 
 def shuffled(rng, T, bs):
@@ -46,7 +47,7 @@ def shuffled(rng, T, bs):
 
 @pytest.mark.parametrize("H,d,bs", [(2, 64, 16), (3, 64, 128), (5, 128, 32), (2, 256, 64)])
 def test_rounds_are_one_round(H, d, bs):
-    T, short = in_rounds(H, d), 4000
+    T, short = in_rounds(H, d)
     rng = np.random.default_rng(H * d)
     slots, NB = shuffled(rng, T, bs)
     ids = i32(slots)
@@ -69,3 +70,23 @@ def test_rounds_are_one_round(H, d, bs):
         pages, where = torch.unique(at // bs, return_inverse=True)
         for z, x in enumerate(co.unpack(*(y[pages] for y in one))):
             assert same_values(out[part, z], x[where, :, at % bs])
+
+
+@pytest.mark.parametrize("H,d,bs", [(3, 64, 16), (2, 256, 64)])
+@pytest.mark.parametrize("ctas", [0.9, 1.1, 2.9, 3.1, 31.5])
+def test_around_the_rounds(H, d, bs, ctas):
+    """Calls of just under and over one CTA an SM (a second round), three (four rounds), and under 32 (eight)."""
+    T = int(ctas * in_rounds(H, d)[1] * 2) + 1
+    rng = np.random.default_rng(T)
+    slots, NB = shuffled(rng, T, bs)
+    ids = i32(slots)
+    kv = torch.randn(T, 2, H, d, device="cuda").bfloat16()
+    one = [torch.from_numpy(x).cuda() for x in cache(rng, NB, H, bs, d)]
+    many, short = [x.clone() for x in one], in_rounds(H, d)[1]
+    gdn.gdn_cache4_append(kv[:, 0], kv[:, 1], ids, *one)
+    out, parts = torch.full((2, 2, T, H, d), 3.0, dtype=torch.bfloat16, device="cuda")
+    gdn.gdn_cache4_read(*one, ids, out[0], out[1])
+    for t in range(0, T, short):
+        gdn.gdn_cache4_append(kv[t:t + short, 0], kv[t:t + short, 1], ids[t:t + short], *many)
+        gdn.gdn_cache4_read(*one, ids[t:t + short], parts[0, t:t + short], parts[1, t:t + short])
+    assert all(torch.equal(a, b) for a, b in zip(one, many)) and torch.equal(out, parts)

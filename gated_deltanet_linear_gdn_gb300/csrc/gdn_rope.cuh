@@ -10,7 +10,7 @@ namespace gdn {
 
 constexpr int kRopeMaxDim = 1024;  // of a head: its items fit in 64 threads, sines and cosines of kRopeTokens tokens in 16 KB
 constexpr int kRopeTokens = 4;     // tokens of a CTA of narrow items
-constexpr int kRopeFew = 1024;     // tokens up to which each has more threads
+constexpr int kRopeFew = 256, kRopeMany = 1024;  // tokens up to which each has 256 threads, and 128
 
 struct RopeArgs {
   const uint16_t* q;

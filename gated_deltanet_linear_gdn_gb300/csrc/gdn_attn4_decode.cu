@@ -673,8 +673,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) attn4_decode_kern
 
 // Joins the units of one request, kv head and head chunk in unit order; an empty request gets zeros. The units' weights are
 // made once for a head, in shared memory; a thread then has four d of a head. Up to kJoinFew units it takes in order; more are
-// taken by kJoinRows4 threads, unit u by u mod kJoinRows4, whose sums are taken in order then.
-constexpr int kJoinFew = 32, kJoinRows4 = 16;
+// taken by kJoinRows4 threads, unit u by u mod kJoinRows4, whose sums are taken in order then. The whole call (16 / 2 heads of 256)
+// with kJoinFew 8, 16 and 32: one request of 32,768 keys (32 units) 18.8, 18.8, 21.4 us; one of 24,000 25.1, 24.8, 26.8; 512 of up to
+// 3,000 (12 units) 149, 123, 124, as eight makes a join of all requests wide.
+constexpr int kJoinFew = 16, kJoinRows4 = 16;
+static_assert(kJoinFew <= 32, "a lane for each unit");
 constexpr int kJoinUnits = 1024;  // weights that are kept at a time
 
 template <int D>

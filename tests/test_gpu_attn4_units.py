@@ -1,5 +1,5 @@
-"""Single tokens over the 4-bit cache whose requests have more units than the join takes in one go: more than a warp has lanes
-(32), and more than it keeps weights of at a time (1,024). How many units a length has is read off the workspace's size, so a
+"""Single tokens over the 4-bit cache whose requests have more units than the join takes in one go: more than a
+thread takes in order (16), and more than it keeps weights of at a time (1,024). How many units a length has is read off the workspace's size, so a
 change of the rule that makes a request's units fewer fails here."""
 import pytest
 import torch
@@ -12,7 +12,7 @@ from test_gpu_attn4 import Case
 pytestmark = pytest.mark.gpu
 
 UNIT = {64: 2048, 128: 2048, 256: 1024}     # keys of a long request's unit
-LANES, WEIGHTS = 32, 1024
+IN_ORDER, WEIGHTS = 16, 1024
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -30,10 +30,10 @@ def units(keys, Hq, H, d):
 
 
 @pytest.mark.parametrize("Hq,H,d", [(2, 1, 64), (9, 1, 128), (8, 1, 256)])
-def test_more_units_than_lanes(Hq, H, d):
-    n = (LANES + 1) * UNIT[d]
-    assert units(n, Hq, H, d) == LANES + 1
-    lens = [n - UNIT[d], n - UNIT[d] + 1, n - 3, 5]        # 32 units, 33 and 33
+def test_more_units_than_one_thread_takes(Hq, H, d):
+    n = (2 * IN_ORDER + 1) * UNIT[d]
+    assert units(n, Hq, H, d) == 2 * IN_ORDER + 1
+    lens = [x * UNIT[d] for x in (IN_ORDER, IN_ORDER + 1, 2 * IN_ORDER)] + [IN_ORDER * UNIT[d] + 1, n - 3, 5]
     c = Case(d + 1, [1] * len(lens), [x - 1 for x in lens], Hq, H, d, 128)
     c.check(c.decode(), "decode")
 

@@ -38,7 +38,9 @@
 // order.
 //
 // Measured: 256 requests of 7,000 to 8,192 tokens (16 / 2 heads of 256) 204 us, 5.2 TB/s (copies alone 158 without partial sums
-// and join); 64 of 1 to 8,192 (28 / 4 of 128) 46 us; 2 of 131,071 38 us; one of 4,097 12.6 us.
+// and join); 64 of 1 to 8,192 (28 / 4 of 128) 46 us; 2 of 131,071 38 us; one of 4,097 12.6 us; 128 of 4,096 (32 / 8 of 64) 91 us, 3.1
+// TB/s. Groups of 16 heads (NT = 2), 64 requests of 7,000 to 8,192: 94 us at 256 (8 heads 66), 57 at 128 (41); of 32, two chunks that
+// read the cache once each, 94 at 128.
 #include "gdn_attn.cuh"
 #include "gdn_attn_units.cuh"
 #include "gdn_cache4.cuh"
@@ -56,8 +58,8 @@ constexpr float kFarAbove = 90.0f;     // log2 of the scales of V next to which 
 
 // Small units shorten the chain that a small batch waits for, and cost a large one partial sums and the start of a pipeline;
 // a unit of 256 keys of 256, 512 of 128 or 1,024 of 64 is the same 70 KB. 256 requests of about 8,000 tokens (16 / 2 heads of
-// 256) 216 us in up to 24 of the smaller ones and 206 in up to 12, one of 4,097 11.9 and 12.5; 128 of 4,096 (32 / 8 of 64) 99 us
-// from 512 keys on and 89 from 1,024.
+// 256) 214 us in up to 24 of the smaller ones and 204 in up to 12, one of 4,097 10.9 and 12.6; 128 of 4,096 (32 / 8 of 64) 101 us
+// from 512 keys on and 91 from 1,024.
 template <int D>
 using Units = UnitRule<D == 256 ? 8 : D == 128 ? 9 : 10, D == 256 ? 10 : 11, 12>;
 static_assert(kWarps == 4 && (1 << 11) / 16 / kWarps <= 32, "a lane for each 16 of a warp's keys of a unit");
@@ -190,7 +192,7 @@ struct Cfg {
                        kAtQ = kAtP + kWarps * kT * NT * 256, kAtFactor = kAtQ + NT * kG * 512, kAtMax = kAtFactor + 64, kAtSum = kAtMax + kWarps * 64,
                        kAtLens = kAtSum + kWarps * 64;
   // CTAs of an SM. One more costs registers, and with them instructions that are computed again: 256 requests of about 8,000
-  // tokens (D = 256, 8 heads) 213 us with 4 and 217 with 5.
+  // tokens (D = 256, 8 heads) 204 us with 4, 213 with 5 and 216 with 3. 16 heads: 3 and 4 the same.
   static constexpr int kCtas = NT == 2 ? 3 : 4;
   static constexpr int smem_of(int nb) { return 128 + kAtLens + 4 * (nb + nb / kCoarse + 2); }
   static_assert(kKeys % 128 == 0 && kAtP % 16 == 0 && kStep * kG == 128, "alignment: a place in a row is changed by bits of the address; 4 scales a lane");

@@ -2,7 +2,8 @@
 //
 // Format. e2m1 codes (a sign and 0, 0.5, 1, 1.5, 2, 3, 4, 6) in groups of 32 along the head; a group has one byte e and its
 // values are code * 2^(e - 127). A power of two for a scale makes both directions exact but for the one rounding to a code:
-// value * 2^(127 - e) is exact in fp32, and code * 2^(e - 127) is a bf16 value below 2^128.
+// value * 2^(127 - e) is exact in fp32, and code * 2^(e - 127) a bf16 value, but for 2^128 and above: what is larger than
+// 1.75 * 2^127 (byte 253, code 4) and the codes of a foreign cache's 253 and 254 read back infinite.
 //
 // Writer. Per token, head and group, with a the largest |x| of the finite values: e the least with a <= 7 * 2^(e - 127), at
 // least 63. (Up to 7 rounds to 6 by no more than the half step that 4 to 6 have anyway, so a limit of 6 would only make
@@ -13,10 +14,11 @@
 // pairs as they lie. The token with the even slot writes for both where the next one follows it in the call; a token alone
 // changes its half of the bytes by atomics (each bit has one writer, so the result has no order).
 //
-// Bound by memory, 2 bytes read and 17 / 32 written a value (the read-back the other way round), and next to that by
-// instructions: about 120 to a thread's 16 values, 2.2 to 2.6 issued a clock. 131,071 tokens (2 heads of 256) read back in 59 us,
-// 5.8 TB/s (61 with three CTAs an SM, of 67 registers); 24,200 tokens of prompts (8 heads of 128) written in 32 us, 3.9 TB/s,
-// and read back in 27; 256 single tokens 2.4 us each way.
+// Bound by memory, 2 bytes read and 17 / 32 written a value (the read-back the other way round); next to that the read-back by
+// instructions (181 to a thread's 16 values, 2.9 issued a clock, the ALU at 59%), the writer by waiting for its loads (164, 2.1 a
+// clock, the ALU at 52%). 131,071 tokens (2 heads of 256) read back in 58 us, 5.9 TB/s (61 with three CTAs an SM, of 67
+// registers); 26,734 tokens of prompts (8 heads of 128, 139 MB) written in 30 us, 4.7 TB/s, and read back in 27; 256 single
+// tokens 2.1 and 2.4 us.
 #include "gdn_attn.cuh"
 #include "gdn_cache4.cuh"
 #include "gdn_internal.h"
@@ -549,6 +551,8 @@ cudaError_t launch_cache4_read(const Read4Args& a, cudaStream_t s) {
 cudaError_t launch_cache4_expand(const Expand4Args& a, cudaStream_t s) {
   // warps of an item: one for each 4,096 values
   const int size = a.c.bs * a.c.d, ts = size >= 32768 ? 8 : size >= 16384 ? 4 : size >= 8192 ? 2 : 1, teams = kThreads / 32 / ts;
+  // eight CTAs an SM, two rounds of those that fit: with four, prompts over pages of 16 (4 heads of 64, 20,000 keys) 37.4 us for 39.4
+  // and 64 tokens at 131,000 (2 heads of 256) 180 for 178; with 64, 39.3 and 185
   const int64_t items = (static_cast<int64_t>(a.held) * a.c.H * 2 + teams - 1) / teams, most = 8 * static_cast<int64_t>(sm_count());
   const int grid = static_cast<int>(items < most ? items : most);
   auto kern = ts == 8 ? cache4_expand_kernel<8> : ts == 4 ? cache4_expand_kernel<4> : ts == 2 ? cache4_expand_kernel<2> : cache4_expand_kernel<1>;

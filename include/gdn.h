@@ -528,7 +528,7 @@ gdn_status gdn_attn_prefill(const void* q, int64_t q_stride, const int32_t* cu_t
  * Per token with position p, head, and pair i of the head's first rot_dim elements (HALVES: elements i and i + rot_dim / 2;
  * INTERLEAVED: 2 i and 2 i + 1), with a = p * w_i:
  *   (x1, x2) -> factor * (x1 cos a - x2 sin a, x2 cos a + x1 sin a)
- * The elements past rot_dim are copied, as bits. Angles are exact to 2^-31 of a turn at any position, but for what the table is
+ * The elements past rot_dim are copied, as bits. Angles are exact to 2^-26 of a turn at any position, but for what the table is
  * rounded to (2^-55 of a turn a position); sines and products are fp32, and the result is rounded once.
  *
  *   q, k       [total_tokens] rows of heads * head_dim bf16, q_stride and k_stride elements apart (slices of one projection are

@@ -468,7 +468,10 @@ class RopeTable:
         half = rot_dim // 2
         w, f = (ctypes.c_double * half)(), ctypes.c_float(float(factor))
         if freqs is None:
-            kind = {"none": GDN_ROPE_PLAIN, "linear": GDN_ROPE_LINEAR, "ntk": GDN_ROPE_NTK, "yarn": GDN_ROPE_YARN}[scaling]
+            kinds = {"none": GDN_ROPE_PLAIN, "linear": GDN_ROPE_LINEAR, "ntk": GDN_ROPE_NTK, "yarn": GDN_ROPE_YARN}
+            if scaling not in kinds:
+                raise ValueError(f"scaling must be one of {', '.join(kinds)}, not {scaling!r}")
+            kind = kinds[scaling]
             _check(lib().gdn_rope_frequencies(rot_dim, float(base), kind, float(factor), int(trained_len), w, ctypes.byref(f)))
         else:
             if len(freqs) != half:

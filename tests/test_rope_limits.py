@@ -31,3 +31,8 @@ def test_an_output_without_its_input():
     q, pos = torch.zeros(3, 2, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
     with pytest.raises(ValueError, match="k_out without k"):
         gdn.gdn_rope(q, None, pos, q, q, gdn.RopeTable(64, device="cpu"))
+
+
+def test_a_scaling_that_is_none_of_them():
+    with pytest.raises(ValueError, match="none, linear, ntk, yarn"):
+        gdn.RopeTable(64, scaling="dynamic", device="cpu")

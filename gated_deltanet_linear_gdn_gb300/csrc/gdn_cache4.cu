@@ -372,10 +372,11 @@ __global__ void __launch_bounds__(kThreads, 4) cache4_expand_kernel(const __grid
   const Cache4& c = a.c;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, team = warp / TS, in = tid - team * kLanes;
   const int cap = a.max_blocks * c.bs, block = 31 - __clz(c.bs);
-  // pages of the requests that have new tokens. One that there is no room for gets a table of no pages, as those behind it
+  // pages of the requests that have new tokens, in a range of rows that there is (the attention takes no others). One that there is
+  // no room for gets a table of no pages, as those behind it
   auto pages_of = [&](int b) {
-    const int len = min(max(a.lens[b], 0), cap);
-    return a.cu_tokens[b + 1] > a.cu_tokens[b] ? (len + c.bs - 1) >> block : 0;
+    const int len = min(max(a.lens[b], 0), cap), from = a.cu_tokens[b], to = a.cu_tokens[b + 1];
+    return from >= 0 && to > from && to <= a.T ? (len + c.bs - 1) >> block : 0;
   };
   {
     int carry = 0;

@@ -51,7 +51,7 @@ struct Expand4Args {
   int max_blocks;
   const int32_t* lens;
   const int32_t* cu_tokens;
-  int B;
+  int B, T;
   int held;               // pages that there is room for
   int32_t* table;         // [B, max_blocks]
   uint8_t* k;             // [held, H, bs, d] e4m3

@@ -307,6 +307,7 @@ gdn_status gdn_attn4_prefill(const void* q, int64_t q_stride, const int32_t* cu_
   x.lens = lens;
   x.cu_tokens = cu_tokens;
   x.B = num_seqs;
+  x.T = total_tokens;
   x.held = L.held;
   x.table = reinterpret_cast<int32_t*>(ws);
   x.k = ws + L.k;

@@ -128,3 +128,35 @@ def test_a_large_value_in_a_unit(up, d, Hq, k):
     c.check(got, "decode", v_exp=up)
     share = n * 2.0 ** (-k * 0.5 * d ** 0.5 * 1.4427)
     assert share > 0.08 and bool((got.double() < 2.0 ** (up - 1) / (1 + 0.9 * share)).all())
+
+
+@pytest.mark.parametrize("which,T,up", [("decode", 3, 108), ("prefill", 40, 72)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_large_value_over_the_8_bit_cache(which, T, up, d):
+    """What the header says of a row's sum: with a v_scale of up to 2^100 (prompts 2^64) it has what is far below its largest.
+    One value of 2^up, 1,500 keys with about 2^-12 of its probability."""
+    r = eight.rand(d)
+    u = torch.sign(r(d)) * 0.5
+    k = 0.2 * r(1500, 1, d)
+    k[0] = u * (8 / (0.25 * d ** 0.5))
+    v = 1.0 + 0.3 * r(1500, 1, d)
+    v[0] = 2.0 ** up * (1.0 + 0.3 * r(d).clamp(-2, 2))
+    q = (u + 0.02 * r(T, 4, d)).bfloat16()
+    c = eight.Pages(k, v, 16)
+    assert up - 9 < float(torch.log2(c.vs.max())) < up - 8 + 0.1
+    eight.check(c, q, which)
+
+
+@pytest.mark.parametrize("d,k", [(64, 2.0), (128, 1.5), (256, 1.0)])
+def test_a_large_value_in_prompts(d, k):
+    """The same over the 4-bit cache: a group's scale of 2^70 is a block's of 2^64."""
+    n, bs, at = 1024, 32, 100
+    c = Case(211, [9], [n - 9], 2, 1, d, bs)
+    c.q[:] = torch.where(c.q[:1, :1] > 0, 0.5, -0.5)
+    c.cache[0].zero_()
+    c.cache[2][:] = 127
+    page = c.table[0, at // bs].long()
+    sign = torch.signbit(c.q[0, 0]).to(torch.uint8) * 8 + {2.0: 4, 1.5: 3, 1.0: 2}[k]
+    c.cache[0][page, 0, at % bs] = sign[0::2] | sign[1::2] << 4
+    c.cache[3][page, 0, at % bs] = 127 + 70
+    c.check(c.prefill(), "prefill", v_exp=70)

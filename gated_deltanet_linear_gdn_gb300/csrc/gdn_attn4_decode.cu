@@ -54,7 +54,9 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kRise = 5.0f;          // log2 of what a score may pass the running maximum by
 constexpr float kTop = 9.0f;           // log2 of what the running maximum stands for
-constexpr float kFarAbove = 90.0f;     // log2 of the scales of V next to which p in the sum may be below 2^-126, and of the largest not below 2^-34
+// log2 of the scales of V next to which a p of the sum that is not below 2^-34 of the largest may be below 2^-126 (from 2^101 on). A
+// byte behind a request's keys may set this off, too: up to 2^90 what is added is below half a step of any sum.
+constexpr float kFarAbove = 90.0f;
 
 // Small units shorten the chain that a small batch waits for, and cost a large one partial sums and the start of a pipeline;
 // a unit of 256 keys of 256, 512 of 128 or 1,024 of 64 is the same 70 KB. 256 requests of about 8,000 tokens (16 / 2 heads of

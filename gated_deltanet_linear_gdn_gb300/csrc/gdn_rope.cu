@@ -170,9 +170,9 @@ cudaError_t launch_rope(RopeArgs a, cudaStream_t s) {
   a.by_rows = reciprocal(a.Hq + a.H);
   const int half = a.rot / 2;
   if (wide) {
-    // Threads of a token: few tokens want short turns over their heads, many want each thread to have several rows for its sines. With 256, 128
-    // and 64: 8 tokens of 136 heads of 128 2.9, 3.2, 4.8 us; 256 of 40 2.7, 2.6, 2.8 and of 136 3.9, 4.2, 5.1; 1,024 of 40 5.6, 3.8,
-    // 4.0; 1,536 9.1, 6.5, 6.1; 8,192 41.5, 27.4, 27.0.
+    // Threads of a token: few tokens want short turns over their heads, many want each thread to have several rows for its sines.
+    // With 256, 128 and 64: 8 tokens of 136 heads of 128 2.9, 3.2, 4.8 us; 256 of 40 2.7, 2.6, 2.8 and of 136 3.9, 4.2, 5.1; 1,024 of
+    // 40 5.6, 3.8, 4.0; 1,536 9.1, 6.5, 6.1; 8,192 41.5, 27.4, 27.0.
     const int threads = a.T <= kRopeFew ? kRopeWide : a.T <= kRopeMany ? 128 : 64;
     auto kern = a.interleaved ? rope_wide_kernel<true> : rope_wide_kernel<false>;
     kern<<<a.T, threads, 2 * half * sizeof(float), s>>>(a);

@@ -612,7 +612,7 @@ gdn_status gdn_attn4_decode(const void* q, int64_t q_stride, const void* k_cache
  * gdn_attn4_prefill -- gdn_attn_prefill over the 4-bit cache. The call first writes the pages that its requests with new
  * tokens hold into its workspace, in 8 bits (values down to 2^-14 of a block's and head's largest scale as they are, below
  * that rounded to 2^-18 of its largest value; V's largest scale counts as 2^-84 at least, so that of smaller values multiples of
- * 2^-99 remain); the rest is that call, with its arithmetic.
+ * 2^-99 remain); the rest is that call, with its arithmetic (a block's v_scale is 2^-6 of its largest scale).
  *   held_blocks  what there is room for: a bound on the blocks that those requests hold together (a block that two of them
  *                hold counts twice). Requests past it, in row order, set GDN_DEVERR_BLOCKS and have no block (which sets
  *                GDN_DEVERR_BLOCK_RANGE, too): zeros come out
